@@ -17,11 +17,15 @@ EP_LAYOUT_CONTIGUOUS, EP_LAYOUT_PADDED = 0, 1
 (EP_QUANT_BF16, EP_QUANT_FP8_E4M3_G128, EP_QUANT_FP8_E4M3_TOKEN, EP_QUANT_INT8_TOKEN,
  EP_QUANT_MXFP8_E4M3, EP_QUANT_MXFP8_E5M2, EP_QUANT_MXFP4_E2M1) = range(7)
 
+EP_DTYPE_BF16, EP_DTYPE_F32 = 0, 1
+EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = 0, 1
+
 # name -> (restype, argtypes); every pointer is passed as an integer address
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
 _ST = ctypes.c_int
+_F = ctypes.c_float
 SIGNATURES = {
     "ep_status_string": (ctypes.c_char_p, [_ST]),
     "ep_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
@@ -43,6 +47,11 @@ SIGNATURES = {
     "ep_combine_ranks": (_ST, [_P, _I, _I, _P, _I, _I, _P, _P]),
     "ep_dispatch_expert_choice": (_ST, [_P, _I, _I, _P, _I, _I, _P, _P, _P, _P, _P, _SZ, _P]),
     "ep_combine_expert_choice": (_ST, [_P, _P, _I, _I, _I, _P, _P, _I, _P, _P]),
+    "ep_route": (_ST, [_P, _I, _I, _I, _I, _I, _P, _I, _F, _P, _P, _P, _P]),
+    "ep_balance_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "ep_balance_loss": (_ST, [_P, _I, _I, _I, _P, _I, _I, _P, _I, _F, _P, _P, _P, _P, _P, _SZ,
+                              _P]),
+    "ep_router_backward": (_ST, [_P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P, _I, _P, _P, _P]),
 }
 
 _lib = None
@@ -173,3 +182,28 @@ def ep_combine_partial(y, y_rows, H, slot, weights, S, K, partial, stream, check
 def ep_combine_ranks(partial, rows, H, pack_pos, T, R, out, stream, check=True):
     st = lib().ep_combine_ranks(partial, rows, H, pack_pos, T, R, out, stream)
     return _check("ep_combine_ranks", st) if check else st
+
+
+def ep_route(logits, dtype, T, E, K, score, bias, renormalise, scale, topk_idx, topk_weights,
+             num_invalid, stream, check=True):
+    st = lib().ep_route(logits, dtype, T, E, K, score, bias, renormalise, scale, topk_idx,
+                        topk_weights, num_invalid, stream)
+    return _check("ep_route", st) if check else st
+
+
+def ep_balance_workspace_bytes(T: int, E: int, S: int) -> int:
+    return lib().ep_balance_workspace_bytes(T, E, S)
+
+
+def ep_balance_loss(logits, dtype, T, E, topk_idx, K, score, seq_offsets, S, coef, counts, slope,
+                    loss, num_invalid, ws, ws_bytes, stream, check=True):
+    st = lib().ep_balance_loss(logits, dtype, T, E, topk_idx, K, score, seq_offsets, S, coef,
+                               counts, slope, loss, num_invalid, ws, ws_bytes, stream)
+    return _check("ep_balance_loss", st) if check else st
+
+
+def ep_router_backward(logits, dtype, T, E, K, score, renormalise, scale, topk_idx, d_weights,
+                       slope, seq_offsets, S, d_loss, d_logits, stream, check=True):
+    st = lib().ep_router_backward(logits, dtype, T, E, K, score, renormalise, scale, topk_idx,
+                                  d_weights, slope, seq_offsets, S, d_loss, d_logits, stream)
+    return _check("ep_router_backward", st) if check else st

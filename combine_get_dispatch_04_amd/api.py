@@ -506,3 +506,164 @@ def combine_ranks(partial: torch.Tensor, pack: RankPack,
         N.ep_combine_ranks(_ptr(partial), partial.shape[0], H, _ptr(pack.pack_pos), T, R,
                            _ptr(out), _stream(dev))
     return out
+
+
+# ---------------------------------------------------------------- the router
+_SCORES = {"softmax": N.EP_SCORE_SOFTMAX, "sigmoid": N.EP_SCORE_SIGMOID}
+_LOGIT_DTYPES = {torch.bfloat16: N.EP_DTYPE_BF16, torch.float32: N.EP_DTYPE_F32}
+
+
+def _logits_dtype(logits: torch.Tensor, score: str) -> int:
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a tensor")
+    if logits.dtype not in _LOGIT_DTYPES:
+        raise ValueError(f"logits must be torch.bfloat16 or torch.float32, got {logits.dtype}")
+    _need(logits, "logits", logits.dtype, 2)
+    if score not in _SCORES:
+        raise ValueError(f"unknown score {score!r}")
+    return _LOGIT_DTYPES[logits.dtype]
+
+
+@dataclass
+class Routing:
+    """Result of route, and what route_backward needs of it.  The logits must
+    still hold their values when the backward runs."""
+    topk_idx: torch.Tensor                     # [T, K] int32, -1 = nothing left to choose
+    topk_weights: torch.Tensor                 # [T, K] float32
+    num_invalid: torch.Tensor                  # [T] int32: NaN and +inf logits of each token
+    logits: torch.Tensor
+    score: str
+    renormalise: bool
+    scale: float
+
+
+@dataclass
+class BalanceLoss:
+    """Result of balance_loss, and what its backward needs of it."""
+    loss: torch.Tensor                         # [1] float32
+    num_tokens_per_expert: torch.Tensor        # [S, E] int32: entries of topk_idx per sequence
+    num_invalid: torch.Tensor                  # [2] int32: bad entries of topk_idx, bad logits
+    slope: torch.Tensor                        # [S*E + 1] float32
+    logits: torch.Tensor
+    score: str
+    seq_offsets: Optional[torch.Tensor]
+
+
+def route(logits: torch.Tensor, num_topk: int, *, score: str = "softmax",
+          bias: Optional[torch.Tensor] = None, renormalise: bool = True,
+          scale: float = 1.0) -> Routing:
+    """The router in front of dispatch: each token's num_topk experts with the
+    largest scores (descending, ties to the lower expert) and their weights.
+    logits: bf16 or fp32 [T, E]; a -inf logit masks its expert, a row of them
+    is padding (topk_idx -1).  score: "softmax" or "sigmoid"; with "sigmoid" a
+    `bias` [E] (fp32) may be added to the scores for the choice alone.  The
+    weights are scale times the scores, renormalised over the chosen experts
+    (as workloads.router_topk draws them) or as they are.  Tensors carry no
+    autograd graph: the gradient is route_backward."""
+    dt = _logits_dtype(logits, score)
+    T, E = logits.shape
+    K = int(num_topk)
+    if bias is not None:
+        if score != "sigmoid":
+            raise ValueError("a selection bias needs sigmoid scores")
+        _need(bias, "bias", torch.float32, 1)
+        if bias.shape[0] != E:
+            raise ValueError("bias must be [E]")
+    if K < 1 or K > E:
+        raise ValueError(f"num_topk must be in [1, {E}], got {K}")
+    dev = logits.device
+    _same_device(dev, bias=bias)
+    idx = torch.empty((T, K), dtype=torch.int32, device=dev)
+    w = torch.empty((T, K), dtype=torch.float32, device=dev)
+    ninv = torch.empty(T, dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        N.ep_route(_ptr(logits), dt, T, E, K, _SCORES[score], _ptr(bias), int(renormalise),
+                   float(scale), _ptr(idx), _ptr(w), _ptr(ninv), _stream(dev))
+    return Routing(idx, w, ninv, logits, score, bool(renormalise), float(scale))
+
+
+def balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, *, score: str = "softmax",
+                 coef: float = 1.0, seq_offsets: Optional[torch.Tensor] = None) -> BalanceLoss:
+    """The balance loss of a choice of experts, with their counts:
+    coef * mean over the sequences of sum_e f_e P_e, where f_e is the share of
+    expert e among the sequence's entries of topk_idx, times E, and P_e its
+    mean probability.  seq_offsets: int32 [S+1], non-decreasing (default: all
+    tokens are one sequence); tokens outside all sequences take no part.  Its
+    gradient is balance_loss_backward, or route_backward with balance=."""
+    dt = _logits_dtype(logits, score)
+    _need(topk_idx, "topk_idx", torch.int32, 2)
+    T, E = logits.shape
+    if topk_idx.shape[0] != T:
+        raise ValueError("logits and topk_idx disagree on the number of tokens")
+    K = topk_idx.shape[1]
+    S = 1
+    if seq_offsets is not None:
+        _need(seq_offsets, "seq_offsets", torch.int32, 1)
+        S = seq_offsets.shape[0] - 1
+        if S < 1:
+            raise ValueError("seq_offsets needs at least two entries")
+    dev = logits.device
+    _same_device(dev, topk_idx=topk_idx, seq_offsets=seq_offsets)
+    ws_bytes = N.ep_balance_workspace_bytes(T, E, S)
+    if ws_bytes == 0:
+        raise N.EpError("ep_balance_workspace_bytes", N.EP_ERR_INVALID_ARG)
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    counts = torch.empty((S, E), dtype=torch.int32, device=dev)
+    slope = torch.empty(S * E + 1, dtype=torch.float32, device=dev)
+    loss = torch.empty(1, dtype=torch.float32, device=dev)
+    ninv = torch.empty(2, dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        N.ep_balance_loss(_ptr(logits), dt, T, E, _ptr(topk_idx), K, _SCORES[score],
+                          _ptr(seq_offsets), S, float(coef), _ptr(counts), _ptr(slope),
+                          _ptr(loss), _ptr(ninv), _ptr(ws), ws_bytes, _stream(dev))
+    return BalanceLoss(loss, counts, ninv, slope, logits, score, seq_offsets)
+
+
+def _router_backward(logits, score, d_w, routing, d_loss, balance):
+    T, E = logits.shape
+    dev = logits.device
+    K, renorm, scale, idx = 1, False, 1.0, None
+    if d_w is not None:
+        _need(d_w, "d_weights", torch.float32, 2)
+        idx, renorm, scale = routing.topk_idx, routing.renormalise, routing.scale
+        if tuple(d_w.shape) != tuple(idx.shape):
+            raise ValueError("d_weights must be [T, K] like the weights")
+        K = idx.shape[1]
+    slope, seq, S = None, None, 1
+    if balance is not None:
+        if d_loss is None:
+            raise ValueError("the balance loss's gradient needs d_loss")
+        _need(d_loss, "d_loss", torch.float32, 1)
+        if d_loss.shape[0] != 1:
+            raise ValueError("d_loss must be [1]")
+        slope, seq = balance.slope, balance.seq_offsets
+        S = 1 if seq is None else seq.shape[0] - 1
+    _same_device(dev, d_weights=d_w, topk_idx=idx, d_loss=d_loss, slope=slope, seq_offsets=seq)
+    d_logits = torch.empty_like(logits)
+    with torch.cuda.device(dev):
+        N.ep_router_backward(_ptr(logits), _LOGIT_DTYPES[logits.dtype], T, E, K, _SCORES[score],
+                             int(renorm), scale, _ptr(idx), _ptr(d_w), _ptr(slope), _ptr(seq), S,
+                             _ptr(d_loss), _ptr(d_logits), _stream(dev))
+    return d_logits
+
+
+def route_backward(d_weights: torch.Tensor, routing: Routing, *,
+                   balance: Optional[BalanceLoss] = None,
+                   d_loss: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """d_logits [T, E] (the logits' dtype) from d_weights [T, K] fp32.  With
+    `balance` and `d_loss` ([1] fp32, on the GPU) the balance loss's gradient
+    is added in the same pass; it must be of the same logits and score."""
+    if balance is None and d_loss is not None:
+        raise ValueError("d_loss needs balance")
+    if balance is not None and (balance.logits.data_ptr() != routing.logits.data_ptr() or
+                                balance.logits.shape != routing.logits.shape or
+                                balance.logits.dtype != routing.logits.dtype or
+                                balance.score != routing.score):
+        raise ValueError("balance is of other logits or another score than routing")
+    return _router_backward(routing.logits, routing.score, d_weights, routing, d_loss, balance)
+
+
+def balance_loss_backward(d_loss: torch.Tensor, balance: BalanceLoss) -> torch.Tensor:
+    """d_logits [T, E] (the logits' dtype) of the balance loss; zero for tokens
+    outside all sequences.  d_loss: [1] fp32, on the GPU."""
+    return _router_backward(balance.logits, balance.score, None, None, d_loss, balance)

@@ -474,4 +474,114 @@ ep_status_t ep_combine_expert_choice(const uint16_t *y, const float *weights, in
                                             static_cast<hipStream_t>(stream)));
 }
 
+// ---------------------------------------------------------------- the router
+namespace {
+
+ep_status_t check_router_sizes(int T, int E, int K, ep_dtype_t dtype, ep_score_t score)
+{
+    if (T < 0 || E < 1 || K < 1 || (int64_t)T * K > kI32)
+        return EP_ERR_INVALID_ARG;
+    if (dtype != EP_DTYPE_BF16 && dtype != EP_DTYPE_F32)
+        return EP_ERR_INVALID_ARG;
+    if (score != EP_SCORE_SOFTMAX && score != EP_SCORE_SIGMOID)
+        return EP_ERR_INVALID_ARG;
+    if (E > kMaxExperts)
+        return EP_ERR_UNSUPPORTED;
+    return EP_OK;
+}
+
+ep_status_t check_sequences(int E, const int32_t *seq_offsets, int S)
+{
+    if (S < 1 || (!seq_offsets && S != 1) || (int64_t)S * E > kI32)
+        return EP_ERR_INVALID_ARG;
+    // one block of 1024 threads per 64 experts of a sequence: 32-bit grid
+    if ((int64_t)S * ((E + 63) / 64) >= 1 << 22)
+        return EP_ERR_UNSUPPORTED;
+    return EP_OK;
+}
+
+}  // namespace
+
+ep_status_t ep_route(const void *logits, ep_dtype_t dtype, int T, int E, int K, ep_score_t score,
+                     const float *bias, int renormalise, float scale, int32_t *topk_idx,
+                     float *topk_weights, int32_t *num_invalid, void *stream)
+{
+    ep_status_t st = check_router_sizes(T, E, K, dtype, score);
+    if (st != EP_OK)
+        return st;
+    if (K > E || (bias && score != EP_SCORE_SIGMOID))
+        return EP_ERR_INVALID_ARG;
+    if (K > ep::kMaxRouteTopk)
+        return EP_ERR_UNSUPPORTED;
+    if (T > 0 && (!logits || !topk_idx || !topk_weights))
+        return EP_ERR_INVALID_ARG;
+    if (!aligned(logits, 16) || !aligned(bias, 4) || !aligned(topk_idx, 4) ||
+        !aligned(topk_weights, 4) || !aligned(num_invalid, 4))
+        return EP_ERR_INVALID_ARG;
+    return hip_status(ep::launch_route(logits, dtype == EP_DTYPE_BF16, T, E, K,
+                                       score == EP_SCORE_SIGMOID, bias, renormalise != 0, scale,
+                                       topk_idx, topk_weights, num_invalid,
+                                       static_cast<hipStream_t>(stream)));
+}
+
+size_t ep_balance_workspace_bytes(int T, int E, int S)
+{
+    if (check_router_sizes(T, E, 1, EP_DTYPE_F32, EP_SCORE_SOFTMAX) != EP_OK || S < 1 ||
+        (int64_t)S * E > kI32)
+        return 0;
+    return ep::make_balance_plan(T, E, S).bytes;
+}
+
+ep_status_t ep_balance_loss(const void *logits, ep_dtype_t dtype, int T, int E,
+                            const int32_t *topk_idx, int K, ep_score_t score,
+                            const int32_t *seq_offsets, int S, float coef, int32_t *counts,
+                            float *slope, float *loss, int32_t *num_invalid, void *ws,
+                            size_t ws_bytes, void *stream)
+{
+    ep_status_t st = check_router_sizes(T, E, K, dtype, score);
+    if (st == EP_OK)
+        st = check_sequences(E, seq_offsets, S);
+    if (st != EP_OK)
+        return st;
+    if ((T > 0 && (!logits || !topk_idx)) || !counts || !slope || !loss || !num_invalid)
+        return EP_ERR_INVALID_ARG;
+    if (!aligned(logits, 16) || !aligned(topk_idx, 4) || !aligned(seq_offsets, 4) ||
+        !aligned(counts, 4) || !aligned(slope, 4) || !aligned(loss, 4) || !aligned(num_invalid, 4))
+        return EP_ERR_INVALID_ARG;
+    const ep::BalancePlan p = ep::make_balance_plan(T, E, S);
+    if ((st = check_ws(ws, ws_bytes, p.bytes)) != EP_OK)
+        return st;
+    return hip_status(ep::launch_balance(p, logits, dtype == EP_DTYPE_BF16, topk_idx, K,
+                                         score == EP_SCORE_SIGMOID, seq_offsets, coef, counts,
+                                         slope, loss, num_invalid, static_cast<char *>(ws),
+                                         static_cast<hipStream_t>(stream)));
+}
+
+ep_status_t ep_router_backward(const void *logits, ep_dtype_t dtype, int T, int E, int K,
+                               ep_score_t score, int renormalise, float scale,
+                               const int32_t *topk_idx, const float *d_weights, const float *slope,
+                               const int32_t *seq_offsets, int S, const float *d_loss,
+                               void *d_logits, void *stream)
+{
+    ep_status_t st = check_router_sizes(T, E, K, dtype, score);
+    if (st == EP_OK && slope)
+        st = check_sequences(E, seq_offsets, S);
+    if (st != EP_OK)
+        return st;
+    if (T > 0 && !d_weights && !slope)
+        return EP_ERR_INVALID_ARG;
+    if (d_weights && K > ep::kMaxRouteTopk)
+        return EP_ERR_UNSUPPORTED;
+    if ((slope && !d_loss) || (T > 0 && (!logits || !d_logits || (d_weights && !topk_idx))))
+        return EP_ERR_INVALID_ARG;
+    if (!aligned(logits, 16) || !aligned(d_logits, 16) || !aligned(topk_idx, 4) ||
+        !aligned(d_weights, 4) || !aligned(slope, 4) || !aligned(seq_offsets, 4) ||
+        !aligned(d_loss, 4))
+        return EP_ERR_INVALID_ARG;
+    return hip_status(ep::launch_router_backward(
+        logits, dtype == EP_DTYPE_BF16, T, E, K, score == EP_SCORE_SIGMOID, renormalise != 0,
+        scale, topk_idx, d_weights, slope, seq_offsets, S, d_loss, d_logits,
+        static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

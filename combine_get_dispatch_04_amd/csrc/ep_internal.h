@@ -102,6 +102,29 @@ hipError_t launch_ec_combine(const uint16_t *y, const float *w, int E, int C, in
                              const int32_t *tok_off, const int32_t *tok_ent, int T,
                              uint16_t *out, hipStream_t s);
 
+// The router (ep_router.hip).  `bf16`: logits in bf16, else fp32.
+constexpr int kMaxRouteTopk = 64;     // one lane per choice
+
+struct BalancePlan {
+    int T, E, S;
+    int CT, nchunk;   // tokens per chunk, chunks
+    int eb;           // blocks of 64 experts
+    size_t off_arrived, off_part, off_parts, off_tails, bytes;
+};
+BalancePlan make_balance_plan(int T, int E, int S);
+
+hipError_t launch_route(const void *logits, bool bf16, int T, int E, int K, bool sigmoid,
+                        const float *bias, bool renorm, float scale, int32_t *topk_idx,
+                        float *topk_w, int32_t *num_invalid, hipStream_t s);
+hipError_t launch_balance(const BalancePlan &p, const void *logits, bool bf16,
+                          const int32_t *topk_idx, int K, bool sigmoid, const int32_t *seq,
+                          float coef, int32_t *counts, float *slope, float *loss,
+                          int32_t *num_invalid, char *ws, hipStream_t s);
+hipError_t launch_router_backward(const void *logits, bool bf16, int T, int E, int K, bool sigmoid,
+                                  bool renorm, float scale, const int32_t *topk_idx,
+                                  const float *d_w, const float *slope, const int32_t *seq, int S,
+                                  const float *d_loss, void *d_logits, hipStream_t s);
+
 inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // LDS bytes one block may take on the current device (cached per device).

@@ -1,0 +1,807 @@
+// ep_router.hip -- the router in front of the dispatch: the choice of K
+// experts per token with their weights, the balance loss with the experts'
+// counts, and one backward kernel for both.
+//
+// Scores.  z is a row of logits; a NaN or +inf logit counts as masked, like
+// -inf: it is never chosen and its score is 0.  softmax: s_e = exp(z_e - m),
+// m = max z.  sigmoid: s_e = 1 / (1 + exp(-z_e)); where every z_e of the sum
+// lies below kSmallSigmoid, exp(z_e - m) stands for it, which differs from
+// s_e / s_m by less than 2^-28 and does not underflow.
+//
+// Everything here is one wave per row (lane l holds experts l, 64 + l, ...):
+// a row's logits are read once into registers, and sums, maxima and the
+// choice are reductions over the 64 lanes, with no shared memory but the
+// scatter of the backward.
+#include "ep_common.h"
+#include "ep_internal.h"
+
+namespace ep {
+
+namespace {
+
+constexpr float kNegInf = -__builtin_huge_valf();
+
+template <int V>
+struct vpl_t {
+    static constexpr int value = V;
+};
+constexpr float kSmallSigmoid = -20.0f;
+
+// ---------------------------------------------------------------- reductions
+// Row shifts inside 16 lanes, then the row broadcasts, as in
+// wave_inclusive_scan: lane 63 ends up with all 64 lanes' value.  The order
+// of the additions is fixed, so sums are the same for every run.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_f(float old, float v)
+{
+    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
+        (int)__float_as_uint(old), (int)__float_as_uint(v), CTRL, ROWS, 0xF, false));
+}
+__device__ __forceinline__ float last_lane(float v)
+{
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), kWave - 1));
+}
+__device__ __forceinline__ float lane_value(float v, int lane)
+{
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
+}
+__device__ __forceinline__ float wave_sum_f(float v)
+{
+    v += dpp_f<0x111, 0xF>(0.0f, v);
+    v += dpp_f<0x112, 0xF>(0.0f, v);
+    v += dpp_f<0x114, 0xF>(0.0f, v);
+    v += dpp_f<0x118, 0xF>(0.0f, v);
+    v += dpp_f<0x142, 0xA>(0.0f, v);
+    v += dpp_f<0x143, 0xC>(0.0f, v);
+    return last_lane(v);
+}
+__device__ __forceinline__ float wave_max_f(float v)
+{
+    v = fmaxf(v, dpp_f<0x111, 0xF>(kNegInf, v));
+    v = fmaxf(v, dpp_f<0x112, 0xF>(kNegInf, v));
+    v = fmaxf(v, dpp_f<0x114, 0xF>(kNegInf, v));
+    v = fmaxf(v, dpp_f<0x118, 0xF>(kNegInf, v));
+    v = fmaxf(v, dpp_f<0x142, 0xA>(kNegInf, v));
+    v = fmaxf(v, dpp_f<0x143, 0xC>(kNegInf, v));
+    return last_lane(v);
+}
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_u(uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ uint32_t wave_max_u(uint32_t v)
+{
+    v = umax(v, dpp_u<0x111, 0xF>(v));
+    v = umax(v, dpp_u<0x112, 0xF>(v));
+    v = umax(v, dpp_u<0x114, 0xF>(v));
+    v = umax(v, dpp_u<0x118, 0xF>(v));
+    v = umax(v, dpp_u<0x142, 0xA>(v));
+    v = umax(v, dpp_u<0x143, 0xC>(v));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, kWave - 1);
+}
+
+// ---------------------------------------------------------------- a row
+// A logit as fp32; invalid ones (NaN, +inf) give -inf and are flagged.  The
+// addition of +0 turns -0 into +0, so that the two are one value in the order.
+struct F32 {
+    typedef float type;
+    static __device__ __forceinline__ float get(const float *p) { return *p; }
+    static __device__ __forceinline__ void put(float *p, float v) { *p = v; }
+};
+struct Bf16 {
+    typedef uint16_t type;
+    static __device__ __forceinline__ float get(const uint16_t *p) { return bf16_lo(*p); }
+    static __device__ __forceinline__ void put(uint16_t *p, float v)
+    {
+        *p = (uint16_t)f32_to_bf16_rne(v);
+    }
+};
+__device__ __forceinline__ bool bad_logit(float z)
+{
+    return !(z < __builtin_huge_valf());
+}
+__device__ __forceinline__ float clean_logit(float z)
+{
+    return bad_logit(z) ? kNegInf : z + 0.0f;
+}
+__device__ __forceinline__ float sigmoid_f(float z) { return 1.0f / (1.0f + expf(-z)); }
+
+// Order-preserving bits: larger float, larger integer; 0 is below them all
+// and stands for a masked entry.
+__device__ __forceinline__ uint32_t order_bits(float v)
+{
+    const uint32_t u = __float_as_uint(v);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_order_bits(uint32_t k)
+{
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+// Row scores for the probabilities: see the head of the file.  `top` is the
+// row's maximum (-inf in a row that is masked throughout).
+__device__ __forceinline__ float row_score(float z, float top, bool sigmoid)
+{
+    if (!(z > kNegInf))
+        return 0.0f;
+    return sigmoid && top >= kSmallSigmoid ? sigmoid_f(z) : expf(z - top);
+}
+
+// ---------------------------------------------------------------- the choice
+// The order of two keys sigmoid(z) + bias that lie this close (relative to
+// max(1, |key|)) is not settled in fp32: expf is off by at most 2^-23 of its
+// value, the sum and the quotient by 2^-24 each, so a score by less than
+// 2^-22, and the addition of the bias by 2^-24 of the key; two keys by twice
+// that, below 2^-20.
+constexpr float kKeyGap = 0x1p-20f;
+
+// The choice by sigmoid(z) + bias in fp64, for the rows that fp32 does not
+// settle: K rounds over the row in memory, each taking the first entry after
+// the last one in the order (key descending, index ascending).  Slow, and
+// rare: 0.2 % of rows at E = 256, K = 8.
+template <typename L>
+__device__ void choose_fp64(const typename L::type *row, const float *bias, int E, int K, int lane,
+                            int &my_e, float &my_z)
+{
+    double last_d = __builtin_huge_val();
+    int last_e = -1;
+    my_e = -1;
+    my_z = kNegInf;
+    for (int k = 0; k < K; ++k) {
+        double best = -__builtin_huge_val();
+        int be = 0x7FFFFFFF;
+        for (int e = lane; e < E; e += kWave) {
+            const float z = clean_logit(L::get(row + e));
+            if (!(z > kNegInf) || !(fabsf(sigmoid_f(z) + bias[e]) < __builtin_huge_valf()))
+                continue;
+            const double d = 1.0 / (1.0 + exp(-(double)z)) + (double)bias[e];
+            if (!(d < last_d || (d == last_d && e > last_e)))
+                continue;
+            if (be == 0x7FFFFFFF || d > best) {
+                best = d;
+                be = e;
+            }
+        }
+        for (int m = 1; m < kWave; m <<= 1) {
+            const double od = __shfl_xor(best, m);
+            const int oe = __shfl_xor(be, m);
+            if (oe != 0x7FFFFFFF && (be == 0x7FFFFFFF || od > best || (od == best && oe < be))) {
+                best = od;
+                be = oe;
+            }
+        }
+        if (be == 0x7FFFFFFF)
+            return;
+        if (lane == k) {
+            my_e = be;
+            my_z = clean_logit(L::get(row + be));
+        }
+        last_d = best;
+        last_e = be;
+    }
+}
+
+// One wave per token.  K rounds: each lane's best remaining key, the maximum
+// over the lanes, and the lowest index among the lanes that hold it; lane k
+// keeps the k-th choice.  Without a bias the keys are the logits themselves
+// (both scores are monotone in them), so the order is exact.
+template <typename L, int VPL>
+__global__ void __launch_bounds__(256)
+route_kernel(const typename L::type *__restrict__ logits, int T, int E, int K, int sigmoid,
+             const float *__restrict__ bias, int renorm, float scale,
+             int32_t *__restrict__ topk_idx, float *__restrict__ topk_w,
+             int32_t *__restrict__ num_invalid)
+{
+    const int lane = threadIdx.x & (kWave - 1);
+    const int nw = gridDim.x * (blockDim.x / kWave);
+    for (int64_t t = blockIdx.x * (blockDim.x / kWave) + threadIdx.x / kWave; t < T; t += nw) {
+        const typename L::type *row = logits + t * E;
+        float z[VPL];
+        uint32_t key[VPL];
+        int bad = 0;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            const int e = j * kWave + lane;
+            const float v = e < E ? L::get(row + e) : kNegInf;
+            bad += bad_logit(v);
+            z[j] = clean_logit(v);
+        }
+        if (bias) {
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+                const int e = j * kWave + lane;
+                const float v = z[j] > kNegInf ? sigmoid_f(z[j]) + bias[e] + 0.0f : kNegInf;
+                key[j] = fabsf(v) < __builtin_huge_valf() ? order_bits(v) : 0u;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                key[j] = z[j] > kNegInf ? order_bits(z[j]) : 0u;
+        }
+        if (num_invalid) {
+            const int n = wave_sum(bad);
+            if (lane == 0)
+                num_invalid[t] = n;
+        }
+
+        float top = kNegInf, total = 0.0f;
+        if (!sigmoid && !renorm) {
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                top = fmaxf(top, z[j]);
+            top = wave_max_f(top);
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                total += row_score(z[j], top, false);
+            total = wave_sum_f(total);
+        }
+
+        int my_e = -1;
+        float my_z = kNegInf;
+        bool unsettled = false;
+        uint32_t prev = 0u;
+        const int rounds = bias && K < E ? K + 1 : K;
+        for (int k = 0; k < rounds; ++k) {
+            uint32_t best = 0u;
+            int be = 0;
+            float bz = kNegInf;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                if (key[j] > best) {
+                    best = key[j];
+                    be = j * kWave + lane;
+                    bz = z[j];
+                }
+            const uint32_t m = wave_max_u(best);
+            if (m == 0u)
+                break;                  // the rest is masked
+            if (bias && k > 0) {
+                const float a = from_order_bits(prev), b = from_order_bits(m);
+                unsettled = unsettled || a - b <= kKeyGap * fmaxf(1.0f, fmaxf(fabsf(a), fabsf(b)));
+            }
+            prev = m;
+            // the lowest index among equal keys, as the largest of ~index
+            const uint32_t inv = wave_max_u(best == m ? ~(uint32_t)be : 0u);
+            const int win = (int)~inv;
+            const float wz = lane_value(bz, win & (kWave - 1));
+            if (lane == k && k < K) {
+                my_e = win;
+                my_z = wz;
+            }
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                if (j * kWave + lane == win)
+                    key[j] = 0u;
+        }
+        if (unsettled)
+            choose_fp64<L>(row, bias, E, K, lane, my_e, my_z);
+
+        float w;
+        if (!renorm) {
+            if (sigmoid)
+                w = my_e >= 0 ? sigmoid_f(my_z) : 0.0f;
+            else
+                w = total > 0.0f ? row_score(my_z, top, false) / total : 0.0f;
+        } else {
+            const float zt = wave_max_f(my_z);
+            const float s = row_score(my_z, zt, sigmoid);
+            const float sum = wave_sum_f(s);
+            w = sum > 0.0f ? s / sum : 0.0f;
+        }
+        if (lane < K) {
+            topk_idx[t * K + lane] = my_e;
+            topk_w[t * K + lane] = scale * w;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- the balance loss
+// Sequence of token t: the last s with seq[s] <= t (T tokens, seq[S] ends the
+// last one); -1 or S outside all of them.
+__device__ __forceinline__ int find_sequence(const int32_t *seq, int S, int t)
+{
+    int lo = 0, hi = S + 1;             // the first index with seq[] > t
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (seq[mid] > t)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    return lo - 1;
+}
+
+__device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
+
+// Partial sums of one chunk of CT tokens: for every sequence s that meets
+// chunk c, row c + s of the partials gets the column sums of the
+// probabilities, the counts, the live rows and the bad data.  Chunks and
+// sequences both run along the tokens, so c + s is another row for every pair
+// that meets: nchunk + S rows hold all of them.
+//   partial row: E floats (sums), E ints (counts), live, bad index, bad logit
+struct BalanceRow {
+    float *sum;
+    int32_t *count, *live;
+};
+__device__ __forceinline__ BalanceRow balance_row(float *part, int E, int64_t row)
+{
+    float *p = part + row * (2 * (int64_t)E + 4);
+    int32_t *c = reinterpret_cast<int32_t *>(p + E);
+    return {p, c, c + E};
+}
+
+// Threads of a block by the row length: a wave keeps E column sums in shared
+// memory and 2 VPL values per lane in registers (48 KB at E = 4096, and no
+// spills: 16 waves leave 128 registers, 2 leave 512).
+constexpr int balance_threads(int vpl) { return vpl <= 8 ? 1024 : (vpl <= 16 ? 512 : 128); }
+
+template <typename L, int VPL>
+__global__ void __launch_bounds__(balance_threads(VPL))
+balance_partial_kernel(const typename L::type *__restrict__ logits, int T, int E,
+                       const int32_t *__restrict__ topk_idx, int K, int sigmoid,
+                       const int32_t *__restrict__ seq, int S, int CT, float *__restrict__ part,
+                       unsigned *__restrict__ arrived)
+{
+    extern __shared__ float lds[];      // [waves][E] sums, then [E] counts, then 3 counters
+    const int tid = threadIdx.x, bd = blockDim.x;
+    const int lane = tid & (kWave - 1), wave = tid / kWave, nw = bd / kWave;
+    int32_t *hist = reinterpret_cast<int32_t *>(lds + (size_t)nw * E);
+    int32_t *misc = hist + E;
+    if (blockIdx.x == 0 && tid == 0)
+        *arrived = 0u;
+    const int c = blockIdx.x;
+    const int c0 = c * CT, c1 = T - c0 > CT ? c0 + CT : T;
+    int s = seq ? clampi(find_sequence(seq, S, c0), 0, S - 1) : 0;
+    for (; s < S; ++s) {
+        const int q0 = seq ? clampi(seq[s], 0, T) : 0, q1 = seq ? clampi(seq[s + 1], 0, T) : T;
+        if (q0 >= c1)
+            break;
+        const int lo = q0 > c0 ? q0 : c0, hi = q1 < c1 ? q1 : c1;
+        if (lo >= hi)
+            continue;
+        for (int e = tid; e < E + 3; e += bd)
+            hist[e] = 0;
+        __syncthreads();
+        // counts: integer adds, the same in any order
+        int bad_i = 0;
+        const int64_t i1 = (int64_t)hi * K;
+        for (int64_t i = (int64_t)lo * K + tid; i < i1; i += bd) {
+            const int e = topk_idx[i];
+            if ((unsigned)e < (unsigned)E)
+                atomicAdd(&hist[e], 1);
+            else
+                bad_i += e != -1;
+        }
+        if (bad_i)
+            atomicAdd(&misc[1], bad_i);
+        float acc[VPL];
+#pragma unroll
+        for (int j = 0; j < VPL; ++j)
+            acc[j] = 0.0f;
+        int live = 0, bad_z = 0;
+        for (int t = lo + wave; t < hi; t += nw) {
+            const typename L::type *row = logits + (int64_t)t * E;
+            float z[VPL], top = kNegInf, sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+                const int e = j * kWave + lane;
+                const float v = e < E ? L::get(row + e) : kNegInf;
+                bad_z += bad_logit(v);
+                z[j] = clean_logit(v);
+                top = fmaxf(top, z[j]);
+            }
+            top = wave_max_f(top);
+            if (!(top > kNegInf))
+                continue;
+            ++live;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+                z[j] = row_score(z[j], top, sigmoid);
+                sum += z[j];
+            }
+            const float inv = 1.0f / wave_sum_f(sum);
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                acc[j] = fmaf(z[j], inv, acc[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            const int e = j * kWave + lane;
+            if (e < E)
+                lds[wave * E + e] = acc[j];
+        }
+        const int bz = wave_sum(bad_z);
+        if (lane == 0) {
+            atomicAdd(&misc[0], live);
+            if (bz)
+                atomicAdd(&misc[2], bz);
+        }
+        __syncthreads();
+        const BalanceRow r = balance_row(part, E, (int64_t)c + s);
+        for (int e = tid; e < E; e += bd) {
+            float v = 0.0f;
+            for (int w = 0; w < nw; ++w)
+                v += lds[w * E + e];
+            r.sum[e] = v;
+            r.count[e] = hist[e];
+        }
+        if (tid < 3)
+            r.live[tid] = misc[tid];
+        __syncthreads();
+    }
+}
+
+constexpr int kFinalThreads = 1024;
+
+// One block per (64 experts, sequence): the sums over the sequence's partial
+// rows (in row order, in fp64: a sum over all tokens), the counts, the table
+// the backward reads, slope[s][e] = E c_se / (K n_s^2), and the block's part
+// of sum_e f_se P_se.  The block that arrives last adds the parts in a fixed
+// order: the loss does not depend on which one that is.
+__global__ void __launch_bounds__(kFinalThreads)
+balance_final_kernel(const float *__restrict__ part, int T, int E, int K,
+                     const int32_t *__restrict__ seq, int S, int CT, float coef, int eb,
+                     int32_t *__restrict__ counts, float *__restrict__ slope,
+                     float *__restrict__ loss, int32_t *__restrict__ num_invalid,
+                     double *__restrict__ parts, int32_t *__restrict__ tails,
+                     unsigned *__restrict__ arrived)
+{
+    constexpr int NW = kFinalThreads / kWave;
+    __shared__ double sums[NW][kWave];
+    __shared__ int32_t cnts[NW][kWave];
+    __shared__ int32_t misc[3];
+    __shared__ bool last;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+    const int s = blockIdx.x / eb, b = blockIdx.x % eb;
+    const int e = b * kWave + lane;
+    const int q0 = seq ? clampi(seq[s], 0, T) : 0, q1 = seq ? clampi(seq[s + 1], 0, T) : T;
+    const int r0 = q0 < q1 ? q0 / CT : 0, r1 = q0 < q1 ? (q1 - 1) / CT + 1 : 0;
+    if (tid < 3)
+        misc[tid] = 0;
+    __syncthreads();
+    double sum = 0.0;
+    int cnt = 0;
+    for (int c = r0 + wave; c < r1; c += NW) {
+        const BalanceRow r = balance_row(const_cast<float *>(part), E, (int64_t)c + s);
+        if (e < E) {
+            sum += (double)r.sum[e];
+            cnt += r.count[e];
+        }
+        if (lane < 3)
+            atomicAdd(&misc[lane], r.live[lane]);
+    }
+    sums[wave][lane] = sum;
+    cnts[wave][lane] = cnt;
+    __syncthreads();
+    const int n = misc[0];
+    if (wave == 0) {
+        for (int w = 1; w < NW; ++w) {
+            sum += sums[w][lane];
+            cnt += cnts[w][lane];
+        }
+        const double inv = n > 0 ? 1.0 / n : 0.0;
+        const double f = (double)E * cnt / K * inv;
+        if (e < E) {
+            counts[(int64_t)s * E + e] = cnt;
+            slope[(int64_t)s * E + e] = (float)(f * inv);
+        }
+        double v = e < E ? f * sum * inv : 0.0;
+        for (int m = kWave / 2; m > 0; m >>= 1)
+            v += __shfl_down(v, m);
+        if (lane == 0) {
+            // agent scope: the last block may run on another XCD
+            __hip_atomic_store(&parts[blockIdx.x], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (b == 0)
+                for (int i = 0; i < 3; ++i)
+                    __hip_atomic_store(&tails[3 * (int64_t)s + i], misc[i], __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_AGENT);
+            const unsigned before = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_ACQ_REL,
+                                                           __HIP_MEMORY_SCOPE_AGENT);
+            last = before + 1u == gridDim.x;
+        }
+    }
+    __syncthreads();
+    if (!last || wave != 0)
+        return;
+    double all = 0.0;
+    int n_live = 0, bad_i = 0, bad_z = 0;
+    for (int64_t i = lane; i < (int64_t)S * eb; i += kWave)
+        all += __hip_atomic_load(&parts[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int i = lane; i < S; i += kWave) {
+        n_live += __hip_atomic_load(&tails[3 * (int64_t)i], __ATOMIC_RELAXED,
+                                    __HIP_MEMORY_SCOPE_AGENT) > 0;
+        bad_i += __hip_atomic_load(&tails[3 * (int64_t)i + 1], __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+        bad_z += __hip_atomic_load(&tails[3 * (int64_t)i + 2], __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+    }
+    for (int m = kWave / 2; m > 0; m >>= 1)
+        all += __shfl_down(all, m);
+    n_live = wave_sum(n_live);
+    bad_i = wave_sum(bad_i);
+    bad_z = wave_sum(bad_z);
+    if (lane == 0) {
+        const double per = n_live > 0 ? 1.0 / n_live : 0.0;
+        loss[0] = (float)(coef * all * per);
+        slope[(int64_t)S * E] = (float)(coef * per);
+        num_invalid[0] = bad_i;
+        num_invalid[1] = bad_z;
+    }
+}
+
+// ---------------------------------------------------------------- the gradient
+// d_logits of sum(topk_weights * d_w) + d_loss * loss, one wave per row.
+//   weights, renormalised: q_k = w_k / scale, G = scale d_w:
+//     d = q_k (G_k - sum_j q_j G_j) [1 - s_k], at the chosen experts only
+//   softmax as it is: p_e (G_e - sum_k p_k G_k);  sigmoid as it is: G_k s_k (1 - s_k)
+//   balance: g p_e (slope_se - sum_j slope_sj p_j) [1 - s_e],
+//     g = d_loss coef / live sequences; zero outside every sequence
+// (the factors in brackets for the sigmoid).  The chosen entries' parts meet
+// their columns in a row of shared memory; a row of logits is read once, and
+// only where probabilities of the whole row are needed.
+template <typename L, int VPL>
+__global__ void __launch_bounds__(256)
+router_backward_kernel(const typename L::type *__restrict__ logits, int T, int E, int K,
+                       int sigmoid, int renorm, float scale, const int32_t *__restrict__ topk_idx,
+                       const float *__restrict__ d_w, const float *__restrict__ slope,
+                       const int32_t *__restrict__ seq, int S, const float *__restrict__ d_loss,
+                       typename L::type *__restrict__ d_logits)
+{
+    extern __shared__ float lds[];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int nw = gridDim.x * (blockDim.x / kWave);
+    float *mine = lds + wave * E;
+    const bool dense_w = d_w && !sigmoid && !renorm;
+    const bool whole = dense_w || slope;
+    const float g = slope ? d_loss[0] * slope[(int64_t)S * E] : 0.0f;
+    for (int64_t t = blockIdx.x * (blockDim.x / kWave) + wave; t < T; t += nw) {
+        const typename L::type *row = logits + t * E;
+        float z[VPL], p[VPL], d[VPL];
+        float top = kNegInf, inv = 0.0f;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j)
+            d[j] = 0.0f;
+        if (whole) {
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+                const int e = j * kWave + lane;
+                z[j] = e < E ? clean_logit(L::get(row + e)) : kNegInf;
+                top = fmaxf(top, z[j]);
+            }
+            top = wave_max_f(top);
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+                p[j] = row_score(z[j], top, sigmoid);
+                sum += p[j];
+            }
+            sum = wave_sum_f(sum);
+            inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                p[j] *= inv;
+        }
+        if (d_w) {
+            int e = -1;
+            float G = 0.0f;
+            if (lane < K) {
+                e = topk_idx[t * K + lane];
+                G = scale * d_w[t * K + lane];
+            }
+            float zk = kNegInf;
+            if ((unsigned)e < (unsigned)E)
+                zk = clean_logit(L::get(row + e));
+            const bool in = zk > kNegInf;
+            float v = in ? G : 0.0f;
+            if (renorm) {
+                const float zt = wave_max_f(zk);
+                const float s = row_score(zk, zt, sigmoid);
+                const float sum = wave_sum_f(s);
+                const float q = sum > 0.0f ? s / sum : 0.0f;
+                v = q * (v - wave_sum_f(q * v));
+                if (sigmoid && in)
+                    v *= sigmoid_f(-zk);
+            } else if (sigmoid && in) {
+                v *= sigmoid_f(zk) * sigmoid_f(-zk);
+            }
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+                const int c = j * kWave + lane;
+                if (c < E)
+                    mine[c] = 0.0f;
+            }
+            __builtin_amdgcn_wave_barrier();
+            if (in)
+                atomicAdd(&mine[e], v);
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+                const int c = j * kWave + lane;
+                d[j] = c < E ? mine[c] : 0.0f;
+            }
+            __builtin_amdgcn_wave_barrier();
+            if (dense_w) {
+                float dot = 0.0f;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j)
+                    dot = fmaf(p[j], d[j], dot);
+                dot = wave_sum_f(dot);
+#pragma unroll
+                for (int j = 0; j < VPL; ++j)
+                    d[j] = p[j] * (d[j] - dot);
+            }
+        }
+        if (slope) {
+            const int s = seq ? find_sequence(seq, S, (int)t) : 0;
+            if (s >= 0 && s < S) {
+                const float *f = slope + (int64_t)s * E;
+                float fe[VPL], dot = 0.0f;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) {
+                    const int e = j * kWave + lane;
+                    fe[j] = e < E ? f[e] : 0.0f;
+                    dot = fmaf(p[j], fe[j], dot);
+                }
+                dot = wave_sum_f(dot);
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) {
+                    float v = g * p[j] * (fe[j] - dot);
+                    if (sigmoid && z[j] > kNegInf)
+                        v *= sigmoid_f(-z[j]);
+                    d[j] += v;
+                }
+            }
+        }
+        typename L::type *out = d_logits + t * E;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            const int e = j * kWave + lane;
+            if (e < E)
+                L::put(out + e, d[j]);
+        }
+    }
+}
+
+// Waves of one row each, at most this many blocks of four; beyond it a wave
+// takes several rows.
+constexpr int kMaxRowBlocks = 1 << 20;
+int row_blocks(int T)
+{
+    const int b = (T + 3) / 4;
+    return b < kMaxRowBlocks ? b : kMaxRowBlocks;
+}
+
+// Values per lane for E experts: f(VPL).
+template <typename F>
+hipError_t with_vpl(int E, F f)
+{
+    if (E <= 64)
+        return f(vpl_t<1>());
+    if (E <= 128)
+        return f(vpl_t<2>());
+    if (E <= 256)
+        return f(vpl_t<4>());
+    if (E <= 512)
+        return f(vpl_t<8>());
+    if (E <= 1024)
+        return f(vpl_t<16>());
+    return f(vpl_t<64>());
+}
+
+template <typename L>
+hipError_t route_t(const void *logits, int T, int E, int K, bool sigmoid, const float *bias,
+                   bool renorm, float scale, int32_t *topk_idx, float *topk_w,
+                   int32_t *num_invalid, hipStream_t s)
+{
+    return with_vpl(E, [&](auto v) {
+        route_kernel<L, decltype(v)::value><<<row_blocks(T), 256, 0, s>>>(
+            static_cast<const typename L::type *>(logits), T, E, K, sigmoid, bias, renorm, scale,
+            topk_idx, topk_w, num_invalid);
+        return hipGetLastError();
+    });
+}
+
+template <typename L>
+hipError_t balance_t(const BalancePlan &p, const void *logits, const int32_t *topk_idx, int K,
+                     bool sigmoid, const int32_t *seq, float *part, unsigned *arrived,
+                     hipStream_t s)
+{
+    return with_vpl(p.E, [&](auto v) {
+        constexpr int threads = balance_threads(decltype(v)::value);
+        const size_t lds = ((size_t)(threads / kWave) * p.E + p.E + 3) * 4;
+        balance_partial_kernel<L, decltype(v)::value><<<p.nchunk, threads, lds, s>>>(
+            static_cast<const typename L::type *>(logits), p.T, p.E, topk_idx, K, sigmoid, seq,
+            p.S, p.CT, part, arrived);
+        return hipGetLastError();
+    });
+}
+
+template <typename L>
+hipError_t router_backward_t(const void *logits, int T, int E, int K, bool sigmoid, bool renorm,
+                             float scale, const int32_t *topk_idx, const float *d_w,
+                             const float *slope, const int32_t *seq, int S, const float *d_loss,
+                             void *d_logits, hipStream_t s)
+{
+    return with_vpl(E, [&](auto v) {
+        router_backward_kernel<L, decltype(v)::value>
+            <<<row_blocks(T), 256, 4 * (size_t)E * sizeof(float), s>>>(
+                static_cast<const typename L::type *>(logits), T, E, K, sigmoid, renorm, scale,
+                topk_idx, d_w, slope, seq, S, d_loss,
+                static_cast<typename L::type *>(d_logits));
+        return hipGetLastError();
+    });
+}
+
+}  // namespace
+
+BalancePlan make_balance_plan(int T, int E, int S)
+{
+    BalancePlan p{};
+    p.T = T;
+    p.E = E;
+    p.S = S;
+    // up to 256 chunks (one per CU) of at least 16 tokens
+    p.CT = (T + 255) / 256;
+    if (p.CT < 16)
+        p.CT = 16;
+    p.nchunk = T > 0 ? (T + p.CT - 1) / p.CT : 1;
+    p.eb = (E + kWave - 1) / kWave;
+    size_t off = 0;
+    p.off_arrived = off;
+    off = align256(off + 4);
+    p.off_part = off;
+    off = align256(off + ((size_t)p.nchunk + S) * (2 * (size_t)E + 4) * 4);
+    p.off_parts = off;
+    off = align256(off + (size_t)S * p.eb * 8);
+    p.off_tails = off;
+    off = align256(off + (size_t)S * 3 * 4);
+    p.bytes = off;
+    return p;
+}
+
+hipError_t launch_route(const void *logits, bool bf16, int T, int E, int K, bool sigmoid,
+                        const float *bias, bool renorm, float scale, int32_t *topk_idx,
+                        float *topk_w, int32_t *num_invalid, hipStream_t s)
+{
+    if (T == 0)
+        return hipSuccess;
+    return bf16 ? route_t<Bf16>(logits, T, E, K, sigmoid, bias, renorm, scale, topk_idx, topk_w,
+                                num_invalid, s)
+                : route_t<F32>(logits, T, E, K, sigmoid, bias, renorm, scale, topk_idx, topk_w,
+                               num_invalid, s);
+}
+
+hipError_t launch_balance(const BalancePlan &p, const void *logits, bool bf16,
+                          const int32_t *topk_idx, int K, bool sigmoid, const int32_t *seq,
+                          float coef, int32_t *counts, float *slope, float *loss,
+                          int32_t *num_invalid, char *ws, hipStream_t s)
+{
+    float *part = reinterpret_cast<float *>(ws + p.off_part);
+    unsigned *arrived = reinterpret_cast<unsigned *>(ws + p.off_arrived);
+    hipError_t e = bf16 ? balance_t<Bf16>(p, logits, topk_idx, K, sigmoid, seq, part, arrived, s)
+                        : balance_t<F32>(p, logits, topk_idx, K, sigmoid, seq, part, arrived, s);
+    if (e != hipSuccess)
+        return e;
+    balance_final_kernel<<<p.S * p.eb, kFinalThreads, 0, s>>>(
+        part, p.T, p.E, K, seq, p.S, p.CT, coef, p.eb, counts, slope, loss, num_invalid,
+        reinterpret_cast<double *>(ws + p.off_parts), reinterpret_cast<int32_t *>(ws + p.off_tails),
+        arrived);
+    return hipGetLastError();
+}
+
+hipError_t launch_router_backward(const void *logits, bool bf16, int T, int E, int K, bool sigmoid,
+                                  bool renorm, float scale, const int32_t *topk_idx,
+                                  const float *d_w, const float *slope, const int32_t *seq, int S,
+                                  const float *d_loss, void *d_logits, hipStream_t s)
+{
+    if (T == 0)
+        return hipSuccess;
+    return bf16 ? router_backward_t<Bf16>(logits, T, E, K, sigmoid, renorm, scale, topk_idx, d_w,
+                                          slope, seq, S, d_loss, d_logits, s)
+                : router_backward_t<F32>(logits, T, E, K, sigmoid, renorm, scale, topk_idx, d_w,
+                                         slope, seq, S, d_loss, d_logits, s);
+}
+
+}  // namespace ep

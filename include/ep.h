@@ -411,6 +411,98 @@ ep_status_t ep_combine_partial(const uint16_t *y, int y_rows, int H, const int32
 ep_status_t ep_combine_ranks(const float *partial, int rows, int H, const int32_t *pack_pos,
                              int T, int R, uint16_t *out, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The router: what produces topk_idx and topk_weights, the loss that keeps
+ * its experts evenly used, and the gradients of both.
+ *
+ * Scores of a token's logits z[0..E):
+ *   EP_SCORE_SOFTMAX:  s_e = exp(z_e - max z)     EP_SCORE_SIGMOID:  s_e = 1 / (1 + exp(-z_e))
+ * and its probabilities p_e = s_e / sum s.  A logit of -inf is masked: its
+ * expert is never chosen and has score 0.  NaN and +inf are bad data: they
+ * count as masked, and are counted.  A row that is masked throughout chooses
+ * nothing (topk_idx -1, weights 0): so a padding row is one of -inf.
+ * Arithmetic is fp32; logits and d_logits are bf16 or fp32 (dtype), d_logits
+ * rounded once to nearest even.
+ */
+typedef int32_t ep_dtype_t;
+enum { EP_DTYPE_BF16 = 0, EP_DTYPE_F32 = 1 };
+typedef int32_t ep_score_t;
+enum { EP_SCORE_SOFTMAX = 0, EP_SCORE_SIGMOID = 1 };
+
+/*
+ * ep_route -- the K experts with the largest scores, in descending order,
+ * ties to the lower expert.
+ *   logits        [T, E] in.
+ *   bias          [E] fp32 in or NULL (EP_SCORE_SIGMOID only): the choice is by
+ *                 s_e + bias[e], ordered as in 64 bits (rows that fp32 does not
+ *                 settle are ordered in fp64); the weights do not see it.  An
+ *                 entry that is not finite masks its expert for the choice.
+ *   topk_idx      [T, K] int32 out; -1 once no unmasked expert is left.
+ *   topk_weights  [T, K] fp32 out: scale * s_e / (sum of the K chosen scores)
+ *                 if renormalise, else scale * p_e (softmax) or scale * s_e
+ *                 (sigmoid); 0 where topk_idx is -1.
+ *   num_invalid   [T] int32 out or NULL: bad logits of each token.
+ * Constraints: 1 <= K <= E <= 4096, K <= 64 (EP_ERR_UNSUPPORTED beyond).
+ * One launch, no workspace.
+ */
+ep_status_t ep_route(const void *logits, ep_dtype_t dtype, int T, int E, int K, ep_score_t score,
+                     const float *bias, int renormalise, float scale, int32_t *topk_idx,
+                     float *topk_weights, int32_t *num_invalid, void *stream);
+
+/* Bytes of device workspace that ep_balance_loss needs. */
+size_t ep_balance_workspace_bytes(int T, int E, int S);
+
+/*
+ * ep_balance_loss -- the balance loss of S sequences, with the counts of
+ * their experts.  Sequence s is the tokens [seq_offsets[s], seq_offsets[s+1]);
+ * n_s of them are live (have an unmasked logit), and S_live sequences have a
+ * live token.
+ *   c_se = entries of topk_idx with expert e,  f_se = E c_se / (K n_s),
+ *   P_se = (sum of p_te over the tokens) / n_s,
+ *   loss = coef / S_live * sum_s sum_e f_se P_se      (0 if S_live is 0)
+ *   logits        [T, E] in.
+ *   topk_idx      [T, K] int32 in (any choice of experts; -1 is not counted,
+ *                 other values outside [0, E) are bad data).
+ *   seq_offsets   [S+1] int32 in, non-decreasing within [0, T], or NULL for one
+ *                 sequence of all T tokens (S = 1).  Sequences may be empty;
+ *                 tokens outside all of them take no part.  (Offsets that
+ *                 decrease give unspecified values, but no access outside the
+ *                 arrays.)
+ *   counts        [S, E] int32 out: c_se.
+ *   slope         [S*E + 1] fp32 out: what the gradient needs of the loss,
+ *                 f_se / n_s, then coef / S_live.  The counts are taken as
+ *                 constants in it.
+ *   loss          [1] fp32 out.
+ *   num_invalid   [2] int32 out: bad entries of topk_idx, bad logits (of the
+ *                 tokens in sequences).
+ *   ws, ws_bytes  >= ep_balance_workspace_bytes(T, E, S) bytes; free after the call.
+ * Constraints: E <= 4096, S >= 1, S*E < 2^31, S * ceil(E / 64) < 2^22.
+ */
+ep_status_t ep_balance_loss(const void *logits, ep_dtype_t dtype, int T, int E,
+                            const int32_t *topk_idx, int K, ep_score_t score,
+                            const int32_t *seq_offsets, int S, float coef, int32_t *counts,
+                            float *slope, float *loss, int32_t *num_invalid, void *ws,
+                            size_t ws_bytes, void *stream);
+
+/*
+ * ep_router_backward -- the logits' gradient of
+ *     sum over t, k of topk_weights[t,k] * d_weights[t,k]  +  d_loss * loss,
+ * either part alone if the other's pointers are NULL.
+ *   logits, dtype, score          as given to the forward calls.
+ *   renormalise, scale, topk_idx  as given to and returned by ep_route (not
+ *                 read if d_weights is NULL).  Entries outside [0, E) get nothing.
+ *   d_weights     [T, K] fp32 in or NULL.
+ *   slope, seq_offsets, S         from ep_balance_loss; slope NULL: no loss.
+ *   d_loss        [1] fp32 in, device memory.
+ *   d_logits      [T, E] out, every element written (0 where masked).
+ * The choice itself, the bias and the counts have no gradient.
+ */
+ep_status_t ep_router_backward(const void *logits, ep_dtype_t dtype, int T, int E, int K,
+                               ep_score_t score, int renormalise, float scale,
+                               const int32_t *topk_idx, const float *d_weights, const float *slope,
+                               const int32_t *seq_offsets, int S, const float *d_loss,
+                               void *d_logits, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

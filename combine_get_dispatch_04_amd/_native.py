@@ -52,6 +52,12 @@ SIGNATURES = {
     "ep_balance_loss": (_ST, [_P, _I, _I, _I, _P, _I, _I, _P, _I, _F, _P, _P, _P, _P, _P, _SZ,
                               _P]),
     "ep_router_backward": (_ST, [_P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P, _I, _P, _P, _P]),
+    "ep_adapter_state_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "ep_adapter_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
+    "ep_adapter_project": (_ST, [_P, _I, _I, _P, _I, _P, _P, _I, _I, _P, _P, _I, _F, _P, _P, _P,
+                                 _SZ, _P, _SZ, _P]),
+    "ep_adapter_project_backward": (_ST, [_P, _P, _I, _I, _P, _I, _P, _P, _I, _I, _P, _P, _I, _F,
+                                          _P, _SZ, _P, _P, _P, _P, _P, _SZ, _P]),
 }
 
 _lib = None
@@ -207,3 +213,28 @@ def ep_router_backward(logits, dtype, T, E, K, score, renormalise, scale, topk_i
     st = lib().ep_router_backward(logits, dtype, T, E, K, score, renormalise, scale, topk_idx,
                                   d_weights, slope, seq_offsets, S, d_loss, d_logits, stream)
     return _check("ep_router_backward", st) if check else st
+
+
+def ep_adapter_state_bytes(T: int, H: int, O: int, E: int, K: int, r: int) -> int:
+    return lib().ep_adapter_state_bytes(T, H, O, E, K, r)
+
+
+def ep_adapter_workspace_bytes(T: int, H: int, O: int, E: int, K: int, r: int,
+                               backward: int) -> int:
+    return lib().ep_adapter_workspace_bytes(T, H, O, E, K, r, backward)
+
+
+def ep_adapter_project(x, T, H, weight, O, a, b, E, r, topk_idx, topk_weights, K, scale, out,
+                       num_invalid, state, state_bytes, ws, ws_bytes, stream, check=True):
+    st = lib().ep_adapter_project(x, T, H, weight, O, a, b, E, r, topk_idx, topk_weights, K, scale,
+                                  out, num_invalid, state, state_bytes, ws, ws_bytes, stream)
+    return _check("ep_adapter_project", st) if check else st
+
+
+def ep_adapter_project_backward(d_out, x, T, H, weight, O, a, b, E, r, topk_idx, topk_weights, K,
+                                scale, state, state_bytes, dx, da, db, d_weights, ws, ws_bytes,
+                                stream, check=True):
+    st = lib().ep_adapter_project_backward(d_out, x, T, H, weight, O, a, b, E, r, topk_idx,
+                                           topk_weights, K, scale, state, state_bytes, dx, da, db,
+                                           d_weights, ws, ws_bytes, stream)
+    return _check("ep_adapter_project_backward", st) if check else st

@@ -667,3 +667,92 @@ def balance_loss_backward(d_loss: torch.Tensor, balance: BalanceLoss) -> torch.T
     """d_logits [T, E] (the logits' dtype) of the balance loss; zero for tokens
     outside all sequences.  d_loss: [1] fp32, on the GPU."""
     return _router_backward(balance.logits, balance.score, None, None, d_loss, balance)
+
+
+# ---------------------------------------------------------------- adapters
+@dataclass
+class AdapterHandle:
+    """What adapter_project_backward needs from adapter_project.  The operands
+    must still hold their values when the backward runs."""
+    x: torch.Tensor
+    weight: torch.Tensor
+    a: torch.Tensor
+    b: torch.Tensor
+    topk_idx: torch.Tensor
+    topk_weights: Optional[torch.Tensor]
+    scale: float
+    num_invalid: torch.Tensor                  # [1] int32: entries neither -1 nor in [0, E)
+    state: torch.Tensor
+
+
+def adapter_project(x: torch.Tensor, weight: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
+                    topk_idx: torch.Tensor, topk_weights: Optional[torch.Tensor] = None, *,
+                    scale: float = 1.0, out: Optional[torch.Tensor] = None):
+    """Low-rank adapters beside a shared projection:
+    out[t] = bf16(weight x_t + sum_k scale * topk_weights[t,k] * b[e] (a[e] x_t)),
+    e = topk_idx[t,k] (-1 = none; weights 1 if None).  One adapter per request:
+    topk_idx [T, 1]; low-rank experts beside a shared one: the topk_idx and
+    topk_weights of route.  x [T, H], weight [O, H], a [E, r, H], b [E, O, r],
+    all bf16; r a multiple of 8 up to 128.  -> (out [T, O] bf16,
+    AdapterHandle).  Tensors carry no autograd graph: the gradients are
+    adapter_project_backward."""
+    _need(x, "x", torch.bfloat16, 2)
+    _need(weight, "weight", torch.bfloat16, 2)
+    _need(a, "a", torch.bfloat16, 3)
+    _need(b, "b", torch.bfloat16, 3)
+    _need(topk_idx, "topk_idx", torch.int32, 2)
+    T, H = x.shape
+    O = weight.shape[0]
+    E, r = a.shape[:2]
+    if weight.shape[1] != H or a.shape[2] != H:
+        raise ValueError("weight and a must have x's H channels")
+    if tuple(b.shape) != (E, O, r):
+        raise ValueError(f"b must be [E, O, r] = {(E, O, r)}, got {tuple(b.shape)}")
+    if topk_idx.shape[0] != T:
+        raise ValueError("x and topk_idx disagree on the number of tokens")
+    K = topk_idx.shape[1]
+    if topk_weights is not None:
+        _need(topk_weights, "topk_weights", torch.float32, 2)
+        if tuple(topk_weights.shape) != (T, K):
+            raise ValueError("topk_weights must be [T, K]")
+    dev = x.device
+    _same_device(dev, weight=weight, a=a, b=b, topk_idx=topk_idx, topk_weights=topk_weights)
+    state_bytes = N.ep_adapter_state_bytes(T, H, O, E, K, r)
+    ws_bytes = N.ep_adapter_workspace_bytes(T, H, O, E, K, r, 0)
+    out = _out(out, (T, O), dev)
+    ninv = torch.empty(1, dtype=torch.int32, device=dev)
+    state = torch.empty(state_bytes, dtype=torch.uint8, device=dev)
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        N.ep_adapter_project(_ptr(x), T, H, _ptr(weight), O, _ptr(a), _ptr(b), E, r,
+                             _ptr(topk_idx), _ptr(topk_weights), K, float(scale), _ptr(out),
+                             _ptr(ninv), _ptr(state), state_bytes, _ptr(ws), ws_bytes,
+                             _stream(dev))
+    return out, AdapterHandle(x, weight, a, b, topk_idx, topk_weights, float(scale), ninv, state)
+
+
+def adapter_project_backward(d_out: torch.Tensor, handle: AdapterHandle):
+    """-> (dx [T, H] bf16, da [E, r, H] bf16, db [E, O, r] bf16, d_weights
+    [T, K] fp32): the gradients for d_out [T, O] bf16.  The shared weight is
+    frozen and has none; adapters that no token names get 0."""
+    _need(d_out, "d_out", torch.bfloat16, 2)
+    x, weight, a, b, idx = handle.x, handle.weight, handle.a, handle.b, handle.topk_idx
+    T, H = x.shape
+    O = weight.shape[0]
+    E, r = a.shape[:2]
+    K = idx.shape[1]
+    if tuple(d_out.shape) != (T, O):
+        raise ValueError(f"d_out must be {(T, O)}, got {tuple(d_out.shape)}")
+    dev = x.device
+    _same_device(dev, d_out=d_out)
+    ws_bytes = N.ep_adapter_workspace_bytes(T, H, O, E, K, r, 1)
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    dx, da, db = torch.empty_like(x), torch.empty_like(a), torch.empty_like(b)
+    dw = torch.empty((T, K), dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        N.ep_adapter_project_backward(_ptr(d_out), _ptr(x), T, H, _ptr(weight), O, _ptr(a),
+                                      _ptr(b), E, r, _ptr(idx), _ptr(handle.topk_weights), K,
+                                      handle.scale, _ptr(handle.state), handle.state.numel(),
+                                      _ptr(dx), _ptr(da), _ptr(db), _ptr(dw), _ptr(ws), ws_bytes,
+                                      _stream(dev))
+    return dx, da, db, dw

@@ -1,0 +1,858 @@
+// ep_adapter.hip -- low-rank adapters beside a shared projection:
+//   out_t = W x_t + sum_k c_tk B_e A_e x_t,   e = topk_idx[t,k],  c_tk = scale w_tk
+// and its gradients, with v_tk = B_e^T d_t for the output's gradient d:
+//   dx_t = W^T d_t + sum_k c_tk A_e^T v_tk      dA_e = sum c_tk v_tk x_t^T
+//   dw_tk = scale <A_e x_t, v_tk>               dB_e = sum c_tk d_t (A_e x_t)^T
+//
+// Tokens go in tiles of BM.  A tile's list holds the adapters that its tokens
+// name, ascending; its dense matrix U holds in row t, columns l*rp .. l*rp+r-1,
+// the bf16 of c * (A_e x_t) for the l-th adapter of the list, 0 where the
+// token does not name it (rp = r rounded up to 16, c summed over the entries
+// that name it).  So the adapters' part of a tile is one more stretch of the
+// inner dimension of the projection's own matrix product, over U and the
+// list's B, and the gradients of A and B are products of U's and V's columns
+// with the tile's rows of d and x.
+//
+//   tiles      lists, and every adapter's place in each tile's list
+//   shrink     A_e x_t (or B_e^T d_t) of every entry, MFMA over the list's
+//              rows, the inner dimension split over blocks; fp32
+//   gather     sums the splits, writes U (or V) and the fp32 sums; dw
+//   project    the product with W, and U's stretch in front of it
+//   grads      dA, dB
+//
+// Products of tokens and adapters that do not belong together meet zeros of
+// U.  A zero does not stop an infinity or a NaN (of another token's row, or of
+// another request's adapter): where a wave's sums over U are not all finite it
+// takes them again with every such product left out.
+#include "ep_common.h"
+#include "ep_internal.h"
+
+namespace ep {
+
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int BK = 64;                 // inner elements per stage
+
+// ---------------------------------------------------------------- LDS tiles
+// A tile of rows with 64 consecutive inner elements: 8 pieces of 16 bytes per
+// row, piece c of row r in slot c ^ (r & 7), so that the 16 rows a fragment
+// reads at one c spread over the banks.
+__device__ __forceinline__ int off_k(int row, int piece)
+{
+    return row * 128 + ((piece ^ (row & 7)) << 4);
+}
+// A tile of 64 inner rows with C consecutive columns, read transposed: units
+// of 16 columns (32 bytes), unit u of row k in slot u ^ f(k).  A transposing
+// read takes rows {0..3, 8..11, 16..19, 24..27} of one unit: f tells eight of
+// them apart.
+template <int C>
+__device__ __forceinline__ int off_n(int k, int unit)
+{
+    const int f = ((k & 3) | ((k >> 1) & 4)) & (C / 16 - 1);
+    return k * (C * 2) + ((unit ^ f) << 5);
+}
+
+__device__ __forceinline__ bf16x8 frag_k(const char *tile, int row0, int ks, int lane)
+{
+    const int row = row0 + (lane & 15);
+    return __builtin_bit_cast(bf16x8,
+                              *reinterpret_cast<const u32x4 *>(tile + off_k(row, ks * 4 + (lane >> 4))));
+}
+// Lane: column unit*16 + (lane & 15), inner elements ks*32 + (lane >> 4)*8 ..+7.
+template <int C>
+__device__ __forceinline__ bf16x8 frag_n(const char *tile, int unit, int ks, int lane)
+{
+    typedef __attribute__((address_space(3))) s16x4 *lds_ptr;
+    const int i = lane & 15, k = ks * 32 + (lane >> 4) * 8 + (i >> 2);
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_ptr)(tile + off_n<C>(k, unit) + (i & 3) * 8));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_ptr)(tile + off_n<C>(k + 4, unit) + (i & 3) * 8));
+    typedef short s16x8 __attribute__((ext_vector_type(8)));
+    const s16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    return __builtin_bit_cast(bf16x8, v);
+}
+__device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// ---------------------------------------------------------------- a block's product
+// BM tokens x BN columns, WM x WN waves.  acc[i][j]: token i*16 + (lane & 15)
+// of the wave's rows, columns j*16 + (lane >> 4)*4 ..+3 of its columns.  The
+// tokens' operand always has consecutive inner elements; the other one has
+// them too (NN = false: rows of W, A_e) or lies across (NN = true: W read as
+// its transpose).  Stages go through registers into one of two LDS buffers,
+// the next stage's loads in flight over a stage's MFMAs.
+template <int BM, int BN, int WM, int WN, bool NN>
+struct Product {
+    static constexpr int threads = WM * WN * kWave;
+    static constexpr int TI = BM / WM / 16, TJ = BN / WN / 16;
+    static constexpr int bytes_a = BM * BK * 2, bytes_b = BN * BK * 2;
+    static constexpr int lds_bytes = 2 * (bytes_a + bytes_b);
+    static constexpr int PA = BM * 8 / threads, PB = BN * 8 / threads;
+    static_assert(PA * threads == BM * 8 && PB * threads == BN * 8, "whole pieces per thread");
+
+    f32x4 acc[TI][TJ];
+
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+#pragma unroll
+            for (int j = 0; j < TJ; ++j)
+                acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    // ga(row, k): 8 elements of the tokens' operand from inner element k.
+    // gb(n, k): 8 elements of column n from inner element k (NN = false), or
+    // of inner element k from column n (NN = true).  Both give zeros outside.
+    template <typename GA, typename GB>
+    __device__ __forceinline__ void load(GA ga, GB gb, int k0, u32x4 (&ra)[PA], u32x4 (&rb)[PB])
+    {
+        const int tid = threadIdx.x;
+#pragma unroll
+        for (int p = 0; p < PA; ++p) {
+            const int q = p * threads + tid;
+            ra[p] = ga(q >> 3, k0 + (q & 7) * 8);
+        }
+#pragma unroll
+        for (int p = 0; p < PB; ++p) {
+            const int q = p * threads + tid;
+            if constexpr (NN)
+                rb[p] = gb((q % (BN / 8)) * 8, k0 + q / (BN / 8));
+            else
+                rb[p] = gb(q >> 3, k0 + (q & 7) * 8);
+        }
+    }
+    __device__ __forceinline__ void store(char *buf, const u32x4 (&ra)[PA], const u32x4 (&rb)[PB])
+    {
+        const int tid = threadIdx.x;
+#pragma unroll
+        for (int p = 0; p < PA; ++p) {
+            const int q = p * threads + tid;
+            *reinterpret_cast<u32x4 *>(buf + off_k(q >> 3, q & 7)) = ra[p];
+        }
+        char *b = buf + bytes_a;
+#pragma unroll
+        for (int p = 0; p < PB; ++p) {
+            const int q = p * threads + tid;
+            if constexpr (NN) {
+                const int c = q % (BN / 8);
+                *reinterpret_cast<u32x4 *>(b + off_n<BN>(q / (BN / 8), c >> 1) + (c & 1) * 16) = rb[p];
+            } else {
+                *reinterpret_cast<u32x4 *>(b + off_k(q >> 3, q & 7)) = rb[p];
+            }
+        }
+    }
+    __device__ __forceinline__ void stage(const char *buf, int wm, int wn, int lane)
+    {
+        const char *b = buf + bytes_a;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            bf16x8 fa[TI], fb[TJ];
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+                fa[i] = frag_k(buf, wm * (BM / WM) + i * 16, ks, lane);
+#pragma unroll
+            for (int j = 0; j < TJ; ++j) {
+                if constexpr (NN)
+                    fb[j] = frag_n<BN>(b, wn * (BN / WN / 16) + j, ks, lane);
+                else
+                    fb[j] = frag_k(b, wn * (BN / WN) + j * 16, ks, lane);
+            }
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+#pragma unroll
+                for (int j = 0; j < TJ; ++j)
+                    acc[i][j] = mfma(fb[j], fa[i], acc[i][j]);
+        }
+    }
+    // Adds the inner elements of stages [s0, s1).  Ends with the block in step.
+    template <typename GA, typename GB>
+    __device__ __forceinline__ void run(char *lds, GA ga, GB gb, int s0, int s1)
+    {
+        const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+        const int wm = wave / WN, wn = wave % WN;
+        if (s0 >= s1)
+            return;
+        u32x4 ra[PA], rb[PB];
+        load(ga, gb, s0 * BK, ra, rb);
+        store(lds, ra, rb);
+        __syncthreads();
+        for (int s = s0; s < s1; ++s) {
+            const int cur = (s - s0) & 1;
+            if (s + 1 < s1)
+                load(ga, gb, (s + 1) * BK, ra, rb);
+            stage(lds + cur * (bytes_a + bytes_b), wm, wn, lane);
+            if (s + 1 < s1)
+                store(lds + (cur ^ 1) * (bytes_a + bytes_b), ra, rb);
+            __syncthreads();
+        }
+    }
+    __device__ __forceinline__ bool finite() const
+    {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+#pragma unroll
+            for (int j = 0; j < TJ; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    s = fmaf(acc[i][j][q], 0.0f, s);
+        return s == 0.0f;       // an infinity or a NaN anywhere makes it NaN
+    }
+};
+
+// ---------------------------------------------------------------- tiles
+struct Tiles {
+    int T, K, E, r, rp, BM, Lmax, LW;
+    const int32_t *idx;         // [T, K]
+    int32_t *cnt;               // [ntile] adapters in the list
+    int32_t *list;              // [ntile, Lmax]
+    int32_t *place;             // [ntile, E] place in the list, or -1
+    int32_t *bad;               // [ntile] invalid entries
+};
+
+__device__ __forceinline__ u32x4 zero4() { return u32x4{0u, 0u, 0u, 0u}; }
+
+__global__ void __launch_bounds__(256)
+adapter_tiles_kernel(Tiles m)
+{
+    extern __shared__ int32_t flags[];      // [E]
+    __shared__ int tmp[17];
+    __shared__ int n_bad;
+    const int tile = blockIdx.x, tid = threadIdx.x;
+    for (int e = tid; e < m.E; e += 256)
+        flags[e] = 0;
+    if (tid == 0)
+        n_bad = 0;
+    __syncthreads();
+    const int t0 = tile * m.BM, t1 = m.T - t0 < m.BM ? m.T : t0 + m.BM;
+    int bad = 0;
+    for (int64_t i = (int64_t)t0 * m.K + tid; i < (int64_t)t1 * m.K; i += 256) {
+        const int e = m.idx[i];
+        if ((unsigned)e < (unsigned)m.E)
+            flags[e] = 1;
+        else
+            bad += e != -1;
+    }
+    if (bad)
+        atomicAdd(&n_bad, bad);
+    __syncthreads();
+    const int per = (m.E + 255) / 256;
+    const int e0 = tid * per, e1 = e0 + per < m.E ? e0 + per : m.E;
+    int n = 0;
+    for (int e = e0; e < e1; ++e)
+        n += flags[e];
+    int total;
+    int at = block_exclusive_scan(n, tmp, &total);
+    int32_t *place = m.place + (int64_t)tile * m.E;
+    int32_t *list = m.list + (int64_t)tile * m.Lmax;
+    for (int e = e0; e < e1; ++e) {
+        place[e] = flags[e] ? at : -1;
+        if (flags[e])
+            list[at++] = e;
+    }
+    if (tid == 0) {
+        m.cnt[tile] = total;
+        m.bad[tile] = n_bad;
+    }
+}
+
+__global__ void adapter_zero_kernel(int32_t *p) { *p = 0; }
+
+// Splits of the inner dimension that a tile's shrink takes with a list of
+// `cols` columns: its `slots` blocks share the 64-column chunks.
+__device__ __forceinline__ int shrink_splits(int cols, int slots)
+{
+    const int chunks = (cols + 63) / 64;
+    return chunks >= slots ? 1 : (chunks > 0 ? slots / chunks : 1);
+}
+
+// ---------------------------------------------------------------- shrink
+// part[split][t*K + k][r] = sum over the split's inner elements of src[t][.]
+// times the entry's adapter: A [E, r, D] (NN = false), or B [E, D, r] (NN =
+// true).  Columns of the list in chunks of 64; products of a token and an
+// adapter it does not name are dropped.
+template <int BM, bool NN>
+__global__ void __launch_bounds__(BM / 32 * kWave)
+adapter_shrink_kernel(Tiles m, const uint16_t *__restrict__ src, const uint16_t *__restrict__ ad,
+                      int D, int slots, float *__restrict__ part)
+{
+    extern __shared__ char lds[];
+    typedef Product<BM, 64, BM / 32, 1, NN> P;
+    const int tile = blockIdx.x / slots, slot = blockIdx.x % slots;
+    const int cols = m.cnt[tile] * m.rp;
+    const int chunks = (cols + 63) / 64;
+    const int splits = shrink_splits(cols, slots);
+    const int split = chunks >= slots ? 0 : (chunks > 0 ? slot / chunks : 0);
+    if (split >= splits)
+        return;
+    const int step = chunks >= slots ? slots : chunks;
+    const int steps = (D + BK - 1) / BK;
+    const int s0 = (int)((int64_t)steps * split / splits);
+    const int s1 = (int)((int64_t)steps * (split + 1) / splits);
+    const int t0 = tile * BM;
+    const int32_t *list = m.list + (int64_t)tile * m.Lmax;
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    for (int chunk = chunks >= slots ? slot : (chunks > 0 ? slot % chunks : 0); chunk < chunks;
+         chunk += step) {
+        const int n0 = chunk * 64;
+        P p;
+        p.zero();
+        auto ga = [&](int row, int k) -> u32x4 {
+            const int t = t0 + row;
+            return t < m.T && k < D ? ld16(src + (int64_t)t * D + k) : zero4();
+        };
+        auto gb = [&](int n, int k) -> u32x4 {
+            const int l = (n0 + n) / m.rp, j = (n0 + n) % m.rp;
+            if (n0 + n >= cols || j >= m.r || k >= D)
+                return zero4();
+            const int64_t e = list[l];
+            return NN ? ld16(ad + (e * D + k) * m.r + j) : ld16(ad + (e * m.r + j) * D + k);
+        };
+        p.run(lds, ga, gb, s0, s1);
+#pragma unroll
+        for (int i = 0; i < P::TI; ++i) {
+            const int t = t0 + wave * 32 + i * 16 + (lane & 15);
+#pragma unroll
+            for (int j = 0; j < P::TJ; ++j) {
+                const int n = n0 + j * 16 + (lane >> 4) * 4;
+                const int l = n / m.rp, jj = n % m.rp;
+                if (n >= cols || jj >= m.r || t >= m.T)
+                    continue;
+                const int e = list[l];
+                for (int k = 0; k < m.K; ++k)
+                    if (m.idx[(int64_t)t * m.K + k] == e)
+                        *reinterpret_cast<f32x4 *>(
+                            part + (((int64_t)split * m.T + t) * m.K + k) * m.r + jj) = p.acc[i][j];
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- gather
+// Sums the splits: sums[t*K + k][r] in fp32, and the tile's dense matrix in
+// bf16 (one rounding of c times the sum: the operand of the next MFMA), zeros
+// up to the next 64 columns.  With `u` given, dw[t,k] = scale <u, sums>.
+// A block takes 32 rows of a tile.
+constexpr int kGatherRows = 32;
+__global__ void __launch_bounds__(256)
+adapter_gather_kernel(Tiles m, const float *__restrict__ w, float scale, int slots,
+                      const float *__restrict__ part, float *__restrict__ sums,
+                      uint16_t *__restrict__ dense, const float *__restrict__ u,
+                      float *__restrict__ dw, int ntile, int32_t *__restrict__ num_invalid)
+{
+    const int per = m.BM / kGatherRows;
+    const int tile = blockIdx.x / per, row0 = (blockIdx.x % per) * kGatherRows;
+    const int tid = threadIdx.x;
+    const int c = m.cnt[tile], cols = c * m.rp;
+    const int pieces = ((cols + BK - 1) / BK) * (BK / 8);
+    const int splits = shrink_splits(cols, slots);
+    const int32_t *list = m.list + (int64_t)tile * m.Lmax;
+    const int64_t stride = (int64_t)m.T * m.K * m.r;
+    for (int i = tid; i < kGatherRows * pieces; i += 256) {
+        const int row = row0 + i / pieces, n = (i % pieces) * 8;
+        const int t = tile * m.BM + row;
+        float s[8] = {0, 0, 0, 0, 0, 0, 0, 0}, coef = 0.0f;
+        const int l = n / m.rp, j = n % m.rp;
+        if (t < m.T && n < cols && j < m.r) {
+            const int e = list[l];
+            bool found = false;
+            for (int k = 0; k < m.K; ++k) {
+                const int64_t tk = (int64_t)t * m.K + k;
+                if (m.idx[tk] != e)
+                    continue;
+                coef += w ? w[tk] : 1.0f;
+                if (!found) {
+                    const float *p = part + tk * m.r + j;
+                    for (int q = 0; q < splits; ++q) {
+                        const f32x4 lo = *reinterpret_cast<const f32x4 *>(p + q * stride);
+                        const f32x4 hi = *reinterpret_cast<const f32x4 *>(p + q * stride + 4);
+#pragma unroll
+                        for (int d = 0; d < 4; ++d) {
+                            s[d] += lo[d];
+                            s[4 + d] += hi[d];
+                        }
+                    }
+                    found = true;
+                }
+                float *o = sums + tk * m.r + j;
+                *reinterpret_cast<f32x4 *>(o) = f32x4{s[0], s[1], s[2], s[3]};
+                *reinterpret_cast<f32x4 *>(o + 4) = f32x4{s[4], s[5], s[6], s[7]};
+            }
+            if (found)
+#pragma unroll
+                for (int d = 0; d < 8; ++d)
+                    s[d] *= scale * coef;
+        }
+        u32x4 v;
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+            v[d] = pack_bf16_any(s[2 * d], s[2 * d + 1]);
+        st16(dense + ((int64_t)tile * m.BM + row) * m.LW + n, v);
+    }
+    if (u && dw) {
+        __syncthreads();        // the block's own sums are read back
+        for (int i = tid; i < kGatherRows * m.K; i += 256) {
+            const int t = tile * m.BM + row0 + i / m.K;
+            if (t >= m.T)
+                break;
+            const int64_t tk = (int64_t)t * m.K + i % m.K;
+            float d = 0.0f;
+            if ((unsigned)m.idx[tk] < (unsigned)m.E)
+                for (int j = 0; j < m.r; ++j)
+                    d = fmaf(u[tk * m.r + j], sums[tk * m.r + j], d);
+            dw[tk] = scale * d;
+        }
+    }
+    if (num_invalid && blockIdx.x == 0 && tid < kWave) {
+        int n = 0;
+        for (int i = tid; i < ntile; i += kWave)
+            n += m.bad[i];
+        n = wave_sum(n);
+        if (tid == 0)
+            num_invalid[0] = n;
+    }
+}
+
+// ---------------------------------------------------------------- project
+// out[t][n] = sum_l dense[t][l] adapter_l[.][n] + sum_k src[t][k] W: W [N, D]
+// and B [E, N, r] for the forward (NN = false), W [D, N] and A [E, r, N] for
+// the gradient of x (NN = true).
+template <int BM, int BN, int WM, int WN, bool NN>
+__global__ void __launch_bounds__(WM * WN * kWave)
+adapter_project_kernel(Tiles m, const uint16_t *__restrict__ src, int D,
+                       const uint16_t *__restrict__ weight, int N, const uint16_t *__restrict__ ad,
+                       const uint16_t *__restrict__ dense, uint16_t *__restrict__ out)
+{
+    extern __shared__ char lds[];
+    typedef Product<BM, BN, WM, WN, NN> P;
+    const int nb = (N + BN - 1) / BN;
+    const int tile = blockIdx.x / nb, n0 = (blockIdx.x % nb) * BN;
+    const int t0 = tile * BM;
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int wm = wave / WN, wn = wave % WN;
+    const int32_t *list = m.list + (int64_t)tile * m.Lmax;
+    const int cols = m.cnt[tile] * m.rp;
+    const uint16_t *du = dense + (int64_t)t0 * m.LW;
+    P p;
+    p.zero();
+    if (cols > 0) {
+        auto ga = [&](int row, int k) -> u32x4 { return ld16(du + (int64_t)row * m.LW + k); };
+        auto gb = [&](int n, int k) -> u32x4 {
+            const int l = k / m.rp, j = k % m.rp;
+            if (k >= cols || j >= m.r || n0 + n >= N)
+                return zero4();
+            const int64_t e = list[l];
+            return NN ? ld16(ad + (e * m.r + j) * N + n0 + n) : ld16(ad + (e * N + n0 + n) * m.r + j);
+        };
+        p.run(lds, ga, gb, 0, (cols + BK - 1) / BK);
+        if (__any(!p.finite())) {
+            // again, one adapter at a time, for the tokens that name it only
+            p.zero();
+            for (int l = 0; l < cols / m.rp; ++l) {
+                const int64_t e = list[l];
+#pragma unroll
+                for (int i = 0; i < P::TI; ++i) {
+                    const int row = wm * (BM / WM) + i * 16 + (lane & 15), t = t0 + row;
+                    bool named = false;
+                    if (t < m.T)
+                        for (int k = 0; k < m.K; ++k)
+                            named = named || m.idx[(int64_t)t * m.K + k] == (int)e;
+#pragma unroll
+                    for (int j = 0; j < P::TJ; ++j) {
+                        const int n = n0 + wn * (BN / WN) + j * 16 + (lane & 15);
+                        f32x4 one = {0.0f, 0.0f, 0.0f, 0.0f};
+                        for (int k0 = 0; k0 < m.rp; k0 += 32) {
+                            const int k = k0 + (lane >> 4) * 8;
+                            u32x4 fu = zero4(), fb = zero4();
+                            if (k < m.r) {
+                                fu = ld16(du + (int64_t)row * m.LW + l * m.rp + k);
+                                if (n < N) {
+                                    if constexpr (NN) {
+                                        const uint16_t *a = ad + (e * m.r + k) * N + n;
+                                        for (int q = 0; q < 4; ++q)
+                                            fb[q] = a[(2 * q) * (int64_t)N] |
+                                                    ((uint32_t)a[(2 * q + 1) * (int64_t)N] << 16);
+                                    } else {
+                                        fb = ld16(ad + (e * N + n) * m.r + k);
+                                    }
+                                }
+                            }
+                            one = mfma(__builtin_bit_cast(bf16x8, fb), __builtin_bit_cast(bf16x8, fu), one);
+                        }
+                        if (named)
+                            p.acc[i][j] += one;
+                    }
+                }
+            }
+        }
+    }
+    {
+        auto ga = [&](int row, int k) -> u32x4 {
+            const int t = t0 + row;
+            return t < m.T && k < D ? ld16(src + (int64_t)t * D + k) : zero4();
+        };
+        auto gb = [&](int n, int k) -> u32x4 {
+            if (n0 + n >= N || k >= D)
+                return zero4();
+            return NN ? ld16(weight + (int64_t)k * N + n0 + n) : ld16(weight + (int64_t)(n0 + n) * D + k);
+        };
+        p.run(lds, ga, gb, 0, (D + BK - 1) / BK);
+    }
+#pragma unroll
+    for (int i = 0; i < P::TI; ++i) {
+        const int t = t0 + wm * (BM / WM) + i * 16 + (lane & 15);
+#pragma unroll
+        for (int j = 0; j < P::TJ; ++j) {
+            const int n = n0 + wn * (BN / WN) + j * 16 + (lane >> 4) * 4;
+            if (t < m.T && n < N) {
+                const f32x4 v = p.acc[i][j];
+                *reinterpret_cast<u32x2 *>(out + (int64_t)t * N + n) =
+                    u32x2{pack_bf16_any(v[0], v[1]), pack_bf16_any(v[2], v[3])};
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- grads
+// dA[e][j][h] = sum_t V[t][e, j] x[t][h]  (OUTER = false: big = x, N = H)
+// dB[e][o][j] = sum_t d[t][o] U[t][e, j]  (OUTER = true: big = d, N = O)
+// A block takes 128 columns of `big` and G = 128 / rp adapters with consecutive
+// ids, over the tiles of its split that name one of them; both operands lie
+// across and are read transposed.  With one split the result is rounded and
+// stored, else fp32 sums go to `part` (laid out like the result) to be added.
+constexpr int kGradCols = 128;
+template <bool OUTER>
+__global__ void __launch_bounds__(256)
+adapter_grads_kernel(Tiles m, const uint16_t *__restrict__ big, int N,
+                     const uint16_t *__restrict__ dense, int ntile, int splits,
+                     uint16_t *__restrict__ out, float *__restrict__ part)
+{
+    __shared__ __attribute__((aligned(16))) char lds[2 * BK * kGradCols * 2];
+    __shared__ int32_t at[kGradCols / 16];
+    const int G = kGradCols / m.rp;
+    const int n0 = blockIdx.x * kGradCols, e0 = blockIdx.y * G, split = blockIdx.z;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+    const int wb = wave >> 1, wd = wave & 1;        // the wave's half of the big columns, of the dense ones
+    const int i0 = (int)((int64_t)ntile * split / splits), i1 = (int)((int64_t)ntile * (split + 1) / splits);
+    f32x4 acc[4][4];        // [big unit][dense unit]
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+            acc[b][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    char *lb = lds, *ld = lds + BK * kGradCols * 2;
+    for (int tile = i0; tile < i1; ++tile) {
+        const int32_t *place = m.place + (int64_t)tile * m.E;
+        bool any = false;
+        for (int g = 0; g < G; ++g)
+            any = any || (e0 + g < m.E && place[e0 + g] >= 0);
+        if (!any)
+            continue;
+        __syncthreads();
+        if (tid < kGradCols / 16) {
+            const int g = tid * 16 / m.rp;
+            at[tid] = g < G && e0 + g < m.E && place[e0 + g] >= 0 ? place[e0 + g] * m.rp + tid * 16 % m.rp : -1;
+        }
+        __syncthreads();
+        bool on[4];
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+            on[d] = at[wd * 4 + d] >= 0;
+        const int rows = m.T - tile * m.BM < m.BM ? m.T - tile * m.BM : m.BM;
+        for (int r0 = 0; r0 < rows; r0 += BK) {
+            u32x4 rb[4], rd[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const int q = p * 256 + tid, row = r0 + q / 16, c = (q % 16) * 8;
+                const int64_t t = (int64_t)tile * m.BM + row;
+                rb[p] = t < m.T && n0 + c < N ? ld16(big + t * N + n0 + c) : zero4();
+                const int a = at[c / 16];
+                rd[p] = t < m.T && a >= 0 ? ld16(dense + t * m.LW + a + c % 16) : zero4();
+            }
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const int q = p * 256 + tid, k = q / 16, c = q % 16;
+                *reinterpret_cast<u32x4 *>(lb + off_n<kGradCols>(k, c >> 1) + (c & 1) * 16) = rb[p];
+                *reinterpret_cast<u32x4 *>(ld + off_n<kGradCols>(k, c >> 1) + (c & 1) * 16) = rd[p];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                bf16x8 fb[4];
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    fb[b] = frag_n<kGradCols>(lb, wb * 4 + b, ks, lane);
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    if (!on[d])
+                        continue;
+                    const bf16x8 fd = frag_n<kGradCols>(ld, wd * 4 + d, ks, lane);
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                        acc[b][d] = OUTER ? mfma(fd, fb[b], acc[b][d]) : mfma(fb[b], fd, acc[b][d]);
+                }
+            }
+            __syncthreads();
+        }
+    }
+    float s = 0.0f;
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                s = fmaf(acc[b][d][q], 0.0f, s);
+    const bool again = __any(!(s == 0.0f));
+    const int64_t total = (int64_t)m.E * m.r * N;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            // the four results of a lane: dense columns dn + (OUTER ? q : 0),
+            // big columns bn + (OUTER ? 0 : q)
+            const int dn = (wd * 4 + d) * 16 + (OUTER ? (lane >> 4) * 4 : (lane & 15));
+            const int bn = n0 + (wb * 4 + b) * 16 + (OUTER ? (lane & 15) : (lane >> 4) * 4);
+            const int g = dn / m.rp, j = dn % m.rp, e = e0 + g;
+            if (g >= G || e >= m.E || j >= m.r || bn >= N)
+                continue;
+            f32x4 v = acc[b][d];
+            if (again) {
+                // again, over the tokens that name the adapter only
+                v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                for (int tile = i0; tile < i1; ++tile) {
+                    const int l = m.place[(int64_t)tile * m.E + e];
+                    for (int row = 0; l >= 0 && row < m.BM; ++row) {
+                        const int64_t t = (int64_t)tile * m.BM + row;
+                        bool named = false;
+                        if (t < m.T)
+                            for (int k = 0; k < m.K; ++k)
+                                named = named || m.idx[t * m.K + k] == e;
+                        if (!named)
+                            continue;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint16_t x = big[t * N + bn + (OUTER ? 0 : q)];
+                            const uint16_t y = dense[t * m.LW + l * m.rp + j + (OUTER ? q : 0)];
+                            v[q] = fmaf(bf16_lo(x), bf16_lo(y), v[q]);
+                        }
+                    }
+                }
+            }
+            const int64_t o = OUTER ? ((int64_t)e * N + bn) * m.r + j : ((int64_t)e * m.r + j) * N + bn;
+            if (splits > 1)
+                *reinterpret_cast<f32x4 *>(part + split * total + o) = v;
+            else
+                *reinterpret_cast<u32x2 *>(out + o) =
+                    u32x2{pack_bf16_any(v[0], v[1]), pack_bf16_any(v[2], v[3])};
+        }
+    }
+}
+
+// The splits' sum, in split order, rounded to bf16.
+__global__ void __launch_bounds__(256)
+adapter_grads_sum_kernel(const float *__restrict__ part, int splits, int64_t total,
+                         uint16_t *__restrict__ out)
+{
+    const int64_t step = (int64_t)gridDim.x * 256 * 4;
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < total; i += step) {
+        f32x4 v = *reinterpret_cast<const f32x4 *>(part + i);
+        for (int z = 1; z < splits; ++z)
+            v += *reinterpret_cast<const f32x4 *>(part + z * total + i);
+        *reinterpret_cast<u32x2 *>(out + i) = u32x2{pack_bf16_any(v[0], v[1]), pack_bf16_any(v[2], v[3])};
+    }
+}
+
+Tiles make_tiles(const AdapterPlan &p, const int32_t *idx, char *state)
+{
+    Tiles m{};
+    m.T = p.T;
+    m.K = p.K;
+    m.E = p.E;
+    m.r = p.r;
+    m.rp = p.rp;
+    m.BM = p.BM;
+    m.Lmax = p.Lmax;
+    m.LW = p.LW;
+    m.idx = idx;
+    m.cnt = reinterpret_cast<int32_t *>(state + p.off_cnt);
+    m.bad = m.cnt + p.ntile;
+    m.list = reinterpret_cast<int32_t *>(state + p.off_list);
+    m.place = reinterpret_cast<int32_t *>(state + p.off_place);
+    return m;
+}
+
+template <int BM, bool NN>
+hipError_t shrink(const AdapterPlan &p, const Tiles &m, const uint16_t *src, const uint16_t *ad,
+                  int D, float *part, hipStream_t s)
+{
+    adapter_shrink_kernel<BM, NN><<<p.ntile * p.slots, BM / 32 * kWave,
+                                    (Product<BM, 64, BM / 32, 1, NN>::lds_bytes), s>>>(
+        m, src, ad, D, p.slots, part);
+    return hipGetLastError();
+}
+
+template <int BM, int BN, int WM, int WN, bool NN>
+hipError_t project(const AdapterPlan &p, const Tiles &m, const uint16_t *src, int D,
+                   const uint16_t *weight, int N, const uint16_t *ad, const uint16_t *dense,
+                   uint16_t *out, hipStream_t s)
+{
+    typedef Product<BM, BN, WM, WN, NN> P;
+    adapter_project_kernel<BM, BN, WM, WN, NN>
+        <<<p.ntile * ((N + BN - 1) / BN), P::threads, P::lds_bytes, s>>>(m, src, D, weight, N, ad,
+                                                                        dense, out);
+    return hipGetLastError();
+}
+
+// shrink + gather + project of one direction.
+template <bool NN>
+hipError_t pass(const AdapterPlan &p, const Tiles &m, const uint16_t *src, int D,
+                const uint16_t *weight, int N, const uint16_t *shrinker, const uint16_t *expander,
+                const float *w, float scale, float *part, float *sums, uint16_t *dense,
+                const float *u, float *dw, int32_t *num_invalid, uint16_t *out, hipStream_t s)
+{
+    hipError_t e = shrink<128, NN>(p, m, src, shrinker, D, part, s);
+    if (e != hipSuccess)
+        return e;
+    adapter_gather_kernel<<<p.ntile * (p.BM / kGatherRows), 256, 0, s>>>(
+        m, w, scale, p.slots, part, sums, dense, u, dw, p.ntile, num_invalid);
+    if ((e = hipGetLastError()) != hipSuccess || !out)
+        return e;
+    return project<128, 128, 2, 2, NN>(p, m, src, D, weight, N, expander, dense, out, s);
+}
+
+template <bool OUTER>
+hipError_t grads(const AdapterPlan &p, const Tiles &m, const uint16_t *big, int N,
+                 const uint16_t *dense, uint16_t *out, float *part, hipStream_t s)
+{
+    const int G = kGradCols / p.rp;
+    const int splits = adapter_grad_splits(p, N);
+    const dim3 grid((N + kGradCols - 1) / kGradCols, (p.E + G - 1) / G, splits);
+    adapter_grads_kernel<OUTER><<<grid, 256, 0, s>>>(m, big, N, dense, p.ntile, splits, out, part);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || splits == 1)
+        return e;
+    const int64_t total = (int64_t)p.E * p.r * N;
+    const int64_t blocks = (total / 4 + 255) / 256;
+    adapter_grads_sum_kernel<<<blocks < 4096 ? (int)blocks : 4096, 256, 0, s>>>(part, splits, total, out);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int adapter_grad_splits(const AdapterPlan &p, int N)
+{
+    const int G = kGradCols / p.rp;
+    const int64_t blocks = (int64_t)((N + kGradCols - 1) / kGradCols) * ((p.E + G - 1) / G);
+    int64_t splits = 512 / (blocks > 0 ? blocks : 1);
+    if (splits > 16)
+        splits = 16;
+    if (splits > p.ntile)
+        splits = p.ntile;
+    return splits < 1 ? 1 : (int)splits;
+}
+
+AdapterPlan make_adapter_plan(int T, int H, int O, int E, int K, int r)
+{
+    AdapterPlan p{};
+    p.T = T;
+    p.H = H;
+    p.O = O;
+    p.E = E;
+    p.K = K;
+    p.r = r;
+    p.rp = (r + 15) / 16 * 16;
+    p.BM = 128;
+    p.ntile = (T + p.BM - 1) / p.BM;
+    const int64_t rows = T < p.BM ? T : p.BM;
+    p.Lmax = (int)(rows * K < E ? (rows * K > 0 ? rows * K : 1) : E);
+    p.LW = (int)(((int64_t)p.Lmax * p.rp + BK - 1) / BK * BK);
+    p.slots = p.ntile > 0 ? 1024 / p.ntile : 1;
+    if (p.slots > 16)
+        p.slots = 16;
+    if (p.slots < 4)
+        p.slots = 4;
+    const size_t entries = (size_t)T * K * r * 4;
+    size_t off = 0;
+    p.off_cnt = off;
+    off = align256(off + 2 * (size_t)p.ntile * 4);
+    p.off_list = off;
+    off = align256(off + (size_t)p.ntile * p.Lmax * 4);
+    p.off_place = off;
+    off = align256(off + (size_t)p.ntile * E * 4);
+    p.off_u = off;
+    off = align256(off + entries);
+    p.off_dense = off;
+    off = align256(off + (size_t)p.ntile * p.BM * p.LW * 2);
+    p.state_bytes = off > 256 ? off : 256;
+    // forward: the splits' sums
+    p.off_part = 0;
+    p.ws_bytes = align256((size_t)p.slots * entries) + 256;
+    // backward: the splits' sums or those of the gradients, v and V
+    size_t part = (size_t)p.slots * entries;
+    for (const int n : {H, O}) {
+        const int z = adapter_grad_splits(p, n);
+        const size_t b = z > 1 ? (size_t)z * E * r * n * 4 : 0;
+        part = b > part ? b : part;
+    }
+    off = align256(part);
+    p.off_v = off;
+    off = align256(off + entries);
+    p.off_vdense = off;
+    off = align256(off + (size_t)p.ntile * p.BM * p.LW * 2);
+    p.back_bytes = off + 256;
+    return p;
+}
+
+hipError_t launch_adapter(const AdapterPlan &p, const uint16_t *x, const uint16_t *weight,
+                          const uint16_t *a, const uint16_t *b, const int32_t *idx, const float *w,
+                          float scale, uint16_t *out, int32_t *num_invalid, char *state, char *ws,
+                          hipStream_t s)
+{
+    if (p.T == 0) {
+        adapter_zero_kernel<<<1, 1, 0, s>>>(num_invalid);
+        return hipGetLastError();
+    }
+    const Tiles m = make_tiles(p, idx, state);
+    adapter_tiles_kernel<<<p.ntile, 256, (size_t)p.E * 4, s>>>(m);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return e;
+    return pass<false>(p, m, x, p.H, weight, p.O, a, b, w, scale,
+                       reinterpret_cast<float *>(ws + p.off_part),
+                       reinterpret_cast<float *>(state + p.off_u),
+                       reinterpret_cast<uint16_t *>(state + p.off_dense), nullptr, nullptr,
+                       num_invalid, out, s);
+}
+
+hipError_t launch_adapter_backward(const AdapterPlan &p, const uint16_t *d_out, const uint16_t *x,
+                                   const uint16_t *weight, const uint16_t *a, const uint16_t *b,
+                                   const int32_t *idx, const float *w, float scale, char *state,
+                                   uint16_t *dx, uint16_t *da, uint16_t *db, float *dw, char *ws,
+                                   hipStream_t s)
+{
+    const Tiles m = make_tiles(p, idx, state);
+    float *part = reinterpret_cast<float *>(ws + p.off_part);
+    uint16_t *vdense = reinterpret_cast<uint16_t *>(ws + p.off_vdense);
+    hipError_t e = hipSuccess;
+    if (p.T > 0)
+        e = pass<true>(p, m, d_out, p.O, weight, p.H, b, a, w, scale, part,
+                       reinterpret_cast<float *>(ws + p.off_v), vdense,
+                       reinterpret_cast<const float *>(state + p.off_u), dw, nullptr, dx, s);
+    if (e == hipSuccess && da)
+        e = grads<false>(p, m, x, p.H, vdense, da, part, s);
+    if (e == hipSuccess && db)
+        e = grads<true>(p, m, d_out, p.O, reinterpret_cast<const uint16_t *>(state + p.off_dense), db,
+                        part, s);
+    return e;
+}
+
+}  // namespace ep

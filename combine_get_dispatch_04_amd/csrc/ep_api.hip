@@ -584,4 +584,101 @@ ep_status_t ep_router_backward(const void *logits, ep_dtype_t dtype, int T, int 
         static_cast<hipStream_t>(stream)));
 }
 
+// ---------------------------------------------------------------- adapters
+namespace {
+
+ep_status_t check_adapter_sizes(int T, int H, int O, int E, int K, int r)
+{
+    if (T < 0 || K < 1 || E < 1 || H < 8 || H % 8 != 0 || O < 8 || O % 8 != 0 || r < 8 ||
+        r % 8 != 0 || (int64_t)T * K > kI32)
+        return EP_ERR_INVALID_ARG;
+    if (E > kMaxExperts || H > kMaxHidden || O > kMaxHidden || r > ep::kMaxAdapterRank ||
+        K > ep::kMaxAdapterTopk)
+        return EP_ERR_UNSUPPORTED;
+    // tiles of 128 tokens times blocks of 128 channels, 256 threads each: 32-bit grids
+    const int64_t tiles = ((int64_t)T + 127) / 128, blocks = ((H > O ? H : O) + 127) / 128;
+    if (tiles * (blocks > 16 ? blocks : 16) >= 1 << 23)
+        return EP_ERR_UNSUPPORTED;
+    return EP_OK;
+}
+
+// The operands of both directions.
+ep_status_t check_adapter_args(const uint16_t *x, int T, const uint16_t *weight, const uint16_t *a,
+                               const uint16_t *b, const int32_t *topk_idx,
+                               const float *topk_weights, const void *state)
+{
+    if (!weight || !a || !b || (T > 0 && (!x || !topk_idx)))
+        return EP_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(weight, 16) || !aligned(a, 16) || !aligned(b, 16) ||
+        !aligned(topk_idx, 4) || !aligned(topk_weights, 4) || !aligned(state, 256))
+        return EP_ERR_INVALID_ARG;
+    return EP_OK;
+}
+
+}  // namespace
+
+size_t ep_adapter_state_bytes(int T, int H, int O, int E, int K, int r)
+{
+    if (check_adapter_sizes(T, H, O, E, K, r) != EP_OK)
+        return 0;
+    return ep::make_adapter_plan(T, H, O, E, K, r).state_bytes;
+}
+
+size_t ep_adapter_workspace_bytes(int T, int H, int O, int E, int K, int r, int backward)
+{
+    if (check_adapter_sizes(T, H, O, E, K, r) != EP_OK)
+        return 0;
+    const ep::AdapterPlan p = ep::make_adapter_plan(T, H, O, E, K, r);
+    return backward ? p.back_bytes : p.ws_bytes;
+}
+
+ep_status_t ep_adapter_project(const uint16_t *x, int T, int H, const uint16_t *weight, int O,
+                               const uint16_t *a, const uint16_t *b, int E, int r,
+                               const int32_t *topk_idx, const float *topk_weights, int K,
+                               float scale, uint16_t *out, int32_t *num_invalid, void *state,
+                               size_t state_bytes, void *ws, size_t ws_bytes, void *stream)
+{
+    ep_status_t st = check_adapter_sizes(T, H, O, E, K, r);
+    if (st == EP_OK)
+        st = check_adapter_args(x, T, weight, a, b, topk_idx, topk_weights, state);
+    if (st != EP_OK)
+        return st;
+    if ((T > 0 && !out) || !aligned(out, 16) || !num_invalid || !aligned(num_invalid, 4))
+        return EP_ERR_INVALID_ARG;
+    const ep::AdapterPlan p = ep::make_adapter_plan(T, H, O, E, K, r);
+    if ((st = check_ws(state, state_bytes, p.state_bytes)) != EP_OK ||
+        (st = check_ws(ws, ws_bytes, p.ws_bytes)) != EP_OK)
+        return st;
+    return hip_status(ep::launch_adapter(p, x, weight, a, b, topk_idx, topk_weights, scale, out,
+                                         num_invalid, static_cast<char *>(state),
+                                         static_cast<char *>(ws),
+                                         static_cast<hipStream_t>(stream)));
+}
+
+ep_status_t ep_adapter_project_backward(const uint16_t *d_out, const uint16_t *x, int T, int H,
+                                        const uint16_t *weight, int O, const uint16_t *a,
+                                        const uint16_t *b, int E, int r, const int32_t *topk_idx,
+                                        const float *topk_weights, int K, float scale,
+                                        const void *state, size_t state_bytes, uint16_t *dx,
+                                        uint16_t *da, uint16_t *db, float *d_weights, void *ws,
+                                        size_t ws_bytes, void *stream)
+{
+    ep_status_t st = check_adapter_sizes(T, H, O, E, K, r);
+    if (st == EP_OK)
+        st = check_adapter_args(x, T, weight, a, b, topk_idx, topk_weights, state);
+    if (st != EP_OK)
+        return st;
+    if ((T > 0 && (!d_out || (!dx && !da && !db && !d_weights))) || !aligned(d_out, 16) ||
+        !aligned(dx, 16) || !aligned(da, 16) || !aligned(db, 16) || !aligned(d_weights, 4))
+        return EP_ERR_INVALID_ARG;
+    const ep::AdapterPlan p = ep::make_adapter_plan(T, H, O, E, K, r);
+    if ((st = check_ws(state, state_bytes, p.state_bytes)) != EP_OK ||
+        (st = check_ws(ws, ws_bytes, p.back_bytes)) != EP_OK)
+        return st;
+    return hip_status(ep::launch_adapter_backward(
+        p, d_out, x, weight, a, b, topk_idx, topk_weights, scale,
+        static_cast<char *>(const_cast<void *>(state)), dx, da, db, d_weights,
+        static_cast<char *>(ws), static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -89,6 +89,15 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
     return f32_to_bf16_rne(lo) | (f32_to_bf16_rne(hi) << 16);
 }
 
+// The same for any fp32 input: a NaN stays one (the sum above could carry its
+// payload away into an infinity).
+__device__ __forceinline__ uint32_t pack_bf16_any(float lo, float hi)
+{
+    typedef __bf16 b16x2 __attribute__((ext_vector_type(2)));
+    const b16x2 v = {(__bf16)lo, (__bf16)hi};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
 // ---------------------------------------------------------------- fp8 / fp4
 // gfx950 converts fp32 to the OCP 8-bit formats (E4M3: bias 7, largest
 // finite 448, no infinity; E5M2: bias 15, largest finite 57344) and to E2M1

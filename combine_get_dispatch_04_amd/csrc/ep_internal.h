@@ -125,6 +125,34 @@ hipError_t launch_router_backward(const void *logits, bool bf16, int T, int E, i
                                   const float *d_w, const float *slope, const int32_t *seq, int S,
                                   const float *d_loss, void *d_logits, hipStream_t s);
 
+// Low-rank adapters beside a shared projection (ep_adapter.hip).
+constexpr int kMaxAdapterRank = 128;
+constexpr int kMaxAdapterTopk = 64;
+
+struct AdapterPlan {
+    int T, H, O, E, K, r;
+    int rp;           // r rounded up to 16
+    int BM, ntile;    // tokens per tile, tiles
+    int Lmax, LW;     // adapters a tile can name, columns of its dense matrix
+    int slots;        // blocks that share a tile's shrink
+    // the state kept from the forward for the backward
+    size_t off_cnt, off_list, off_place, off_u, off_dense, state_bytes;
+    // the workspaces of the forward (ws_bytes) and the backward (back_bytes)
+    size_t off_part, ws_bytes, off_v, off_vdense, back_bytes;
+};
+AdapterPlan make_adapter_plan(int T, int H, int O, int E, int K, int r);
+int adapter_grad_splits(const AdapterPlan &p, int N);
+
+hipError_t launch_adapter(const AdapterPlan &p, const uint16_t *x, const uint16_t *weight,
+                          const uint16_t *a, const uint16_t *b, const int32_t *idx, const float *w,
+                          float scale, uint16_t *out, int32_t *num_invalid, char *state, char *ws,
+                          hipStream_t s);
+hipError_t launch_adapter_backward(const AdapterPlan &p, const uint16_t *d_out, const uint16_t *x,
+                                   const uint16_t *weight, const uint16_t *a, const uint16_t *b,
+                                   const int32_t *idx, const float *w, float scale, char *state,
+                                   uint16_t *dx, uint16_t *da, uint16_t *db, float *dw, char *ws,
+                                   hipStream_t s);
+
 inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // LDS bytes one block may take on the current device (cached per device).

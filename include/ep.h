@@ -503,6 +503,65 @@ ep_status_t ep_router_backward(const void *logits, ep_dtype_t dtype, int T, int 
                                const int32_t *seq_offsets, int S, const float *d_loss,
                                void *d_logits, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a shared projection (K = 1,
+ * topk_weights NULL), or low-rank experts beside a shared one, mixed by a
+ * router's choice (K > 1, its topk_idx and topk_weights):
+ *   out[t, :] = bf16( W x_t + sum over k with e = topk_idx[t,k] in [0, E) of
+ *                     scale * w[t,k] * B_e (A_e x_t) ),   w = 1 if topk_weights is NULL.
+ * bf16 operands, fp32 sums.  scale * w * (A_e x_t) is rounded to bf16 once (it is the
+ * operand of the product with B_e; an expert that a token names twice has its
+ * weights summed first), and the result once; likewise the gradients below.
+ * An infinity or a NaN in one adapter, or in one token, stays with the tokens
+ * that name the adapter, or with that token.
+ */
+
+/* Bytes of device memory that a forward call leaves for its backward (state),
+ * and of workspace that a call needs (backward != 0: the backward's). */
+size_t ep_adapter_state_bytes(int T, int H, int O, int E, int K, int r);
+size_t ep_adapter_workspace_bytes(int T, int H, int O, int E, int K, int r, int backward);
+
+/*
+ * ep_adapter_project
+ *   x             [T, H] bf16 in.
+ *   weight        [O, H] bf16 in: W, shared by all tokens.
+ *   a, b          [E, r, H], [E, O, r] bf16 in: A_e, B_e of the E adapters, of rank r.
+ *   topk_idx      [T, K] int32 in: -1 = none; other values outside [0, E) are
+ *                 counted in num_invalid and skipped.
+ *   topk_weights  [T, K] fp32 in or NULL.
+ *   out           [T, O] bf16 out; must not overlap an input.
+ *   num_invalid   [1] int32 out.
+ *   state         >= ep_adapter_state_bytes bytes, 256-byte aligned: read by the
+ *                 backward of this call; unused after it, or if there is none.
+ *   ws, ws_bytes  >= ep_adapter_workspace_bytes(..., 0); free after the call.
+ * Constraints: H % 8 == 0, O % 8 == 0, r % 8 == 0, r <= 128, E <= 4096,
+ * K <= 64, T*K < 2^31, ceil(T / 128) * ceil(max(H, O) / 128) < 2^23.
+ */
+ep_status_t ep_adapter_project(const uint16_t *x, int T, int H, const uint16_t *weight, int O,
+                               const uint16_t *a, const uint16_t *b, int E, int r,
+                               const int32_t *topk_idx, const float *topk_weights, int K,
+                               float scale, uint16_t *out, int32_t *num_invalid, void *state,
+                               size_t state_bytes, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * ep_adapter_project_backward -- the gradients for d_out [T, O] bf16; W is
+ * frozen and has none.  The other operands are those of the forward call,
+ * unchanged, with the state it left (read only: it serves any number of
+ * backward calls).  Any output may be NULL, but not all of them:
+ *   dx            [T, H] bf16 out.
+ *   da, db        [E, r, H], [E, O, r] bf16 out (0 for an adapter no token names).
+ *   d_weights     [T, K] fp32 out: scale * <A_e x_t, B_e^T d_out_t>, 0 for an
+ *                 entry outside [0, E).
+ *   ws, ws_bytes  >= ep_adapter_workspace_bytes(..., 1); free after the call.
+ */
+ep_status_t ep_adapter_project_backward(const uint16_t *d_out, const uint16_t *x, int T, int H,
+                                        const uint16_t *weight, int O, const uint16_t *a,
+                                        const uint16_t *b, int E, int r, const int32_t *topk_idx,
+                                        const float *topk_weights, int K, float scale,
+                                        const void *state, size_t state_bytes, uint16_t *dx,
+                                        uint16_t *da, uint16_t *db, float *d_weights, void *ws,
+                                        size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -56,24 +56,33 @@ __device__ __forceinline__ int off_n(int k, int unit)
     return k * (C * 2) + ((unit ^ f) << 5);
 }
 
-__device__ __forceinline__ bf16x8 frag_k(const char *tile, int row0, int ks, int lane)
+// A lane's operand of one 16 x 32 fragment: 8 consecutive inner elements from
+// ks*32 + (lane >> 4)*8, of row (or column) lane & 15 of its 16.  The lane's
+// own offset is worked out once (at_k, at_n); fragments, stages and halves are
+// constants on top of it, as row0 is a multiple of 16 and f(k) the same for k,
+// k + 4 and k + 32.
+__device__ __forceinline__ int at_k(int ks, int lane)
 {
-    const int row = row0 + (lane & 15);
-    return __builtin_bit_cast(bf16x8,
-                              *reinterpret_cast<const u32x4 *>(tile + off_k(row, ks * 4 + (lane >> 4))));
+    return off_k(lane & 15, ks * 4 + (lane >> 4));
 }
-// Lane: column unit*16 + (lane & 15), inner elements ks*32 + (lane >> 4)*8 ..+7.
-template <int C>
-__device__ __forceinline__ bf16x8 frag_n(const char *tile, int unit, int ks, int lane)
+__device__ __forceinline__ bf16x8 frag_k(const char *tile, int row0, int at)
 {
-    typedef __attribute__((address_space(3))) s16x4 *lds_ptr;
-    const int i = lane & 15, k = ks * 32 + (lane >> 4) * 8 + (i >> 2);
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (lds_ptr)(tile + off_n<C>(k, unit) + (i & 3) * 8));
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (lds_ptr)(tile + off_n<C>(k + 4, unit) + (i & 3) * 8));
+    return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(tile + row0 * 128 + at));
+}
+template <int C>
+__device__ __forceinline__ int at_n(int unit, int lane)
+{
+    return off_n<C>((lane >> 4) * 8 + ((lane & 15) >> 2), unit) + (lane & 3) * 8;
+}
+template <int C>
+__device__ __forceinline__ bf16x8 frag_n(const char *tile, int ks, int at)
+{
+    typedef __attribute__((address_space(3))) s16x4 *lds4_ptr;
     typedef short s16x8 __attribute__((ext_vector_type(8)));
-    const s16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_ptr)(tile + at + ks * 32 * C * 2));
+    const s16x4 hi =
+        __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_ptr)(tile + at + (ks * 32 + 4) * C * 2));
+    const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     return __builtin_bit_cast(bf16x8, v);
 }
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c)
@@ -86,14 +95,33 @@ __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c)
 // of the wave's rows, columns j*16 + (lane >> 4)*4 ..+3 of its columns.  The
 // tokens' operand always has consecutive inner elements; the other one has
 // them too (NN = false: rows of W, A_e) or lies across (NN = true: W read as
-// its transpose).  Stages go through registers into one of two LDS buffers,
-// the next stage's loads in flight over a stage's MFMAs.
-template <int BM, int BN, int WM, int WN, bool NN>
+// its transpose).
+//
+// A stage of 64 inner elements goes from memory straight to LDS, into one of
+// NS buffers, NS - 1 stages ahead of the MFMAs.  The wave's 64 pieces of 16
+// bytes land one after the other, so the swizzle is in the addresses: a lane
+// fetches the piece that belongs into its slot.  One barrier per stage: it
+// says that stage s is there for all waves, and that stage s - 1, whose buffer
+// the next loads take, has been read.
+typedef __attribute__((address_space(1))) const void *global_ptr;
+typedef __attribute__((address_space(3))) void *lds_ptr;
+
+template <int N>
+__device__ __forceinline__ void wait_and_meet()     // at most N loads in flight, no LDS access
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+template <int BM_, int BN_, int WM_, int WN_, int NS_, bool NN>
 struct Product {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_;
     static constexpr int threads = WM * WN * kWave;
     static constexpr int TI = BM / WM / 16, TJ = BN / WN / 16;
     static constexpr int bytes_a = BM * BK * 2, bytes_b = BN * BK * 2;
-    static constexpr int lds_bytes = 2 * (bytes_a + bytes_b);
+    static constexpr int bytes = bytes_a + bytes_b, lds_bytes = NS * bytes;
     static constexpr int PA = BM * 8 / threads, PB = BN * 8 / threads;
     static_assert(PA * threads == BM * 8 && PB * threads == BN * 8, "whole pieces per thread");
 
@@ -107,64 +135,66 @@ struct Product {
             for (int j = 0; j < TJ; ++j)
                 acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-
-    // ga(row, k): 8 elements of the tokens' operand from inner element k.
-    // gb(n, k): 8 elements of column n from inner element k (NN = false), or
-    // of inner element k from column n (NN = true).  Both give zeros outside.
-    template <typename GA, typename GB>
-    __device__ __forceinline__ void load(GA ga, GB gb, int k0, u32x4 (&ra)[PA], u32x4 (&rb)[PB])
+    // What piece q of a buffer holds: row and first inner element (tokens, and
+    // columns if NN = false) ...
+    static __device__ __forceinline__ int row_of(int q) { return q >> 3; }
+    static __device__ __forceinline__ int k_of(int q) { return ((q & 7) ^ (row_of(q) & 7)) * 8; }
+    // ... or inner row and first column (NN = true).
+    static __device__ __forceinline__ int kn_of(int q) { return q / (BN / 8); }
+    static __device__ __forceinline__ int n_of(int q)
     {
-        const int tid = threadIdx.x;
-#pragma unroll
-        for (int p = 0; p < PA; ++p) {
-            const int q = p * threads + tid;
-            ra[p] = ga(q >> 3, k0 + (q & 7) * 8);
-        }
-#pragma unroll
-        for (int p = 0; p < PB; ++p) {
-            const int q = p * threads + tid;
-            if constexpr (NN)
-                rb[p] = gb((q % (BN / 8)) * 8, k0 + q / (BN / 8));
-            else
-                rb[p] = gb(q >> 3, k0 + (q & 7) * 8);
-        }
+        const int k = kn_of(q), slot = q % (BN / 8);
+        const int f = ((k & 3) | ((k >> 1) & 4)) & (BN / 16 - 1);
+        return ((slot >> 1) ^ f) * 16 + (slot & 1) * 8;
     }
-    __device__ __forceinline__ void store(char *buf, const u32x4 (&ra)[PA], const u32x4 (&rb)[PB])
+    // Starts the loads of one stage into `buf`: pa(p), pb(p) are the addresses
+    // of the thread's pieces p*threads + threadIdx.x.
+    template <typename FA, typename FB>
+    static __device__ __forceinline__ void fetch(char *buf, FA pa, FB pb)
     {
-        const int tid = threadIdx.x;
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
 #pragma unroll
-        for (int p = 0; p < PA; ++p) {
-            const int q = p * threads + tid;
-            *reinterpret_cast<u32x4 *>(buf + off_k(q >> 3, q & 7)) = ra[p];
-        }
-        char *b = buf + bytes_a;
+        for (int p = 0; p < PA; ++p)
+            __builtin_amdgcn_global_load_lds((global_ptr)pa(p),
+                                             (lds_ptr)(buf + (p * threads + wave * kWave) * 16), 16, 0, 0);
 #pragma unroll
-        for (int p = 0; p < PB; ++p) {
-            const int q = p * threads + tid;
-            if constexpr (NN) {
-                const int c = q % (BN / 8);
-                *reinterpret_cast<u32x4 *>(b + off_n<BN>(q / (BN / 8), c >> 1) + (c & 1) * 16) = rb[p];
-            } else {
-                *reinterpret_cast<u32x4 *>(b + off_k(q >> 3, q & 7)) = rb[p];
-            }
-        }
+        for (int p = 0; p < PB; ++p)
+            __builtin_amdgcn_global_load_lds(
+                (global_ptr)pb(p), (lds_ptr)(buf + bytes_a + (p * threads + wave * kWave) * 16), 16, 0, 0);
+    }
+    // The same through registers, for a stage that ends beyond the inner
+    // dimension: va(p), vb(p) give the pieces, zeros where there is nothing.
+    template <typename FA, typename FB>
+    static __device__ __forceinline__ void fill(char *buf, FA va, FB vb)
+    {
+#pragma unroll 1
+        for (int p = 0; p < PA; ++p)
+            *reinterpret_cast<u32x4 *>(buf + (p * threads + threadIdx.x) * 16) = va(p);
+#pragma unroll 1
+        for (int p = 0; p < PB; ++p)
+            *reinterpret_cast<u32x4 *>(buf + bytes_a + (p * threads + threadIdx.x) * 16) = vb(p);
     }
     __device__ __forceinline__ void stage(const char *buf, int wm, int wn, int lane)
     {
         const char *b = buf + bytes_a;
+        int an[TJ];
+#pragma unroll
+        for (int j = 0; NN && j < TJ; ++j)
+            an[j] = at_n<BN>(wn * (BN / WN / 16) + j, lane);
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
+            const int ak = at_k(ks, lane);
             bf16x8 fa[TI], fb[TJ];
-#pragma unroll
-            for (int i = 0; i < TI; ++i)
-                fa[i] = frag_k(buf, wm * (BM / WM) + i * 16, ks, lane);
 #pragma unroll
             for (int j = 0; j < TJ; ++j) {
                 if constexpr (NN)
-                    fb[j] = frag_n<BN>(b, wn * (BN / WN / 16) + j, ks, lane);
+                    fb[j] = frag_n<BN>(b, ks, an[j]);
                 else
-                    fb[j] = frag_k(b, wn * (BN / WN) + j * 16, ks, lane);
+                    fb[j] = frag_k(b, wn * (BN / WN) + j * 16, ak);
             }
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+                fa[i] = frag_k(buf, wm * (BM / WM) + i * 16, ak);
 #pragma unroll
             for (int i = 0; i < TI; ++i)
 #pragma unroll
@@ -172,27 +202,40 @@ struct Product {
                     acc[i][j] = mfma(fb[j], fa[i], acc[i][j]);
         }
     }
-    // Adds the inner elements of stages [s0, s1).  Ends with the block in step.
-    template <typename GA, typename GB>
-    __device__ __forceinline__ void run(char *lds, GA ga, GB gb, int s0, int s1)
+    // Stages [0, n): issue(s, buf) starts the loads of stage s; called in order.
+    // Ends with every buffer free.
+    template <typename FI>
+    __device__ __forceinline__ void run(char *lds, int n, FI issue)
     {
-        const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+        const int lane = threadIdx.x & (kWave - 1);
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
         const int wm = wave / WN, wn = wave % WN;
-        if (s0 >= s1)
-            return;
-        u32x4 ra[PA], rb[PB];
-        load(ga, gb, s0 * BK, ra, rb);
-        store(lds, ra, rb);
-        __syncthreads();
-        for (int s = s0; s < s1; ++s) {
-            const int cur = (s - s0) & 1;
-            if (s + 1 < s1)
-                load(ga, gb, (s + 1) * BK, ra, rb);
-            stage(lds + cur * (bytes_a + bytes_b), wm, wn, lane);
-            if (s + 1 < s1)
-                store(lds + (cur ^ 1) * (bytes_a + bytes_b), ra, rb);
-            __syncthreads();
+        for (int s = 0; s < NS - 1 && s < n; ++s)
+            issue(s, lds + s * bytes);
+        int cur = 0, next = NS - 1;
+        for (int s = 0; s < n; ++s) {
+            if (s + NS - 1 <= n)
+                wait_and_meet<(NS - 2) * (PA + PB)>();
+            else
+                wait_and_meet<0>();
+            if (s + NS - 1 < n)
+                issue(s + NS - 1, lds + next * bytes);
+            stage(lds + cur * bytes, wm, wn, lane);
+            cur = cur + 1 == NS ? 0 : cur + 1;
+            next = next + 1 == NS ? 0 : next + 1;
         }
+        wait_and_meet<0>();
+    }
+    // One stage through registers (fill).
+    template <typename FA, typename FB>
+    __device__ __forceinline__ void run_filled(char *lds, FA va, FB vb)
+    {
+        const int lane = threadIdx.x & (kWave - 1);
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+        fill(lds, va, vb);
+        __syncthreads();
+        stage(lds, wave / WN, wave % WN, lane);
+        __syncthreads();
     }
     __device__ __forceinline__ bool finite() const
     {
@@ -207,6 +250,16 @@ struct Product {
         return s == 0.0f;       // an infinity or a NaN anywhere makes it NaN
     }
 };
+
+__device__ __forceinline__ int least(int a, int b) { return a < b ? a : b; }
+
+// Blocks are dealt to the 8 XCDs in turn; this gives each XCD a run of
+// consecutive tiles, so that its L2 sees the operands they share.
+__device__ __forceinline__ int xcd_order(int b, int n)
+{
+    const int each = n / 8, rest = n % 8, x = b % 8;
+    return x * each + least(x, rest) + b / 8;
+}
 
 // ---------------------------------------------------------------- tiles
 struct Tiles {
@@ -279,14 +332,22 @@ __device__ __forceinline__ int shrink_splits(int cols, int slots)
 // times the entry's adapter: A [E, r, D] (NN = false), or B [E, D, r] (NN =
 // true).  Columns of the list in chunks of 64; products of a token and an
 // adapter it does not name are dropped.
-template <int BM, bool NN>
-__global__ void __launch_bounds__(BM / 32 * kWave)
+// A block takes RB tokens of a tile.
+template <int RB, bool NN>
+struct Shrink {
+    typedef Product<RB, 64, RB / 32, 1, 3, NN> P;
+};
+template <int RB, bool NN>
+__global__ void __launch_bounds__(RB * 2)
 adapter_shrink_kernel(Tiles m, const uint16_t *__restrict__ src, const uint16_t *__restrict__ ad,
                       int D, int slots, float *__restrict__ part)
 {
-    extern __shared__ char lds[];
-    typedef Product<BM, 64, BM / 32, 1, NN> P;
-    const int tile = blockIdx.x / slots, slot = blockIdx.x % slots;
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    typedef typename Shrink<RB, NN>::P P;
+    const int block = blockIdx.x / slots, slot = blockIdx.x % slots;
+    const int tile = block / (m.BM / RB), t0 = block * RB;
+    if (t0 >= m.T)
+        return;
     const int cols = m.cnt[tile] * m.rp;
     const int chunks = (cols + 63) / 64;
     const int splits = shrink_splits(cols, slots);
@@ -297,26 +358,60 @@ adapter_shrink_kernel(Tiles m, const uint16_t *__restrict__ src, const uint16_t 
     const int steps = (D + BK - 1) / BK;
     const int s0 = (int)((int64_t)steps * split / splits);
     const int s1 = (int)((int64_t)steps * (split + 1) / splits);
-    const int t0 = tile * BM;
     const int32_t *list = m.list + (int64_t)tile * m.Lmax;
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+    const int whole = least(s1, D / BK) - s0;       // without the stage that ends beyond D
     for (int chunk = chunks >= slots ? slot : (chunks > 0 ? slot % chunks : 0); chunk < chunks;
          chunk += step) {
         const int n0 = chunk * 64;
         P p;
         p.zero();
-        auto ga = [&](int row, int k) -> u32x4 {
-            const int t = t0 + row;
-            return t < m.T && k < D ? ld16(src + (int64_t)t * D + k) : zero4();
-        };
-        auto gb = [&](int n, int k) -> u32x4 {
-            const int l = (n0 + n) / m.rp, j = (n0 + n) % m.rp;
-            if (n0 + n >= cols || j >= m.r || k >= D)
-                return zero4();
+        // rows behind the last token and columns behind the list's last repeat
+        // a row and a column that exist: their products are not stored
+        const uint16_t *pa[P::PA], *pb[P::PB];
+#pragma unroll
+        for (int i = 0; i < P::PA; ++i) {
+            const int q = i * P::threads + tid;
+            pa[i] = src + (int64_t)least(t0 + P::row_of(q), m.T - 1) * D + (s0 * BK + P::k_of(q));
+        }
+#pragma unroll
+        for (int i = 0; i < P::PB; ++i) {
+            const int q = i * P::threads + tid;
+            const int n = n0 + (NN ? P::n_of(q) : P::row_of(q));
+            const int l = n < cols ? n / m.rp : 0, j = n < cols && n % m.rp < m.r ? n % m.rp : 0;
             const int64_t e = list[l];
-            return NN ? ld16(ad + (e * D + k) * m.r + j) : ld16(ad + (e * m.r + j) * D + k);
-        };
-        p.run(lds, ga, gb, s0, s1);
+            pb[i] = NN ? ad + (e * D + s0 * BK + P::kn_of(q)) * m.r + j
+                       : ad + (e * m.r + j) * D + (s0 * BK + P::k_of(q));
+        }
+        p.run(lds, whole, [&](int, char *buf) {
+            P::fetch(buf, [&](int i) { return pa[i]; }, [&](int i) { return pb[i]; });
+#pragma unroll
+            for (int i = 0; i < P::PA; ++i)
+                pa[i] += BK;
+#pragma unroll
+            for (int i = 0; i < P::PB; ++i)
+                pb[i] += NN ? BK * m.r : BK;
+        });
+        if (whole < s1 - s0) {
+            const int k0 = (s0 + whole) * BK, left = D - k0;
+            p.run_filled(
+                lds,
+                [&](int i) {
+                    const int q = i * P::threads + tid, k = P::k_of(q);
+                    return k < left ? ld16(src + (int64_t)least(t0 + P::row_of(q), m.T - 1) * D + k0 + k)
+                                    : zero4();
+                },
+                [&](int i) {
+                    const int q = i * P::threads + tid;
+                    const int n = n0 + (NN ? P::n_of(q) : P::row_of(q));
+                    const int k = NN ? P::kn_of(q) : P::k_of(q);
+                    if (k >= left || n >= cols || n % m.rp >= m.r)
+                        return zero4();
+                    const int64_t e = list[n / m.rp];
+                    return NN ? ld16(ad + (e * D + k0 + k) * m.r + n % m.rp)
+                              : ld16(ad + (e * m.r + n % m.rp) * D + k0 + k);
+                });
+        }
 #pragma unroll
         for (int i = 0; i < P::TI; ++i) {
             const int t = t0 + wave * 32 + i * 16 + (lane & 15);
@@ -425,98 +520,149 @@ adapter_gather_kernel(Tiles m, const float *__restrict__ w, float scale, int slo
 // out[t][n] = sum_l dense[t][l] adapter_l[.][n] + sum_k src[t][k] W: W [N, D]
 // and B [E, N, r] for the forward (NN = false), W [D, N] and A [E, r, N] for
 // the gradient of x (NN = true).
-template <int BM, int BN, int WM, int WN, bool NN>
-__global__ void __launch_bounds__(WM * WN * kWave)
+
+// The adapters' part of 16 tokens (lane & 15: token t with its row u of U) by
+// columns c .. c+15, one adapter at a time, each for the tokens that name it
+// only: where the sum over U is not finite.
+template <bool NN>
+__device__ __forceinline__ f32x4 adapters_apart(const Tiles &m, const int32_t *list, int n_list,
+                                                const uint16_t *u, int t, const uint16_t *ad, int N,
+                                                int c, int lane)
+{
+    const int n = c + (lane & 15);
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+    for (int l = 0; l < n_list; ++l) {
+        const int64_t e = list[l];
+        bool named = false;
+        for (int k = 0; t < m.T && k < m.K; ++k)
+            named = named || m.idx[(int64_t)t * m.K + k] == (int)e;
+        f32x4 one = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+        for (int k0 = 0; k0 < m.rp; k0 += 32) {
+            const int k = k0 + (lane >> 4) * 8;
+            u32x4 fu = zero4(), fa = zero4();
+            if (k < m.r) {
+                fu = ld16(u + l * m.rp + k);
+                if (n < N) {
+                    if constexpr (NN) {
+                        const uint16_t *a = ad + (e * m.r + k) * N + n;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            fa[q] = a[(2 * q) * (int64_t)N] | ((uint32_t)a[(2 * q + 1) * (int64_t)N] << 16);
+                    } else {
+                        fa = ld16(ad + (e * N + n) * m.r + k);
+                    }
+                }
+            }
+            one = mfma(__builtin_bit_cast(bf16x8, fa), __builtin_bit_cast(bf16x8, fu), one);
+        }
+        if (named)
+            sum += one;
+    }
+    return sum;
+}
+
+template <typename P, bool NN>
+__global__ void __launch_bounds__(P::threads)
 adapter_project_kernel(Tiles m, const uint16_t *__restrict__ src, int D,
                        const uint16_t *__restrict__ weight, int N, const uint16_t *__restrict__ ad,
-                       const uint16_t *__restrict__ dense, uint16_t *__restrict__ out)
+                       const uint16_t *__restrict__ dense, int ntile, uint16_t *__restrict__ out)
 {
-    extern __shared__ char lds[];
-    typedef Product<BM, BN, WM, WN, NN> P;
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    constexpr int BM = P::BM, BN = P::BN, WM = P::WM, WN = P::WN;
+    // tiles in groups of 8 token tiles by all columns, column by column
     const int nb = (N + BN - 1) / BN;
-    const int tile = blockIdx.x / nb, n0 = (blockIdx.x % nb) * BN;
+    const int id = xcd_order(blockIdx.x, ntile * nb);
+    const int group = id / (8 * nb), first = group * 8;
+    const int rows = least(8, ntile - first);
+    const int tile = first + (id - group * 8 * nb) % rows, n0 = (id - group * 8 * nb) / rows * BN;
     const int t0 = tile * BM;
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
     const int wm = wave / WN, wn = wave % WN;
     const int32_t *list = m.list + (int64_t)tile * m.Lmax;
     const int cols = m.cnt[tile] * m.rp;
     const uint16_t *du = dense + (int64_t)t0 * m.LW;
     P p;
     p.zero();
+    bool apart = false;
     if (cols > 0) {
-        auto ga = [&](int row, int k) -> u32x4 { return ld16(du + (int64_t)row * m.LW + k); };
-        auto gb = [&](int n, int k) -> u32x4 {
-            const int l = k / m.rp, j = k % m.rp;
-            if (k >= cols || j >= m.r || n0 + n >= N)
-                return zero4();
-            const int64_t e = list[l];
-            return NN ? ld16(ad + (e * m.r + j) * N + n0 + n) : ld16(ad + (e * N + n0 + n) * m.r + j);
-        };
-        p.run(lds, ga, gb, 0, (cols + BK - 1) / BK);
-        if (__any(!p.finite())) {
-            // again, one adapter at a time, for the tokens that name it only
+        // columns behind the list's last meet zeros of U
+        p.run(lds, (cols + BK - 1) / BK, [&](int s, char *buf) {
+            P::fetch(
+                buf,
+                [&](int i) {
+                    const int q = i * P::threads + tid;
+                    return du + (int64_t)P::row_of(q) * m.LW + s * BK + P::k_of(q);
+                },
+                [&](int i) {
+                    const int q = i * P::threads + tid;
+                    const int k = s * BK + (NN ? P::kn_of(q) : P::k_of(q));
+                    const int l = k < cols ? k / m.rp : 0, j = k < cols && k % m.rp < m.r ? k % m.rp : 0;
+                    const int64_t e = list[l];
+                    return NN ? ad + (e * m.r + j) * N + least(n0 + P::n_of(q), N - 8)
+                              : ad + (e * N + least(n0 + P::row_of(q), N - 1)) * m.r + j;
+                });
+        });
+        apart = __any(!p.finite());
+        if (apart)
             p.zero();
-            for (int l = 0; l < cols / m.rp; ++l) {
-                const int64_t e = list[l];
-#pragma unroll
-                for (int i = 0; i < P::TI; ++i) {
-                    const int row = wm * (BM / WM) + i * 16 + (lane & 15), t = t0 + row;
-                    bool named = false;
-                    if (t < m.T)
-                        for (int k = 0; k < m.K; ++k)
-                            named = named || m.idx[(int64_t)t * m.K + k] == (int)e;
-#pragma unroll
-                    for (int j = 0; j < P::TJ; ++j) {
-                        const int n = n0 + wn * (BN / WN) + j * 16 + (lane & 15);
-                        f32x4 one = {0.0f, 0.0f, 0.0f, 0.0f};
-                        for (int k0 = 0; k0 < m.rp; k0 += 32) {
-                            const int k = k0 + (lane >> 4) * 8;
-                            u32x4 fu = zero4(), fb = zero4();
-                            if (k < m.r) {
-                                fu = ld16(du + (int64_t)row * m.LW + l * m.rp + k);
-                                if (n < N) {
-                                    if constexpr (NN) {
-                                        const uint16_t *a = ad + (e * m.r + k) * N + n;
-                                        for (int q = 0; q < 4; ++q)
-                                            fb[q] = a[(2 * q) * (int64_t)N] |
-                                                    ((uint32_t)a[(2 * q + 1) * (int64_t)N] << 16);
-                                    } else {
-                                        fb = ld16(ad + (e * N + n) * m.r + k);
-                                    }
-                                }
-                            }
-                            one = mfma(__builtin_bit_cast(bf16x8, fb), __builtin_bit_cast(bf16x8, fu), one);
-                        }
-                        if (named)
-                            p.acc[i][j] += one;
-                    }
-                }
-            }
-        }
     }
     {
-        auto ga = [&](int row, int k) -> u32x4 {
-            const int t = t0 + row;
-            return t < m.T && k < D ? ld16(src + (int64_t)t * D + k) : zero4();
-        };
-        auto gb = [&](int n, int k) -> u32x4 {
-            if (n0 + n >= N || k >= D)
-                return zero4();
-            return NN ? ld16(weight + (int64_t)k * N + n0 + n) : ld16(weight + (int64_t)(n0 + n) * D + k);
-        };
-        p.run(lds, ga, gb, 0, (D + BK - 1) / BK);
+        // rows and columns behind the last repeat one that exists: not stored
+        const uint16_t *pa[P::PA], *pb[P::PB];
+#pragma unroll
+        for (int i = 0; i < P::PA; ++i) {
+            const int q = i * P::threads + tid;
+            pa[i] = src + (int64_t)least(t0 + P::row_of(q), m.T - 1) * D + P::k_of(q);
+        }
+#pragma unroll
+        for (int i = 0; i < P::PB; ++i) {
+            const int q = i * P::threads + tid;
+            // n_of is a multiple of 8, as is N
+            pb[i] = NN ? weight + (int64_t)P::kn_of(q) * N + least(n0 + P::n_of(q), N - 8)
+                       : weight + (int64_t)least(n0 + P::row_of(q), N - 1) * D + P::k_of(q);
+        }
+        p.run(lds, D / BK, [&](int, char *buf) {
+            P::fetch(buf, [&](int i) { return pa[i]; }, [&](int i) { return pb[i]; });
+#pragma unroll
+            for (int i = 0; i < P::PA; ++i)
+                pa[i] += BK;
+#pragma unroll
+            for (int i = 0; i < P::PB; ++i)
+                pb[i] += NN ? (int64_t)BK * N : BK;
+        });
+    }
+    if (D % BK) {
+        const int k0 = D / BK * BK, left = D - k0;
+        p.run_filled(
+            lds,
+            [&](int i) {
+                const int q = i * P::threads + tid, k = P::k_of(q);
+                return k < left ? ld16(src + (int64_t)least(t0 + P::row_of(q), m.T - 1) * D + k0 + k)
+                                : zero4();
+            },
+            [&](int i) {
+                const int q = i * P::threads + tid, k = NN ? P::kn_of(q) : P::k_of(q);
+                if (k >= left)
+                    return zero4();
+                return NN ? ld16(weight + (int64_t)(k0 + k) * N + least(n0 + P::n_of(q), N - 8))
+                          : ld16(weight + (int64_t)least(n0 + P::row_of(q), N - 1) * D + k0 + k);
+            });
     }
 #pragma unroll
     for (int i = 0; i < P::TI; ++i) {
-        const int t = t0 + wm * (BM / WM) + i * 16 + (lane & 15);
+        const int row = wm * (BM / WM) + i * 16 + (lane & 15), t = t0 + row;
 #pragma unroll
         for (int j = 0; j < P::TJ; ++j) {
-            const int n = n0 + wn * (BN / WN) + j * 16 + (lane >> 4) * 4;
-            if (t < m.T && n < N) {
-                const f32x4 v = p.acc[i][j];
+            const int c = n0 + wn * (BN / WN) + j * 16;
+            f32x4 v = p.acc[i][j];
+            if (apart)
+                v += adapters_apart<NN>(m, list, cols / m.rp, du + (int64_t)row * m.LW, t, ad, N, c, lane);
+            const int n = c + (lane >> 4) * 4;
+            if (t < m.T && n < N)
                 *reinterpret_cast<u32x2 *>(out + (int64_t)t * N + n) =
                     u32x2{pack_bf16_any(v[0], v[1]), pack_bf16_any(v[2], v[3])};
-            }
         }
     }
 }
@@ -589,12 +735,12 @@ adapter_grads_kernel(Tiles m, const uint16_t *__restrict__ big, int N,
                 bf16x8 fb[4];
 #pragma unroll
                 for (int b = 0; b < 4; ++b)
-                    fb[b] = frag_n<kGradCols>(lb, wb * 4 + b, ks, lane);
+                    fb[b] = frag_n<kGradCols>(lb, ks, at_n<kGradCols>(wb * 4 + b, lane));
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
                     if (!on[d])
                         continue;
-                    const bf16x8 fd = frag_n<kGradCols>(ld, wd * 4 + d, ks, lane);
+                    const bf16x8 fd = frag_n<kGradCols>(ld, ks, at_n<kGradCols>(wd * 4 + d, lane));
 #pragma unroll
                     for (int b = 0; b < 4; ++b)
                         acc[b][d] = OUTER ? mfma(fd, fb[b], acc[b][d]) : mfma(fb[b], fd, acc[b][d]);
@@ -690,25 +836,40 @@ Tiles make_tiles(const AdapterPlan &p, const int32_t *idx, char *state)
     return m;
 }
 
-template <int BM, bool NN>
+// More than 64 KB of shared memory need the attribute.
+template <typename F>
+hipError_t allow_lds(F *kernel, int bytes)
+{
+    if (bytes <= 64 * 1024)
+        return hipSuccess;
+    return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                               hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <int RB, bool NN>
 hipError_t shrink(const AdapterPlan &p, const Tiles &m, const uint16_t *src, const uint16_t *ad,
                   int D, float *part, hipStream_t s)
 {
-    adapter_shrink_kernel<BM, NN><<<p.ntile * p.slots, BM / 32 * kWave,
-                                    (Product<BM, 64, BM / 32, 1, NN>::lds_bytes), s>>>(
+    typedef typename Shrink<RB, NN>::P P;
+    const hipError_t e = allow_lds(adapter_shrink_kernel<RB, NN>, P::lds_bytes);
+    if (e != hipSuccess)
+        return e;
+    adapter_shrink_kernel<RB, NN><<<p.ntile * (p.BM / RB) * p.slots, P::threads, P::lds_bytes, s>>>(
         m, src, ad, D, p.slots, part);
     return hipGetLastError();
 }
 
-template <int BM, int BN, int WM, int WN, bool NN>
+template <int BM, int BN, int WM, int WN, int NS, bool NN>
 hipError_t project(const AdapterPlan &p, const Tiles &m, const uint16_t *src, int D,
                    const uint16_t *weight, int N, const uint16_t *ad, const uint16_t *dense,
                    uint16_t *out, hipStream_t s)
 {
-    typedef Product<BM, BN, WM, WN, NN> P;
-    adapter_project_kernel<BM, BN, WM, WN, NN>
-        <<<p.ntile * ((N + BN - 1) / BN), P::threads, P::lds_bytes, s>>>(m, src, D, weight, N, ad,
-                                                                        dense, out);
+    typedef Product<BM, BN, WM, WN, NS, NN> P;
+    const hipError_t e = allow_lds(adapter_project_kernel<P, NN>, P::lds_bytes);
+    if (e != hipSuccess)
+        return e;
+    adapter_project_kernel<P, NN><<<p.ntile * ((N + BN - 1) / BN), P::threads, P::lds_bytes, s>>>(
+        m, src, D, weight, N, ad, dense, p.ntile, out);
     return hipGetLastError();
 }
 
@@ -719,14 +880,21 @@ hipError_t pass(const AdapterPlan &p, const Tiles &m, const uint16_t *src, int D
                 const float *w, float scale, float *part, float *sums, uint16_t *dense,
                 const float *u, float *dw, int32_t *num_invalid, uint16_t *out, hipStream_t s)
 {
-    hipError_t e = shrink<128, NN>(p, m, src, shrinker, D, part, s);
+    hipError_t e = p.BM == 64 ? shrink<64, NN>(p, m, src, shrinker, D, part, s)
+                              : shrink<128, NN>(p, m, src, shrinker, D, part, s);
     if (e != hipSuccess)
         return e;
     adapter_gather_kernel<<<p.ntile * (p.BM / kGatherRows), 256, 0, s>>>(
         m, w, scale, p.slots, part, sums, dense, u, dw, p.ntile, num_invalid);
     if ((e = hipGetLastError()) != hipSuccess || !out)
         return e;
-    return project<128, 128, 2, 2, NN>(p, m, src, D, weight, N, expander, dense, out, s);
+    switch (p.BM) {
+    case 64:
+        return project<64, 64, 2, 2, 4, NN>(p, m, src, D, weight, N, expander, dense, out, s);
+    case 128:
+        return project<128, 128, 2, 2, 2, NN>(p, m, src, D, weight, N, expander, dense, out, s);
+    }
+    return project<256, 256, 2, 4, 2, NN>(p, m, src, D, weight, N, expander, dense, out, s);
 }
 
 template <bool OUTER>
@@ -770,12 +938,14 @@ AdapterPlan make_adapter_plan(int T, int H, int O, int E, int K, int r)
     p.K = K;
     p.r = r;
     p.rp = (r + 15) / 16 * 16;
-    p.BM = 128;
+    const int N = H < O ? H : O;
+    auto blocks = [&](int b) { return ((int64_t)T + b - 1) / b * ((N + b - 1) / b); };
+    p.BM = blocks(256) >= 192 ? 256 : (blocks(128) >= 192 ? 128 : 64);
     p.ntile = (T + p.BM - 1) / p.BM;
     const int64_t rows = T < p.BM ? T : p.BM;
     p.Lmax = (int)(rows * K < E ? (rows * K > 0 ? rows * K : 1) : E);
     p.LW = (int)(((int64_t)p.Lmax * p.rp + BK - 1) / BK * BK);
-    p.slots = p.ntile > 0 ? 1024 / p.ntile : 1;
+    p.slots = T > 0 ? 1024 / ((T + 127) / 128) : 1;
     if (p.slots > 16)
         p.slots = 16;
     if (p.slots < 4)

@@ -35,7 +35,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int BK = 64;                 // inner elements per stage
+constexpr int BK = 64;                 // inner elements per stage: two slices of 32, one MFMA each
 
 // ---------------------------------------------------------------- LDS tiles
 // A tile of rows with 64 consecutive inner elements: 8 pieces of 16 bytes per
@@ -45,21 +45,21 @@ __device__ __forceinline__ int off_k(int row, int piece)
 {
     return row * 128 + ((piece ^ (row & 7)) << 4);
 }
-// A tile of 64 inner rows with C consecutive columns, read transposed: units
-// of 16 columns (32 bytes), unit u of row k in slot u ^ f(k).  A transposing
-// read takes rows {0..3, 8..11, 16..19, 24..27} of one unit: f tells eight of
-// them apart.
-template <int C>
+// A tile of 64 inner rows with consecutive columns, read transposed: blocks
+// of 64 columns, each 64 rows of 128 bytes, so that the loads fetch whole
+// 128-byte lines of 8 rows at a time as above.  A row has 4 units of 16
+// columns (32 bytes), unit u of row k in slot u ^ g(k).  A transposing read
+// takes rows {0..3, 8..11, 16..19, 24..27} of one unit: the row's parity and
+// g tell eight of them apart.
+__device__ __forceinline__ int unit_swizzle(int k) { return ((k >> 1) & 1) | ((k >> 2) & 2); }
 __device__ __forceinline__ int off_n(int k, int unit)
 {
-    const int f = ((k & 3) | ((k >> 1) & 4)) & (C / 16 - 1);
-    return k * (C * 2) + ((unit ^ f) << 5);
+    return (unit >> 2) * (BK * 128) + k * 128 + (((unit & 3) ^ unit_swizzle(k)) << 5);
 }
-
 // A lane's operand of one 16 x 32 fragment: 8 consecutive inner elements from
 // ks*32 + (lane >> 4)*8, of row (or column) lane & 15 of its 16.  The lane's
 // own offset is worked out once (at_k, at_n); fragments, stages and halves are
-// constants on top of it, as row0 is a multiple of 16 and f(k) the same for k,
+// constants on top of it, as row0 is a multiple of 16 and g(k) the same for k,
 // k + 4 and k + 32.
 __device__ __forceinline__ int at_k(int ks, int lane)
 {
@@ -69,21 +69,68 @@ __device__ __forceinline__ bf16x8 frag_k(const char *tile, int row0, int at)
 {
     return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(tile + row0 * 128 + at));
 }
-template <int C>
 __device__ __forceinline__ int at_n(int unit, int lane)
 {
-    return off_n<C>((lane >> 4) * 8 + ((lane & 15) >> 2), unit) + (lane & 3) * 8;
+    return off_n((lane >> 4) * 8 + ((lane & 15) >> 2), unit) + (lane & 3) * 8;
 }
-template <int C>
 __device__ __forceinline__ bf16x8 frag_n(const char *tile, int ks, int at)
 {
     typedef __attribute__((address_space(3))) s16x4 *lds4_ptr;
     typedef short s16x8 __attribute__((ext_vector_type(8)));
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_ptr)(tile + at + ks * 32 * C * 2));
-    const s16x4 hi =
-        __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_ptr)(tile + at + (ks * 32 + 4) * C * 2));
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_ptr)(tile + at + ks * 32 * 128));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_ptr)(tile + at + (ks * 32 + 4) * 128));
     const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     return __builtin_bit_cast(bf16x8, v);
+}
+// The operands of N neighbouring units at once, while loads into LDS are in
+// flight: the compiler would wait for those before each transposing read of
+// its own (it cannot tell their buffers apart), so the reads and their wait are
+// one block of assembly.  `at` is unit 0's address; unit j's differs in bits 5
+// and 6, the other half of a fragment lies 4 rows (512 bytes) on, slice 1 32
+// rows (4096 bytes).
+template <int KS>
+__device__ __forceinline__ void frags_n(const char *tile, int at, bf16x8 (&b)[4])
+{
+    typedef __attribute__((address_space(3))) const char *lds_char;
+    const uint32_t base = (uint32_t)(uintptr_t)(lds_char)tile;
+    const uint32_t p0 = base + at, p1 = base + (at ^ 32), p2 = base + (at ^ 64), p3 = base + (at ^ 96);
+    typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+    u2 r0, r1, r2, r3, r4, r5, r6, r7;
+    asm volatile("ds_read_b64_tr_b16 %0, %8 offset:%12\n\t"
+                 "ds_read_b64_tr_b16 %1, %8 offset:%13\n\t"
+                 "ds_read_b64_tr_b16 %2, %9 offset:%12\n\t"
+                 "ds_read_b64_tr_b16 %3, %9 offset:%13\n\t"
+                 "ds_read_b64_tr_b16 %4, %10 offset:%12\n\t"
+                 "ds_read_b64_tr_b16 %5, %10 offset:%13\n\t"
+                 "ds_read_b64_tr_b16 %6, %11 offset:%12\n\t"
+                 "ds_read_b64_tr_b16 %7, %11 offset:%13\n\t"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(r0), "=&v"(r1), "=&v"(r2), "=&v"(r3), "=&v"(r4), "=&v"(r5), "=&v"(r6), "=&v"(r7)
+                 : "v"(p0), "v"(p1), "v"(p2), "v"(p3), "n"(KS * 4096), "n"(KS * 4096 + 512)
+                 : "memory");
+    b[0] = __builtin_bit_cast(bf16x8, u32x4{r0[0], r0[1], r1[0], r1[1]});
+    b[1] = __builtin_bit_cast(bf16x8, u32x4{r2[0], r2[1], r3[0], r3[1]});
+    b[2] = __builtin_bit_cast(bf16x8, u32x4{r4[0], r4[1], r5[0], r5[1]});
+    b[3] = __builtin_bit_cast(bf16x8, u32x4{r6[0], r6[1], r7[0], r7[1]});
+}
+template <int KS>
+__device__ __forceinline__ void frags_n(const char *tile, int at, bf16x8 (&b)[2])
+{
+    typedef __attribute__((address_space(3))) const char *lds_char;
+    const uint32_t base = (uint32_t)(uintptr_t)(lds_char)tile;
+    const uint32_t p0 = base + at, p1 = base + (at ^ 32);
+    typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+    u2 r0, r1, r2, r3;
+    asm volatile("ds_read_b64_tr_b16 %0, %4 offset:%6\n\t"
+                 "ds_read_b64_tr_b16 %1, %4 offset:%7\n\t"
+                 "ds_read_b64_tr_b16 %2, %5 offset:%6\n\t"
+                 "ds_read_b64_tr_b16 %3, %5 offset:%7\n\t"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(r0), "=&v"(r1), "=&v"(r2), "=&v"(r3)
+                 : "v"(p0), "v"(p1), "n"(KS * 4096), "n"(KS * 4096 + 512)
+                 : "memory");
+    b[0] = __builtin_bit_cast(bf16x8, u32x4{r0[0], r0[1], r1[0], r1[1]});
+    b[1] = __builtin_bit_cast(bf16x8, u32x4{r2[0], r2[1], r3[0], r3[1]});
 }
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c)
 {
@@ -97,12 +144,16 @@ __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c)
 // them too (NN = false: rows of W, A_e) or lies across (NN = true: W read as
 // its transpose).
 //
-// A stage of 64 inner elements goes from memory straight to LDS, into one of
-// NS buffers, NS - 1 stages ahead of the MFMAs.  The wave's 64 pieces of 16
-// bytes land one after the other, so the swizzle is in the addresses: a lane
-// fetches the piece that belongs into its slot.  One barrier per stage: it
-// says that stage s is there for all waves, and that stage s - 1, whose buffer
-// the next loads take, has been read.
+// A stage goes from memory straight to LDS, into one of NS buffers, up to NS
+// stages ahead of the MFMAs.  The wave's 64 pieces of 16 bytes land one after
+// the other, so the swizzle is in the addresses: a lane fetches the piece that
+// belongs into its slot.  The MFMAs go in TI groups of TJ, one row of
+// fragments each; after a group the row's fragment of the next slice is read
+// into the same registers, and a few of the next stage's loads are started:
+// each keeps its own unit busy, and a wave that handed over all its loads at
+// once would keep the matrix pipe waiting for the memory pipe to take them.
+// One barrier per stage, some groups into its second slice, when every wave
+// holds the rest of the stage in registers: its buffer is free.
 typedef __attribute__((address_space(1))) const void *global_ptr;
 typedef __attribute__((address_space(3))) void *lds_ptr;
 
@@ -140,27 +191,25 @@ struct Product {
     static __device__ __forceinline__ int row_of(int q) { return q >> 3; }
     static __device__ __forceinline__ int k_of(int q) { return ((q & 7) ^ (row_of(q) & 7)) * 8; }
     // ... or inner row and first column (NN = true).
-    static __device__ __forceinline__ int kn_of(int q) { return q / (BN / 8); }
+    static __device__ __forceinline__ int kn_of(int q) { return q / 8 % BK; }
     static __device__ __forceinline__ int n_of(int q)
     {
-        const int k = kn_of(q), slot = q % (BN / 8);
-        const int f = ((k & 3) | ((k >> 1) & 4)) & (BN / 16 - 1);
-        return ((slot >> 1) ^ f) * 16 + (slot & 1) * 8;
+        return q / (BK * 8) * 64 + ((q % 8 >> 1) ^ unit_swizzle(kn_of(q))) * 16 + (q & 1) * 8;
     }
-    // Starts the loads of one stage into `buf`: pa(p), pb(p) are the addresses
-    // of the thread's pieces p*threads + threadIdx.x.
+    // Starts the load of the thread's piece number i of a stage into `buf`
+    // (the tokens' operand first): pa(i), pb(i) are the pieces' addresses.
+    static constexpr int pieces = PA + PB;
     template <typename FA, typename FB>
-    static __device__ __forceinline__ void fetch(char *buf, FA pa, FB pb)
+    static __device__ __forceinline__ void fetch(char *buf, int i, FA pa, FB pb)
     {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-#pragma unroll
-        for (int p = 0; p < PA; ++p)
-            __builtin_amdgcn_global_load_lds((global_ptr)pa(p),
-                                             (lds_ptr)(buf + (p * threads + wave * kWave) * 16), 16, 0, 0);
-#pragma unroll
-        for (int p = 0; p < PB; ++p)
+        if (i < PA)
+            __builtin_amdgcn_global_load_lds((global_ptr)pa(i),
+                                             (lds_ptr)(buf + (i * threads + wave * kWave) * 16), 16, 0, 0);
+        else
             __builtin_amdgcn_global_load_lds(
-                (global_ptr)pb(p), (lds_ptr)(buf + bytes_a + (p * threads + wave * kWave) * 16), 16, 0, 0);
+                (global_ptr)pb(i - PA),
+                (lds_ptr)(buf + bytes_a + ((i - PA) * threads + wave * kWave) * 16), 16, 0, 0);
     }
     // The same through registers, for a stage that ends beyond the inner
     // dimension: va(p), vb(p) give the pieces, zeros where there is nothing.
@@ -174,55 +223,114 @@ struct Product {
         for (int p = 0; p < PB; ++p)
             *reinterpret_cast<u32x4 *>(buf + bytes_a + (p * threads + threadIdx.x) * 16) = vb(p);
     }
-    __device__ __forceinline__ void stage(const char *buf, int wm, int wn, int lane)
-    {
-        const char *b = buf + bytes_a;
-        int an[TJ];
-#pragma unroll
-        for (int j = 0; NN && j < TJ; ++j)
-            an[j] = at_n<BN>(wn * (BN / WN / 16) + j, lane);
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            const int ak = at_k(ks, lane);
-            bf16x8 fa[TI], fb[TJ];
-#pragma unroll
-            for (int j = 0; j < TJ; ++j) {
-                if constexpr (NN)
-                    fb[j] = frag_n<BN>(b, ks, an[j]);
-                else
-                    fb[j] = frag_k(b, wn * (BN / WN) + j * 16, ak);
-            }
-#pragma unroll
-            for (int i = 0; i < TI; ++i)
-                fa[i] = frag_k(buf, wm * (BM / WM) + i * 16, ak);
-#pragma unroll
-            for (int i = 0; i < TI; ++i)
-#pragma unroll
-                for (int j = 0; j < TJ; ++j)
-                    acc[i][j] = mfma(fb[j], fa[i], acc[i][j]);
-        }
-    }
-    // Stages [0, n): issue(s, buf) starts the loads of stage s; called in order.
-    // Ends with every buffer free.
-    template <typename FI>
-    __device__ __forceinline__ void run(char *lds, int n, FI issue)
+    // A lane's offsets of the wave's first fragments in a buffer.  Slice 1 of
+    // consecutive inner elements differs from slice 0 in bit 6.
+    struct Place {
+        int a, b;
+    };
+    static __device__ __forceinline__ Place place()
     {
         const int lane = threadIdx.x & (kWave - 1);
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
         const int wm = wave / WN, wn = wave % WN;
-        for (int s = 0; s < NS - 1 && s < n; ++s)
-            issue(s, lds + s * bytes);
-        int cur = 0, next = NS - 1;
-        for (int s = 0; s < n; ++s) {
-            if (s + NS - 1 <= n)
-                wait_and_meet<(NS - 2) * (PA + PB)>();
-            else
-                wait_and_meet<0>();
-            if (s + NS - 1 < n)
-                issue(s + NS - 1, lds + next * bytes);
-            stage(lds + cur * bytes, wm, wn, lane);
-            cur = cur + 1 == NS ? 0 : cur + 1;
-            next = next + 1 == NS ? 0 : next + 1;
+        return {wm * (BM / WM) * 128 + at_k(0, lane),
+                bytes_a + (NN ? at_n(wn * (BN / WN / 16), lane) : wn * (BN / WN) * 128 + at_k(0, lane))};
+    }
+    template <int KS>
+    static __device__ __forceinline__ void read_b(bf16x8 (&b)[TJ], const char *buf, const Place &w)
+    {
+        if constexpr (NN) {
+            frags_n<KS>(buf, w.b, b);
+        } else {
+#pragma unroll
+            for (int j = 0; j < TJ; ++j)
+                b[j] = frag_k(buf, j * 16, w.b ^ (KS * 64));
+        }
+    }
+    template <int KS>
+    static __device__ __forceinline__ bf16x8 read_a(int i, const char *buf, const Place &w)
+    {
+        return frag_k(buf, i * 16, w.a ^ (KS * 64));
+    }
+    __device__ __forceinline__ void group(int i, const bf16x8 (&a)[TI], const bf16x8 (&b)[TJ])
+    {
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+            acc[i][j] = mfma(b[j], a[i], acc[i][j]);
+    }
+    // Groups [FROM, TI) of a slice; after them, spread out, the reads of the
+    // next slice (KS of `from`; a[0 .. FROM) too) and the loads of a stage into
+    // `to`.
+    template <int FROM, int KS, bool FETCH, typename FF>
+    __device__ __forceinline__ void groups(bf16x8 (&a)[TI], const bf16x8 (&b)[TJ], bf16x8 (&b_next)[TJ],
+                                           const char *from, const Place &w, char *to, FF &fetch_piece)
+    {
+        constexpr int n = TI - FROM, RF = (pieces + n - 1) / n;
+#pragma unroll
+        for (int g = 0; g < n; ++g) {
+            group(FROM + g, a, b);
+            if (g == 0)
+                read_b<KS>(b_next, from, w);
+#pragma unroll
+            for (int i = g == 0 ? 0 : FROM + g; i <= FROM + g; ++i)
+                a[i] = read_a<KS>(i, from, w);
+            if constexpr (FETCH) {
+#pragma unroll
+                for (int f = g * RF; f < (g + 1) * RF && f < pieces; ++f)
+                    fetch_piece(to, f);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    // Stages [0, n): fetch_piece(buf, i) starts the load of piece i of the next
+    // stage, advance() goes on to the one after it.  Ends with every buffer free.
+    template <typename FF, typename FN>
+    __device__ __forceinline__ void run(char *lds, int n, FF fetch_piece, FN advance)
+    {
+        constexpr int LAG = TI > 2 ? 2 : 1;
+        if (n <= 0)
+            return;
+        const Place w = place();
+        for (int s = 0; s < NS && s < n; ++s) {
+#pragma unroll
+            for (int i = 0; i < pieces; ++i)
+                fetch_piece(lds + s * bytes, i);
+            advance();
+        }
+        if (n >= NS)
+            wait_and_meet<(NS - 1) * pieces>();
+        else
+            wait_and_meet<0>();
+        bf16x8 a[TI], b0[TJ], b1[TJ];
+        read_b<0>(b0, lds, w);
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+            a[i] = read_a<0>(i, lds, w);
+        int cur = 0, s = 0;
+        for (; s + NS < n; ++s) {
+            const int nxt = cur + 1 == NS ? 0 : cur + 1;
+            char *buf = lds + cur * bytes;
+            groups<0, 1, false>(a, b0, b1, buf, w, buf, fetch_piece);
+#pragma unroll
+            for (int i = 0; i < LAG; ++i)
+                group(i, a, b1);
+            wait_and_meet<(NS - 2) * pieces>();
+            groups<LAG, 0, true>(a, b1, b0, lds + nxt * bytes, w, buf, fetch_piece);
+            advance();
+            cur = nxt;
+        }
+#pragma unroll 1
+        for (; s < n; ++s) {
+            const int nxt = cur + 1 == NS ? 0 : cur + 1;
+            char *buf = lds + cur * bytes;
+            groups<0, 1, false>(a, b0, b1, buf, w, buf, fetch_piece);
+#pragma unroll
+            for (int i = 0; i < LAG; ++i)
+                group(i, a, b1);
+            wait_and_meet<0>();
+            // behind the last stage: a buffer that is not used any more
+            groups<LAG, 0, false>(a, b1, b0, lds + nxt * bytes, w, buf, fetch_piece);
+            cur = nxt;
         }
         wait_and_meet<0>();
     }
@@ -230,11 +338,24 @@ struct Product {
     template <typename FA, typename FB>
     __device__ __forceinline__ void run_filled(char *lds, FA va, FB vb)
     {
-        const int lane = threadIdx.x & (kWave - 1);
-        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+        const Place w = place();
         fill(lds, va, vb);
         __syncthreads();
-        stage(lds, wave / WN, wave % WN, lane);
+        bf16x8 a[TI], b[TJ];
+        read_b<0>(b, lds, w);
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+            a[i] = read_a<0>(i, lds, w);
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+            group(i, a, b);
+        read_b<1>(b, lds, w);
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+            a[i] = read_a<1>(i, lds, w);
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+            group(i, a, b);
         __syncthreads();
     }
     __device__ __forceinline__ bool finite() const
@@ -383,8 +504,9 @@ adapter_shrink_kernel(Tiles m, const uint16_t *__restrict__ src, const uint16_t 
             pb[i] = NN ? ad + (e * D + s0 * BK + P::kn_of(q)) * m.r + j
                        : ad + (e * m.r + j) * D + (s0 * BK + P::k_of(q));
         }
-        p.run(lds, whole, [&](int, char *buf) {
-            P::fetch(buf, [&](int i) { return pa[i]; }, [&](int i) { return pb[i]; });
+        p.run(lds, whole, [&](char *buf, int i) {
+            P::fetch(buf, i, [&](int i) { return pa[i]; }, [&](int i) { return pb[i]; });
+        }, [&] {
 #pragma unroll
             for (int i = 0; i < P::PA; ++i)
                 pa[i] += BK;
@@ -437,6 +559,7 @@ adapter_shrink_kernel(Tiles m, const uint16_t *__restrict__ src, const uint16_t 
 // up to the next 64 columns.  With `u` given, dw[t,k] = scale <u, sums>.
 // A block takes 32 rows of a tile.
 constexpr int kGatherRows = 32;
+constexpr int kDensePad = BK;          // the project kernel takes whole stages of U
 __global__ void __launch_bounds__(256)
 adapter_gather_kernel(Tiles m, const float *__restrict__ w, float scale, int slots,
                       const float *__restrict__ part, float *__restrict__ sums,
@@ -447,7 +570,7 @@ adapter_gather_kernel(Tiles m, const float *__restrict__ w, float scale, int slo
     const int tile = blockIdx.x / per, row0 = (blockIdx.x % per) * kGatherRows;
     const int tid = threadIdx.x;
     const int c = m.cnt[tile], cols = c * m.rp;
-    const int pieces = ((cols + BK - 1) / BK) * (BK / 8);
+    const int pieces = (cols + kDensePad - 1) / kDensePad * (kDensePad / 8);
     const int splits = shrink_splits(cols, slots);
     const int32_t *list = m.list + (int64_t)tile * m.Lmax;
     const int64_t stride = (int64_t)m.T * m.K * m.r;
@@ -564,7 +687,7 @@ __device__ __forceinline__ f32x4 adapters_apart(const Tiles &m, const int32_t *l
 }
 
 template <typename P, bool NN>
-__global__ void __launch_bounds__(P::threads)
+__global__ void __launch_bounds__(P::threads, 2)     // two waves per SIMD at least
 adapter_project_kernel(Tiles m, const uint16_t *__restrict__ src, int D,
                        const uint16_t *__restrict__ weight, int N, const uint16_t *__restrict__ ad,
                        const uint16_t *__restrict__ dense, int ntile, uint16_t *__restrict__ out)
@@ -588,49 +711,51 @@ adapter_project_kernel(Tiles m, const uint16_t *__restrict__ src, int D,
     bool apart = false;
     if (cols > 0) {
         // columns behind the list's last meet zeros of U
-        p.run(lds, (cols + BK - 1) / BK, [&](int s, char *buf) {
+        int k0 = 0;
+        p.run(lds, (cols + BK - 1) / BK, [&](char *buf, int i) {
             P::fetch(
-                buf,
+                buf, i,
                 [&](int i) {
                     const int q = i * P::threads + tid;
-                    return du + (int64_t)P::row_of(q) * m.LW + s * BK + P::k_of(q);
+                    return du + (int64_t)P::row_of(q) * m.LW + k0 + P::k_of(q);
                 },
                 [&](int i) {
                     const int q = i * P::threads + tid;
-                    const int k = s * BK + (NN ? P::kn_of(q) : P::k_of(q));
+                    const int k = k0 + (NN ? P::kn_of(q) : P::k_of(q));
                     const int l = k < cols ? k / m.rp : 0, j = k < cols && k % m.rp < m.r ? k % m.rp : 0;
                     const int64_t e = list[l];
                     return NN ? ad + (e * m.r + j) * N + least(n0 + P::n_of(q), N - 8)
                               : ad + (e * N + least(n0 + P::row_of(q), N - 1)) * m.r + j;
                 });
-        });
+        }, [&] { k0 += BK; });
         apart = __any(!p.finite());
         if (apart)
             p.zero();
     }
     {
-        // rows and columns behind the last repeat one that exists: not stored
-        const uint16_t *pa[P::PA], *pb[P::PB];
+        // the block's first row of each operand, which moves along, and the
+        // pieces' byte offsets from there, which stay (32 bits: H and O are at
+        // most 2^20); rows and columns behind the last repeat one that exists
+        const char *ba = reinterpret_cast<const char *>(src + (int64_t)t0 * D);
+        const char *bb = reinterpret_cast<const char *>(NN ? weight + n0 : weight + (int64_t)n0 * D);
+        uint32_t oa[P::PA], ob[P::PB];
 #pragma unroll
         for (int i = 0; i < P::PA; ++i) {
             const int q = i * P::threads + tid;
-            pa[i] = src + (int64_t)least(t0 + P::row_of(q), m.T - 1) * D + P::k_of(q);
+            oa[i] = 2u * ((uint32_t)least(P::row_of(q), m.T - 1 - t0) * D + P::k_of(q));
         }
 #pragma unroll
         for (int i = 0; i < P::PB; ++i) {
             const int q = i * P::threads + tid;
             // n_of is a multiple of 8, as is N
-            pb[i] = NN ? weight + (int64_t)P::kn_of(q) * N + least(n0 + P::n_of(q), N - 8)
-                       : weight + (int64_t)least(n0 + P::row_of(q), N - 1) * D + P::k_of(q);
+            ob[i] = NN ? 2u * ((uint32_t)P::kn_of(q) * N + least(P::n_of(q), N - 8 - n0))
+                       : 2u * ((uint32_t)least(P::row_of(q), N - 1 - n0) * D + P::k_of(q));
         }
-        p.run(lds, D / BK, [&](int, char *buf) {
-            P::fetch(buf, [&](int i) { return pa[i]; }, [&](int i) { return pb[i]; });
-#pragma unroll
-            for (int i = 0; i < P::PA; ++i)
-                pa[i] += BK;
-#pragma unroll
-            for (int i = 0; i < P::PB; ++i)
-                pb[i] += NN ? (int64_t)BK * N : BK;
+        p.run(lds, D / BK, [&](char *buf, int i) {
+            P::fetch(buf, i, [&](int i) { return ba + oa[i]; }, [&](int i) { return bb + ob[i]; });
+        }, [&] {
+            ba += BK * 2;
+            bb += NN ? (int64_t)BK * 2 * N : BK * 2;
         });
     }
     if (D % BK) {
@@ -726,8 +851,8 @@ adapter_grads_kernel(Tiles m, const uint16_t *__restrict__ big, int N,
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
                 const int q = p * 256 + tid, k = q / 16, c = q % 16;
-                *reinterpret_cast<u32x4 *>(lb + off_n<kGradCols>(k, c >> 1) + (c & 1) * 16) = rb[p];
-                *reinterpret_cast<u32x4 *>(ld + off_n<kGradCols>(k, c >> 1) + (c & 1) * 16) = rd[p];
+                *reinterpret_cast<u32x4 *>(lb + off_n(k, c >> 1) + (c & 1) * 16) = rb[p];
+                *reinterpret_cast<u32x4 *>(ld + off_n(k, c >> 1) + (c & 1) * 16) = rd[p];
             }
             __syncthreads();
 #pragma unroll
@@ -735,12 +860,12 @@ adapter_grads_kernel(Tiles m, const uint16_t *__restrict__ big, int N,
                 bf16x8 fb[4];
 #pragma unroll
                 for (int b = 0; b < 4; ++b)
-                    fb[b] = frag_n<kGradCols>(lb, ks, at_n<kGradCols>(wb * 4 + b, lane));
+                    fb[b] = frag_n(lb, ks, at_n(wb * 4 + b, lane));
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
                     if (!on[d])
                         continue;
-                    const bf16x8 fd = frag_n<kGradCols>(ld, ks, at_n<kGradCols>(wd * 4 + d, lane));
+                    const bf16x8 fd = frag_n(ld, ks, at_n(wd * 4 + d, lane));
 #pragma unroll
                     for (int b = 0; b < 4; ++b)
                         acc[b][d] = OUTER ? mfma(fd, fb[b], acc[b][d]) : mfma(fb[b], fd, acc[b][d]);
@@ -944,7 +1069,7 @@ AdapterPlan make_adapter_plan(int T, int H, int O, int E, int K, int r)
     p.ntile = (T + p.BM - 1) / p.BM;
     const int64_t rows = T < p.BM ? T : p.BM;
     p.Lmax = (int)(rows * K < E ? (rows * K > 0 ? rows * K : 1) : E);
-    p.LW = (int)(((int64_t)p.Lmax * p.rp + BK - 1) / BK * BK);
+    p.LW = (int)(((int64_t)p.Lmax * p.rp + kDensePad - 1) / kDensePad * kDensePad);
     p.slots = T > 0 ? 1024 / ((T + 127) / 128) : 1;
     if (p.slots > 16)
         p.slots = 16;

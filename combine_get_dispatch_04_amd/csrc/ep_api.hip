@@ -592,7 +592,7 @@ ep_status_t check_adapter_sizes(int T, int H, int O, int E, int K, int r)
     if (T < 0 || K < 1 || E < 1 || H < 8 || H % 8 != 0 || O < 8 || O % 8 != 0 || r < 8 ||
         r % 8 != 0 || (int64_t)T * K > kI32)
         return EP_ERR_INVALID_ARG;
-    if (E > kMaxExperts || H > kMaxHidden || O > kMaxHidden || r > ep::kMaxAdapterRank ||
+    if (E > kMaxExperts || H > ep::kMaxAdapterWidth || O > ep::kMaxAdapterWidth || r > ep::kMaxAdapterRank ||
         K > ep::kMaxAdapterTopk)
         return EP_ERR_UNSUPPORTED;
     // tiles of 128 tokens (larger calls) times blocks of 128 channels, 256 threads each: 32-bit grids

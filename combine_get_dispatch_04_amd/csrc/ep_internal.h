@@ -127,6 +127,7 @@ hipError_t launch_router_backward(const void *logits, bool bf16, int T, int E, i
 
 // Low-rank adapters beside a shared projection (ep_adapter.hip).
 constexpr int kMaxAdapterRank = 128;
+constexpr int kMaxAdapterWidth = 1 << 20;   // H, O: a tile's rows span 32-bit offsets
 constexpr int kMaxAdapterTopk = 64;
 
 struct AdapterPlan {

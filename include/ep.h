@@ -534,7 +534,7 @@ size_t ep_adapter_workspace_bytes(int T, int H, int O, int E, int K, int r, int 
  *   state         >= ep_adapter_state_bytes bytes, 256-byte aligned: read by the
  *                 backward of this call; unused after it, or if there is none.
  *   ws, ws_bytes  >= ep_adapter_workspace_bytes(..., 0); free after the call.
- * Constraints: H % 8 == 0, O % 8 == 0, r % 8 == 0, r <= 128, E <= 4096,
+ * Constraints: H % 8 == 0, O % 8 == 0, H, O <= 2^20, r % 8 == 0, r <= 128, E <= 4096,
  * K <= 64, T*K < 2^31, ceil(T / 128) * ceil(max(H, O) / 128) < 2^23.
  */
 ep_status_t ep_adapter_project(const uint16_t *x, int T, int H, const uint16_t *weight, int O,

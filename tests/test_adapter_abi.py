@@ -28,8 +28,8 @@ def _bwd(**kw):
 
 COMMON = [(dict(T=-1), BAD), (dict(K=0), BAD), (dict(E=0), BAD), (dict(H=60), BAD), (dict(H=0), BAD),
           (dict(O=60), BAD), (dict(r=12), BAD), (dict(r=0), BAD), (dict(T=1 << 30, K=2), BAD),
-          (dict(r=136), UNS), (dict(E=4097), UNS), (dict(K=65), UNS), (dict(H=(1 << 24) + 8), UNS),
-          (dict(O=(1 << 24) + 8), UNS), (dict(T=1 << 29, K=1), UNS), (dict(x=None), BAD), (dict(x=A + 8), BAD),
+          (dict(r=136), UNS), (dict(E=4097), UNS), (dict(K=65), UNS), (dict(H=(1 << 20) + 8), UNS),
+          (dict(O=(1 << 20) + 8), UNS), (dict(T=1 << 29, K=1), UNS), (dict(x=None), BAD), (dict(x=A + 8), BAD),
           (dict(weight=None), BAD), (dict(weight=A + 8), BAD), (dict(a=None), BAD), (dict(a=A + 8), BAD),
           (dict(b=None), BAD), (dict(b=A + 8), BAD), (dict(topk_idx=None), BAD), (dict(topk_idx=A + 2), BAD),
           (dict(topk_weights=A + 2), BAD), (dict(state=None), WSP), (dict(state=WS + 128), BAD),

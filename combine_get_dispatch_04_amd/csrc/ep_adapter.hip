@@ -942,6 +942,178 @@ adapter_grads_sum_kernel(const float *__restrict__ part, int splits, int64_t tot
     }
 }
 
+// ---------------------------------------------------------------- a few tokens
+// Up to kSmallTokens tokens (a decode batch) are bound by the weights' bytes:
+// every block then reads a piece of W, or of an entry's A, and nothing waits
+// for a list.  One launch computes both,
+//   part_w[split][t][o] = the split's share of W x_t       (MFMA, all tokens in one tile)
+//   part_u[split][t, k][j] = the split's share of A_e x_t   (one entry per block)
+// and a second adds the splits and B_e u, in fp32 throughout.
+template <typename P>
+__global__ void __launch_bounds__(256, 2)
+adapter_small_kernel(const uint16_t *__restrict__ x, int T, int H,
+                     const uint16_t *__restrict__ weight, int O, const uint16_t *__restrict__ a,
+                     int E, int r, const int32_t *__restrict__ idx, int nb, int splits, int usplits,
+                     float *__restrict__ part_w, float *__restrict__ part_u, int entries)
+{
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    static_assert(P::threads == 256, "one block shape for both parts");
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    if ((int)blockIdx.x >= nb * splits) {
+        const int id = blockIdx.x - nb * splits;
+        const int entry = id % entries, split = id / entries;
+        const int K = entries / T, e = idx[entry];
+        if ((unsigned)e >= (unsigned)E)
+            return;
+        // runs of 512 channels, a lane 8 of each
+        const int runs = (H + 511) / 512;
+        const int h0 = (int)((int64_t)runs * split / usplits) * 512;
+        const int h1 = least((int)((int64_t)runs * (split + 1) / usplits) * 512, H);
+        const uint16_t *xr = x + (int64_t)(entry / K) * H;
+        for (int j = wave * 2; j < r; j += 8) {
+            const uint16_t *a0 = a + ((int64_t)e * r + j) * H, *a1 = a0 + H;
+            float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll 4
+            for (int h = h0 + lane * 8; h < h1; h += 512) {
+                const u32x4 vx = ld16(xr + h), v0 = ld16(a0 + h), v1 = ld16(a1 + h);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    s0 = fmaf(bf16_lo(vx[q]), bf16_lo(v0[q]), s0);
+                    s0 = fmaf(bf16_hi(vx[q]), bf16_hi(v0[q]), s0);
+                    s1 = fmaf(bf16_lo(vx[q]), bf16_lo(v1[q]), s1);
+                    s1 = fmaf(bf16_hi(vx[q]), bf16_hi(v1[q]), s1);
+                }
+            }
+            s0 = wave_sum_f(s0);
+            s1 = wave_sum_f(s1);
+            if (lane < 2)
+                part_u[((int64_t)split * entries + entry) * r + j + lane] = lane ? s1 : s0;
+        }
+        return;
+    }
+    const int n0 = blockIdx.x % nb * P::BN, split = blockIdx.x / nb;
+    const int stages = (H + BK - 1) / BK;
+    const int s0 = (int)((int64_t)stages * split / splits);
+    const int s1 = (int)((int64_t)stages * (split + 1) / splits);
+    const int whole = least(s1, H / BK) - s0;
+    P p;
+    p.zero();
+    const char *ba = reinterpret_cast<const char *>(x + s0 * BK);
+    const char *bb = reinterpret_cast<const char *>(weight + (int64_t)n0 * H + s0 * BK);
+    uint32_t oa[P::PA], ob[P::PB];
+#pragma unroll
+    for (int i = 0; i < P::PA; ++i) {
+        const int q = i * P::threads + tid;
+        oa[i] = 2u * ((uint32_t)least(P::row_of(q), T - 1) * H + P::k_of(q));
+    }
+#pragma unroll
+    for (int i = 0; i < P::PB; ++i) {
+        const int q = i * P::threads + tid;
+        ob[i] = 2u * ((uint32_t)least(P::row_of(q), O - 1 - n0) * H + P::k_of(q));
+    }
+    p.run(lds, whole, [&](char *buf, int i) {
+        P::fetch(buf, i, [&](int i) { return ba + oa[i]; }, [&](int i) { return bb + ob[i]; });
+    }, [&] {
+        ba += BK * 2;
+        bb += BK * 2;
+    });
+    if (whole < s1 - s0) {
+        const int k0 = (s0 + whole) * BK, left = H - k0;
+        p.run_filled(
+            lds,
+            [&](int i) {
+                const int q = i * P::threads + tid, k = P::k_of(q);
+                return k < left ? ld16(x + (int64_t)least(P::row_of(q), T - 1) * H + k0 + k) : zero4();
+            },
+            [&](int i) {
+                const int q = i * P::threads + tid, k = P::k_of(q);
+                return k < left ? ld16(weight + (int64_t)least(n0 + P::row_of(q), O - 1) * H + k0 + k)
+                                : zero4();
+            });
+    }
+    const int wm = wave / P::WN, wn = wave % P::WN;
+#pragma unroll
+    for (int i = 0; i < P::TI; ++i) {
+        const int t = wm * (P::BM / P::WM) + i * 16 + (lane & 15);
+#pragma unroll
+        for (int j = 0; j < P::TJ; ++j) {
+            const int n = n0 + wn * (P::BN / P::WN) + j * 16 + (lane >> 4) * 4;
+            if (t < T && n < O)
+                *reinterpret_cast<f32x4 *>(part_w + ((int64_t)split * T + t) * O + n) = p.acc[i][j];
+        }
+    }
+}
+
+// out[t][o .. o+3] per thread; the token's u, times its coefficients, in
+// shared memory.  W's splits are asked for first, to be there with u.
+constexpr int kSmallSumThreads = 128;
+__global__ void __launch_bounds__(kSmallSumThreads)
+adapter_small_sum_kernel(const float *__restrict__ part_w, int splits, const float *__restrict__ part_u,
+                         int usplits, int T, int O, const uint16_t *__restrict__ b, int E, int r,
+                         const int32_t *__restrict__ idx, const float *__restrict__ w, int K,
+                         float scale, uint16_t *__restrict__ out, int32_t *__restrict__ num_invalid)
+{
+    extern __shared__ float u[];        // [K, r]
+    const int tid = threadIdx.x, t = blockIdx.y;
+    const int32_t *row = idx + (int64_t)t * K;
+    const int o = (blockIdx.x * kSmallSumThreads + tid) * 4;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (o < O) {
+        const float *p = part_w + (int64_t)t * O + o;
+#pragma unroll 8
+        for (int q = 0; q < splits; ++q)
+            v += *reinterpret_cast<const f32x4 *>(p + (int64_t)q * T * O);
+    }
+    for (int i = tid; i < K * r; i += kSmallSumThreads) {
+        const int k = i / r;
+        float s = 0.0f;
+        if ((unsigned)row[k] < (unsigned)E) {
+            const float c = scale * (w ? w[(int64_t)t * K + k] : 1.0f);
+            const float *p = part_u + (int64_t)t * K * r + i;
+#pragma unroll 8
+            for (int q = 0; q < usplits; ++q)
+                s += p[(int64_t)q * T * K * r];
+            s *= c;
+        }
+        u[i] = s;
+    }
+    __syncthreads();
+    if (o < O) {
+        for (int k = 0; k < K; ++k) {
+            const int e = row[k];
+            if ((unsigned)e >= (unsigned)E)
+                continue;
+            const uint16_t *be = b + ((int64_t)e * O + o) * r;
+#pragma unroll 2
+            for (int j = 0; j < r; j += 8) {
+                const float *uj = u + k * r + j;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const u32x4 bv = ld16(be + c * r + j);
+                    float s = 0.0f;
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        s = fmaf(bf16_lo(bv[d]), uj[2 * d], s);
+                        s = fmaf(bf16_hi(bv[d]), uj[2 * d + 1], s);
+                    }
+                    v[c] += s;
+                }
+            }
+        }
+        *reinterpret_cast<u32x2 *>(out + (int64_t)t * O + o) =
+            u32x2{pack_bf16_any(v[0], v[1]), pack_bf16_any(v[2], v[3])};
+    }
+    if (blockIdx.x == 0 && t == 0 && tid < kWave) {
+        int n = 0;
+        for (int i = tid; i < T * K; i += kWave)
+            n += (unsigned)idx[i] >= (unsigned)E && idx[i] != -1;
+        n = wave_sum(n);
+        if (tid == 0)
+            num_invalid[0] = n;
+    }
+}
+
 Tiles make_tiles(const AdapterPlan &p, const int32_t *idx, char *state)
 {
     Tiles m{};
@@ -998,12 +1170,25 @@ hipError_t project(const AdapterPlan &p, const Tiles &m, const uint16_t *src, in
     return hipGetLastError();
 }
 
-// shrink + gather + project of one direction.
+template <int BM, int WM, int WN>
+hipError_t small(const AdapterPlan &p, const uint16_t *x, const uint16_t *weight, const uint16_t *a,
+                 const int32_t *idx, float *part_w, float *part_u, hipStream_t s)
+{
+    typedef Product<BM, 64, WM, WN, 3, false> P;
+    const hipError_t e = allow_lds(adapter_small_kernel<P>, P::lds_bytes);
+    if (e != hipSuccess)
+        return e;
+    const int nb = (p.O + 63) / 64;
+    adapter_small_kernel<P><<<nb * p.wsplits + p.T * p.K * p.usplits, 256, P::lds_bytes, s>>>(
+        x, p.T, p.H, weight, p.O, a, p.E, p.r, idx, nb, p.wsplits, p.usplits, part_w, part_u, p.T * p.K);
+    return hipGetLastError();
+}
+
+// shrink + gather of one direction, and its project.
 template <bool NN>
-hipError_t pass(const AdapterPlan &p, const Tiles &m, const uint16_t *src, int D,
-                const uint16_t *weight, int N, const uint16_t *shrinker, const uint16_t *expander,
-                const float *w, float scale, float *part, float *sums, uint16_t *dense,
-                const float *u, float *dw, int32_t *num_invalid, uint16_t *out, hipStream_t s)
+hipError_t gather(const AdapterPlan &p, const Tiles &m, const uint16_t *src, int D,
+                  const uint16_t *shrinker, const float *w, float scale, float *part, float *sums,
+                  uint16_t *dense, const float *u, float *dw, int32_t *num_invalid, hipStream_t s)
 {
     hipError_t e = p.BM == 64 ? shrink<64, NN>(p, m, src, shrinker, D, part, s)
                               : shrink<128, NN>(p, m, src, shrinker, D, part, s);
@@ -1011,15 +1196,21 @@ hipError_t pass(const AdapterPlan &p, const Tiles &m, const uint16_t *src, int D
         return e;
     adapter_gather_kernel<<<p.ntile * (p.BM / kGatherRows), 256, 0, s>>>(
         m, w, scale, p.slots, part, sums, dense, u, dw, p.ntile, num_invalid);
-    if ((e = hipGetLastError()) != hipSuccess || !out)
-        return e;
+    return hipGetLastError();
+}
+
+template <bool NN>
+hipError_t project_any(const AdapterPlan &p, const Tiles &m, const uint16_t *src, int D,
+                       const uint16_t *weight, int N, const uint16_t *ad, const uint16_t *dense,
+                       uint16_t *out, hipStream_t s)
+{
     switch (p.BM) {
     case 64:
-        return project<64, 64, 2, 2, 4, NN>(p, m, src, D, weight, N, expander, dense, out, s);
+        return project<64, 64, 2, 2, 4, NN>(p, m, src, D, weight, N, ad, dense, out, s);
     case 128:
-        return project<128, 128, 2, 2, 2, NN>(p, m, src, D, weight, N, expander, dense, out, s);
+        return project<128, 128, 2, 2, 2, NN>(p, m, src, D, weight, N, ad, dense, out, s);
     }
-    return project<256, 256, 2, 4, 2, NN>(p, m, src, D, weight, N, expander, dense, out, s);
+    return project<256, 256, 2, 4, 2, NN>(p, m, src, D, weight, N, ad, dense, out, s);
 }
 
 template <bool OUTER>
@@ -1087,10 +1278,22 @@ AdapterPlan make_adapter_plan(int T, int H, int O, int E, int K, int r)
     off = align256(off + entries);
     p.off_dense = off;
     off = align256(off + (size_t)p.ntile * p.BM * p.LW * 2);
-    p.state_bytes = off > 256 ? off : 256;
-    // forward: the splits' sums
+    const size_t state = off > 256 ? off : 256;
+    p.small = T > 0 && T <= kSmallTokens;
     p.off_part = 0;
-    p.ws_bytes = align256((size_t)p.slots * entries) + 256;
+    if (p.small) {
+        // about two blocks per CU for W, of 4 stages at least, and as many for A x
+        const int nb = (O + 63) / 64, stages = (H + BK - 1) / BK, runs = (H + 511) / 512;
+        auto within = [](int v, int hi) { return v < 1 ? 1 : (v > hi ? hi : v); };
+        p.wsplits = within(512 / nb, stages > 4 ? stages / 4 : 1);
+        p.usplits = within(1024 / (T * K), runs);
+        p.off_partw = align256((size_t)p.usplits * entries);
+        p.ws_bytes = p.off_partw + align256((size_t)p.wsplits * T * O * 4);
+        p.state_bytes = 256;        // the backward makes its own
+    } else {
+        p.ws_bytes = align256((size_t)p.slots * entries) + 256;
+        p.state_bytes = state;
+    }
     // backward: the splits' sums or those of the gradients, v and V
     size_t part = (size_t)p.slots * entries;
     for (const int n : {H, O}) {
@@ -1103,7 +1306,8 @@ AdapterPlan make_adapter_plan(int T, int H, int O, int E, int K, int r)
     off = align256(off + entries);
     p.off_vdense = off;
     off = align256(off + (size_t)p.ntile * p.BM * p.LW * 2);
-    p.back_bytes = off + 256;
+    p.off_state = off;
+    p.back_bytes = off + (p.small ? state : 256);
     return p;
 }
 
@@ -1116,16 +1320,30 @@ hipError_t launch_adapter(const AdapterPlan &p, const uint16_t *x, const uint16_
         adapter_zero_kernel<<<1, 1, 0, s>>>(num_invalid);
         return hipGetLastError();
     }
+    float *part = reinterpret_cast<float *>(ws + p.off_part);
+    if (p.small) {
+        float *part_w = reinterpret_cast<float *>(ws + p.off_partw);
+        const hipError_t e = p.T <= 32   ? small<32, 1, 4>(p, x, weight, a, idx, part_w, part, s)
+                             : p.T <= 64 ? small<64, 2, 2>(p, x, weight, a, idx, part_w, part, s)
+                                         : small<128, 4, 1>(p, x, weight, a, idx, part_w, part, s);
+        if (e != hipSuccess)
+            return e;
+        adapter_small_sum_kernel<<<dim3((p.O / 4 + kSmallSumThreads - 1) / kSmallSumThreads, p.T),
+                                   kSmallSumThreads, (size_t)p.K * p.r * 4, s>>>(part_w, p.wsplits, part, p.usplits, p.T, p.O,
+                                                               b, p.E, p.r, idx, w, p.K, scale, out,
+                                                               num_invalid);
+        return hipGetLastError();
+    }
     const Tiles m = make_tiles(p, idx, state);
     adapter_tiles_kernel<<<p.ntile, 256, (size_t)p.E * 4, s>>>(m);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess)
-        return e;
-    return pass<false>(p, m, x, p.H, weight, p.O, a, b, w, scale,
-                       reinterpret_cast<float *>(ws + p.off_part),
-                       reinterpret_cast<float *>(state + p.off_u),
-                       reinterpret_cast<uint16_t *>(state + p.off_dense), nullptr, nullptr,
-                       num_invalid, out, s);
+    uint16_t *dense = reinterpret_cast<uint16_t *>(state + p.off_dense);
+    if (e == hipSuccess)
+        e = gather<false>(p, m, x, p.H, a, w, scale, part, reinterpret_cast<float *>(state + p.off_u), dense,
+                          nullptr, nullptr, num_invalid, s);
+    if (e == hipSuccess)
+        e = project_any<false>(p, m, x, p.H, weight, p.O, b, dense, out, s);
+    return e;
 }
 
 hipError_t launch_adapter_backward(const AdapterPlan &p, const uint16_t *d_out, const uint16_t *x,
@@ -1134,19 +1352,28 @@ hipError_t launch_adapter_backward(const AdapterPlan &p, const uint16_t *d_out, 
                                    uint16_t *dx, uint16_t *da, uint16_t *db, float *dw, char *ws,
                                    hipStream_t s)
 {
+    if (p.small)
+        state = ws + p.off_state;
     const Tiles m = make_tiles(p, idx, state);
     float *part = reinterpret_cast<float *>(ws + p.off_part);
+    float *u = reinterpret_cast<float *>(state + p.off_u);
+    uint16_t *dense = reinterpret_cast<uint16_t *>(state + p.off_dense);
     uint16_t *vdense = reinterpret_cast<uint16_t *>(ws + p.off_vdense);
     hipError_t e = hipSuccess;
-    if (p.T > 0)
-        e = pass<true>(p, m, d_out, p.O, weight, p.H, b, a, w, scale, part,
-                       reinterpret_cast<float *>(ws + p.off_v), vdense,
-                       reinterpret_cast<const float *>(state + p.off_u), dw, nullptr, dx, s);
+    if (p.small) {
+        adapter_tiles_kernel<<<p.ntile, 256, (size_t)p.E * 4, s>>>(m);
+        if ((e = hipGetLastError()) == hipSuccess)
+            e = gather<false>(p, m, x, p.H, a, w, scale, part, u, dense, nullptr, nullptr, nullptr, s);
+    }
+    if (e == hipSuccess && p.T > 0)
+        e = gather<true>(p, m, d_out, p.O, b, w, scale, part, reinterpret_cast<float *>(ws + p.off_v),
+                         vdense, u, dw, nullptr, s);
+    if (e == hipSuccess && p.T > 0 && dx)
+        e = project_any<true>(p, m, d_out, p.O, weight, p.H, a, vdense, dx, s);
     if (e == hipSuccess && da)
         e = grads<false>(p, m, x, p.H, vdense, da, part, s);
     if (e == hipSuccess && db)
-        e = grads<true>(p, m, d_out, p.O, reinterpret_cast<const uint16_t *>(state + p.off_dense), db,
-                        part, s);
+        e = grads<true>(p, m, d_out, p.O, dense, db, part, s);
     return e;
 }
 

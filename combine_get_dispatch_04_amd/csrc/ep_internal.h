@@ -129,6 +129,7 @@ hipError_t launch_router_backward(const void *logits, bool bf16, int T, int E, i
 constexpr int kMaxAdapterRank = 128;
 constexpr int kMaxAdapterWidth = 1 << 20;   // H, O: a tile's rows span 32-bit offsets
 constexpr int kMaxAdapterTopk = 64;
+constexpr int kSmallTokens = 128;
 
 struct AdapterPlan {
     int T, H, O, E, K, r;
@@ -136,10 +137,12 @@ struct AdapterPlan {
     int BM, ntile;    // tokens per tile, tiles
     int Lmax, LW;     // adapters a tile can name, columns of its dense matrix
     int slots;        // blocks that share a tile's shrink
+    bool small;       // a few tokens: two launches, no tiles
+    int wsplits, usplits;   // splits of the inner dimension then, for W x and A x
     // the state kept from the forward for the backward
     size_t off_cnt, off_list, off_place, off_u, off_dense, state_bytes;
     // the workspaces of the forward (ws_bytes) and the backward (back_bytes)
-    size_t off_part, ws_bytes, off_v, off_vdense, back_bytes;
+    size_t off_part, off_partw, ws_bytes, off_v, off_vdense, off_state, back_bytes;
 };
 AdapterPlan make_adapter_plan(int T, int H, int O, int E, int K, int r);
 int adapter_grad_splits(const AdapterPlan &p, int N);

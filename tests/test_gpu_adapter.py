@@ -113,6 +113,36 @@ def test_no_tokens():
     assert dx.shape == (0, 64) and dw.shape == (0, 2) and not da.any() and not db.any()
 
 
+@pytest.mark.parametrize("T,H,O,E,K,r", [(12300, 264, 280, 30, 1, 16), (6100, 2056, 2064, 12, 1, 24),
+                                         (6200, 2048, 2048, 6, 2, 16)])
+def test_larger_tiles(T, H, O, E, K, r):
+    """Calls that take tiles of 128 and of 256 tokens."""
+    say("adapter", T, H, O, E, K, r)
+    c = Case(T + H + O, T, H, O, E, K, r, "requests" if K == 1 else "mixed", K > 1)
+    out, h = api.adapter_project(*c.gpu(), scale=c.scale)
+    want, bound, saved = c.ref()
+    close("out", out, want, bound)
+    grads = dict(zip(("dx", "da", "db", "dw"), api.adapter_project_backward(c.dy.to(DEV), h)))
+    for name, (g, b) in c.ref_back(saved).items():
+        close(name, grads[name], g, b)
+
+
+def test_larger_tiles_keep_a_broken_adapter_apart():
+    T, H, O, E, K, r = 6100, 2048, 2048, 6, 2, 16
+    clean, c = (Case(4, T, H, O, E, K, r) for _ in range(2))
+    c.b[2, 7, 2] = c.a[2, 1, 5] = float("inf")
+    out, h = api.adapter_project(*c.gpu(), scale=c.scale)
+    dx, da, db, dw = api.adapter_project_backward(c.dy.to(DEV), h)
+    want, bound, saved = clean.ref()
+    back = clean.ref_back(saved)
+    rows = torch.from_numpy(~(c.idx == 2).any(axis=1))
+    rest = torch.tensor([0, 1, 3, 4, 5])
+    for name, got, g, b, at in (("out", out, want, bound, rows), ("dx", dx, *back["dx"], rows),
+                                ("dw", dw, *back["dw"], rows), ("da", da, *back["da"], rest),
+                                ("db", db, *back["db"], rest)):
+        close(name, got[at.to(DEV)], g[at.numpy()], b[at.numpy()])
+
+
 @pytest.mark.parametrize("where", ["a", "b", "x", "dy", "w"])
 @pytest.mark.parametrize("what", [float("nan"), float("inf")])
 @pytest.mark.parametrize("T,K", [(8, 1), (150, 1), (150, 3)])

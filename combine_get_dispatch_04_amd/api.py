@@ -12,6 +12,7 @@ EpError (a ValueError).
 """
 from __future__ import annotations
 
+import contextlib
 from dataclasses import dataclass
 from typing import List, Optional
 
@@ -20,8 +21,23 @@ import torch
 from . import _native as N
 
 
+# The current stream's handle without a Stream object around it, where torch
+# offers it: 0.1 us instead of 1.9 us a call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(dev: torch.device) -> int:
+    if _raw_stream is not None and dev.index is not None:
+        return _raw_stream(dev.index)
     return torch.cuda.current_stream(dev).cuda_stream
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(dev: torch.device):
+    """Makes dev the current device, if it is another one."""
+    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -576,7 +592,7 @@ def route(logits: torch.Tensor, num_topk: int, *, score: str = "softmax",
     idx = torch.empty((T, K), dtype=torch.int32, device=dev)
     w = torch.empty((T, K), dtype=torch.float32, device=dev)
     ninv = torch.empty(T, dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         N.ep_route(_ptr(logits), dt, T, E, K, _SCORES[score], _ptr(bias), int(renormalise),
                    float(scale), _ptr(idx), _ptr(w), _ptr(ninv), _stream(dev))
     return Routing(idx, w, ninv, logits, score, bool(renormalise), float(scale))
@@ -612,7 +628,7 @@ def balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, *, score: str = "
     slope = torch.empty(S * E + 1, dtype=torch.float32, device=dev)
     loss = torch.empty(1, dtype=torch.float32, device=dev)
     ninv = torch.empty(2, dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         N.ep_balance_loss(_ptr(logits), dt, T, E, _ptr(topk_idx), K, _SCORES[score],
                           _ptr(seq_offsets), S, float(coef), _ptr(counts), _ptr(slope),
                           _ptr(loss), _ptr(ninv), _ptr(ws), ws_bytes, _stream(dev))
@@ -640,7 +656,7 @@ def _router_backward(logits, score, d_w, routing, d_loss, balance):
         S = 1 if seq is None else seq.shape[0] - 1
     _same_device(dev, d_weights=d_w, topk_idx=idx, d_loss=d_loss, slope=slope, seq_offsets=seq)
     d_logits = torch.empty_like(logits)
-    with torch.cuda.device(dev):
+    with _on(dev):
         N.ep_router_backward(_ptr(logits), _LOGIT_DTYPES[logits.dtype], T, E, K, _SCORES[score],
                              int(renorm), scale, _ptr(idx), _ptr(d_w), _ptr(slope), _ptr(seq), S,
                              _ptr(d_loss), _ptr(d_logits), _stream(dev))
@@ -723,7 +739,7 @@ def adapter_project(x: torch.Tensor, weight: torch.Tensor, a: torch.Tensor, b: t
     ninv = torch.empty(1, dtype=torch.int32, device=dev)
     state = torch.empty(state_bytes, dtype=torch.uint8, device=dev)
     ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         N.ep_adapter_project(_ptr(x), T, H, _ptr(weight), O, _ptr(a), _ptr(b), E, r,
                              _ptr(topk_idx), _ptr(topk_weights), K, float(scale), _ptr(out),
                              _ptr(ninv), _ptr(state), state_bytes, _ptr(ws), ws_bytes,
@@ -749,7 +765,7 @@ def adapter_project_backward(d_out: torch.Tensor, handle: AdapterHandle):
     ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
     dx, da, db = torch.empty_like(x), torch.empty_like(a), torch.empty_like(b)
     dw = torch.empty((T, K), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         N.ep_adapter_project_backward(_ptr(d_out), _ptr(x), T, H, _ptr(weight), O, _ptr(a),
                                       _ptr(b), E, r, _ptr(idx), _ptr(handle.topk_weights), K,
                                       handle.scale, _ptr(handle.state), handle.state.numel(),

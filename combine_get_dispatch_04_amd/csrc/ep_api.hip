@@ -494,8 +494,8 @@ ep_status_t check_sequences(int E, const int32_t *seq_offsets, int S)
 {
     if (S < 1 || (!seq_offsets && S != 1) || (int64_t)S * E > kI32)
         return EP_ERR_INVALID_ARG;
-    // one block of 1024 threads per 64 experts of a sequence: 32-bit grid
-    if ((int64_t)S * ((E + 63) / 64) >= 1 << 22)
+    // one block of 512 threads per 16 experts of a sequence: 32-bit grid
+    if ((int64_t)S * ((E + 15) / 16) >= 1 << 22)
         return EP_ERR_UNSUPPORTED;
     return EP_OK;
 }

@@ -108,7 +108,7 @@ constexpr int kMaxRouteTopk = 64;     // one lane per choice
 struct BalancePlan {
     int T, E, S;
     int CT, nchunk;   // tokens per chunk, chunks
-    int eb;           // blocks of 64 experts
+    int eb;           // blocks of 16 experts
     size_t off_arrived, off_part, off_parts, off_tails, bytes;
 };
 BalancePlan make_balance_plan(int T, int E, int S);

@@ -75,32 +75,50 @@ __device__ __forceinline__ float row_score(float z, float top, bool sigmoid)
 
 // ---------------------------------------------------------------- the choice
 // The order of two keys sigmoid(z) + bias that lie this close (relative to
-// max(1, |key|)) is not settled in fp32: expf is off by at most 2^-23 of its
-// value, the sum and the quotient by 2^-24 each, so a score by less than
-// 2^-22, and the addition of the bias by 2^-24 of the key; two keys by twice
-// that, below 2^-20.
+// max(1, |key|)) is not settled in fp32.  With u = 2^-24: v_exp_f32 of
+// -z log2(e) and v_rcp_f32 are off by 2u of their values, the product by u of
+// its own; as |z| sigmoid'(z) <= 0.3 that makes a score off by less than 4u,
+// and the addition of the bias by u of the key.  Two keys: below 10u < 2^-20.
 constexpr float kKeyGap = 0x1p-20f;
+constexpr float kLog2e = 1.44269504f;
 
-// The choice by sigmoid(z) + bias in fp64, for the rows that fp32 does not
-// settle: K rounds over the row in memory, each taking the first entry after
-// the last one in the order (key descending, index ascending).  Slow, and
-// rare: 0.2 % of rows at E = 256, K = 8.
+__device__ __forceinline__ float key_sigmoid(float z)
+{
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * z));
+}
+__device__ __forceinline__ bool finite_f(float v) { return fabsf(v) < __builtin_huge_valf(); }
+__device__ __forceinline__ double lane_value_d(double v, int lane)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), lane);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double exact_key(float z, float bias)
+{
+    return 1.0 / (1.0 + exp(-(double)z)) + (double)bias;
+}
+
+// The choice by sigmoid(z) + bias in fp64 over the row in memory: K rounds,
+// each taking the first entry after the last one in the order (key descending,
+// index ascending).  Only for rows with more than 64 candidates.
 template <typename L>
 __device__ void choose_fp64(const typename L::type *row, const float *bias, int E, int K, int lane,
-                            int &my_e, float &my_z)
+                            int &my_e, float &my_z, int &rank)
 {
     double last_d = __builtin_huge_val();
     int last_e = -1;
     my_e = -1;
     my_z = kNegInf;
+    rank = lane;
     for (int k = 0; k < K; ++k) {
         double best = -__builtin_huge_val();
         int be = 0x7FFFFFFF;
         for (int e = lane; e < E; e += kWave) {
             const float z = clean_logit(L::get(row + e));
-            if (!(z > kNegInf) || !(fabsf(sigmoid_f(z) + bias[e]) < __builtin_huge_valf()))
+            if (!(z > kNegInf) || !finite_f(key_sigmoid(z) + bias[e]))
                 continue;
-            const double d = 1.0 / (1.0 + exp(-(double)z)) + (double)bias[e];
+            const double d = exact_key(z, bias[e]);
             if (!(d < last_d || (d == last_d && e > last_e)))
                 continue;
             if (be == 0x7FFFFFFF || d > best) {
@@ -127,10 +145,27 @@ __device__ void choose_fp64(const typename L::type *row, const float *bias, int 
     }
 }
 
-// One wave per token.  K rounds: each lane's best remaining key, the maximum
-// over the lanes, and the lowest index among the lanes that hold it; lane k
-// keeps the k-th choice.  Without a bias the keys are the logits themselves
-// (both scores are monotone in them), so the order is exact.
+// How many of the wave's keys are at least `t`.
+template <int VPL>
+__device__ __forceinline__ int count_from(const uint32_t (&key)[VPL], uint32_t t)
+{
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j)
+        n += __popcll(ballot(key[j] >= t));
+    return n;
+}
+
+// One wave per token.  The keys are order-preserving bits of the logits (both
+// scores are monotone in them, so without a bias the order is exact), or of
+// sigmoid(z) + bias.  A border between the K chosen and the rest is bisected
+// with ballots: halfway between two keys as numbers, which is quick for logits
+// as they are, and every fourth time as bits, which bounds it by 128 rounds;
+// the chosen go to one lane each through shared memory, in index order, and
+// each counts those before it.  A border inside equal keys gives the places
+// left to the lowest indices.  This costs about 8 ballots per 64 experts, where K
+// rounds of a maximum over the wave cost K reductions: 43.5 us at 16384 x 384,
+// K = 16, with those.
 template <typename L, int VPL>
 __global__ void __launch_bounds__(256)
 route_kernel(const typename L::type *__restrict__ logits, int T, int E, int K, int sigmoid,
@@ -138,9 +173,11 @@ route_kernel(const typename L::type *__restrict__ logits, int T, int E, int K, i
              int32_t *__restrict__ topk_idx, float *__restrict__ topk_w,
              int32_t *__restrict__ num_invalid)
 {
-    const int lane = threadIdx.x & (kWave - 1);
+    __shared__ int chosen_e[4][kWave];
+    __shared__ float chosen_z[4][kWave];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int nw = gridDim.x * (blockDim.x / kWave);
-    for (int64_t t = blockIdx.x * (blockDim.x / kWave) + threadIdx.x / kWave; t < T; t += nw) {
+    for (int64_t t = blockIdx.x * (blockDim.x / kWave) + wave; t < T; t += nw) {
         const typename L::type *row = logits + t * E;
         float z[VPL];
         uint32_t key[VPL];
@@ -148,95 +185,156 @@ route_kernel(const typename L::type *__restrict__ logits, int T, int E, int K, i
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
             const int e = j * kWave + lane;
-            const float v = e < E ? L::get(row + e) : kNegInf;
-            bad += bad_logit(v);
-            z[j] = clean_logit(v);
+            z[j] = e < E ? L::get(row + e) : kNegInf;
         }
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            bad += __popcll(ballot(bad_logit(z[j])));
+            z[j] = clean_logit(z[j]);
+        }
+        if (num_invalid && lane == 0)
+            num_invalid[t] = bad;
+        uint32_t best = 0u;
         if (bias) {
 #pragma unroll
             for (int j = 0; j < VPL; ++j) {
                 const int e = j * kWave + lane;
-                const float v = z[j] > kNegInf ? sigmoid_f(z[j]) + bias[e] + 0.0f : kNegInf;
-                key[j] = fabsf(v) < __builtin_huge_valf() ? order_bits(v) : 0u;
+                const float v = z[j] > kNegInf ? key_sigmoid(z[j]) + bias[e] + 0.0f : kNegInf;
+                key[j] = finite_f(v) ? order_bits(v) : 0u;
+                best = umax(best, key[j]);
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < VPL; ++j)
+            for (int j = 0; j < VPL; ++j) {
                 key[j] = z[j] > kNegInf ? order_bits(z[j]) : 0u;
-        }
-        if (num_invalid) {
-            const int n = wave_sum(bad);
-            if (lane == 0)
-                num_invalid[t] = n;
+                best = umax(best, key[j]);
+            }
         }
 
-        float top = kNegInf, total = 0.0f;
-        if (!sigmoid && !renorm) {
-#pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                top = fmaxf(top, z[j]);
-            top = wave_max_f(top);
-#pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                total += row_score(z[j], top, false);
-            total = wave_sum_f(total);
+        // the border: `from` keys are >= lo, no more than `want` are >= hi
+        const uint32_t top_key = wave_max_u(best);
+        const int able = count_from(key, 1u);           // not masked
+        const int want = able < K ? able : K;
+        uint32_t lo = 1u, hi = top_key + 1u;
+        int from = able;
+        for (int round = 0; from > want && hi - lo > 1u; ++round) {
+            uint32_t mid = lo + (hi - lo) / 2u;
+            if ((round & 3) != 3) {
+                const uint32_t m = order_bits(0.5f * from_order_bits(lo) + 0.5f * from_order_bits(hi - 1u));
+                mid = m > lo && m < hi ? m : mid;
+            }
+            const int n = count_from(key, mid);
+            if (n >= want) {
+                lo = mid;
+                from = n;
+            } else {
+                hi = mid;
+            }
         }
-
-        int my_e = -1;
+        // now either exactly `want` keys are >= lo, or more are because several equal lo
+        uint32_t take = lo;
+        int n = from;
+        if (bias && want > 0) {
+            // candidates that fp64 might put before the border
+            const float v = from_order_bits(lo);
+            const uint32_t c = order_bits(v - kKeyGap * fmaxf(1.0f, fabsf(v)));
+            take = c > 1u ? c : 1u;
+            n = count_from(key, take);
+        }
+        // one lane each, in index order; without a bias equal keys at the border
+        // fill the places that the greater ones leave, and no more
+        int my_e = -1, rank = lane;
         float my_z = kNegInf;
-        bool unsettled = false;
-        uint32_t prev = 0u;
-        const int rounds = bias && K < E ? K + 1 : K;
-        for (int k = 0; k < rounds; ++k) {
-            uint32_t best = 0u;
-            int be = 0;
-            float bz = kNegInf;
+        if (want > 0 && (!bias || n <= kWave)) {
+            const int above = from > want && !bias ? count_from(key, lo + 1u) : 0;
+            int base = 0, equal = 0;
 #pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                if (key[j] > best) {
-                    best = key[j];
-                    be = j * kWave + lane;
-                    bz = z[j];
+            for (int j = 0; j < VPL; ++j) {
+                bool in = key[j] >= take;
+                if (!bias && from > want) {
+                    const uint64_t eq = ballot(key[j] == lo);
+                    in = key[j] > lo || (key[j] == lo && equal + lanes_below(eq) < want - above);
+                    equal += __popcll(eq);
                 }
-            const uint32_t m = wave_max_u(best);
-            if (m == 0u)
-                break;                  // the rest is masked
-            if (bias && k > 0) {
-                const float a = from_order_bits(prev), b = from_order_bits(m);
-                unsettled = unsettled || a - b <= kKeyGap * fmaxf(1.0f, fmaxf(fabsf(a), fabsf(b)));
+                const uint64_t m = ballot(in);
+                if (in) {
+                    const int at = base + lanes_below(m);
+                    chosen_e[wave][at] = j * kWave + lane;
+                    chosen_z[wave][at] = z[j];
+                }
+                base += __popcll(m);
             }
-            prev = m;
-            // the lowest index among equal keys, as the largest of ~index
-            const uint32_t inv = wave_max_u(best == m ? ~(uint32_t)be : 0u);
-            const int win = (int)~inv;
-            const float wz = lane_value(bz, win & (kWave - 1));
-            if (lane == k && k < K) {
-                my_e = win;
-                my_z = wz;
+            n = base;
+            __builtin_amdgcn_wave_barrier();
+            if (lane < n) {
+                my_e = chosen_e[wave][lane];
+                my_z = chosen_z[wave][lane];
             }
-#pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                if (j * kWave + lane == win)
-                    key[j] = 0u;
+            __builtin_amdgcn_wave_barrier();
+            // the place of each: the ones with a greater key, or an equal one of a lower index
+            rank = 0;
+            bool settled = true;
+            if (!bias) {
+                for (int i = 0; i < n; ++i) {
+                    const float o = lane_value(my_z, i);
+                    rank += o > my_z || (o == my_z && i < lane);
+                }
+            } else {
+                const float mine = lane < n ? key_sigmoid(my_z) + bias[my_e] + 0.0f : kNegInf;
+                bool near = n > want;
+                for (int i = 0; i < n; ++i) {
+                    const float o = lane_value(mine, i);
+                    rank += o > mine || (o == mine && i < lane);
+                    near = near || (i != lane && lane < n &&
+                                    fabsf(o - mine) <= kKeyGap * fmaxf(1.0f, fabsf(mine)));
+                }
+                settled = ballot(near) == 0;
+            }
+            if (!settled) {
+                const double mine = lane < n ? exact_key(my_z, bias[my_e]) : -__builtin_huge_val();
+                rank = 0;
+                for (int i = 0; i < n; ++i) {
+                    const double o = lane_value_d(mine, i);
+                    rank += o > mine || (o == mine && i < lane);
+                }
+            }
+            if (lane >= n)
+                rank = lane;
+            if (rank >= want && lane < n) {         // a candidate that was not chosen
+                my_e = -1;
+                my_z = kNegInf;
+                rank = kWave;
+            }
+        } else if (want > 0) {
+            choose_fp64<L>(row, bias, E, K, lane, my_e, my_z, rank);
         }
-        if (unsettled)
-            choose_fp64<L>(row, bias, E, K, lane, my_e, my_z);
 
         float w;
         if (!renorm) {
-            if (sigmoid)
+            if (sigmoid) {
                 w = my_e >= 0 ? sigmoid_f(my_z) : 0.0f;
-            else
-                w = total > 0.0f ? row_score(my_z, top, false) / total : 0.0f;
+            } else {
+                const float top = from_order_bits(top_key);     // keys are the logits here
+                float total = 0.0f;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j)
+                    total += row_score(z[j], top, false);
+                total = wave_sum_f(total);
+                w = my_e >= 0 ? row_score(my_z, top, false) / total : 0.0f;
+            }
         } else {
             const float zt = wave_max_f(my_z);
             const float s = row_score(my_z, zt, sigmoid);
             const float sum = wave_sum_f(s);
             w = sum > 0.0f ? s / sum : 0.0f;
         }
-        if (lane < K) {
-            topk_idx[t * K + lane] = my_e;
-            topk_w[t * K + lane] = scale * w;
+        // places without a choice: the lanes behind the chosen, in order
+        const uint64_t have = ballot(my_e >= 0);
+        const int spare = want + lanes_below(~have);
+        const int place = my_e >= 0 ? rank : spare;
+        if (place < K) {
+            topk_idx[t * K + place] = my_e;
+            topk_w[t * K + place] = scale * w;
         }
     }
 }
@@ -325,15 +423,26 @@ balance_partial_kernel(const typename L::type *__restrict__ logits, int T, int E
         for (int j = 0; j < VPL; ++j)
             acc[j] = 0.0f;
         int live = 0, bad_z = 0;
-        for (int t = lo + wave; t < hi; t += nw) {
-            const typename L::type *row = logits + (int64_t)t * E;
-            float z[VPL], top = kNegInf, sum = 0.0f;
+        // the next row's loads are in flight over a row's sums
+        float next[VPL];
+        auto load = [&](int64_t t) {
 #pragma unroll
             for (int j = 0; j < VPL; ++j) {
                 const int e = j * kWave + lane;
-                const float v = e < E ? L::get(row + e) : kNegInf;
-                bad_z += bad_logit(v);
-                z[j] = clean_logit(v);
+                next[j] = e < E && t < hi ? L::get(logits + t * E + e) : kNegInf;
+            }
+        };
+        load((int64_t)lo + wave);
+        for (int64_t t = (int64_t)lo + wave; t < hi; t += nw) {
+            float z[VPL], top = kNegInf, sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                z[j] = next[j];
+            load(t + nw);
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+                bad_z += bad_logit(z[j]);
+                z[j] = clean_logit(z[j]);
                 top = fmaxf(top, z[j]);
             }
             top = wave_max_f(top);
@@ -377,13 +486,16 @@ balance_partial_kernel(const typename L::type *__restrict__ logits, int T, int E
     }
 }
 
-constexpr int kFinalThreads = 1024;
+constexpr int kFinalCols = 16, kFinalStrips = 32, kFinalThreads = kFinalCols * kFinalStrips;
 
-// One block per (64 experts, sequence): the sums over the sequence's partial
-// rows (in row order, in fp64: a sum over all tokens), the counts, the table
-// the backward reads, slope[s][e] = E c_se / (K n_s^2), and the block's part
-// of sum_e f_se P_se.  The block that arrives last adds the parts in a fixed
-// order: the loss does not depend on which one that is.
+// One block per (16 experts, sequence): the sums over the sequence's partial
+// rows (in fp64: a sum over all tokens; in a fixed order), the counts, the
+// table the backward reads, slope[s][e] = E c_se / (K n_s^2), and the block's
+// part of sum_e f_se P_se.  The block that arrives last adds the parts in a
+// fixed order: the loss does not depend on which one that is.  It is latency
+// that counts here (256 rows of partials, 0.8 MB at E = 384): 32 strips take
+// 8 rows each with all their loads in flight; 16 waves of 16 rows, one after
+// the other, took 14 us.
 __global__ void __launch_bounds__(kFinalThreads)
 balance_final_kernel(const float *__restrict__ part, int T, int E, int K,
                      const int32_t *__restrict__ seq, int S, int CT, float coef, int eb,
@@ -392,49 +504,55 @@ balance_final_kernel(const float *__restrict__ part, int T, int E, int K,
                      double *__restrict__ parts, int32_t *__restrict__ tails,
                      unsigned *__restrict__ arrived)
 {
-    constexpr int NW = kFinalThreads / kWave;
-    __shared__ double sums[NW][kWave];
-    __shared__ int32_t cnts[NW][kWave];
+    __shared__ double sums[kFinalStrips][kFinalCols];
+    __shared__ int32_t cnts[kFinalStrips][kFinalCols];
     __shared__ int32_t misc[3];
     __shared__ bool last;
-    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+    const int tid = threadIdx.x, col = tid % kFinalCols, strip = tid / kFinalCols;
     const int s = blockIdx.x / eb, b = blockIdx.x % eb;
-    const int e = b * kWave + lane;
+    const int e = b * kFinalCols + col;
     const int q0 = seq ? clampi(seq[s], 0, T) : 0, q1 = seq ? clampi(seq[s + 1], 0, T) : T;
     const int r0 = q0 < q1 ? q0 / CT : 0, r1 = q0 < q1 ? (q1 - 1) / CT + 1 : 0;
     if (tid < 3)
         misc[tid] = 0;
     __syncthreads();
+    const int64_t stride = 2 * (int64_t)E + 4;
+    const float *p = part + ((int64_t)s + r0) * stride;
     double sum = 0.0;
     int cnt = 0;
-    for (int c = r0 + wave; c < r1; c += NW) {
-        const BalanceRow r = balance_row(const_cast<float *>(part), E, (int64_t)c + s);
-        if (e < E) {
-            sum += (double)r.sum[e];
-            cnt += r.count[e];
+    if (e < E) {
+#pragma unroll 8
+        for (int c = strip; c < r1 - r0; c += kFinalStrips) {
+            sum += (double)p[c * stride + e];
+            cnt += reinterpret_cast<const int32_t *>(p)[c * stride + E + e];
         }
-        if (lane < 3)
-            atomicAdd(&misc[lane], r.live[lane]);
     }
-    sums[wave][lane] = sum;
-    cnts[wave][lane] = cnt;
+    for (int i = tid; i < 3 * (r1 - r0); i += kFinalThreads)
+        if (const int v = reinterpret_cast<const int32_t *>(p)[i / 3 * stride + 2 * E + i % 3])
+            atomicAdd(&misc[i % 3], v);
+    sums[strip][col] = sum;
+    cnts[strip][col] = cnt;
     __syncthreads();
+    for (int half = kFinalStrips / 2; half > 0; half >>= 1) {
+        if (strip < half) {
+            sums[strip][col] += sums[strip + half][col];
+            cnts[strip][col] += cnts[strip + half][col];
+        }
+        __syncthreads();
+    }
     const int n = misc[0];
-    if (wave == 0) {
-        for (int w = 1; w < NW; ++w) {
-            sum += sums[w][lane];
-            cnt += cnts[w][lane];
-        }
-        const double inv = n > 0 ? 1.0 / n : 0.0;
-        const double f = (double)E * cnt / K * inv;
-        if (e < E) {
-            counts[(int64_t)s * E + e] = cnt;
+    if (tid < kWave) {
+        double v = 0.0;
+        if (tid < kFinalCols && e < E) {
+            const double inv = n > 0 ? 1.0 / n : 0.0;
+            const double f = (double)E * cnts[0][col] / K * inv;
+            counts[(int64_t)s * E + e] = cnts[0][col];
             slope[(int64_t)s * E + e] = (float)(f * inv);
+            v = f * sums[0][col] * inv;
         }
-        double v = e < E ? f * sum * inv : 0.0;
-        for (int m = kWave / 2; m > 0; m >>= 1)
+        for (int m = kFinalCols / 2; m > 0; m >>= 1)
             v += __shfl_down(v, m);
-        if (lane == 0) {
+        if (tid == 0) {
             // agent scope: the last block may run on another XCD
             __hip_atomic_store(&parts[blockIdx.x], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             if (b == 0)
@@ -447,13 +565,13 @@ balance_final_kernel(const float *__restrict__ part, int T, int E, int K,
         }
     }
     __syncthreads();
-    if (!last || wave != 0)
+    if (!last || tid >= kWave)
         return;
     double all = 0.0;
     int n_live = 0, bad_i = 0, bad_z = 0;
-    for (int64_t i = lane; i < (int64_t)S * eb; i += kWave)
+    for (int64_t i = tid; i < (int64_t)S * eb; i += kWave)
         all += __hip_atomic_load(&parts[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    for (int i = lane; i < S; i += kWave) {
+    for (int i = tid; i < S; i += kWave) {
         n_live += __hip_atomic_load(&tails[3 * (int64_t)i], __ATOMIC_RELAXED,
                                     __HIP_MEMORY_SCOPE_AGENT) > 0;
         bad_i += __hip_atomic_load(&tails[3 * (int64_t)i + 1], __ATOMIC_RELAXED,
@@ -466,7 +584,7 @@ balance_final_kernel(const float *__restrict__ part, int T, int E, int K,
     n_live = wave_sum(n_live);
     bad_i = wave_sum(bad_i);
     bad_z = wave_sum(bad_z);
-    if (lane == 0) {
+    if (tid == 0) {
         const double per = n_live > 0 ? 1.0 / n_live : 0.0;
         loss[0] = (float)(coef * all * per);
         slope[(int64_t)S * E] = (float)(coef * per);
@@ -627,6 +745,8 @@ hipError_t with_vpl(int E, F f)
         return f(vpl_t<2>());
     if (E <= 256)
         return f(vpl_t<4>());
+    if (E <= 384)
+        return f(vpl_t<6>());
     if (E <= 512)
         return f(vpl_t<8>());
     if (E <= 1024)
@@ -691,7 +811,7 @@ BalancePlan make_balance_plan(int T, int E, int S)
     if (p.CT < 16)
         p.CT = 16;
     p.nchunk = T > 0 ? (T + p.CT - 1) / p.CT : 1;
-    p.eb = (E + kWave - 1) / kWave;
+    p.eb = (E + kFinalCols - 1) / kFinalCols;
     size_t off = 0;
     p.off_arrived = off;
     off = align256(off + 4);

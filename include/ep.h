@@ -476,7 +476,7 @@ size_t ep_balance_workspace_bytes(int T, int E, int S);
  *   num_invalid   [2] int32 out: bad entries of topk_idx, bad logits (of the
  *                 tokens in sequences).
  *   ws, ws_bytes  >= ep_balance_workspace_bytes(T, E, S) bytes; free after the call.
- * Constraints: E <= 4096, S >= 1, S*E < 2^31, S * ceil(E / 64) < 2^22.
+ * Constraints: E <= 4096, S >= 1, S*E < 2^31, S * ceil(E / 16) < 2^22.
  */
 ep_status_t ep_balance_loss(const void *logits, ep_dtype_t dtype, int T, int E,
                             const int32_t *topk_idx, int K, ep_score_t score,

@@ -33,13 +33,34 @@ struct F32 {
     typedef float type;
     static __device__ __forceinline__ float get(const float *p) { return *p; }
     static __device__ __forceinline__ void put(float *p, float v) { *p = v; }
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    static __device__ __forceinline__ void get2(const float *p, float &a, float &b)
+    {
+        const f2 v = *reinterpret_cast<const f2 *>(p);
+        a = v[0];
+        b = v[1];
+    }
+    static __device__ __forceinline__ void put2(float *p, float a, float b)
+    {
+        *reinterpret_cast<f2 *>(p) = f2{a, b};
+    }
 };
 struct Bf16 {
     typedef uint16_t type;
     static __device__ __forceinline__ float get(const uint16_t *p) { return bf16_lo(*p); }
     static __device__ __forceinline__ void put(uint16_t *p, float v)
     {
-        *p = (uint16_t)f32_to_bf16_rne(v);
+        *p = (uint16_t)pack_bf16_any(v, v);
+    }
+    static __device__ __forceinline__ void get2(const uint16_t *p, float &a, float &b)
+    {
+        const uint32_t v = *reinterpret_cast<const uint32_t *>(p);
+        a = bf16_lo(v);
+        b = bf16_hi(v);
+    }
+    static __device__ __forceinline__ void put2(uint16_t *p, float a, float b)
+    {
+        *reinterpret_cast<uint32_t *>(p) = pack_bf16_any(a, b);
     }
 };
 __device__ __forceinline__ bool bad_logit(float z)
@@ -50,7 +71,27 @@ __device__ __forceinline__ float clean_logit(float z)
 {
     return bad_logit(z) ? kNegInf : z + 0.0f;
 }
-__device__ __forceinline__ float sigmoid_f(float z) { return 1.0f / (1.0f + expf(-z)); }
+
+// exp(x) for x <= 0, to 4u (u = 2^-24) of its value, 0 below 2^-126: 2^t with
+// t = x log2(e) as a rounded product and what it lost, and log2(e) in two parts.
+// 7 instructions, one of them v_exp_f32, where the library's expf takes about twice
+// as many for arguments and results that do not occur here.
+__device__ __forceinline__ float exp_f(float x)
+{
+    constexpr float hi = 1.44269502f, lo = 1.92596299e-8f, ln2 = 0.693147182f;
+    x = fmaxf(x, -200.0f);          // -inf too
+    const float t = x * hi;
+    const float rest = fmaf(x, lo, fmaf(x, hi, -t));
+    const float p = __builtin_amdgcn_exp2f(t);
+    return fmaf(p, rest * ln2, p);
+}
+// 1 / (1 + exp(-z)), to 8u of its value (v_rcp_f32: 2u), and 1 minus that.
+__device__ __forceinline__ float sigmoid_f(float z)
+{
+    const float e = exp_f(-fabsf(z));
+    return (z < 0.0f ? e : 1.0f) * __builtin_amdgcn_rcpf(1.0f + e);
+}
+__device__ __forceinline__ float one_minus_sigmoid_f(float z) { return sigmoid_f(-z); }
 
 // Order-preserving bits: larger float, larger integer; 0 is below them all
 // and stands for a masked entry.
@@ -59,10 +100,46 @@ __device__ __forceinline__ uint32_t order_bits(float v)
     const uint32_t u = __float_as_uint(v);
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
-__device__ __forceinline__ float from_order_bits(uint32_t k)
-{
-    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
-}
+// How a wave's lanes share a row where the order does not matter: value j of a
+// lane is expert at(j).  In pairs (E even: rows keep their alignment), a lane's
+// loads and stores take two neighbours at once.
+template <typename L, int VPL, bool PAIR>
+struct Row {
+    static_assert(!PAIR || VPL % 2 == 0, "whole pairs");
+    static __device__ __forceinline__ int at(int j, int lane)
+    {
+        return PAIR ? (j >> 1) * (2 * kWave) + lane * 2 + (j & 1) : j * kWave + lane;
+    }
+    static __device__ __forceinline__ void load(const typename L::type *row, int E, int lane,
+                                                float (&z)[VPL])
+    {
+#pragma unroll
+        for (int j = 0; j < VPL; j += PAIR ? 2 : 1) {
+            const int e = at(j, lane);
+            if constexpr (PAIR) {
+                z[j] = z[j + 1] = kNegInf;
+                if (e < E)
+                    L::get2(row + e, z[j], z[j + 1]);
+            } else {
+                z[j] = e < E ? L::get(row + e) : kNegInf;
+            }
+        }
+    }
+    static __device__ __forceinline__ void store(typename L::type *row, int E, int lane,
+                                                 const float (&d)[VPL])
+    {
+#pragma unroll
+        for (int j = 0; j < VPL; j += PAIR ? 2 : 1) {
+            const int e = at(j, lane);
+            if (e >= E)
+                continue;
+            if constexpr (PAIR)
+                L::put2(row + e, d[j], d[j + 1]);
+            else
+                L::put(row + e, d[j]);
+        }
+    }
+};
 
 // Row scores for the probabilities: see the head of the file.  `top` is the
 // row's maximum (-inf in a row that is masked throughout).
@@ -70,7 +147,7 @@ __device__ __forceinline__ float row_score(float z, float top, bool sigmoid)
 {
     if (!(z > kNegInf))
         return 0.0f;
-    return sigmoid && top >= kSmallSigmoid ? sigmoid_f(z) : expf(z - top);
+    return sigmoid && top >= kSmallSigmoid ? sigmoid_f(z) : exp_f(z - top);
 }
 
 // ---------------------------------------------------------------- the choice
@@ -145,27 +222,19 @@ __device__ void choose_fp64(const typename L::type *row, const float *bias, int 
     }
 }
 
-// How many of the wave's keys are at least `t`.
-template <int VPL>
-__device__ __forceinline__ int count_from(const uint32_t (&key)[VPL], uint32_t t)
-{
-    int n = 0;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j)
-        n += __popcll(ballot(key[j] >= t));
-    return n;
-}
-
-// One wave per token.  The keys are order-preserving bits of the logits (both
-// scores are monotone in them, so without a bias the order is exact), or of
-// sigmoid(z) + bias.  A border between the K chosen and the rest is bisected
-// with ballots: halfway between two keys as numbers, which is quick for logits
-// as they are, and every fourth time as bits, which bounds it by 128 rounds;
-// the chosen go to one lane each through shared memory, in index order, and
-// each counts those before it.  A border inside equal keys gives the places
-// left to the lowest indices.  This costs about 8 ballots per 64 experts, where K
-// rounds of a maximum over the wave cost K reductions: 43.5 us at 16384 x 384,
-// K = 16, with those.
+// One wave per token.  The keys are the logits (both scores are monotone in
+// them, so without a bias the order is exact), or sigmoid(z) + bias.
+//
+// Candidates: a histogram of the keys over 64 equal steps between the largest
+// key and a key that at least K reach (the least of the lanes' best ones) gives
+// the step that the K-th falls into; everything from that step up, K and a few
+// more, goes to one lane each through shared memory, in index order.  The step
+// of a key is monotone in it, whatever the rounding, so nothing below can be
+// among the K.  Each candidate then counts those before it.  Rows with more
+// than 64 candidates (many equal keys, or a huge range) bisect the border
+// between the K and the rest instead, with ballots.
+// At 16384 x 384 in bf16, K = 16: K maxima over the wave, one after the other,
+// took 43.5 us; bisecting the border in every row 27 us.
 template <typename L, int VPL>
 __global__ void __launch_bounds__(256)
 route_kernel(const typename L::type *__restrict__ logits, int T, int E, int K, int sigmoid,
@@ -175,138 +244,161 @@ route_kernel(const typename L::type *__restrict__ logits, int T, int E, int K, i
 {
     __shared__ int chosen_e[4][kWave];
     __shared__ float chosen_z[4][kWave];
+    __shared__ int steps[4][kWave];
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int nw = gridDim.x * (blockDim.x / kWave);
     for (int64_t t = blockIdx.x * (blockDim.x / kWave) + wave; t < T; t += nw) {
         const typename L::type *row = logits + t * E;
-        float z[VPL];
-        uint32_t key[VPL];
-        int bad = 0;
+        float z[VPL], key[VPL];
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
             const int e = j * kWave + lane;
             z[j] = e < E ? L::get(row + e) : kNegInf;
         }
+        int bad = 0;
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
-            bad += __popcll(ballot(bad_logit(z[j])));
+            bad += bad_logit(z[j]);
             z[j] = clean_logit(z[j]);
+            key[j] = z[j];
         }
-        if (num_invalid && lane == 0)
-            num_invalid[t] = bad;
-        uint32_t best = 0u;
+        if (num_invalid) {
+            bad = ballot(bad != 0) ? wave_sum(bad) : 0;
+            if (lane == 0)
+                num_invalid[t] = bad;
+        }
         if (bias) {
 #pragma unroll
             for (int j = 0; j < VPL; ++j) {
                 const int e = j * kWave + lane;
                 const float v = z[j] > kNegInf ? key_sigmoid(z[j]) + bias[e] + 0.0f : kNegInf;
-                key[j] = finite_f(v) ? order_bits(v) : 0u;
-                best = umax(best, key[j]);
+                key[j] = finite_f(v) ? v : kNegInf;
             }
+        }
+        float best = kNegInf, least_key = __builtin_huge_valf();
+        int able = 0;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            best = fmaxf(best, key[j]);
+            able += __popcll(ballot(key[j] > kNegInf));
+        }
+        const int want = able < K ? able : K;
+        const float top = wave_max_f(best);
+        // a key that `want` keys reach
+        const uint64_t lanes_with = ballot(best > kNegInf);
+        if (__popcll(lanes_with) >= want) {
+            least_key = best > kNegInf ? best : __builtin_huge_valf();
         } else {
 #pragma unroll
-            for (int j = 0; j < VPL; ++j) {
-                key[j] = z[j] > kNegInf ? order_bits(z[j]) : 0u;
-                best = umax(best, key[j]);
-            }
+            for (int j = 0; j < VPL; ++j)
+                least_key = fminf(least_key, key[j] > kNegInf ? key[j] : __builtin_huge_valf());
         }
-
-        // the border: `from` keys are >= lo, no more than `want` are >= hi
-        const uint32_t top_key = wave_max_u(best);
-        const int able = count_from(key, 1u);           // not masked
-        const int want = able < K ? able : K;
-        uint32_t lo = 1u, hi = top_key + 1u;
-        int from = able;
-        for (int round = 0; from > want && hi - lo > 1u; ++round) {
-            uint32_t mid = lo + (hi - lo) / 2u;
-            if ((round & 3) != 3) {
-                const uint32_t m = order_bits(0.5f * from_order_bits(lo) + 0.5f * from_order_bits(hi - 1u));
-                mid = m > lo && m < hi ? m : mid;
-            }
-            const int n = count_from(key, mid);
-            if (n >= want) {
-                lo = mid;
-                from = n;
-            } else {
-                hi = mid;
-            }
-        }
-        // now either exactly `want` keys are >= lo, or more are because several equal lo
-        uint32_t take = lo;
-        int n = from;
-        if (bias && want > 0) {
-            // candidates that fp64 might put before the border
-            const float v = from_order_bits(lo);
-            const uint32_t c = order_bits(v - kKeyGap * fmaxf(1.0f, fabsf(v)));
-            take = c > 1u ? c : 1u;
-            n = count_from(key, take);
-        }
-        // one lane each, in index order; without a bias equal keys at the border
-        // fill the places that the greater ones leave, and no more
-        int my_e = -1, rank = lane;
+        const float low = -wave_max_f(-least_key);
+        const float per = 63.0f * __builtin_amdgcn_rcpf(top - low);
+        auto step_of = [&](float k) {       // 0 .. 63, monotone; NaN (no range) gives 0
+            const int b = (int)((k - low) * per);
+            return b < 0 ? 0 : (b > 63 ? 63 : b);
+        };
+        int my_e = -1, rank = lane, n = 0;
         float my_z = kNegInf;
-        if (want > 0 && (!bias || n <= kWave)) {
-            const int above = from > want && !bias ? count_from(key, lo + 1u) : 0;
-            int base = 0, equal = 0;
+        if (want > 0) {
+            steps[wave][lane] = 0;
+            __builtin_amdgcn_wave_barrier();
 #pragma unroll
-            for (int j = 0; j < VPL; ++j) {
-                bool in = key[j] >= take;
-                if (!bias && from > want) {
-                    const uint64_t eq = ballot(key[j] == lo);
-                    in = key[j] > lo || (key[j] == lo && equal + lanes_below(eq) < want - above);
-                    equal += __popcll(eq);
-                }
-                const uint64_t m = ballot(in);
-                if (in) {
-                    const int at = base + lanes_below(m);
-                    chosen_e[wave][at] = j * kWave + lane;
-                    chosen_z[wave][at] = z[j];
-                }
-                base += __popcll(m);
-            }
-            n = base;
+            for (int j = 0; j < VPL; ++j)
+                if (key[j] >= low)
+                    atomicAdd(&steps[wave][step_of(key[j])], 1);
             __builtin_amdgcn_wave_barrier();
-            if (lane < n) {
-                my_e = chosen_e[wave][lane];
-                my_z = chosen_z[wave][lane];
+            const int upto = wave_inclusive_scan(steps[wave][kWave - 1 - lane], lane);
+            const int at = __ffsll((unsigned long long)ballot(upto >= want)) - 1;
+            const int border = kWave - 1 - at;
+            n = __builtin_amdgcn_readlane(upto, at);
+            // with a bias, also what fp64 might put before the K-th
+            const float near_by = bias ? kKeyGap * fmaxf(1.0f, fmaxf(fabsf(top), fabsf(low))) : 0.0f;
+            auto candidate = [&](float k) { return k > kNegInf && k + near_by >= low && step_of(k + near_by) >= border; };
+            if (bias) {
+                n = 0;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j)
+                    n += __popcll(ballot(candidate(key[j])));
             }
-            __builtin_amdgcn_wave_barrier();
-            // the place of each: the ones with a greater key, or an equal one of a lower index
-            rank = 0;
-            bool settled = true;
-            if (!bias) {
-                for (int i = 0; i < n; ++i) {
-                    const float o = lane_value(my_z, i);
-                    rank += o > my_z || (o == my_z && i < lane);
+            uint32_t lo = 0u;               // border of the rows that bisect, as order bits
+            int above = 0;
+            const bool many = n > kWave;
+            if (many && !bias) {
+                // lo: the largest key that `want` keys reach
+                uint32_t hi = order_bits(top) + 1u;
+                lo = order_bits(low);
+                while (hi - lo > 1u) {
+                    const uint32_t mid = lo + (hi - lo) / 2u;
+                    int c = 0;
+#pragma unroll
+                    for (int j = 0; j < VPL; ++j)
+                        c += __popcll(ballot(key[j] > kNegInf && order_bits(key[j]) >= mid));
+                    if (c >= want)
+                        lo = mid;
+                    else
+                        hi = mid;
                 }
-            } else {
-                const float mine = lane < n ? key_sigmoid(my_z) + bias[my_e] + 0.0f : kNegInf;
-                bool near = n > want;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j)
+                    above += __popcll(ballot(key[j] > kNegInf && order_bits(key[j]) > lo));
+            }
+            if (!many || !bias) {
+                int base = 0, equal = 0;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) {
+                    bool in;
+                    if (!many) {
+                        in = candidate(key[j]);
+                    } else {
+                        // all greater ones, and the lowest indices among the equal
+                        const uint32_t k = key[j] > kNegInf ? order_bits(key[j]) : 0u;
+                        const uint64_t eq = ballot(k == lo);
+                        in = k > lo || (k == lo && equal + lanes_below(eq) < want - above);
+                        equal += __popcll(eq);
+                    }
+                    const uint64_t m = ballot(in);
+                    if (in) {
+                        const int to = base + lanes_below(m);
+                        chosen_e[wave][to] = j * kWave + lane;
+                        chosen_z[wave][to] = z[j];
+                    }
+                    base += __popcll(m);
+                }
+                n = base;
+                __builtin_amdgcn_wave_barrier();
+                if (lane < n) {
+                    my_e = chosen_e[wave][lane];
+                    my_z = chosen_z[wave][lane];
+                }
+                __builtin_amdgcn_wave_barrier();
+                // the place of each: those with a greater key, or an equal one of a lower index
+                float mine = my_z;
+                if (bias)
+                    mine = lane < n ? key_sigmoid(my_z) + bias[my_e] + 0.0f : kNegInf;
+                rank = 0;
+                bool near = false;
                 for (int i = 0; i < n; ++i) {
                     const float o = lane_value(mine, i);
                     rank += o > mine || (o == mine && i < lane);
-                    near = near || (i != lane && lane < n &&
-                                    fabsf(o - mine) <= kKeyGap * fmaxf(1.0f, fabsf(mine)));
+                    near = near || (bias && i != lane && lane < n && fabsf(o - mine) <= near_by);
                 }
-                settled = ballot(near) == 0;
-            }
-            if (!settled) {
-                const double mine = lane < n ? exact_key(my_z, bias[my_e]) : -__builtin_huge_val();
-                rank = 0;
-                for (int i = 0; i < n; ++i) {
-                    const double o = lane_value_d(mine, i);
-                    rank += o > mine || (o == mine && i < lane);
+                if (ballot(near)) {
+                    const double d = lane < n ? exact_key(my_z, bias[my_e]) : -__builtin_huge_val();
+                    rank = 0;
+                    for (int i = 0; i < n; ++i) {
+                        const double o = lane_value_d(d, i);
+                        rank += o > d || (o == d && i < lane);
+                    }
                 }
+                if (lane >= n || rank >= want) {        // no candidate, or not chosen
+                    my_e = -1;
+                    my_z = kNegInf;
+                }
+            } else {
+                choose_fp64<L>(row, bias, E, K, lane, my_e, my_z, rank);
             }
-            if (lane >= n)
-                rank = lane;
-            if (rank >= want && lane < n) {         // a candidate that was not chosen
-                my_e = -1;
-                my_z = kNegInf;
-                rank = kWave;
-            }
-        } else if (want > 0) {
-            choose_fp64<L>(row, bias, E, K, lane, my_e, my_z, rank);
         }
 
         float w;
@@ -314,7 +406,7 @@ route_kernel(const typename L::type *__restrict__ logits, int T, int E, int K, i
             if (sigmoid) {
                 w = my_e >= 0 ? sigmoid_f(my_z) : 0.0f;
             } else {
-                const float top = from_order_bits(top_key);     // keys are the logits here
+                // keys are the logits here: top is their maximum
                 float total = 0.0f;
 #pragma unroll
                 for (int j = 0; j < VPL; ++j)
@@ -379,7 +471,7 @@ __device__ __forceinline__ BalanceRow balance_row(float *part, int E, int64_t ro
 // spills: 16 waves leave 128 registers, 2 leave 512).
 constexpr int balance_threads(int vpl) { return vpl <= 8 ? 1024 : (vpl <= 16 ? 512 : 128); }
 
-template <typename L, int VPL>
+template <typename L, int VPL, bool PAIR>
 __global__ void __launch_bounds__(balance_threads(VPL))
 balance_partial_kernel(const typename L::type *__restrict__ logits, int T, int E,
                        const int32_t *__restrict__ topk_idx, int K, int sigmoid,
@@ -426,11 +518,7 @@ balance_partial_kernel(const typename L::type *__restrict__ logits, int T, int E
         // the next row's loads are in flight over a row's sums
         float next[VPL];
         auto load = [&](int64_t t) {
-#pragma unroll
-            for (int j = 0; j < VPL; ++j) {
-                const int e = j * kWave + lane;
-                next[j] = e < E && t < hi ? L::get(logits + t * E + e) : kNegInf;
-            }
+            Row<L, VPL, PAIR>::load(logits + t * E, t < hi ? E : 0, lane, next);
         };
         load((int64_t)lo + wave);
         for (int64_t t = (int64_t)lo + wave; t < hi; t += nw) {
@@ -454,14 +542,14 @@ balance_partial_kernel(const typename L::type *__restrict__ logits, int T, int E
                 z[j] = row_score(z[j], top, sigmoid);
                 sum += z[j];
             }
-            const float inv = 1.0f / wave_sum_f(sum);
+            const float inv = __builtin_amdgcn_rcpf(wave_sum_f(sum));
 #pragma unroll
             for (int j = 0; j < VPL; ++j)
                 acc[j] = fmaf(z[j], inv, acc[j]);
         }
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
-            const int e = j * kWave + lane;
+            const int e = Row<L, VPL, PAIR>::at(j, lane);
             if (e < E)
                 lds[wave * E + e] = acc[j];
         }
@@ -603,7 +691,7 @@ balance_final_kernel(const float *__restrict__ part, int T, int E, int K,
 // (the factors in brackets for the sigmoid).  The chosen entries' parts meet
 // their columns in a row of shared memory; a row of logits is read once, and
 // only where probabilities of the whole row are needed.
-template <typename L, int VPL>
+template <typename L, int VPL, bool PAIR>
 __global__ void __launch_bounds__(256)
 router_backward_kernel(const typename L::type *__restrict__ logits, int T, int E, int K,
                        int sigmoid, int renorm, float scale, const int32_t *__restrict__ topk_idx,
@@ -626,10 +714,10 @@ router_backward_kernel(const typename L::type *__restrict__ logits, int T, int E
         for (int j = 0; j < VPL; ++j)
             d[j] = 0.0f;
         if (whole) {
+            Row<L, VPL, PAIR>::load(row, E, lane, z);
 #pragma unroll
             for (int j = 0; j < VPL; ++j) {
-                const int e = j * kWave + lane;
-                z[j] = e < E ? clean_logit(L::get(row + e)) : kNegInf;
+                z[j] = clean_logit(z[j]);
                 top = fmaxf(top, z[j]);
             }
             top = wave_max_f(top);
@@ -640,7 +728,7 @@ router_backward_kernel(const typename L::type *__restrict__ logits, int T, int E
                 sum += p[j];
             }
             sum = wave_sum_f(sum);
-            inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+            inv = sum > 0.0f ? __builtin_amdgcn_rcpf(sum) : 0.0f;
 #pragma unroll
             for (int j = 0; j < VPL; ++j)
                 p[j] *= inv;
@@ -664,13 +752,13 @@ router_backward_kernel(const typename L::type *__restrict__ logits, int T, int E
                 const float q = sum > 0.0f ? s / sum : 0.0f;
                 v = q * (v - wave_sum_f(q * v));
                 if (sigmoid && in)
-                    v *= sigmoid_f(-zk);
+                    v *= one_minus_sigmoid_f(zk);
             } else if (sigmoid && in) {
-                v *= sigmoid_f(zk) * sigmoid_f(-zk);
+                v *= sigmoid_f(zk) * one_minus_sigmoid_f(zk);
             }
 #pragma unroll
             for (int j = 0; j < VPL; ++j) {
-                const int c = j * kWave + lane;
+                const int c = Row<L, VPL, PAIR>::at(j, lane);
                 if (c < E)
                     mine[c] = 0.0f;
             }
@@ -680,7 +768,7 @@ router_backward_kernel(const typename L::type *__restrict__ logits, int T, int E
             __builtin_amdgcn_wave_barrier();
 #pragma unroll
             for (int j = 0; j < VPL; ++j) {
-                const int c = j * kWave + lane;
+                const int c = Row<L, VPL, PAIR>::at(j, lane);
                 d[j] = c < E ? mine[c] : 0.0f;
             }
             __builtin_amdgcn_wave_barrier();
@@ -702,7 +790,7 @@ router_backward_kernel(const typename L::type *__restrict__ logits, int T, int E
                 float fe[VPL], dot = 0.0f;
 #pragma unroll
                 for (int j = 0; j < VPL; ++j) {
-                    const int e = j * kWave + lane;
+                    const int e = Row<L, VPL, PAIR>::at(j, lane);
                     fe[j] = e < E ? f[e] : 0.0f;
                     dot = fmaf(p[j], fe[j], dot);
                 }
@@ -711,18 +799,12 @@ router_backward_kernel(const typename L::type *__restrict__ logits, int T, int E
                 for (int j = 0; j < VPL; ++j) {
                     float v = g * p[j] * (fe[j] - dot);
                     if (sigmoid && z[j] > kNegInf)
-                        v *= sigmoid_f(-z[j]);
+                        v *= one_minus_sigmoid_f(z[j]);
                     d[j] += v;
                 }
             }
         }
-        typename L::type *out = d_logits + t * E;
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) {
-            const int e = j * kWave + lane;
-            if (e < E)
-                L::put(out + e, d[j]);
-        }
+        Row<L, VPL, PAIR>::store(d_logits + t * E, E, lane, d);
     }
 }
 
@@ -775,9 +857,13 @@ hipError_t balance_t(const BalancePlan &p, const void *logits, const int32_t *to
     return with_vpl(p.E, [&](auto v) {
         constexpr int threads = balance_threads(decltype(v)::value);
         const size_t lds = ((size_t)(threads / kWave) * p.E + p.E + 3) * 4;
-        balance_partial_kernel<L, decltype(v)::value><<<p.nchunk, threads, lds, s>>>(
-            static_cast<const typename L::type *>(logits), p.T, p.E, topk_idx, K, sigmoid, seq,
-            p.S, p.CT, part, arrived);
+        constexpr int VPL = decltype(v)::value;
+        auto *kernel = balance_partial_kernel<L, VPL, false>;
+        if constexpr (VPL % 2 == 0)
+            if (p.E % 2 == 0)
+                kernel = balance_partial_kernel<L, VPL, true>;
+        kernel<<<p.nchunk, threads, lds, s>>>(static_cast<const typename L::type *>(logits), p.T, p.E,
+                                              topk_idx, K, sigmoid, seq, p.S, p.CT, part, arrived);
         return hipGetLastError();
     });
 }
@@ -789,11 +875,14 @@ hipError_t router_backward_t(const void *logits, int T, int E, int K, bool sigmo
                              void *d_logits, hipStream_t s)
 {
     return with_vpl(E, [&](auto v) {
-        router_backward_kernel<L, decltype(v)::value>
-            <<<row_blocks(T), 256, 4 * (size_t)E * sizeof(float), s>>>(
-                static_cast<const typename L::type *>(logits), T, E, K, sigmoid, renorm, scale,
-                topk_idx, d_w, slope, seq, S, d_loss,
-                static_cast<typename L::type *>(d_logits));
+        constexpr int VPL = decltype(v)::value;
+        auto *kernel = router_backward_kernel<L, VPL, false>;
+        if constexpr (VPL % 2 == 0)
+            if (E % 2 == 0)
+                kernel = router_backward_kernel<L, VPL, true>;
+        kernel<<<row_blocks(T), 256, 4 * (size_t)E * sizeof(float), s>>>(
+            static_cast<const typename L::type *>(logits), T, E, K, sigmoid, renorm, scale, topk_idx,
+            d_w, slope, seq, S, d_loss, static_cast<typename L::type *>(d_logits));
         return hipGetLastError();
     });
 }

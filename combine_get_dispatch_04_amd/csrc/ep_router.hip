@@ -242,11 +242,14 @@ route_kernel(const typename L::type *__restrict__ logits, int T, int E, int K, i
              int32_t *__restrict__ topk_idx, float *__restrict__ topk_w,
              int32_t *__restrict__ num_invalid)
 {
-    __shared__ int chosen_e[4][kWave];
-    __shared__ float chosen_z[4][kWave];
-    __shared__ int steps[4][kWave];
+    // the upper half of both takes what has no place, a slot per lane: cheaper
+    // than a branch per value
+    __shared__ u32x2 chosen[4][2 * kWave];      // expert, logit
+    __shared__ int steps[4][2 * kWave];
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int nowhere = kWave + lane;
     const int nw = gridDim.x * (blockDim.x / kWave);
+    constexpr float kInf = __builtin_huge_valf();
     for (int64_t t = blockIdx.x * (blockDim.x / kWave) + wave; t < T; t += nw) {
         const typename L::type *row = logits + t * E;
         float z[VPL], key[VPL];
@@ -258,8 +261,9 @@ route_kernel(const typename L::type *__restrict__ logits, int T, int E, int K, i
         int bad = 0;
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
-            bad += bad_logit(z[j]);
-            z[j] = clean_logit(z[j]);
+            const bool wrong = bad_logit(z[j]);
+            bad += wrong;
+            z[j] = wrong ? kNegInf : z[j];
             key[j] = z[j];
         }
         if (num_invalid) {
@@ -271,43 +275,52 @@ route_kernel(const typename L::type *__restrict__ logits, int T, int E, int K, i
 #pragma unroll
             for (int j = 0; j < VPL; ++j) {
                 const int e = j * kWave + lane;
-                const float v = z[j] > kNegInf ? key_sigmoid(z[j]) + bias[e] + 0.0f : kNegInf;
+                const float v = z[j] > kNegInf ? key_sigmoid(z[j]) + bias[e] : kNegInf;
                 key[j] = finite_f(v) ? v : kNegInf;
             }
         }
-        float best = kNegInf, least_key = __builtin_huge_valf();
-        int able = 0;
+        // the largest key; the least of the lanes' best, which `want` keys reach
+        // if as many lanes have one, else the least key of all
+        float best = kNegInf, worst = kInf;
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
             best = fmaxf(best, key[j]);
-            able += __popcll(ballot(key[j] > kNegInf));
+            worst = fminf(worst, j * kWave + lane < E ? key[j] : kInf);
+        }
+        int able = E;
+        if (ballot(worst == kNegInf)) {         // some are masked
+            able = 0;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                able += __popcll(ballot(key[j] > kNegInf));
         }
         const int want = able < K ? able : K;
         const float top = wave_max_f(best);
-        // a key that `want` keys reach
-        const uint64_t lanes_with = ballot(best > kNegInf);
-        if (__popcll(lanes_with) >= want) {
-            least_key = best > kNegInf ? best : __builtin_huge_valf();
-        } else {
+        float floor_key = best > kNegInf ? best : kInf;
+        if (__popcll(ballot(best > kNegInf)) < want) {
 #pragma unroll
             for (int j = 0; j < VPL; ++j)
-                least_key = fminf(least_key, key[j] > kNegInf ? key[j] : __builtin_huge_valf());
+                floor_key = fminf(floor_key, key[j] > kNegInf ? key[j] : kInf);
         }
-        const float low = -wave_max_f(-least_key);
+        const float low = -wave_max_f(-floor_key);
         const float per = 63.0f * __builtin_amdgcn_rcpf(top - low);
-        auto step_of = [&](float k) {       // 0 .. 63, monotone; NaN (no range) gives 0
+        // 0 .. 63, monotone; NaN (no range to divide) gives 0; below low and masked: nowhere
+        auto step_of = [&](float k) {
             const int b = (int)((k - low) * per);
-            return b < 0 ? 0 : (b > 63 ? 63 : b);
+            const int c = b < 0 ? 0 : (b > kWave - 1 ? kWave - 1 : b);
+            return k >= low ? c : nowhere;
         };
         int my_e = -1, rank = lane, n = 0;
         float my_z = kNegInf;
         if (want > 0) {
+            int at_step[VPL];
             steps[wave][lane] = 0;
             __builtin_amdgcn_wave_barrier();
 #pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                if (key[j] >= low)
-                    atomicAdd(&steps[wave][step_of(key[j])], 1);
+            for (int j = 0; j < VPL; ++j) {
+                at_step[j] = step_of(key[j]);
+                atomicAdd(&steps[wave][at_step[j]], 1);
+            }
             __builtin_amdgcn_wave_barrier();
             const int upto = wave_inclusive_scan(steps[wave][kWave - 1 - lane], lane);
             const int at = __ffsll((unsigned long long)ballot(upto >= want)) - 1;
@@ -315,81 +328,103 @@ route_kernel(const typename L::type *__restrict__ logits, int T, int E, int K, i
             n = __builtin_amdgcn_readlane(upto, at);
             // with a bias, also what fp64 might put before the K-th
             const float near_by = bias ? kKeyGap * fmaxf(1.0f, fmaxf(fabsf(top), fabsf(low))) : 0.0f;
-            auto candidate = [&](float k) { return k > kNegInf && k + near_by >= low && step_of(k + near_by) >= border; };
             if (bias) {
                 n = 0;
 #pragma unroll
-                for (int j = 0; j < VPL; ++j)
-                    n += __popcll(ballot(candidate(key[j])));
+                for (int j = 0; j < VPL; ++j) {
+                    at_step[j] = key[j] > kNegInf ? step_of(key[j] + near_by) : nowhere;
+                    n += __popcll(ballot((unsigned)(at_step[j] - border) < (unsigned)(kWave - border)));
+                }
             }
-            uint32_t lo = 0u;               // border of the rows that bisect, as order bits
-            int above = 0;
-            const bool many = n > kWave;
-            if (many && !bias) {
-                // lo: the largest key that `want` keys reach
-                uint32_t hi = order_bits(top) + 1u;
-                lo = order_bits(low);
+            if (n <= kWave) {
+                int base = 0;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) {
+                    const bool in = (unsigned)(at_step[j] - border) < (unsigned)(kWave - border);
+                    const uint64_t m = ballot(in);
+                    const int to = in ? base + lanes_below(m) : nowhere;
+                    chosen[wave][to] = u32x2{(uint32_t)(j * kWave + lane), __float_as_uint(z[j])};
+                    base += __popcll(m);
+                }
+            } else if (!bias) {
+                // lo: the largest key that `want` keys reach, in order bits; then all
+                // greater ones, and the lowest indices among the equal
+                uint32_t lo = order_bits(low + 0.0f), hi = order_bits(top + 0.0f) + 1u;
+                auto bits = [&](float k) { return k > kNegInf ? order_bits(k + 0.0f) : 0u; };
                 while (hi - lo > 1u) {
                     const uint32_t mid = lo + (hi - lo) / 2u;
                     int c = 0;
 #pragma unroll
                     for (int j = 0; j < VPL; ++j)
-                        c += __popcll(ballot(key[j] > kNegInf && order_bits(key[j]) >= mid));
+                        c += __popcll(ballot(bits(key[j]) >= mid));
                     if (c >= want)
                         lo = mid;
                     else
                         hi = mid;
                 }
+                int above = 0, base = 0, equal = 0;
 #pragma unroll
                 for (int j = 0; j < VPL; ++j)
-                    above += __popcll(ballot(key[j] > kNegInf && order_bits(key[j]) > lo));
-            }
-            if (!many || !bias) {
-                int base = 0, equal = 0;
+                    above += __popcll(ballot(bits(key[j]) > lo));
 #pragma unroll
                 for (int j = 0; j < VPL; ++j) {
-                    bool in;
-                    if (!many) {
-                        in = candidate(key[j]);
-                    } else {
-                        // all greater ones, and the lowest indices among the equal
-                        const uint32_t k = key[j] > kNegInf ? order_bits(key[j]) : 0u;
-                        const uint64_t eq = ballot(k == lo);
-                        in = k > lo || (k == lo && equal + lanes_below(eq) < want - above);
-                        equal += __popcll(eq);
-                    }
+                    const uint32_t k = bits(key[j]);
+                    const uint64_t eq = ballot(k == lo);
+                    const bool in = k > lo || (k == lo && equal + lanes_below(eq) < want - above);
+                    equal += __popcll(eq);
                     const uint64_t m = ballot(in);
-                    if (in) {
-                        const int to = base + lanes_below(m);
-                        chosen_e[wave][to] = j * kWave + lane;
-                        chosen_z[wave][to] = z[j];
-                    }
+                    const int to = in ? base + lanes_below(m) : nowhere;
+                    chosen[wave][to] = u32x2{(uint32_t)(j * kWave + lane), __float_as_uint(z[j])};
                     base += __popcll(m);
                 }
                 n = base;
-                __builtin_amdgcn_wave_barrier();
+            }
+            __builtin_amdgcn_wave_barrier();
+            if (n <= kWave) {
                 if (lane < n) {
-                    my_e = chosen_e[wave][lane];
-                    my_z = chosen_z[wave][lane];
+                    const u32x2 c = chosen[wave][lane];
+                    my_e = (int)c[0];
+                    my_z = __uint_as_float(c[1]) + 0.0f;
                 }
-                __builtin_amdgcn_wave_barrier();
-                // the place of each: those with a greater key, or an equal one of a lower index
-                float mine = my_z;
-                if (bias)
-                    mine = lane < n ? key_sigmoid(my_z) + bias[my_e] + 0.0f : kNegInf;
+                // the place of each: those with a greater key, or an equal one of a
+                // lower index (that is, in a lower lane).  Lanes behind the last
+                // candidate hold the least key, so whole fours of them do no harm.
+                const int n4 = (n + 3) & ~3;
                 rank = 0;
-                bool near = false;
-                for (int i = 0; i < n; ++i) {
-                    const float o = lane_value(mine, i);
-                    rank += o > mine || (o == mine && i < lane);
-                    near = near || (bias && i != lane && lane < n && fabsf(o - mine) <= near_by);
-                }
-                if (ballot(near)) {
-                    const double d = lane < n ? exact_key(my_z, bias[my_e]) : -__builtin_huge_val();
-                    rank = 0;
+                if (sizeof(typename L::type) == 2 && !bias) {
+                    // 16 bits of order, 16 of the index: all different
+                    const uint32_t mine = lane < n ? (order_bits(my_z) & 0xFFFF0000u) | (kWave - 1 - lane) : 0u;
+                    for (int i = 0; i < n4; i += 4) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            rank += (uint32_t)__builtin_amdgcn_readlane((int)mine, i + q) > mine;
+                    }
+                } else if (!bias) {
+                    for (int i = 0; i < n4; i += 4) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            rank += lane_value(my_z, i + q) > my_z;
+                    }
+                    // the pairs in order are all there are, unless some are equal
+                    if (wave_sum(lane < n ? rank : 0) != n * (n - 1) / 2) {
+                        for (int i = 0; i < n; ++i)
+                            rank += i < lane && lane_value(my_z, i) == my_z;
+                    }
+                } else {
+                    const float mine = lane < n ? key_sigmoid(my_z) + bias[my_e] : kNegInf;
+                    int close = 0;
                     for (int i = 0; i < n; ++i) {
-                        const double o = lane_value_d(d, i);
-                        rank += o > d || (o == d && i < lane);
+                        const float o = lane_value(mine, i);
+                        rank += o > mine;
+                        close += fabsf(o - mine) <= near_by;
+                    }
+                    if (ballot(lane < n && close > 1)) {        // more than itself
+                        const double d = lane < n ? exact_key(my_z, bias[my_e]) : -__builtin_huge_val();
+                        rank = 0;
+                        for (int i = 0; i < n; ++i) {
+                            const double o = lane_value_d(d, i);
+                            rank += o > d || (o == d && i < lane);
+                        }
                     }
                 }
                 if (lane >= n || rank >= want) {        // no candidate, or not chosen
@@ -399,6 +434,7 @@ route_kernel(const typename L::type *__restrict__ logits, int T, int E, int K, i
             } else {
                 choose_fp64<L>(row, bias, E, K, lane, my_e, my_z, rank);
             }
+            __builtin_amdgcn_wave_barrier();
         }
 
         float w;

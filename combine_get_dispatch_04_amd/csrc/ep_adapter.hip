@@ -197,19 +197,17 @@ struct Product {
         return q / (BK * 8) * 64 + ((q % 8 >> 1) ^ unit_swizzle(kn_of(q))) * 16 + (q & 1) * 8;
     }
     // Starts the load of the thread's piece number i of a stage into `buf`
-    // (the tokens' operand first): pa(i), pb(i) are the pieces' addresses.
+    // (the tokens' operand first; `buf` moved on to the wave's pieces, see run):
+    // pa(i), pb(i) are the pieces' addresses.
     static constexpr int pieces = PA + PB;
     template <typename FA, typename FB>
     static __device__ __forceinline__ void fetch(char *buf, int i, FA pa, FB pb)
     {
-        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
         if (i < PA)
-            __builtin_amdgcn_global_load_lds((global_ptr)pa(i),
-                                             (lds_ptr)(buf + (i * threads + wave * kWave) * 16), 16, 0, 0);
+            __builtin_amdgcn_global_load_lds((global_ptr)pa(i), (lds_ptr)(buf + i * threads * 16), 16, 0, 0);
         else
-            __builtin_amdgcn_global_load_lds(
-                (global_ptr)pb(i - PA),
-                (lds_ptr)(buf + bytes_a + ((i - PA) * threads + wave * kWave) * 16), 16, 0, 0);
+            __builtin_amdgcn_global_load_lds((global_ptr)pb(i - PA),
+                                             (lds_ptr)(buf + bytes_a + (i - PA) * threads * 16), 16, 0, 0);
     }
     // The same through registers, for a stage that ends beyond the inner
     // dimension: va(p), vb(p) give the pieces, zeros where there is nothing.
@@ -269,6 +267,8 @@ struct Product {
 #pragma unroll
         for (int g = 0; g < n; ++g) {
             group(FROM + g, a, b);
+            // not before these MFMAs, which would wait for the reads as well
+            __builtin_amdgcn_sched_barrier(0);
             if (g == 0)
                 read_b<KS>(b_next, from, w);
 #pragma unroll
@@ -291,10 +291,12 @@ struct Product {
         if (n <= 0)
             return;
         const Place w = place();
+        // where the wave's pieces go, in scalar registers for the loads into LDS
+        char *const mine = lds + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * (kWave * 16);
         for (int s = 0; s < NS && s < n; ++s) {
 #pragma unroll
             for (int i = 0; i < pieces; ++i)
-                fetch_piece(lds + s * bytes, i);
+                fetch_piece(mine + s * bytes, i);
             advance();
         }
         if (n >= NS)
@@ -315,7 +317,7 @@ struct Product {
             for (int i = 0; i < LAG; ++i)
                 group(i, a, b1);
             wait_and_meet<(NS - 2) * pieces>();
-            groups<LAG, 0, true>(a, b1, b0, lds + nxt * bytes, w, buf, fetch_piece);
+            groups<LAG, 0, true>(a, b1, b0, lds + nxt * bytes, w, mine + cur * bytes, fetch_piece);
             advance();
             cur = nxt;
         }
@@ -440,38 +442,121 @@ adapter_tiles_kernel(Tiles m)
 
 __global__ void adapter_zero_kernel(int32_t *p) { *p = 0; }
 
-// Splits of the inner dimension that a tile's shrink takes with a list of
-// `cols` columns: its `slots` blocks share the 64-column chunks.
+// How a tile's `slots` blocks share a list of `cols` columns: chunks of 128
+// columns, or of 64 for a short list (the tokens' rows are read once per chunk);
+// blocks beyond the chunks split the inner dimension.
+__device__ __forceinline__ int shrink_width(int cols) { return cols > 64 ? 128 : 64; }
+__device__ __forceinline__ int shrink_chunks(int cols)
+{
+    return (cols + shrink_width(cols) - 1) / shrink_width(cols);
+}
 __device__ __forceinline__ int shrink_splits(int cols, int slots)
 {
-    const int chunks = (cols + 63) / 64;
+    const int chunks = shrink_chunks(cols);
     return chunks >= slots ? 1 : (chunks > 0 ? slots / chunks : 1);
 }
 
 // ---------------------------------------------------------------- shrink
 // part[split][t*K + k][r] = sum over the split's inner elements of src[t][.]
 // times the entry's adapter: A [E, r, D] (NN = false), or B [E, D, r] (NN =
-// true).  Columns of the list in chunks of 64; products of a token and an
-// adapter it does not name are dropped.
+// true).  Products of a token and an adapter it does not name are dropped.
+// One chunk of the list's columns, from column n0, for tokens t0 ..
+template <typename P, bool NN>
+__device__ __forceinline__ void shrink_chunk(const Tiles &m, const uint16_t *src, const uint16_t *ad, int D,
+                                             const int32_t *list, int cols, int t0, int n0, int s0, int s1,
+                                             int split, float *part, char *lds)
+{
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int whole = least(s1, D / BK) - s0;       // without the stage that ends beyond D
+    P p;
+    p.zero();
+    // rows behind the last token and columns behind the list's last repeat
+    // a row and a column that exist: their products are not stored
+    const uint16_t *pa[P::PA], *pb[P::PB];
+#pragma unroll
+    for (int i = 0; i < P::PA; ++i) {
+        const int q = i * P::threads + tid;
+        pa[i] = src + (int64_t)least(t0 + P::row_of(q), m.T - 1) * D + (s0 * BK + P::k_of(q));
+    }
+#pragma unroll
+    for (int i = 0; i < P::PB; ++i) {
+        const int q = i * P::threads + tid;
+        const int n = n0 + (NN ? P::n_of(q) : P::row_of(q));
+        const int l = n < cols ? n / m.rp : 0, j = n < cols && n % m.rp < m.r ? n % m.rp : 0;
+        const int64_t e = list[l];
+        pb[i] = NN ? ad + (e * D + s0 * BK + P::kn_of(q)) * m.r + j
+                   : ad + (e * m.r + j) * D + (s0 * BK + P::k_of(q));
+    }
+    p.run(lds, whole, [&](char *buf, int i) {
+        P::fetch(buf, i, [&](int i) { return pa[i]; }, [&](int i) { return pb[i]; });
+    }, [&] {
+#pragma unroll
+        for (int i = 0; i < P::PA; ++i)
+            pa[i] += BK;
+#pragma unroll
+        for (int i = 0; i < P::PB; ++i)
+            pb[i] += NN ? BK * m.r : BK;
+    });
+    if (whole < s1 - s0) {
+        const int k0 = (s0 + whole) * BK, left = D - k0;
+        p.run_filled(
+            lds,
+            [&](int i) {
+                const int q = i * P::threads + tid, k = P::k_of(q);
+                return k < left ? ld16(src + (int64_t)least(t0 + P::row_of(q), m.T - 1) * D + k0 + k)
+                                : zero4();
+            },
+            [&](int i) {
+                const int q = i * P::threads + tid;
+                const int n = n0 + (NN ? P::n_of(q) : P::row_of(q));
+                const int k = NN ? P::kn_of(q) : P::k_of(q);
+                if (k >= left || n >= cols || n % m.rp >= m.r)
+                    return zero4();
+                const int64_t e = list[n / m.rp];
+                return NN ? ld16(ad + (e * D + k0 + k) * m.r + n % m.rp)
+                          : ld16(ad + (e * m.r + n % m.rp) * D + k0 + k);
+            });
+    }
+#pragma unroll
+    for (int i = 0; i < P::TI; ++i) {
+        const int t = t0 + wave / P::WN * (P::BM / P::WM) + i * 16 + (lane & 15);
+#pragma unroll
+        for (int j = 0; j < P::TJ; ++j) {
+            const int n = n0 + wave % P::WN * (P::BN / P::WN) + j * 16 + (lane >> 4) * 4;
+            const int l = n / m.rp, jj = n % m.rp;
+            if (n >= cols || jj >= m.r || t >= m.T)
+                continue;
+            const int e = list[l];
+            for (int k = 0; k < m.K; ++k)
+                if (m.idx[(int64_t)t * m.K + k] == e)
+                    *reinterpret_cast<f32x4 *>(part + (((int64_t)split * m.T + t) * m.K + k) * m.r + jj) =
+                        p.acc[i][j];
+        }
+    }
+}
+
 // A block takes RB tokens of a tile.
 template <int RB, bool NN>
 struct Shrink {
-    typedef Product<RB, 64, RB / 32, 1, 3, NN> P;
+    typedef Product<RB, 64, RB / 32, 1, 3, NN> Narrow;
+    typedef Product<RB, 128, RB / 64, 2, 2, NN> Wide;
+    static constexpr int lds_bytes = Narrow::lds_bytes > Wide::lds_bytes ? Narrow::lds_bytes : Wide::lds_bytes;
 };
 template <int RB, bool NN>
-__global__ void __launch_bounds__(RB * 2)
+__global__ void __launch_bounds__(RB * 2, 2)
 adapter_shrink_kernel(Tiles m, const uint16_t *__restrict__ src, const uint16_t *__restrict__ ad,
                       int D, int slots, float *__restrict__ part)
 {
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    typedef typename Shrink<RB, NN>::P P;
+    typedef Shrink<RB, NN> S;
+    static_assert(S::Narrow::threads == RB * 2 && S::Wide::threads == RB * 2, "one block shape");
     const int block = blockIdx.x / slots, slot = blockIdx.x % slots;
     const int tile = block / (m.BM / RB), t0 = block * RB;
     if (t0 >= m.T)
         return;
     const int cols = m.cnt[tile] * m.rp;
-    const int chunks = (cols + 63) / 64;
-    const int splits = shrink_splits(cols, slots);
+    const int chunks = shrink_chunks(cols), splits = shrink_splits(cols, slots);
     const int split = chunks >= slots ? 0 : (chunks > 0 ? slot / chunks : 0);
     if (split >= splits)
         return;
@@ -480,76 +565,13 @@ adapter_shrink_kernel(Tiles m, const uint16_t *__restrict__ src, const uint16_t 
     const int s0 = (int)((int64_t)steps * split / splits);
     const int s1 = (int)((int64_t)steps * (split + 1) / splits);
     const int32_t *list = m.list + (int64_t)tile * m.Lmax;
-    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-    const int whole = least(s1, D / BK) - s0;       // without the stage that ends beyond D
     for (int chunk = chunks >= slots ? slot : (chunks > 0 ? slot % chunks : 0); chunk < chunks;
          chunk += step) {
-        const int n0 = chunk * 64;
-        P p;
-        p.zero();
-        // rows behind the last token and columns behind the list's last repeat
-        // a row and a column that exist: their products are not stored
-        const uint16_t *pa[P::PA], *pb[P::PB];
-#pragma unroll
-        for (int i = 0; i < P::PA; ++i) {
-            const int q = i * P::threads + tid;
-            pa[i] = src + (int64_t)least(t0 + P::row_of(q), m.T - 1) * D + (s0 * BK + P::k_of(q));
-        }
-#pragma unroll
-        for (int i = 0; i < P::PB; ++i) {
-            const int q = i * P::threads + tid;
-            const int n = n0 + (NN ? P::n_of(q) : P::row_of(q));
-            const int l = n < cols ? n / m.rp : 0, j = n < cols && n % m.rp < m.r ? n % m.rp : 0;
-            const int64_t e = list[l];
-            pb[i] = NN ? ad + (e * D + s0 * BK + P::kn_of(q)) * m.r + j
-                       : ad + (e * m.r + j) * D + (s0 * BK + P::k_of(q));
-        }
-        p.run(lds, whole, [&](char *buf, int i) {
-            P::fetch(buf, i, [&](int i) { return pa[i]; }, [&](int i) { return pb[i]; });
-        }, [&] {
-#pragma unroll
-            for (int i = 0; i < P::PA; ++i)
-                pa[i] += BK;
-#pragma unroll
-            for (int i = 0; i < P::PB; ++i)
-                pb[i] += NN ? BK * m.r : BK;
-        });
-        if (whole < s1 - s0) {
-            const int k0 = (s0 + whole) * BK, left = D - k0;
-            p.run_filled(
-                lds,
-                [&](int i) {
-                    const int q = i * P::threads + tid, k = P::k_of(q);
-                    return k < left ? ld16(src + (int64_t)least(t0 + P::row_of(q), m.T - 1) * D + k0 + k)
-                                    : zero4();
-                },
-                [&](int i) {
-                    const int q = i * P::threads + tid;
-                    const int n = n0 + (NN ? P::n_of(q) : P::row_of(q));
-                    const int k = NN ? P::kn_of(q) : P::k_of(q);
-                    if (k >= left || n >= cols || n % m.rp >= m.r)
-                        return zero4();
-                    const int64_t e = list[n / m.rp];
-                    return NN ? ld16(ad + (e * D + k0 + k) * m.r + n % m.rp)
-                              : ld16(ad + (e * m.r + n % m.rp) * D + k0 + k);
-                });
-        }
-#pragma unroll
-        for (int i = 0; i < P::TI; ++i) {
-            const int t = t0 + wave * 32 + i * 16 + (lane & 15);
-#pragma unroll
-            for (int j = 0; j < P::TJ; ++j) {
-                const int n = n0 + j * 16 + (lane >> 4) * 4;
-                const int l = n / m.rp, jj = n % m.rp;
-                if (n >= cols || jj >= m.r || t >= m.T)
-                    continue;
-                const int e = list[l];
-                for (int k = 0; k < m.K; ++k)
-                    if (m.idx[(int64_t)t * m.K + k] == e)
-                        *reinterpret_cast<f32x4 *>(
-                            part + (((int64_t)split * m.T + t) * m.K + k) * m.r + jj) = p.acc[i][j];
-            }
-        }
+        if (cols > 64)
+            shrink_chunk<typename S::Wide, NN>(m, src, ad, D, list, cols, t0, chunk * 128, s0, s1, split, part, lds);
+        else
+            shrink_chunk<typename S::Narrow, NN>(m, src, ad, D, list, cols, t0, 0, s0, s1, split, part, lds);
+        __syncthreads();        // the buffers are free for the next chunk
     }
 }
 
@@ -577,10 +599,11 @@ adapter_gather_kernel(Tiles m, const float *__restrict__ w, float scale, int slo
     for (int i = tid; i < kGatherRows * pieces; i += 256) {
         const int row = row0 + i / pieces, n = (i % pieces) * 8;
         const int t = tile * m.BM + row;
-        float s[8] = {0, 0, 0, 0, 0, 0, 0, 0}, coef = 0.0f;
+        f32x4 lo = {0.0f, 0.0f, 0.0f, 0.0f}, hi = lo;
         const int l = n / m.rp, j = n % m.rp;
         if (t < m.T && n < cols && j < m.r) {
             const int e = list[l];
+            float coef = 0.0f;
             bool found = false;
             for (int k = 0; k < m.K; ++k) {
                 const int64_t tk = (int64_t)t * m.K + k;
@@ -589,31 +612,25 @@ adapter_gather_kernel(Tiles m, const float *__restrict__ w, float scale, int slo
                 coef += w ? w[tk] : 1.0f;
                 if (!found) {
                     const float *p = part + tk * m.r + j;
+#pragma unroll 8
                     for (int q = 0; q < splits; ++q) {
-                        const f32x4 lo = *reinterpret_cast<const f32x4 *>(p + q * stride);
-                        const f32x4 hi = *reinterpret_cast<const f32x4 *>(p + q * stride + 4);
-#pragma unroll
-                        for (int d = 0; d < 4; ++d) {
-                            s[d] += lo[d];
-                            s[4 + d] += hi[d];
-                        }
+                        lo += *reinterpret_cast<const f32x4 *>(p + q * stride);
+                        hi += *reinterpret_cast<const f32x4 *>(p + q * stride + 4);
                     }
                     found = true;
                 }
                 float *o = sums + tk * m.r + j;
-                *reinterpret_cast<f32x4 *>(o) = f32x4{s[0], s[1], s[2], s[3]};
-                *reinterpret_cast<f32x4 *>(o + 4) = f32x4{s[4], s[5], s[6], s[7]};
+                *reinterpret_cast<f32x4 *>(o) = lo;
+                *reinterpret_cast<f32x4 *>(o + 4) = hi;
             }
-            if (found)
-#pragma unroll
-                for (int d = 0; d < 8; ++d)
-                    s[d] *= scale * coef;
+            if (found) {
+                lo *= scale * coef;
+                hi *= scale * coef;
+            }
         }
-        u32x4 v;
-#pragma unroll
-        for (int d = 0; d < 4; ++d)
-            v[d] = pack_bf16_any(s[2 * d], s[2 * d + 1]);
-        st16(dense + ((int64_t)tile * m.BM + row) * m.LW + n, v);
+        st16(dense + ((int64_t)tile * m.BM + row) * m.LW + n,
+             u32x4{pack_bf16_any(lo[0], lo[1]), pack_bf16_any(lo[2], lo[3]), pack_bf16_any(hi[0], hi[1]),
+                   pack_bf16_any(hi[2], hi[3])});
     }
     if (u && dw) {
         __syncthreads();        // the block's own sums are read back
@@ -622,11 +639,18 @@ adapter_gather_kernel(Tiles m, const float *__restrict__ w, float scale, int slo
             if (t >= m.T)
                 break;
             const int64_t tk = (int64_t)t * m.K + i % m.K;
-            float d = 0.0f;
-            if ((unsigned)m.idx[tk] < (unsigned)m.E)
-                for (int j = 0; j < m.r; ++j)
-                    d = fmaf(u[tk * m.r + j], sums[tk * m.r + j], d);
-            dw[tk] = scale * d;
+            f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
+            if ((unsigned)m.idx[tk] < (unsigned)m.E) {
+#pragma unroll 4
+                for (int j = 0; j < m.r; j += 4) {
+                    const f32x4 a = *reinterpret_cast<const f32x4 *>(u + tk * m.r + j);
+                    const f32x4 b = *reinterpret_cast<const f32x4 *>(sums + tk * m.r + j);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        d[q] = fmaf(a[q], b[q], d[q]);
+                }
+            }
+            dw[tk] = scale * ((d[0] + d[1]) + (d[2] + d[3]));
         }
     }
     if (num_invalid && blockIdx.x == 0 && tid < kWave) {
@@ -797,82 +821,118 @@ adapter_project_kernel(Tiles m, const uint16_t *__restrict__ src, int D,
 // dB[e][o][j] = sum_t d[t][o] U[t][e, j]  (OUTER = true: big = d, N = O)
 // A block takes 128 columns of `big` and G = 128 / rp adapters with consecutive
 // ids, over the tiles of its split that name one of them; both operands lie
-// across and are read transposed.  With one split the result is rounded and
-// stored, else fp32 sums go to `part` (laid out like the result) to be added.
+// across and are read transposed.  64 tokens at a time, the next ones' loads in
+// flight over the MFMAs of the present ones.  With one split the result is
+// rounded and stored, else fp32 sums go to `part` (laid out like the result)
+// to be added.
 constexpr int kGradCols = 128;
+constexpr int kGradBytes = BK * kGradCols * 2;
+struct GradJob {
+    const uint16_t *big, *dense;
+    uint16_t *out;
+    float *part;
+    int N, splits, chunks;      // columns, splits of the tiles, blocks of 128 columns
+};
 template <bool OUTER>
-__global__ void __launch_bounds__(256)
-adapter_grads_kernel(Tiles m, const uint16_t *__restrict__ big, int N,
-                     const uint16_t *__restrict__ dense, int ntile, int splits,
-                     uint16_t *__restrict__ out, float *__restrict__ part)
+__device__ void adapter_grads(const Tiles &m, const GradJob &g, int ntile, int block, char *lds)
 {
-    __shared__ __attribute__((aligned(16))) char lds[2 * BK * kGradCols * 2];
-    __shared__ int32_t at[kGradCols / 16];
-    const int G = kGradCols / m.rp;
-    const int n0 = blockIdx.x * kGradCols, e0 = blockIdx.y * G, split = blockIdx.z;
-    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+    const int G = kGradCols / m.rp, N = g.N;
+    const int n0 = block % g.chunks * kGradCols;
+    const int split = block / g.chunks % g.splits, e0 = block / g.chunks / g.splits * G;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int wb = wave >> 1, wd = wave & 1;        // the wave's half of the big columns, of the dense ones
-    const int i0 = (int)((int64_t)ntile * split / splits), i1 = (int)((int64_t)ntile * (split + 1) / splits);
+    const int i0 = (int)((int64_t)ntile * split / g.splits);
+    const int i1 = (int)((int64_t)ntile * (split + 1) / g.splits);
+    const int members = least(G, m.E - e0);
     f32x4 acc[4][4];        // [big unit][dense unit]
 #pragma unroll
     for (int b = 0; b < 4; ++b)
 #pragma unroll
         for (int d = 0; d < 4; ++d)
             acc[b][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    char *lb = lds, *ld = lds + BK * kGradCols * 2;
-    for (int tile = i0; tile < i1; ++tile) {
-        const int32_t *place = m.place + (int64_t)tile * m.E;
-        bool any = false;
-        for (int g = 0; g < G; ++g)
-            any = any || (e0 + g < m.E && place[e0 + g] >= 0);
-        if (!any)
-            continue;
-        __syncthreads();
-        if (tid < kGradCols / 16) {
-            const int g = tid * 16 / m.rp;
-            at[tid] = g < G && e0 + g < m.E && place[e0 + g] >= 0 ? place[e0 + g] * m.rp + tid * 16 % m.rp : -1;
+    // the next tile from `tile` on that names one of the adapters
+    auto next_tile = [&](int tile) {
+        for (; tile < i1; ++tile) {
+            const int32_t *place = m.place + (int64_t)tile * m.E + e0;
+            int any = -1;
+            for (int q = 0; q < members; ++q)
+                any = any < place[q] ? place[q] : any;
+            if (any >= 0)
+                break;
         }
+        return tile;
+    };
+    u32x4 rb[4], rd[4];
+    int my_at = -1;         // dense columns of the thread's pieces, -1 if not in this tile's list
+    auto load_at = [&](int tile) {
+        const int32_t *place = m.place + (int64_t)tile * m.E + e0;
+        const int c = tid % 16 * 8, q = c / m.rp;
+        const int p = q < members ? place[q] : -1;
+        my_at = p >= 0 ? p * m.rp + c % m.rp : -1;
+    };
+    auto load = [&](int tile, int r0) {
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const int q = p * 256 + tid, row = r0 + q / 16, c = (q % 16) * 8;
+            const int64_t t = (int64_t)tile * m.BM + row;
+            rb[p] = t < m.T && n0 + c < N ? ld16(g.big + t * N + n0 + c) : zero4();
+            rd[p] = t < m.T && my_at >= 0 ? ld16(g.dense + t * m.LW + my_at) : zero4();
+        }
+    };
+    int tile = next_tile(i0), r0 = 0, buf = 0;
+    if (tile < i1) {
+        load_at(tile);
+        load(tile, 0);
+    }
+    bool on[4] = {false, false, false, false};
+    while (tile < i1) {
+        char *lb = lds + buf * 2 * kGradBytes, *ld = lb + kGradBytes;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const int q = p * 256 + tid, k = q / 16, c = q % 16;
+            *reinterpret_cast<u32x4 *>(lb + off_n(k, c >> 1) + (c & 1) * 16) = rb[p];
+            *reinterpret_cast<u32x4 *>(ld + off_n(k, c >> 1) + (c & 1) * 16) = rd[p];
+        }
+        if (r0 == 0) {
+            // which of the wave's units this tile has
+            const int32_t *place = m.place + (int64_t)tile * m.E + e0;
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                const int q = (wd * 4 + d) * 16 / m.rp;
+                on[d] = q < members && place[q] >= 0;
+            }
+        }
+        int tile2 = tile, r2 = r0 + BK;
+        if (r2 >= m.BM || (int64_t)tile * m.BM + r2 >= m.T) {
+            tile2 = next_tile(tile + 1);
+            r2 = 0;
+            if (tile2 < i1)
+                load_at(tile2);
+        }
+        if (tile2 < i1)
+            load(tile2, r2);
         __syncthreads();
-        bool on[4];
 #pragma unroll
-        for (int d = 0; d < 4; ++d)
-            on[d] = at[wd * 4 + d] >= 0;
-        const int rows = m.T - tile * m.BM < m.BM ? m.T - tile * m.BM : m.BM;
-        for (int r0 = 0; r0 < rows; r0 += BK) {
-            u32x4 rb[4], rd[4];
+        for (int ks = 0; ks < 2; ++ks) {
+            bf16x8 fb[4];
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const int q = p * 256 + tid, row = r0 + q / 16, c = (q % 16) * 8;
-                const int64_t t = (int64_t)tile * m.BM + row;
-                rb[p] = t < m.T && n0 + c < N ? ld16(big + t * N + n0 + c) : zero4();
-                const int a = at[c / 16];
-                rd[p] = t < m.T && a >= 0 ? ld16(dense + t * m.LW + a + c % 16) : zero4();
-            }
+            for (int b = 0; b < 4; ++b)
+                fb[b] = frag_n(lb, ks, at_n(wb * 4 + b, lane));
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const int q = p * 256 + tid, k = q / 16, c = q % 16;
-                *reinterpret_cast<u32x4 *>(lb + off_n(k, c >> 1) + (c & 1) * 16) = rb[p];
-                *reinterpret_cast<u32x4 *>(ld + off_n(k, c >> 1) + (c & 1) * 16) = rd[p];
-            }
-            __syncthreads();
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                bf16x8 fb[4];
+            for (int d = 0; d < 4; ++d) {
+                if (!on[d])
+                    continue;
+                const bf16x8 fd = frag_n(ld, ks, at_n(wd * 4 + d, lane));
 #pragma unroll
                 for (int b = 0; b < 4; ++b)
-                    fb[b] = frag_n(lb, ks, at_n(wb * 4 + b, lane));
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    if (!on[d])
-                        continue;
-                    const bf16x8 fd = frag_n(ld, ks, at_n(wd * 4 + d, lane));
-#pragma unroll
-                    for (int b = 0; b < 4; ++b)
-                        acc[b][d] = OUTER ? mfma(fd, fb[b], acc[b][d]) : mfma(fb[b], fd, acc[b][d]);
-                }
+                    acc[b][d] = OUTER ? mfma(fd, fb[b], acc[b][d]) : mfma(fb[b], fd, acc[b][d]);
             }
-            __syncthreads();
         }
+        // one barrier a step: the other buffer is written while this one is read
+        tile = tile2;
+        r0 = r2;
+        buf ^= 1;
     }
     float s = 0.0f;
 #pragma unroll
@@ -892,8 +952,8 @@ adapter_grads_kernel(Tiles m, const uint16_t *__restrict__ big, int N,
             // big columns bn + (OUTER ? 0 : q)
             const int dn = (wd * 4 + d) * 16 + (OUTER ? (lane >> 4) * 4 : (lane & 15));
             const int bn = n0 + (wb * 4 + b) * 16 + (OUTER ? (lane & 15) : (lane >> 4) * 4);
-            const int g = dn / m.rp, j = dn % m.rp, e = e0 + g;
-            if (g >= G || e >= m.E || j >= m.r || bn >= N)
+            const int j = dn % m.rp, e = e0 + dn / m.rp;
+            if (dn / m.rp >= members || j >= m.r || bn >= N)
                 continue;
             f32x4 v = acc[b][d];
             if (again) {
@@ -911,34 +971,47 @@ adapter_grads_kernel(Tiles m, const uint16_t *__restrict__ big, int N,
                             continue;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const uint16_t x = big[t * N + bn + (OUTER ? 0 : q)];
-                            const uint16_t y = dense[t * m.LW + l * m.rp + j + (OUTER ? q : 0)];
+                            const uint16_t x = g.big[t * N + bn + (OUTER ? 0 : q)];
+                            const uint16_t y = g.dense[t * m.LW + l * m.rp + j + (OUTER ? q : 0)];
                             v[q] = fmaf(bf16_lo(x), bf16_lo(y), v[q]);
                         }
                     }
                 }
             }
             const int64_t o = OUTER ? ((int64_t)e * N + bn) * m.r + j : ((int64_t)e * m.r + j) * N + bn;
-            if (splits > 1)
-                *reinterpret_cast<f32x4 *>(part + split * total + o) = v;
+            if (g.splits > 1)
+                *reinterpret_cast<f32x4 *>(g.part + split * total + o) = v;
             else
-                *reinterpret_cast<u32x2 *>(out + o) =
+                *reinterpret_cast<u32x2 *>(g.out + o) =
                     u32x2{pack_bf16_any(v[0], v[1]), pack_bf16_any(v[2], v[3])};
         }
     }
 }
+// Both gradients in one launch: `blocks_a` blocks of dA's, the rest dB's.
+__global__ void __launch_bounds__(256, 2)
+adapter_grads_kernel(Tiles m, GradJob a, GradJob b, int ntile, int blocks_a)
+{
+    __shared__ __attribute__((aligned(16))) char lds[4 * kGradBytes];
+    if ((int)blockIdx.x < blocks_a)
+        adapter_grads<false>(m, a, ntile, blockIdx.x, lds);
+    else
+        adapter_grads<true>(m, b, ntile, blockIdx.x - blocks_a, lds);
+}
 
-// The splits' sum, in split order, rounded to bf16.
+// The splits' sums, in split order, rounded to bf16: of dA's values, then dB's.
 __global__ void __launch_bounds__(256)
-adapter_grads_sum_kernel(const float *__restrict__ part, int splits, int64_t total,
-                         uint16_t *__restrict__ out)
+adapter_grads_sum_kernel(GradJob a, int64_t total_a, GradJob b, int64_t total_b)
 {
     const int64_t step = (int64_t)gridDim.x * 256 * 4;
-    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < total; i += step) {
-        f32x4 v = *reinterpret_cast<const f32x4 *>(part + i);
-        for (int z = 1; z < splits; ++z)
-            v += *reinterpret_cast<const f32x4 *>(part + z * total + i);
-        *reinterpret_cast<u32x2 *>(out + i) = u32x2{pack_bf16_any(v[0], v[1]), pack_bf16_any(v[2], v[3])};
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < total_a + total_b; i += step) {
+        const bool in_a = i < total_a;
+        const GradJob &g = in_a ? a : b;
+        const int64_t total = in_a ? total_a : total_b, o = in_a ? i : i - total_a;
+        f32x4 v = *reinterpret_cast<const f32x4 *>(g.part + o);
+#pragma unroll 4
+        for (int z = 1; z < g.splits; ++z)
+            v += *reinterpret_cast<const f32x4 *>(g.part + z * total + o);
+        *reinterpret_cast<u32x2 *>(g.out + o) = u32x2{pack_bf16_any(v[0], v[1]), pack_bf16_any(v[2], v[3])};
     }
 }
 
@@ -1147,11 +1220,11 @@ template <int RB, bool NN>
 hipError_t shrink(const AdapterPlan &p, const Tiles &m, const uint16_t *src, const uint16_t *ad,
                   int D, float *part, hipStream_t s)
 {
-    typedef typename Shrink<RB, NN>::P P;
-    const hipError_t e = allow_lds(adapter_shrink_kernel<RB, NN>, P::lds_bytes);
+    constexpr int lds_bytes = Shrink<RB, NN>::lds_bytes;
+    const hipError_t e = allow_lds(adapter_shrink_kernel<RB, NN>, lds_bytes);
     if (e != hipSuccess)
         return e;
-    adapter_shrink_kernel<RB, NN><<<p.ntile * (p.BM / RB) * p.slots, P::threads, P::lds_bytes, s>>>(
+    adapter_shrink_kernel<RB, NN><<<p.ntile * (p.BM / RB) * p.slots, RB * 2, lds_bytes, s>>>(
         m, src, ad, D, p.slots, part);
     return hipGetLastError();
 }
@@ -1213,20 +1286,29 @@ hipError_t project_any(const AdapterPlan &p, const Tiles &m, const uint16_t *src
     return project<256, 256, 2, 4, 2, NN>(p, m, src, D, weight, N, ad, dense, out, s);
 }
 
-template <bool OUTER>
-hipError_t grads(const AdapterPlan &p, const Tiles &m, const uint16_t *big, int N,
-                 const uint16_t *dense, uint16_t *out, float *part, hipStream_t s)
+// dA and dB; either may be left out.
+hipError_t grads(const AdapterPlan &p, const Tiles &m, const uint16_t *x, const uint16_t *d_out,
+                 const uint16_t *u, const uint16_t *v, uint16_t *da, uint16_t *db, float *part,
+                 hipStream_t s)
 {
-    const int G = kGradCols / p.rp;
-    const int splits = adapter_grad_splits(p, N);
-    const dim3 grid((N + kGradCols - 1) / kGradCols, (p.E + G - 1) / G, splits);
-    adapter_grads_kernel<OUTER><<<grid, 256, 0, s>>>(m, big, N, dense, p.ntile, splits, out, part);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || splits == 1)
+    const int groups = (p.E + kGradCols / p.rp - 1) / (kGradCols / p.rp);
+    auto job = [&](const uint16_t *big, const uint16_t *dense, uint16_t *out, int N, float *sums) {
+        return GradJob{big, dense, out, sums, N, adapter_grad_splits(p, N), (N + kGradCols - 1) / kGradCols};
+    };
+    const int64_t elems_a = (int64_t)p.E * p.r * p.H, elems_b = (int64_t)p.E * p.r * p.O;
+    const GradJob a = job(x, v, da, p.H, part);
+    const GradJob b = job(d_out, u, db, p.O, part + (da && a.splits > 1 ? a.splits * elems_a : 0));
+    const int blocks_a = da ? a.chunks * a.splits * groups : 0;
+    const int blocks_b = db ? b.chunks * b.splits * groups : 0;
+    if (blocks_a + blocks_b == 0)
+        return hipSuccess;
+    adapter_grads_kernel<<<blocks_a + blocks_b, 256, 0, s>>>(m, a, b, p.ntile, blocks_a);
+    const hipError_t e = hipGetLastError();
+    const int64_t sum_a = da && a.splits > 1 ? elems_a : 0, sum_b = db && b.splits > 1 ? elems_b : 0;
+    if (e != hipSuccess || sum_a + sum_b == 0)
         return e;
-    const int64_t total = (int64_t)p.E * p.r * N;
-    const int64_t blocks = (total / 4 + 255) / 256;
-    adapter_grads_sum_kernel<<<blocks < 4096 ? (int)blocks : 4096, 256, 0, s>>>(part, splits, total, out);
+    const int64_t blocks = ((sum_a + sum_b) / 4 + 255) / 256;
+    adapter_grads_sum_kernel<<<blocks < 4096 ? (int)blocks : 4096, 256, 0, s>>>(a, sum_a, b, sum_b);
     return hipGetLastError();
 }
 
@@ -1236,7 +1318,8 @@ int adapter_grad_splits(const AdapterPlan &p, int N)
 {
     const int G = kGradCols / p.rp;
     const int64_t blocks = (int64_t)((N + kGradCols - 1) / kGradCols) * ((p.E + G - 1) / G);
-    int64_t splits = 512 / (blocks > 0 ? blocks : 1);
+    // a block per CU for each of the two gradients
+    int64_t splits = 256 / (blocks > 0 ? blocks : 1);
     if (splits > 16)
         splits = 16;
     if (splits > p.ntile)
@@ -1296,11 +1379,12 @@ AdapterPlan make_adapter_plan(int T, int H, int O, int E, int K, int r)
     }
     // backward: the splits' sums or those of the gradients, v and V
     size_t part = (size_t)p.slots * entries;
+    size_t both = 0;
     for (const int n : {H, O}) {
         const int z = adapter_grad_splits(p, n);
-        const size_t b = z > 1 ? (size_t)z * E * r * n * 4 : 0;
-        part = b > part ? b : part;
+        both += z > 1 ? (size_t)z * E * r * n * 4 : 0;
     }
+    part = both > part ? both : part;
     off = align256(part);
     p.off_v = off;
     off = align256(off + entries);
@@ -1370,10 +1454,8 @@ hipError_t launch_adapter_backward(const AdapterPlan &p, const uint16_t *d_out, 
                          vdense, u, dw, nullptr, s);
     if (e == hipSuccess && p.T > 0 && dx)
         e = project_any<true>(p, m, d_out, p.O, weight, p.H, a, vdense, dx, s);
-    if (e == hipSuccess && da)
-        e = grads<false>(p, m, x, p.H, vdense, da, part, s);
-    if (e == hipSuccess && db)
-        e = grads<true>(p, m, d_out, p.O, dense, db, part, s);
+    if (e == hipSuccess)
+        e = grads(p, m, x, d_out, dense, vdense, da, db, part, s);
     return e;
 }
 

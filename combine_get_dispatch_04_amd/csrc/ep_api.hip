@@ -597,7 +597,7 @@ ep_status_t check_adapter_sizes(int T, int H, int O, int E, int K, int r)
         return EP_ERR_UNSUPPORTED;
     // tiles of 128 tokens (larger calls) times blocks of 128 channels, 256 threads each: 32-bit grids
     const int64_t tiles = ((int64_t)T + 127) / 128, blocks = ((H > O ? H : O) + 127) / 128;
-    if (tiles * (blocks > 16 ? blocks : 16) >= 1 << 23)
+    if (tiles * (blocks > 16 ? blocks : 16) >= 1 << 23 || blocks * E >= 1 << 22)
         return EP_ERR_UNSUPPORTED;
     return EP_OK;
 }

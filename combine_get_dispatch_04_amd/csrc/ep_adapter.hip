@@ -13,9 +13,9 @@
 // list's B, and the gradients of A and B are products of U's and V's columns
 // with the tile's rows of d and x.
 //
-//   tiles      lists, and every adapter's place in each tile's list
-//   shrink     A_e x_t (or B_e^T d_t) of every entry, MFMA over the list's
-//              rows, the inner dimension split over blocks; fp32
+//   shrink     the lists, and every adapter's place in them; A_e x_t (or B_e^T d_t)
+//              of every entry, MFMA over the list's rows, the inner dimension split
+//              over blocks; fp32
 //   gather     sums the splits, writes U (or V) and the fp32 sums; dw
 //   project    the product with W, and U's stretch in front of it
 //   grads      dA, dB
@@ -374,7 +374,7 @@ struct Product {
     }
 };
 
-__device__ __forceinline__ int least(int a, int b) { return a < b ? a : b; }
+__host__ __device__ __forceinline__ int least(int a, int b) { return a < b ? a : b; }
 
 // Blocks are dealt to the 8 XCDs in turn; this gives each XCD a run of
 // consecutive tiles, so that its L2 sees the operands they share.
@@ -396,48 +396,74 @@ struct Tiles {
 
 __device__ __forceinline__ u32x4 zero4() { return u32x4{0u, 0u, 0u, 0u}; }
 
-__global__ void __launch_bounds__(256)
-adapter_tiles_kernel(Tiles m)
+// A tile's list, built by a block of at least 128 threads into shared memory
+// (`list`, with bits and firsts of 128 words each); with `write` also to memory,
+// with the places and the invalid entries' count.  Every block of a tile makes its
+// own: that is cheaper than a launch before it.
+constexpr int kListWords = 4096 / 32;       // most adapters
+__device__ int build_list(const Tiles &m, int tile, int32_t *list, uint32_t *bits, int32_t *firsts,
+                          bool write)
 {
-    extern __shared__ int32_t flags[];      // [E]
-    __shared__ int tmp[17];
+    const int tid = threadIdx.x, bd = blockDim.x;
+    const int words = (m.E + 31) / 32;
     __shared__ int n_bad;
-    const int tile = blockIdx.x, tid = threadIdx.x;
-    for (int e = tid; e < m.E; e += 256)
-        flags[e] = 0;
+    if (tid < kListWords)
+        bits[tid] = 0u;
     if (tid == 0)
         n_bad = 0;
     __syncthreads();
     const int t0 = tile * m.BM, t1 = m.T - t0 < m.BM ? m.T : t0 + m.BM;
     int bad = 0;
-    for (int64_t i = (int64_t)t0 * m.K + tid; i < (int64_t)t1 * m.K; i += 256) {
+    for (int64_t i = (int64_t)t0 * m.K + tid; i < (int64_t)t1 * m.K; i += bd) {
         const int e = m.idx[i];
         if ((unsigned)e < (unsigned)m.E)
-            flags[e] = 1;
+            atomicOr(&bits[e >> 5], 1u << (e & 31));
         else
             bad += e != -1;
     }
     if (bad)
         atomicAdd(&n_bad, bad);
     __syncthreads();
-    const int per = (m.E + 255) / 256;
-    const int e0 = tid * per, e1 = e0 + per < m.E ? e0 + per : m.E;
-    int n = 0;
-    for (int e = e0; e < e1; ++e)
-        n += flags[e];
-    int total;
-    int at = block_exclusive_scan(n, tmp, &total);
-    int32_t *place = m.place + (int64_t)tile * m.E;
-    int32_t *list = m.list + (int64_t)tile * m.Lmax;
-    for (int e = e0; e < e1; ++e) {
-        place[e] = flags[e] ? at : -1;
-        if (flags[e])
-            list[at++] = e;
+    if (tid < kWave) {                  // two words a lane
+        const int c0 = __popc(bits[2 * tid]), c1 = __popc(bits[2 * tid + 1]);
+        const int upto = wave_inclusive_scan(c0 + c1, tid);
+        firsts[2 * tid] = upto - c0 - c1;
+        firsts[2 * tid + 1] = upto - c1;
+        if (tid == kWave - 1)
+            firsts[kListWords] = upto;
     }
-    if (tid == 0) {
-        m.cnt[tile] = total;
-        m.bad[tile] = n_bad;
+    __syncthreads();
+    if (tid < words) {
+        int at = firsts[tid];
+        for (uint32_t b = bits[tid]; b; b &= b - 1u)
+            list[at++] = tid * 32 + __ffs(b) - 1;
     }
+    __syncthreads();
+    const int n = firsts[kListWords];
+    if (write) {
+        for (int i = tid; i < n; i += bd)
+            m.list[(int64_t)tile * m.Lmax + i] = list[i];
+        for (int e = tid; e < m.E; e += bd) {
+            const uint32_t b = bits[e >> 5], one = 1u << (e & 31);
+            m.place[(int64_t)tile * m.E + e] = b & one ? firsts[e >> 5] + __popc(b & (one - 1u)) : -1;
+        }
+        if (tid == 0) {
+            m.cnt[tile] = n;
+            m.bad[tile] = n_bad;
+        }
+    }
+    return n;
+}
+// The list that an earlier launch made, into shared memory: the addresses of
+// loads into LDS go by it, and a wait for a list entry from memory would be one
+// for those loads too.
+__device__ __forceinline__ int load_list(const Tiles &m, int tile, int32_t *list)
+{
+    const int n = m.cnt[tile];
+    for (int i = threadIdx.x; i < n; i += blockDim.x)
+        list[i] = m.list[(int64_t)tile * m.Lmax + i];
+    __syncthreads();
+    return n;
 }
 
 __global__ void adapter_zero_kernel(int32_t *p) { *p = 0; }
@@ -555,7 +581,11 @@ adapter_shrink_kernel(Tiles m, const uint16_t *__restrict__ src, const uint16_t 
     const int tile = block / (m.BM / RB), t0 = block * RB;
     if (t0 >= m.T)
         return;
-    const int cols = m.cnt[tile] * m.rp;
+    int32_t *list = reinterpret_cast<int32_t *>(lds + S::lds_bytes);
+    __shared__ uint32_t bits[kListWords];
+    __shared__ int32_t firsts[kListWords + 1];
+    const int cols = m.rp * (NN ? load_list(m, tile, list)
+                                : build_list(m, tile, list, bits, firsts, slot == 0 && t0 == tile * m.BM));
     const int chunks = shrink_chunks(cols), splits = shrink_splits(cols, slots);
     const int split = chunks >= slots ? 0 : (chunks > 0 ? slot / chunks : 0);
     if (split >= splits)
@@ -564,7 +594,6 @@ adapter_shrink_kernel(Tiles m, const uint16_t *__restrict__ src, const uint16_t 
     const int steps = (D + BK - 1) / BK;
     const int s0 = (int)((int64_t)steps * split / splits);
     const int s1 = (int)((int64_t)steps * (split + 1) / splits);
-    const int32_t *list = m.list + (int64_t)tile * m.Lmax;
     for (int chunk = chunks >= slots ? slot : (chunks > 0 ? slot % chunks : 0); chunk < chunks;
          chunk += step) {
         if (cols > 64)
@@ -727,8 +756,8 @@ adapter_project_kernel(Tiles m, const uint16_t *__restrict__ src, int D,
     const int t0 = tile * BM;
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
     const int wm = wave / WN, wn = wave % WN;
-    const int32_t *list = m.list + (int64_t)tile * m.Lmax;
-    const int cols = m.cnt[tile] * m.rp;
+    int32_t *list = reinterpret_cast<int32_t *>(lds + P::lds_bytes);
+    const int cols = load_list(m, tile, list) * m.rp;
     const uint16_t *du = dense + (int64_t)t0 * m.LW;
     P p;
     p.zero();
@@ -1220,7 +1249,7 @@ template <int RB, bool NN>
 hipError_t shrink(const AdapterPlan &p, const Tiles &m, const uint16_t *src, const uint16_t *ad,
                   int D, float *part, hipStream_t s)
 {
-    constexpr int lds_bytes = Shrink<RB, NN>::lds_bytes;
+    const int lds_bytes = Shrink<RB, NN>::lds_bytes + p.Lmax * 4;
     const hipError_t e = allow_lds(adapter_shrink_kernel<RB, NN>, lds_bytes);
     if (e != hipSuccess)
         return e;
@@ -1235,10 +1264,11 @@ hipError_t project(const AdapterPlan &p, const Tiles &m, const uint16_t *src, in
                    uint16_t *out, hipStream_t s)
 {
     typedef Product<BM, BN, WM, WN, NS, NN> P;
-    const hipError_t e = allow_lds(adapter_project_kernel<P, NN>, P::lds_bytes);
+    const int lds_bytes = P::lds_bytes + p.Lmax * 4;
+    const hipError_t e = allow_lds(adapter_project_kernel<P, NN>, lds_bytes);
     if (e != hipSuccess)
         return e;
-    adapter_project_kernel<P, NN><<<p.ntile * ((N + BN - 1) / BN), P::threads, P::lds_bytes, s>>>(
+    adapter_project_kernel<P, NN><<<p.ntile * ((N + BN - 1) / BN), P::threads, lds_bytes, s>>>(
         m, src, D, weight, N, ad, dense, p.ntile, out);
     return hipGetLastError();
 }
@@ -1344,9 +1374,9 @@ AdapterPlan make_adapter_plan(int T, int H, int O, int E, int K, int r)
     const int64_t rows = T < p.BM ? T : p.BM;
     p.Lmax = (int)(rows * K < E ? (rows * K > 0 ? rows * K : 1) : E);
     p.LW = (int)(((int64_t)p.Lmax * p.rp + kDensePad - 1) / kDensePad * kDensePad);
-    p.slots = T > 0 ? 1024 / ((T + 127) / 128) : 1;
-    if (p.slots > 16)
-        p.slots = 16;
+    // two blocks per CU, of about 6 stages at least
+    const int deep = (H > O ? H : O) / (6 * BK);
+    p.slots = T > 0 ? least(512 / ((T + 127) / 128), least(deep, 16)) : 1;
     if (p.slots < 4)
         p.slots = 4;
     const size_t entries = (size_t)T * K * r * 4;
@@ -1419,12 +1449,10 @@ hipError_t launch_adapter(const AdapterPlan &p, const uint16_t *x, const uint16_
         return hipGetLastError();
     }
     const Tiles m = make_tiles(p, idx, state);
-    adapter_tiles_kernel<<<p.ntile, 256, (size_t)p.E * 4, s>>>(m);
-    hipError_t e = hipGetLastError();
     uint16_t *dense = reinterpret_cast<uint16_t *>(state + p.off_dense);
-    if (e == hipSuccess)
-        e = gather<false>(p, m, x, p.H, a, w, scale, part, reinterpret_cast<float *>(state + p.off_u), dense,
-                          nullptr, nullptr, num_invalid, s);
+    hipError_t e = gather<false>(p, m, x, p.H, a, w, scale, part,
+                                 reinterpret_cast<float *>(state + p.off_u), dense, nullptr, nullptr,
+                                 num_invalid, s);
     if (e == hipSuccess)
         e = project_any<false>(p, m, x, p.H, weight, p.O, b, dense, out, s);
     return e;
@@ -1444,11 +1472,8 @@ hipError_t launch_adapter_backward(const AdapterPlan &p, const uint16_t *d_out, 
     uint16_t *dense = reinterpret_cast<uint16_t *>(state + p.off_dense);
     uint16_t *vdense = reinterpret_cast<uint16_t *>(ws + p.off_vdense);
     hipError_t e = hipSuccess;
-    if (p.small) {
-        adapter_tiles_kernel<<<p.ntile, 256, (size_t)p.E * 4, s>>>(m);
-        if ((e = hipGetLastError()) == hipSuccess)
-            e = gather<false>(p, m, x, p.H, a, w, scale, part, u, dense, nullptr, nullptr, nullptr, s);
-    }
+    if (p.small)
+        e = gather<false>(p, m, x, p.H, a, w, scale, part, u, dense, nullptr, nullptr, nullptr, s);
     if (e == hipSuccess && p.T > 0)
         e = gather<true>(p, m, d_out, p.O, b, w, scale, part, reinterpret_cast<float *>(ws + p.off_v),
                          vdense, u, dw, nullptr, s);

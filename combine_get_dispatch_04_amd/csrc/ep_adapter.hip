@@ -374,7 +374,7 @@ struct Product {
     }
 };
 
-__host__ __device__ __forceinline__ int least(int a, int b) { return a < b ? a : b; }
+__host__ __host__ __device__ __forceinline__ int least(int a, int b) { return a < b ? a : b; }
 
 // Blocks are dealt to the 8 XCDs in turn; this gives each XCD a run of
 // consecutive tiles, so that its L2 sees the operands they share.
@@ -1308,8 +1308,19 @@ hipError_t project_any(const AdapterPlan &p, const Tiles &m, const uint16_t *src
                        uint16_t *out, hipStream_t s)
 {
     switch (p.BM) {
-    case 64:
-        return project<64, 64, 2, 2, 4, NN>(p, m, src, D, weight, N, ad, dense, out, s);
+    case 64: {
+        // a CU takes in about 31 bytes a cycle (64 x 64: 16 KB a stage in 0.25 us, 64 x 128:
+        // 24 KB in 0.35 us), so a tile costs its rows and columns, times the most
+        // tiles a CU gets: 1001 x 4096 x 1032: 24.0 us with 64 columns, 19.4 with 128;
+        // 960 x 1024 x 4096: 18.6 and 22.9
+        auto cost = [&](int cols) {
+            const int64_t tiles = (int64_t)p.ntile * ((N + cols - 1) / cols);
+            return (tiles + 255) / 256 * (64 + cols);
+        };
+        if (cost(128) >= cost(64))
+            return project<64, 64, 2, 2, 4, NN>(p, m, src, D, weight, N, ad, dense, out, s);
+        return project<64, 128, NN ? 2 : 1, NN ? 2 : 4, 3, NN>(p, m, src, D, weight, N, ad, dense, out, s);
+    }
     case 128:
         return project<128, 128, 2, 2, 2, NN>(p, m, src, D, weight, N, ad, dense, out, s);
     }

@@ -113,10 +113,10 @@ def test_no_tokens():
     assert dx.shape == (0, 64) and dw.shape == (0, 2) and not da.any() and not db.any()
 
 
-@pytest.mark.parametrize("T,H,O,E,K,r", [(12300, 264, 280, 30, 1, 16), (6100, 2056, 2064, 12, 1, 24),
+@pytest.mark.parametrize("T,H,O,E,K,r", [(1001, 640, 2056, 9, 1, 24), (12300, 264, 280, 30, 1, 16), (6100, 2056, 2064, 12, 1, 24),
                                          (6200, 2048, 2048, 6, 2, 16)])
 def test_larger_tiles(T, H, O, E, K, r):
-    """Calls that take tiles of 128 and of 256 tokens."""
+    """Calls that take tiles of 64 x 128, of 128 and of 256 tokens."""
     say("adapter", T, H, O, E, K, r)
     c = Case(T + H + O, T, H, O, E, K, r, "requests" if K == 1 else "mixed", K > 1)
     out, h = api.adapter_project(*c.gpu(), scale=c.scale)

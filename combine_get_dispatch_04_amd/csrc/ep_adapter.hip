@@ -544,20 +544,30 @@ __device__ __forceinline__ void shrink_chunk(const Tiles &m, const uint16_t *src
                           : ld16(ad + (e * m.r + n % m.rp) * D + k0 + k);
             });
     }
+    // a lane's columns: four of one adapter per fragment, -1 where there is none
+    int e_of[P::TJ], j_of[P::TJ];
 #pragma unroll
-    for (int i = 0; i < P::TI; ++i) {
-        const int t = t0 + wave / P::WN * (P::BM / P::WM) + i * 16 + (lane & 15);
+    for (int j = 0; j < P::TJ; ++j) {
+        const int n = n0 + wave % P::WN * (P::BN / P::WN) + j * 16 + (lane >> 4) * 4;
+        j_of[j] = n % m.rp;
+        e_of[j] = n < cols && j_of[j] < m.r ? list[n / m.rp] : -1;
+    }
+    // the entries are read once each, and before the stores, which for all the
+    // compiler knows might be to them (read again for every fragment: 23 us
+    // instead of 17 at 4096 x 4096, K = 2)
+    const int ta = t0 + wave / P::WN * (P::BM / P::WM) + (lane & 15);
+    for (int k = 0; k < m.K; ++k) {
+        int named[P::TI];
 #pragma unroll
-        for (int j = 0; j < P::TJ; ++j) {
-            const int n = n0 + wave % P::WN * (P::BN / P::WN) + j * 16 + (lane >> 4) * 4;
-            const int l = n / m.rp, jj = n % m.rp;
-            if (n >= cols || jj >= m.r || t >= m.T)
-                continue;
-            const int e = list[l];
-            for (int k = 0; k < m.K; ++k)
-                if (m.idx[(int64_t)t * m.K + k] == e)
-                    *reinterpret_cast<f32x4 *>(part + (((int64_t)split * m.T + t) * m.K + k) * m.r + jj) =
-                        p.acc[i][j];
+        for (int i = 0; i < P::TI; ++i)
+            named[i] = ta + i * 16 < m.T ? m.idx[(int64_t)(ta + i * 16) * m.K + k] : -2;
+#pragma unroll
+        for (int i = 0; i < P::TI; ++i) {
+            float *o = part + (((int64_t)split * m.T + ta + i * 16) * m.K + k) * m.r;
+#pragma unroll
+            for (int j = 0; j < P::TJ; ++j)
+                if (e_of[j] >= 0 && e_of[j] == named[i])
+                    *reinterpret_cast<f32x4 *>(o + j_of[j]) = p.acc[i][j];
         }
     }
 }
@@ -620,44 +630,48 @@ adapter_gather_kernel(Tiles m, const float *__restrict__ w, float scale, int slo
     const int per = m.BM / kGatherRows;
     const int tile = blockIdx.x / per, row0 = (blockIdx.x % per) * kGatherRows;
     const int tid = threadIdx.x;
-    const int c = m.cnt[tile], cols = c * m.rp;
+    const int cols = m.cnt[tile] * m.rp;
     const int pieces = (cols + kDensePad - 1) / kDensePad * (kDensePad / 8);
     const int splits = shrink_splits(cols, slots);
-    const int32_t *list = m.list + (int64_t)tile * m.Lmax;
     const int64_t stride = (int64_t)m.T * m.K * m.r;
-    for (int i = tid; i < kGatherRows * pieces; i += 256) {
-        const int row = row0 + i / pieces, n = (i % pieces) * 8;
-        const int t = tile * m.BM + row;
+    // zeros, then the entries' own columns
+    for (int i = tid; i < kGatherRows * pieces; i += 256)
+        st16(dense + ((int64_t)tile * m.BM + row0 + i / pieces) * m.LW + i % pieces * 8, zero4());
+    __syncthreads();
+    const int per_row = m.K * (m.r / 8);
+    for (int i = tid; i < kGatherRows * per_row; i += 256) {
+        const int t = tile * m.BM + row0 + i / per_row;
+        if (t >= m.T)
+            break;
+        const int k = i % per_row / (m.r / 8), j = i % (m.r / 8) * 8;
+        const int64_t t0 = (int64_t)t * m.K, tk = t0 + k;
+        const int e = m.idx[tk];
+        if ((unsigned)e >= (unsigned)m.E)
+            continue;
+        const float *p = part + tk * m.r + j;
         f32x4 lo = {0.0f, 0.0f, 0.0f, 0.0f}, hi = lo;
-        const int l = n / m.rp, j = n % m.rp;
-        if (t < m.T && n < cols && j < m.r) {
-            const int e = list[l];
-            float coef = 0.0f;
-            bool found = false;
-            for (int k = 0; k < m.K; ++k) {
-                const int64_t tk = (int64_t)t * m.K + k;
-                if (m.idx[tk] != e)
-                    continue;
-                coef += w ? w[tk] : 1.0f;
-                if (!found) {
-                    const float *p = part + tk * m.r + j;
 #pragma unroll 8
-                    for (int q = 0; q < splits; ++q) {
-                        lo += *reinterpret_cast<const f32x4 *>(p + q * stride);
-                        hi += *reinterpret_cast<const f32x4 *>(p + q * stride + 4);
-                    }
-                    found = true;
-                }
-                float *o = sums + tk * m.r + j;
-                *reinterpret_cast<f32x4 *>(o) = lo;
-                *reinterpret_cast<f32x4 *>(o + 4) = hi;
-            }
-            if (found) {
-                lo *= scale * coef;
-                hi *= scale * coef;
-            }
+        for (int q = 0; q < splits; ++q) {
+            lo += *reinterpret_cast<const f32x4 *>(p + q * stride);
+            hi += *reinterpret_cast<const f32x4 *>(p + q * stride + 4);
         }
-        st16(dense + ((int64_t)tile * m.BM + row) * m.LW + n,
+        const int l = m.place[(int64_t)tile * m.E + e];
+        // the coefficients of all entries that name e; the first one writes
+        float coef = 0.0f;
+        bool first = true;
+        for (int o = 0; o < m.K; ++o)
+            if (m.idx[t0 + o] == e) {
+                coef += w ? w[t0 + o] : 1.0f;
+                first = first && o >= k;
+            }
+        float *o = sums + tk * m.r + j;
+        *reinterpret_cast<f32x4 *>(o) = lo;
+        *reinterpret_cast<f32x4 *>(o + 4) = hi;
+        if (!first)
+            continue;
+        lo *= scale * coef;
+        hi *= scale * coef;
+        st16(dense + (int64_t)t * m.LW + l * m.rp + j,
              u32x4{pack_bf16_any(lo[0], lo[1]), pack_bf16_any(lo[2], lo[3]), pack_bf16_any(hi[0], hi[1]),
                    pack_bf16_any(hi[2], hi[3])});
     }

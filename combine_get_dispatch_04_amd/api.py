@@ -5,6 +5,10 @@ get_dispatch_layout, dispatch, combine, low_latency_dispatch /
 low_latency_combine) and the expert-centric calls asked for in "[Feature
 Request] Support Expert-Choice Routing via Native Expert-Centric API"
 (Solution 1: dispatch_expert_choice with token_indices [E, C] and weights).
+In front of them, the router that makes topk_idx and topk_weights, with its
+balance loss and gradients (route, balance_loss, route_backward); and, over
+the same topk_idx, low-rank adapters beside a shared projection
+(adapter_project and its backward).
 
 torch only allocates device memory and supplies the current stream; every
 step runs in the HIP kernels of libep.so.  Errors from the library raise
@@ -559,7 +563,7 @@ class BalanceLoss:
     loss: torch.Tensor                         # [1] float32
     num_tokens_per_expert: torch.Tensor        # [S, E] int32: entries of topk_idx per sequence
     num_invalid: torch.Tensor                  # [2] int32: bad entries of topk_idx, bad logits
-    slope: torch.Tensor                        # [S*E + 1] float32
+    state: torch.Tensor                        # what the gradient needs of the loss (the ABI's slope)
     logits: torch.Tensor
     score: str
     seq_offsets: Optional[torch.Tensor]
@@ -623,16 +627,17 @@ def balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, *, score: str = "
     ws_bytes = N.ep_balance_workspace_bytes(T, E, S)
     if ws_bytes == 0:
         raise N.EpError("ep_balance_workspace_bytes", N.EP_ERR_INVALID_ARG)
-    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    # one allocation: the workspace, then the S*E + 1 floats of slope
+    state = torch.empty(ws_bytes + 4 * (S * E + 1), dtype=torch.uint8, device=dev)
+    ws = state.data_ptr()
     counts = torch.empty((S, E), dtype=torch.int32, device=dev)
-    slope = torch.empty(S * E + 1, dtype=torch.float32, device=dev)
     loss = torch.empty(1, dtype=torch.float32, device=dev)
     ninv = torch.empty(2, dtype=torch.int32, device=dev)
     with _on(dev):
         N.ep_balance_loss(_ptr(logits), dt, T, E, _ptr(topk_idx), K, _SCORES[score],
-                          _ptr(seq_offsets), S, float(coef), _ptr(counts), _ptr(slope),
-                          _ptr(loss), _ptr(ninv), _ptr(ws), ws_bytes, _stream(dev))
-    return BalanceLoss(loss, counts, ninv, slope, logits, score, seq_offsets)
+                          _ptr(seq_offsets), S, float(coef), _ptr(counts), ws + ws_bytes,
+                          _ptr(loss), _ptr(ninv), ws, ws_bytes, _stream(dev))
+    return BalanceLoss(loss, counts, ninv, state, logits, score, seq_offsets)
 
 
 def _router_backward(logits, score, d_w, routing, d_loss, balance):
@@ -652,13 +657,14 @@ def _router_backward(logits, score, d_w, routing, d_loss, balance):
         _need(d_loss, "d_loss", torch.float32, 1)
         if d_loss.shape[0] != 1:
             raise ValueError("d_loss must be [1]")
-        slope, seq = balance.slope, balance.seq_offsets
+        seq = balance.seq_offsets
         S = 1 if seq is None else seq.shape[0] - 1
-    _same_device(dev, d_weights=d_w, topk_idx=idx, d_loss=d_loss, slope=slope, seq_offsets=seq)
+        slope = balance.state.data_ptr() + balance.state.numel() - 4 * (S * E + 1)
+    _same_device(dev, d_weights=d_w, topk_idx=idx, d_loss=d_loss)
     d_logits = torch.empty_like(logits)
     with _on(dev):
         N.ep_router_backward(_ptr(logits), _LOGIT_DTYPES[logits.dtype], T, E, K, _SCORES[score],
-                             int(renorm), scale, _ptr(idx), _ptr(d_w), _ptr(slope), _ptr(seq), S,
+                             int(renorm), scale, _ptr(idx), _ptr(d_w), slope, _ptr(seq), S,
                              _ptr(d_loss), _ptr(d_logits), _stream(dev))
     return d_logits
 

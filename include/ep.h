@@ -533,6 +533,9 @@ size_t ep_adapter_workspace_bytes(int T, int H, int O, int E, int K, int r, int 
  *   num_invalid   [1] int32 out.
  *   state         >= ep_adapter_state_bytes bytes, 256-byte aligned: read by the
  *                 backward of this call; unused after it, or if there is none.
+ *                 (For more than 128 tokens about 2 T min(E, 256 K) (r rounded up
+ *                 to 16) bytes, a row of every adapter that a tile of 64 to 256
+ *                 tokens may name; the backward's workspace has the same again.)
  *   ws, ws_bytes  >= ep_adapter_workspace_bytes(..., 0); free after the call.
  * Constraints: H % 8 == 0, O % 8 == 0, H, O <= 2^20, r % 8 == 0, r <= 128, E <= 4096,
  * K <= 64, T*K < 2^31, ceil(T / 128) * ceil(max(H, O) / 128) < 2^23,

@@ -3,11 +3,12 @@ from the definitions in include/ep.h; and the bounds the fp32 kernels are held
 to.  numpy only.
 
 Bounds, with u = 2^-24 (half a step of fp32).  A score is exp(z - m) or
-1 / (1 + exp(-z)): the difference z - m is off by u |z - m|, which expf turns
-into the same relative error, and expf itself by 2u; a score that is not 0 in
-fp32 has z - m > -104, so `spread` = min(104, max z - min z) bounds the first
-part.  The sum over a row adds at most 64 + 6 terms one after the other (70u,
-for E = 4096), a quotient u, a factor u each.  So a probability or a weight is
+1 / (1 + exp(-z)): the difference z - m is off by u |z - m|, which the
+exponential turns into the same relative error, and the exponential itself by
+4u; a score that is not 0 in fp32 has z - m > -104, so `spread` =
+min(104, max z - min z) bounds the first part.  The sum over a row adds at most
+64 + 6 terms one after the other (70u, for E = 4096; 4u less for its own scores'
+share, which quotients cancel), its reciprocal 2u, a factor u each.  So a probability or a weight is
 off by at most (spread + 80) u of its value; TINY covers scores that leave
 the normal range of fp32.
   A gradient p (G - sum_j p_j G_j) has two such factors, products and the sum:

@@ -617,14 +617,22 @@ adapter_shrink_kernel(Tiles m, const uint16_t *__restrict__ src, const uint16_t 
 // ---------------------------------------------------------------- gather
 // Sums the splits: sums[t*K + k][r] in fp32, and the tile's dense matrix in
 // bf16 (one rounding of c times the sum: the operand of the next MFMA), zeros
-// up to the next 64 columns.  With `u` given, dw[t,k] = scale <u, sums>.
+// up to the next 64 columns; with `low`, what that rounding took away, so many
+// elements on, for the gradients of A and B.  With `u` given, dw[t,k] = scale <u, sums>.
 // A block takes 32 rows of a tile.
 constexpr int kGatherRows = 32;
+// What two values lost in their bf16 forms `v`; nothing if those are not finite.
+__device__ __forceinline__ uint32_t lower_part(float a, float b, uint32_t v)
+{
+    const float da = a - bf16_lo(v), db = b - bf16_hi(v);
+    return pack_bf16_any(fabsf(da) < __builtin_huge_valf() ? da : 0.0f,
+                         fabsf(db) < __builtin_huge_valf() ? db : 0.0f);
+}
 constexpr int kDensePad = BK;          // the project kernel takes whole stages of U
 __global__ void __launch_bounds__(256)
 adapter_gather_kernel(Tiles m, const float *__restrict__ w, float scale, int slots,
                       const float *__restrict__ part, float *__restrict__ sums,
-                      uint16_t *__restrict__ dense, const float *__restrict__ u,
+                      uint16_t *__restrict__ dense, int64_t low, const float *__restrict__ u,
                       float *__restrict__ dw, int ntile, int32_t *__restrict__ num_invalid)
 {
     const int per = m.BM / kGatherRows;
@@ -635,8 +643,12 @@ adapter_gather_kernel(Tiles m, const float *__restrict__ w, float scale, int slo
     const int splits = shrink_splits(cols, slots);
     const int64_t stride = (int64_t)m.T * m.K * m.r;
     // zeros, then the entries' own columns
-    for (int i = tid; i < kGatherRows * pieces; i += 256)
-        st16(dense + ((int64_t)tile * m.BM + row0 + i / pieces) * m.LW + i % pieces * 8, zero4());
+    for (int i = tid; i < kGatherRows * pieces; i += 256) {
+        uint16_t *o = dense + ((int64_t)tile * m.BM + row0 + i / pieces) * m.LW + i % pieces * 8;
+        st16(o, zero4());
+        if (low)
+            st16(o + low, zero4());
+    }
     __syncthreads();
     const int per_row = m.K * (m.r / 8);
     for (int i = tid; i < kGatherRows * per_row; i += 256) {
@@ -671,9 +683,13 @@ adapter_gather_kernel(Tiles m, const float *__restrict__ w, float scale, int slo
             continue;
         lo *= scale * coef;
         hi *= scale * coef;
-        st16(dense + (int64_t)t * m.LW + l * m.rp + j,
-             u32x4{pack_bf16_any(lo[0], lo[1]), pack_bf16_any(lo[2], lo[3]), pack_bf16_any(hi[0], hi[1]),
-                   pack_bf16_any(hi[2], hi[3])});
+        const u32x4 v = {pack_bf16_any(lo[0], lo[1]), pack_bf16_any(lo[2], lo[3]),
+                         pack_bf16_any(hi[0], hi[1]), pack_bf16_any(hi[2], hi[3])};
+        uint16_t *to = dense + (int64_t)t * m.LW + l * m.rp + j;
+        st16(to, v);
+        if (low)            // what the rounding took away
+            st16(to + low, u32x4{lower_part(lo[0], lo[1], v[0]), lower_part(lo[2], lo[3], v[1]),
+                                 lower_part(hi[0], hi[1], v[2]), lower_part(hi[2], hi[3], v[3])});
     }
     if (u && dw) {
         __syncthreads();        // the block's own sums are read back
@@ -865,7 +881,10 @@ adapter_project_kernel(Tiles m, const uint16_t *__restrict__ src, int D,
 // A block takes 128 columns of `big` and G = 128 / rp adapters with consecutive
 // ids, over the tiles of its split that name one of them; both operands lie
 // across and are read transposed.  64 tokens at a time, the next ones' loads in
-// flight over the MFMAs of the present ones.  With one split the result is
+// flight over the MFMAs of the present ones.  Small calls take the dense
+// matrix in two parts of bf16 (passes = 2: tiles ntile .. 2 ntile - 1 stand for
+// the lower parts): its rounding adds about as much error as the result's own
+// where many values average, and more where there are few.  With one split the result is
 // rounded and stored, else fp32 sums go to `part` (laid out like the result)
 // to be added.
 constexpr int kGradCols = 128;
@@ -878,7 +897,7 @@ struct GradJob {
     int N, splits, chunks;      // columns, splits of the tiles, blocks of 128 columns
 };
 template <bool OUTER>
-__device__ void adapter_grads(const Tiles &m, const GradJob &g, int ntile, int block, char *lds,
+__device__ void adapter_grads(const Tiles &m, const GradJob &g, int ntile, int passes, int block, char *lds,
                               int32_t *places)
 {
     const int G = kGradCols / m.rp, N = g.N;
@@ -887,8 +906,10 @@ __device__ void adapter_grads(const Tiles &m, const GradJob &g, int ntile, int b
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int wb = wave >> 1, wd = wave & 1;        // the wave's half of the big columns, of the dense ones
-    const int i0 = (int)((int64_t)ntile * split / g.splits);
-    const int i1 = (int)((int64_t)ntile * (split + 1) / g.splits);
+    const int i0 = (int)((int64_t)ntile * passes * split / g.splits);
+    const int i1 = (int)((int64_t)ntile * passes * (split + 1) / g.splits);
+    auto real = [&](int tile) { return tile < ntile ? tile : tile - ntile; };
+    auto dense_of = [&](int tile) { return tile < ntile ? g.dense : g.dense + (int64_t)ntile * m.BM * m.LW; };
     const int members = least(G, m.E - e0);
     f32x4 acc[4][4];        // [big unit][dense unit]
 #pragma unroll
@@ -907,7 +928,7 @@ __device__ void adapter_grads(const Tiles &m, const GradJob &g, int ntile, int b
                 window = tile;
                 for (int q = tid; q < kGradWindow * G; q += 256) {
                     const int at = tile + q / G;
-                    places[q] = at < i1 && q % G < members ? m.place[(int64_t)at * m.E + e0 + q % G] : -1;
+                    places[q] = at < i1 && q % G < members ? m.place[(int64_t)real(at) * m.E + e0 + q % G] : -1;
                 }
                 __syncthreads();
             }
@@ -930,9 +951,9 @@ __device__ void adapter_grads(const Tiles &m, const GradJob &g, int ntile, int b
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
             const int q = p * 256 + tid, row = r0 + q / 16, c = (q % 16) * 8;
-            const int64_t t = (int64_t)tile * m.BM + row;
+            const int64_t t = (int64_t)real(tile) * m.BM + row;
             rb[p] = t < m.T && n0 + c < N ? ld16(g.big + t * N + n0 + c) : zero4();
-            rd[p] = t < m.T && my_at >= 0 ? ld16(g.dense + t * m.LW + my_at) : zero4();
+            rd[p] = t < m.T && my_at >= 0 ? ld16(dense_of(tile) + t * m.LW + my_at) : zero4();
         }
     };
     int tile = next_tile(i0), r0 = 0, buf = 0;
@@ -964,7 +985,7 @@ __device__ void adapter_grads(const Tiles &m, const GradJob &g, int ntile, int b
             for (int d = 0; d < 4; ++d)
                 on[d] = next_on[d];
         int tile2 = tile, r2 = r0 + BK;
-        if (r2 >= m.BM || (int64_t)tile * m.BM + r2 >= m.T) {
+        if (r2 >= m.BM || (int64_t)real(tile) * m.BM + r2 >= m.T) {
             tile2 = next_tile(tile + 1);
             r2 = 0;
             if (tile2 < i1) {
@@ -1022,9 +1043,9 @@ __device__ void adapter_grads(const Tiles &m, const GradJob &g, int ntile, int b
                 // again, over the tokens that name the adapter only
                 v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                 for (int tile = i0; tile < i1; ++tile) {
-                    const int l = m.place[(int64_t)tile * m.E + e];
+                    const int l = m.place[(int64_t)real(tile) * m.E + e];
                     for (int row = 0; l >= 0 && row < m.BM; ++row) {
-                        const int64_t t = (int64_t)tile * m.BM + row;
+                        const int64_t t = (int64_t)real(tile) * m.BM + row;
                         bool named = false;
                         if (t < m.T)
                             for (int k = 0; k < m.K; ++k)
@@ -1034,7 +1055,7 @@ __device__ void adapter_grads(const Tiles &m, const GradJob &g, int ntile, int b
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const uint16_t x = g.big[t * N + bn + (OUTER ? 0 : q)];
-                            const uint16_t y = g.dense[t * m.LW + l * m.rp + j + (OUTER ? q : 0)];
+                            const uint16_t y = dense_of(tile)[t * m.LW + l * m.rp + j + (OUTER ? q : 0)];
                             v[q] = fmaf(bf16_lo(x), bf16_lo(y), v[q]);
                         }
                     }
@@ -1051,14 +1072,14 @@ __device__ void adapter_grads(const Tiles &m, const GradJob &g, int ntile, int b
 }
 // Both gradients in one launch: `blocks_a` blocks of dA's, the rest dB's.
 __global__ void __launch_bounds__(256, 2)
-adapter_grads_kernel(Tiles m, GradJob a, GradJob b, int ntile, int blocks_a)
+adapter_grads_kernel(Tiles m, GradJob a, GradJob b, int ntile, int passes, int blocks_a)
 {
     __shared__ __attribute__((aligned(16))) char lds[4 * kGradBytes];
     __shared__ int32_t places[kGradWindow * kGradCols / 16];
     if ((int)blockIdx.x < blocks_a)
-        adapter_grads<false>(m, a, ntile, blockIdx.x, lds, places);
+        adapter_grads<false>(m, a, ntile, passes, blockIdx.x, lds, places);
     else
-        adapter_grads<true>(m, b, ntile, blockIdx.x - blocks_a, lds, places);
+        adapter_grads<true>(m, b, ntile, passes, blockIdx.x - blocks_a, lds, places);
 }
 
 // The splits' sums, in split order, rounded to bf16: of dA's values, then dB's.
@@ -1332,7 +1353,8 @@ hipError_t gather(const AdapterPlan &p, const Tiles &m, const uint16_t *src, int
     if (e != hipSuccess)
         return e;
     adapter_gather_kernel<<<p.ntile * (p.BM / kGatherRows), 256, 0, s>>>(
-        m, w, scale, p.slots, part, sums, dense, u, dw, p.ntile, num_invalid);
+        m, w, scale, p.slots, part, sums, dense,
+        p.passes == 2 ? (int64_t)p.ntile * p.BM * p.LW : 0, u, dw, p.ntile, num_invalid);
     return hipGetLastError();
 }
 
@@ -1377,7 +1399,7 @@ hipError_t grads(const AdapterPlan &p, const Tiles &m, const uint16_t *x, const 
     const int blocks_b = db ? b.chunks * b.splits * groups : 0;
     if (blocks_a + blocks_b == 0)
         return hipSuccess;
-    adapter_grads_kernel<<<blocks_a + blocks_b, 256, 0, s>>>(m, a, b, p.ntile, blocks_a);
+    adapter_grads_kernel<<<blocks_a + blocks_b, 256, 0, s>>>(m, a, b, p.ntile, p.passes, blocks_a);
     const hipError_t e = hipGetLastError();
     const int64_t sum_a = da && a.splits > 1 ? elems_a : 0, sum_b = db && b.splits > 1 ? elems_b : 0;
     if (e != hipSuccess || sum_a + sum_b == 0)
@@ -1388,6 +1410,11 @@ hipError_t grads(const AdapterPlan &p, const Tiles &m, const uint16_t *x, const 
 }
 
 }  // namespace
+
+// Calls with at most this many values of A x (and of B^T d) keep them in two
+// parts for the gradients: with N of them the share of their rounding in the
+// result's error strays by about 0.8 / sqrt(N) of itself.
+constexpr int kFewValues = 4096;
 
 int adapter_grad_splits(const AdapterPlan &p, int N)
 {
@@ -1418,6 +1445,7 @@ AdapterPlan make_adapter_plan(int T, int H, int O, int E, int K, int r)
     p.ntile = (T + p.BM - 1) / p.BM;
     const int64_t rows = T < p.BM ? T : p.BM;
     p.Lmax = (int)(rows * K < E ? (rows * K > 0 ? rows * K : 1) : E);
+    p.passes = (int64_t)T * K * r <= kFewValues ? 2 : 1;
     p.LW = (int)(((int64_t)p.Lmax * p.rp + kDensePad - 1) / kDensePad * kDensePad);
     // two blocks per CU, of about 6 stages at least
     const int deep = (H > O ? H : O) / (6 * BK);
@@ -1435,7 +1463,7 @@ AdapterPlan make_adapter_plan(int T, int H, int O, int E, int K, int r)
     p.off_u = off;
     off = align256(off + entries);
     p.off_dense = off;
-    off = align256(off + (size_t)p.ntile * p.BM * p.LW * 2);
+    off = align256(off + (size_t)p.ntile * p.BM * p.LW * 2 * p.passes);
     const size_t state = off > 256 ? off : 256;
     p.small = T > 0 && T <= kSmallTokens;
     p.off_part = 0;
@@ -1464,7 +1492,7 @@ AdapterPlan make_adapter_plan(int T, int H, int O, int E, int K, int r)
     p.off_v = off;
     off = align256(off + entries);
     p.off_vdense = off;
-    off = align256(off + (size_t)p.ntile * p.BM * p.LW * 2);
+    off = align256(off + (size_t)p.ntile * p.BM * p.LW * 2 * p.passes);
     p.off_state = off;
     p.back_bytes = off + (p.small ? state : 256);
     return p;

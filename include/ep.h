@@ -511,7 +511,8 @@ ep_status_t ep_router_backward(const void *logits, ep_dtype_t dtype, int T, int 
  *                     scale * w[t,k] * B_e (A_e x_t) ),   w = 1 if topk_weights is NULL.
  * bf16 operands, fp32 sums.  scale * w * (A_e x_t) is rounded to bf16 once (it is the
  * operand of the product with B_e; an expert that a token names twice has its
- * weights summed first), and the result once; likewise the gradients below.
+ * weights summed first; calls of few tokens keep it in more bits), and the
+ * result once; likewise the gradients below.
  * An infinity or a NaN in one adapter, or in one token, stays with the tokens
  * that name the adapter, or with that token.
  */

@@ -189,6 +189,30 @@ def test_a_broken_adapter_or_token_stays_with_its_own(where, what, T, K):
             assert not torch.isfinite(out[torch.from_numpy(names).to(DEV), 7]).any()
 
 
+@pytest.mark.parametrize("T,K,r", [(1, 1, 8), (7, 1, 8), (40, 2, 16), (256, 1, 16)])
+def test_gradients_of_few_values_round_once(T, K, r):
+    """Few values of A x and B^T d: the gradients of A and B carry them in two
+    parts, so that only the result's own rounding is left, 2^-8 of it, beside
+    2^-15 of the sum of magnitudes (the lower part's half step 2^-8 of at most
+    2^-8 of a value, once more for the fp32 sums' error)."""
+    c = Case(13 + T, T, 128, 72, 3, K, r)
+    _, h = api.adapter_project(*c.gpu(), scale=c.scale)
+    _, da, db, _ = api.adapter_project_backward(c.dy.to(DEV), h)
+    _, _, saved = c.ref()
+    back = c.ref_back(saved)
+    size_a, size_b = np.zeros(c.a64.shape), np.zeros(c.b64.shape)
+    for t, e, ks, coef, cm, u, eu, ec in saved["entries"]:
+        v = c.b64[e].T @ c.dy64[t]
+        # the fp32 sums' own errors (2 n u of magnitudes, n = 128, 72) are below 2^-15 too
+        vm, um = np.abs(c.b64[e]).T @ np.abs(c.dy64[t]), np.abs(c.a64[e]) @ np.abs(c.x64[t])
+        size_a[e] += np.outer(cm * (np.abs(v) + 2.0 ** -1 * vm), np.abs(c.x64[t]))
+        size_b[e] += np.outer(np.abs(c.dy64[t]), cm * (np.abs(u) + 2.0 ** -1 * um))
+    for got, name, size in ((da, "da", size_a), (db, "db", size_b)):
+        want = back[name][0]
+        bound = 2.0 ** -15 * size
+        close(name, got, want, bound + R.H * (np.abs(want) + bound) + R.TINY)
+
+
 def test_same_bits_every_time_on_another_stream_and_for_a_second_backward():
     c = Case(5, 600, 512, 384, 12, 2, 16)
     args, dy = c.gpu(), c.dy.to(DEV)

@@ -374,7 +374,7 @@ struct Product {
     }
 };
 
-__host__ __host__ __device__ __forceinline__ int least(int a, int b) { return a < b ? a : b; }
+__host__ __device__ __forceinline__ int least(int a, int b) { return a < b ? a : b; }
 
 // Blocks are dealt to the 8 XCDs in turn; this gives each XCD a run of
 // consecutive tiles, so that its L2 sees the operands they share.
@@ -470,17 +470,19 @@ __global__ void adapter_zero_kernel(int32_t *p) { *p = 0; }
 
 // How a tile's `slots` blocks share a list of `cols` columns: chunks of 128
 // columns, or of 64 for a short list (the tokens' rows are read once per chunk);
-// blocks beyond the chunks split the inner dimension.
+// blocks beyond the chunks split the inner dimension, into `deep` parts at most.
 __device__ __forceinline__ int shrink_width(int cols) { return cols > 64 ? 128 : 64; }
 __device__ __forceinline__ int shrink_chunks(int cols)
 {
     return (cols + shrink_width(cols) - 1) / shrink_width(cols);
 }
-__device__ __forceinline__ int shrink_splits(int cols, int slots)
+__device__ __forceinline__ int shrink_splits(int cols, int slots, int deep)
 {
     const int chunks = shrink_chunks(cols);
-    return chunks >= slots ? 1 : (chunks > 0 ? slots / chunks : 1);
+    return chunks >= slots || chunks == 0 ? 1 : least(slots / chunks, deep);
 }
+// Parts of about 4 stages.
+__host__ __device__ __forceinline__ int shrink_depth(int D) { return D < 8 * BK ? 1 : D / (4 * BK); }
 
 // ---------------------------------------------------------------- shrink
 // part[split][t*K + k][r] = sum over the split's inner elements of src[t][.]
@@ -596,7 +598,7 @@ adapter_shrink_kernel(Tiles m, const uint16_t *__restrict__ src, const uint16_t 
     __shared__ int32_t firsts[kListWords + 1];
     const int cols = m.rp * (NN ? load_list(m, tile, list)
                                 : build_list(m, tile, list, bits, firsts, slot == 0 && t0 == tile * m.BM));
-    const int chunks = shrink_chunks(cols), splits = shrink_splits(cols, slots);
+    const int chunks = shrink_chunks(cols), splits = shrink_splits(cols, slots, shrink_depth(D));
     const int split = chunks >= slots ? 0 : (chunks > 0 ? slot / chunks : 0);
     if (split >= splits)
         return;
@@ -630,7 +632,7 @@ __device__ __forceinline__ uint32_t lower_part(float a, float b, uint32_t v)
 }
 constexpr int kDensePad = BK;          // the project kernel takes whole stages of U
 __global__ void __launch_bounds__(256)
-adapter_gather_kernel(Tiles m, const float *__restrict__ w, float scale, int slots,
+adapter_gather_kernel(Tiles m, const float *__restrict__ w, float scale, int slots, int deep,
                       const float *__restrict__ part, float *__restrict__ sums,
                       uint16_t *__restrict__ dense, int64_t low, const float *__restrict__ u,
                       float *__restrict__ dw, int ntile, int32_t *__restrict__ num_invalid)
@@ -640,7 +642,7 @@ adapter_gather_kernel(Tiles m, const float *__restrict__ w, float scale, int slo
     const int tid = threadIdx.x;
     const int cols = m.cnt[tile] * m.rp;
     const int pieces = (cols + kDensePad - 1) / kDensePad * (kDensePad / 8);
-    const int splits = shrink_splits(cols, slots);
+    const int splits = shrink_splits(cols, slots, deep);
     const int64_t stride = (int64_t)m.T * m.K * m.r;
     // zeros, then the entries' own columns
     for (int i = tid; i < kGatherRows * pieces; i += 256) {
@@ -1353,7 +1355,7 @@ hipError_t gather(const AdapterPlan &p, const Tiles &m, const uint16_t *src, int
     if (e != hipSuccess)
         return e;
     adapter_gather_kernel<<<p.ntile * (p.BM / kGatherRows), 256, 0, s>>>(
-        m, w, scale, p.slots, part, sums, dense,
+        m, w, scale, p.slots, shrink_depth(D), part, sums, dense,
         p.passes == 2 ? (int64_t)p.ntile * p.BM * p.LW : 0, u, dw, p.ntile, num_invalid);
     return hipGetLastError();
 }
@@ -1447,9 +1449,9 @@ AdapterPlan make_adapter_plan(int T, int H, int O, int E, int K, int r)
     p.Lmax = (int)(rows * K < E ? (rows * K > 0 ? rows * K : 1) : E);
     p.passes = (int64_t)T * K * r <= kFewValues ? 2 : 1;
     p.LW = (int)(((int64_t)p.Lmax * p.rp + kDensePad - 1) / kDensePad * kDensePad);
-    // two blocks per CU, of about 6 stages at least
-    const int deep = (H > O ? H : O) / (6 * BK);
-    p.slots = T > 0 ? least(512 / ((T + 127) / 128), least(deep, 16)) : 1;
+    // two blocks per CU
+    const int rb = p.BM == 64 ? 64 : 128;
+    p.slots = T > 0 ? least(512 / ((T + rb - 1) / rb), 64) : 1;
     if (p.slots < 4)
         p.slots = 4;
     const size_t entries = (size_t)T * K * r * 4;

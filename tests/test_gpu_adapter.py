@@ -232,6 +232,46 @@ def test_same_bits_every_time_on_another_stream_and_for_a_second_backward():
         assert torch.equal(p, q) and torch.equal(p, s)
 
 
+def test_several_threads_at_once():
+    """Calls from four host threads, each on its own stream, equal the same
+    calls one after another: the library keeps nothing between calls."""
+    import threading
+
+    import numpy as np
+    jobs = []
+    for i, (T, K) in enumerate([(3, 1), (120, 2), (400, 1), (900, 3)]):
+        c = Case(90 + i, T, 256, 192, 6, K, 16)
+        z = torch.from_numpy(np.random.default_rng(i).standard_normal((T, 64)).astype(np.float32)).to(DEV)
+        jobs.append((c.gpu(), c.dy.to(DEV), z))
+
+    def step(args, dy, z):
+        rt = api.route(z, 6)
+        bal = api.balance_loss(z, rt.topk_idx)
+        dz = api.route_backward(rt.topk_weights, rt, balance=bal, d_loss=torch.ones(1, device=DEV))
+        out, h = api.adapter_project(*args)
+        return (rt.topk_idx, rt.topk_weights, bal.loss, dz, out) + api.adapter_project_backward(dy, h)
+
+    want = [step(*j) for j in jobs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(5):
+                got = step(*jobs[i])
+                stream.synchronize()
+                if not all(torch.equal(p, q) for p, q in zip(want[i], got)):
+                    wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
 @pytest.mark.parametrize("T", [4, 300])
 def test_captured_step_replays(T):
     c = Case(6, T, 256, 192, 5, 2, 16, weights=True)

@@ -17,6 +17,7 @@ EpError (a ValueError).
 from __future__ import annotations
 
 import contextlib
+import functools
 from dataclasses import dataclass
 from typing import List, Optional
 
@@ -692,6 +693,14 @@ def balance_loss_backward(d_loss: torch.Tensor, balance: BalanceLoss) -> torch.T
 
 
 # ---------------------------------------------------------------- adapters
+@functools.lru_cache(maxsize=256)
+def _adapter_bytes(T: int, H: int, O: int, E: int, K: int, r: int):
+    """The state's and the two workspaces' bytes, which go by the sizes alone."""
+    return (N.ep_adapter_state_bytes(T, H, O, E, K, r),
+            N.ep_adapter_workspace_bytes(T, H, O, E, K, r, 0),
+            N.ep_adapter_workspace_bytes(T, H, O, E, K, r, 1))
+
+
 @dataclass
 class AdapterHandle:
     """What adapter_project_backward needs from adapter_project.  The operands
@@ -739,17 +748,21 @@ def adapter_project(x: torch.Tensor, weight: torch.Tensor, a: torch.Tensor, b: t
             raise ValueError("topk_weights must be [T, K]")
     dev = x.device
     _same_device(dev, weight=weight, a=a, b=b, topk_idx=topk_idx, topk_weights=topk_weights)
-    state_bytes = N.ep_adapter_state_bytes(T, H, O, E, K, r)
-    ws_bytes = N.ep_adapter_workspace_bytes(T, H, O, E, K, r, 0)
+    state_bytes, ws_bytes, _ = _adapter_bytes(T, H, O, E, K, r)
     out = _out(out, (T, O), dev)
     ninv = torch.empty(1, dtype=torch.int32, device=dev)
-    state = torch.empty(state_bytes, dtype=torch.uint8, device=dev)
-    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    if state_bytes <= 256:
+        # a few tokens leave no state: one allocation, kept with the handle
+        state = torch.empty(state_bytes + ws_bytes, dtype=torch.uint8, device=dev)
+        ws = state.data_ptr() + state_bytes
+    else:
+        state = torch.empty(state_bytes, dtype=torch.uint8, device=dev)
+        scratch = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        ws = scratch.data_ptr()
     with _on(dev):
         N.ep_adapter_project(_ptr(x), T, H, _ptr(weight), O, _ptr(a), _ptr(b), E, r,
                              _ptr(topk_idx), _ptr(topk_weights), K, float(scale), _ptr(out),
-                             _ptr(ninv), _ptr(state), state_bytes, _ptr(ws), ws_bytes,
-                             _stream(dev))
+                             _ptr(ninv), _ptr(state), state_bytes, ws, ws_bytes, _stream(dev))
     return out, AdapterHandle(x, weight, a, b, topk_idx, topk_weights, float(scale), ninv, state)
 
 
@@ -767,7 +780,7 @@ def adapter_project_backward(d_out: torch.Tensor, handle: AdapterHandle):
         raise ValueError(f"d_out must be {(T, O)}, got {tuple(d_out.shape)}")
     dev = x.device
     _same_device(dev, d_out=d_out)
-    ws_bytes = N.ep_adapter_workspace_bytes(T, H, O, E, K, r, 1)
+    ws_bytes = _adapter_bytes(T, H, O, E, K, r)[2]
     ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
     dx, da, db = torch.empty_like(x), torch.empty_like(a), torch.empty_like(b)
     dw = torch.empty((T, K), dtype=torch.float32, device=dev)

@@ -693,6 +693,17 @@ def balance_loss_backward(d_loss: torch.Tensor, balance: BalanceLoss) -> torch.T
 
 
 # ---------------------------------------------------------------- adapters
+def _apart(out: torch.Tensor, **inputs):
+    """Refuses an output in an input's memory: other blocks still read it."""
+    lo = out.data_ptr()
+    hi = lo + out.numel() * out.element_size()
+    for name, t in inputs.items():
+        if t is None or lo == hi:
+            continue
+        if t.data_ptr() < hi and lo < t.data_ptr() + t.numel() * t.element_size():
+            raise ValueError(f"out must not overlap {name}")
+
+
 @functools.lru_cache(maxsize=256)
 def _adapter_bytes(T: int, H: int, O: int, E: int, K: int, r: int):
     """The state's and the two workspaces' bytes, which go by the sizes alone."""
@@ -724,9 +735,9 @@ def adapter_project(x: torch.Tensor, weight: torch.Tensor, a: torch.Tensor, b: t
     e = topk_idx[t,k] (-1 = none; weights 1 if None).  One adapter per request:
     topk_idx [T, 1]; low-rank experts beside a shared one: the topk_idx and
     topk_weights of route.  x [T, H], weight [O, H], a [E, r, H], b [E, O, r],
-    all bf16; r a multiple of 8 up to 128.  -> (out [T, O] bf16,
-    AdapterHandle).  Tensors carry no autograd graph: the gradients are
-    adapter_project_backward."""
+    all bf16; r a multiple of 8 up to 128.  `out` may not overlap an operand.
+    -> (out [T, O] bf16, AdapterHandle).  Tensors carry no autograd graph: the
+    gradients are adapter_project_backward."""
     _need(x, "x", torch.bfloat16, 2)
     _need(weight, "weight", torch.bfloat16, 2)
     _need(a, "a", torch.bfloat16, 3)
@@ -749,7 +760,10 @@ def adapter_project(x: torch.Tensor, weight: torch.Tensor, a: torch.Tensor, b: t
     dev = x.device
     _same_device(dev, weight=weight, a=a, b=b, topk_idx=topk_idx, topk_weights=topk_weights)
     state_bytes, ws_bytes, _ = _adapter_bytes(T, H, O, E, K, r)
+    given = out is not None
     out = _out(out, (T, O), dev)
+    if given:
+        _apart(out, x=x, weight=weight, a=a, b=b, topk_idx=topk_idx, topk_weights=topk_weights)
     ninv = torch.empty(1, dtype=torch.int32, device=dev)
     if state_bytes <= 256:
         # a few tokens leave no state: one allocation, kept with the handle

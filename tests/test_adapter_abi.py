@@ -3,9 +3,11 @@ every call is refused by the host's checks), the sizes, and the reference's
 gradients against differences."""
 import numpy as np
 import pytest
+import torch
 
 import adapter_ref as R
 import combine_get_dispatch_04_amd._native as N
+from combine_get_dispatch_04_amd import api
 
 A, WS = 0x10000, 0x100000
 BAD, UNS, WSP = N.EP_ERR_INVALID_ARG, N.EP_ERR_UNSUPPORTED, N.EP_ERR_WORKSPACE
@@ -85,3 +87,12 @@ def test_reference_gradients_against_differences():
                 d.append(float((value()[0] * dy).sum()))
                 arr[at] -= s
             assert abs((d[0] - d[1]) / 2 - g[at]) < 1e-10 * (1 + abs(d[0]) + abs(d[1]))
+
+
+def test_an_output_inside_an_operand_is_refused():
+    buf = torch.zeros(64, 8, dtype=torch.bfloat16)
+    api._apart(buf[:32], x=buf[32:], topk_weights=None)        # neighbours
+    api._apart(buf[8:8], x=buf)                                # nothing to write
+    for out, x in ((buf, buf), (buf[:32], buf[31:]), (buf[31:], buf[:32]), (buf[8:16], buf)):
+        with pytest.raises(ValueError, match="must not overlap x"):
+            api._apart(out, topk_weights=None, x=x)

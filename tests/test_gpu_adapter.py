@@ -397,3 +397,14 @@ def test_out_argument_and_refusals():
     big_r = torch.zeros((1, 136, 64), dtype=torch.bfloat16, device=DEV)
     with pytest.raises(ValueError):
         api.adapter_project(x, W, big_r, torch.zeros((1, 64, 136), dtype=torch.bfloat16, device=DEV), idx, w)
+
+
+def test_an_output_over_an_operand_is_refused_and_nothing_written():
+    x, W, a, b, idx, w = Case(12, 10, 64, 64, 3, 2, 16).gpu()
+    before = x.clone()
+    with pytest.raises(ValueError, match="must not overlap x"):
+        api.adapter_project(x, W, a, b, idx, w, out=x)
+    with pytest.raises(ValueError, match="must not overlap weight"):
+        api.adapter_project(x, W, a, b, idx, w, out=W[:10])
+    torch.cuda.synchronize()
+    assert torch.equal(x, before)

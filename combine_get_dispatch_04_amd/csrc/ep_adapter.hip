@@ -905,11 +905,12 @@ adapter_project_kernel(Tiles m, const uint16_t *__restrict__ src, int D,
 // ids, over the tiles of its split that name one of them; both operands lie
 // across and are read transposed.  64 tokens at a time, the next ones' loads in
 // flight over the MFMAs of the present ones.  Small calls take the dense
-// matrix in two parts of bf16 (passes = 2: tiles ntile .. 2 ntile - 1 stand for
-// the lower parts): its rounding adds about as much error as the result's own
-// where many values average, and more where there are few.  With one split the result is
-// rounded and stored, else fp32 sums go to `part` (laid out like the result)
-// to be added.
+// matrix in two parts of bf16 (`low`: the lower part lies that many elements
+// on): its rounding adds about as much error as the result's own
+// where many values average, and more where there are few.  The two parts of
+// the same tokens are two steps over one fragment of `big`.  With one split the
+// result is rounded and stored, else fp32 sums go to `part` (laid out like the
+// result) to be added.
 constexpr int kGradCols = 128;
 constexpr int kGradBytes = BK * kGradCols * 2;
 constexpr int kGradWindow = 64;
@@ -920,8 +921,8 @@ struct GradJob {
     int N, splits, chunks;      // columns, splits of the tiles, blocks of 128 columns
 };
 template <bool OUTER>
-__device__ void adapter_grads(const Tiles &m, const GradJob &g, int ntile, int passes, int block, char *lds,
-                              int32_t *places)
+__device__ __forceinline__ void adapter_grads(const Tiles &m, const GradJob &g, int ntile, int64_t low, int block,
+                                              char *lds, int32_t *places)
 {
     const int G = kGradCols / m.rp, N = g.N;
     const int n0 = block % g.chunks * kGradCols;
@@ -929,10 +930,8 @@ __device__ void adapter_grads(const Tiles &m, const GradJob &g, int ntile, int p
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int wb = wave >> 1, wd = wave & 1;        // the wave's half of the big columns, of the dense ones
-    const int i0 = (int)((int64_t)ntile * passes * split / g.splits);
-    const int i1 = (int)((int64_t)ntile * passes * (split + 1) / g.splits);
-    auto real = [&](int tile) { return tile < ntile ? tile : tile - ntile; };
-    auto dense_of = [&](int tile) { return tile < ntile ? g.dense : g.dense + (int64_t)ntile * m.BM * m.LW; };
+    const int i0 = (int)((int64_t)ntile * split / g.splits);
+    const int i1 = (int)((int64_t)ntile * (split + 1) / g.splits);
     const int members = least(G, m.E - e0);
     f32x4 acc[4][4];        // [big unit][dense unit]
 #pragma unroll
@@ -951,7 +950,7 @@ __device__ void adapter_grads(const Tiles &m, const GradJob &g, int ntile, int p
                 window = tile;
                 for (int q = tid; q < kGradWindow * G; q += 256) {
                     const int at = tile + q / G;
-                    places[q] = at < i1 && q % G < members ? m.place[(int64_t)real(at) * m.E + e0 + q % G] : -1;
+                    places[q] = at < i1 && q % G < members ? m.place[(int64_t)at * m.E + e0 + q % G] : -1;
                 }
                 __syncthreads();
             }
@@ -963,7 +962,7 @@ __device__ void adapter_grads(const Tiles &m, const GradJob &g, int ntile, int p
         }
         return tile;
     };
-    u32x4 rb[4], rd[4];
+    u32x4 rb[4], rd[4], rl[4] = {zero4(), zero4(), zero4(), zero4()};
     int my_at = -1;         // dense columns of the thread's pieces, -1 if not in this tile's list
     auto load_at = [&](int tile) {
         const int c = tid % 16 * 8, q = c / m.rp;
@@ -974,15 +973,24 @@ __device__ void adapter_grads(const Tiles &m, const GradJob &g, int ntile, int p
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
             const int q = p * 256 + tid, row = r0 + q / 16, c = (q % 16) * 8;
-            const int64_t t = (int64_t)real(tile) * m.BM + row;
+            const int64_t t = (int64_t)tile * m.BM + row;
             rb[p] = t < m.T && n0 + c < N ? ld16(g.big + t * N + n0 + c) : zero4();
-            rd[p] = t < m.T && my_at >= 0 ? ld16(dense_of(tile) + t * m.LW + my_at) : zero4();
+            rd[p] = t < m.T && my_at >= 0 ? ld16(g.dense + t * m.LW + my_at) : zero4();
+        }
+    };
+    auto load_low = [&](int tile, int r0) {
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const int64_t t = (int64_t)tile * m.BM + r0 + (p * 256 + tid) / 16;
+            rl[p] = t < m.T && my_at >= 0 ? ld16(g.dense + low + t * m.LW + my_at) : zero4();
         }
     };
     int tile = next_tile(i0), r0 = 0, buf = 0;
     if (tile < i1) {
         load_at(tile);
         load(tile, 0);
+        if (low)
+            load_low(tile, 0);
     }
     // which of the wave's units the present tile has, and the next one
     bool on[4] = {false, false, false, false}, next_on[4];
@@ -995,20 +1003,25 @@ __device__ void adapter_grads(const Tiles &m, const GradJob &g, int ntile, int p
     };
     if (tile < i1)
         load_on(tile);
-    while (tile < i1) {
-        char *lb = lds + buf * 2 * kGradBytes, *ld = lb + kGradBytes;
+    // LDS: two buffers of `big`, by turns, then the upper and the lower part
+    char *const l_hi = lds + 2 * kGradBytes, *const l_lo = l_hi + kGradBytes;
+    auto put = [&](char *to, const u32x4 (&v)[4]) {
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
             const int q = p * 256 + tid, k = q / 16, c = q % 16;
-            *reinterpret_cast<u32x4 *>(lb + off_n(k, c >> 1) + (c & 1) * 16) = rb[p];
-            *reinterpret_cast<u32x4 *>(ld + off_n(k, c >> 1) + (c & 1) * 16) = rd[p];
+            *reinterpret_cast<u32x4 *>(to + off_n(k, c >> 1) + (c & 1) * 16) = v[p];
         }
+    };
+    while (tile < i1) {
+        char *lb = lds + buf * kGradBytes;
+        put(lb, rb);
+        put(l_hi, rd);
         if (r0 == 0)
 #pragma unroll
             for (int d = 0; d < 4; ++d)
                 on[d] = next_on[d];
         int tile2 = tile, r2 = r0 + BK;
-        if (r2 >= m.BM || (int64_t)real(tile) * m.BM + r2 >= m.T) {
+        if (r2 >= m.BM || (int64_t)tile * m.BM + r2 >= m.T) {
             tile2 = next_tile(tile + 1);
             r2 = 0;
             if (tile2 < i1) {
@@ -1019,12 +1032,8 @@ __device__ void adapter_grads(const Tiles &m, const GradJob &g, int ntile, int p
         if (tile2 < i1)
             load(tile2, r2);
         __syncthreads();
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            bf16x8 fb[4];
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-                fb[b] = frag_n(lb, ks, at_n(wb * 4 + b, lane));
+        bf16x8 fb0[4], fb1[4];
+        auto multiply = [&](const char *ld, int ks, const bf16x8 (&fb)[4]) {
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
                 if (!on[d])
@@ -1034,8 +1043,27 @@ __device__ void adapter_grads(const Tiles &m, const GradJob &g, int ntile, int p
                 for (int b = 0; b < 4; ++b)
                     acc[b][d] = OUTER ? mfma(fd, fb[b], acc[b][d]) : mfma(fb[b], fd, acc[b][d]);
             }
+        };
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            fb0[b] = frag_n(lb, 0, at_n(wb * 4 + b, lane));
+            fb1[b] = frag_n(lb, 1, at_n(wb * 4 + b, lane));
         }
-        // one barrier a step: the other buffer is written while this one is read
+        multiply(l_hi, 0, fb0);
+        multiply(l_hi, 1, fb1);
+        // one barrier a step: what a step writes was read two steps ago at the
+        // latest (`big` by turns, the upper and the lower part one step each;
+        // without a lower part the step is only its barrier)
+        if (low) {
+            put(l_lo, rl);
+            if (tile2 < i1)
+                load_low(tile2, r2);
+        }
+        __syncthreads();
+        if (low) {
+            multiply(l_lo, 0, fb0);
+            multiply(l_lo, 1, fb1);
+        }
         tile = tile2;
         r0 = r2;
         buf ^= 1;
@@ -1066,9 +1094,9 @@ __device__ void adapter_grads(const Tiles &m, const GradJob &g, int ntile, int p
                 // again, over the tokens that name the adapter only
                 v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                 for (int tile = i0; tile < i1; ++tile) {
-                    const int l = m.place[(int64_t)real(tile) * m.E + e];
+                    const int l = m.place[(int64_t)tile * m.E + e];
                     for (int row = 0; l >= 0 && row < m.BM; ++row) {
-                        const int64_t t = (int64_t)real(tile) * m.BM + row;
+                        const int64_t t = (int64_t)tile * m.BM + row;
                         bool named = false;
                         if (t < m.T)
                             for (int k = 0; k < m.K; ++k)
@@ -1077,9 +1105,11 @@ __device__ void adapter_grads(const Tiles &m, const GradJob &g, int ntile, int p
                             continue;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
+                            // both parts in one factor (exact): an infinity times each
+                            // alone could be two of opposite signs
                             const uint16_t x = g.big[t * N + bn + (OUTER ? 0 : q)];
-                            const uint16_t y = dense_of(tile)[t * m.LW + l * m.rp + j + (OUTER ? q : 0)];
-                            v[q] = fmaf(bf16_lo(x), bf16_lo(y), v[q]);
+                            const uint16_t *y = g.dense + t * m.LW + l * m.rp + j + (OUTER ? q : 0);
+                            v[q] = fmaf(bf16_lo(x), bf16_lo(*y) + (low ? bf16_lo(y[low]) : 0.0f), v[q]);
                         }
                     }
                 }
@@ -1095,14 +1125,14 @@ __device__ void adapter_grads(const Tiles &m, const GradJob &g, int ntile, int p
 }
 // Both gradients in one launch: `blocks_a` blocks of dA's, the rest dB's.
 __global__ void __launch_bounds__(256, 2)
-adapter_grads_kernel(Tiles m, GradJob a, GradJob b, int ntile, int passes, int blocks_a)
+adapter_grads_kernel(Tiles m, GradJob a, GradJob b, int ntile, int64_t low, int blocks_a)
 {
     __shared__ __attribute__((aligned(16))) char lds[4 * kGradBytes];
     __shared__ int32_t places[kGradWindow * kGradCols / 16];
     if ((int)blockIdx.x < blocks_a)
-        adapter_grads<false>(m, a, ntile, passes, blockIdx.x, lds, places);
+        adapter_grads<false>(m, a, ntile, low, blockIdx.x, lds, places);
     else
-        adapter_grads<true>(m, b, ntile, passes, blockIdx.x - blocks_a, lds, places);
+        adapter_grads<true>(m, b, ntile, low, blockIdx.x - blocks_a, lds, places);
 }
 
 // The splits' sums, in split order, rounded to bf16: of dA's values, then dB's.
@@ -1315,6 +1345,9 @@ Tiles make_tiles(const AdapterPlan &p, const int32_t *idx, char *state)
     return m;
 }
 
+// Where the lower part of a dense matrix lies behind the upper one, 0 if there is none.
+int64_t low_part(const AdapterPlan &p) { return p.passes == 2 ? (int64_t)p.ntile * p.BM * p.LW : 0; }
+
 // More than 64 KB of shared memory need the attribute.
 template <typename F>
 hipError_t allow_lds(F *kernel, int bytes)
@@ -1379,7 +1412,7 @@ hipError_t gather(const AdapterPlan &p, const Tiles &m, const uint16_t *src, int
         return e;
     adapter_gather_kernel<<<p.ntile * (p.BM / kGatherRows), 256, 0, s>>>(
         m, w, scale, p.slots, shrink_depth(D), part, sums, dense,
-        p.passes == 2 ? (int64_t)p.ntile * p.BM * p.LW : 0, u, dw, p.ntile, num_invalid);
+        low_part(p), u, dw, p.ntile, num_invalid);
     return hipGetLastError();
 }
 
@@ -1427,7 +1460,7 @@ hipError_t grads(const AdapterPlan &p, const Tiles &m, const uint16_t *x, const 
     const int blocks_b = db ? b.chunks * b.splits * groups : 0;
     if (blocks_a + blocks_b == 0)
         return hipSuccess;
-    adapter_grads_kernel<<<blocks_a + blocks_b, 256, 0, s>>>(m, a, b, p.ntile, p.passes, blocks_a);
+    adapter_grads_kernel<<<blocks_a + blocks_b, 256, 0, s>>>(m, a, b, p.ntile, low_part(p), blocks_a);
     const hipError_t e = hipGetLastError();
     const int64_t sum_a = da && a.splits > 1 ? elems_a : 0, sum_b = db && b.splits > 1 ? elems_b : 0;
     if (e != hipSuccess || sum_a + sum_b == 0)

@@ -6,12 +6,20 @@
 //
 // Tokens go in tiles of BM.  A tile's list holds the adapters that its tokens
 // name, ascending; its dense matrix U holds in row t, columns l*rp .. l*rp+r-1,
-// the bf16 of c * (A_e x_t) for the l-th adapter of the list, 0 where the
+// c * (A_e x_t) for the l-th adapter of the list, 0 where the
 // token does not name it (rp = r rounded up to 16, c summed over the entries
 // that name it).  So the adapters' part of a tile is one more stretch of the
 // inner dimension of the projection's own matrix product, over U and the
 // list's B, and the gradients of A and B are products of U's and V's columns
 // with the tile's rows of d and x.
+//
+// U and V are the operands of MFMAs, but not the caller's values: one rounding
+// to bf16 (2^-8 of a value) would be as large as the result's own, and 1.4 times the
+// gradients' error.  So they are two matrices of bf16 each, a value's
+// nearest and what that left over, together within 2^-16 of it; a product with
+// them is one with each.  At 4096 x 4096 x 4096, 2 of 8 adapters of rank 16,
+// the second one costs 6 and 7 us of the two projections' 129 and 141, and 12 of
+// the gradients' 41.
 //
 //   shrink     the lists, and every adapter's place in them; A_e x_t (or B_e^T d_t)
 //              of every entry, MFMA over the list's rows, the inner dimension split
@@ -392,6 +400,7 @@ struct Tiles {
     int32_t *list;              // [ntile, Lmax]
     int32_t *place;             // [ntile, E] place in the list, or -1
     int32_t *bad;               // [ntile] invalid entries
+    int64_t low;                // a dense matrix's lower part, so many elements behind the upper one
 };
 
 __device__ __forceinline__ u32x4 zero4() { return u32x4{0u, 0u, 0u, 0u}; }
@@ -617,10 +626,8 @@ adapter_shrink_kernel(Tiles m, const uint16_t *__restrict__ src, const uint16_t 
 }
 
 // ---------------------------------------------------------------- gather
-// Sums the splits: sums[t*K + k][r] in fp32, and the tile's dense matrix in
-// bf16 (one rounding of c times the sum: the operand of the next MFMA), zeros
-// up to the next 64 columns; with `low`, what that rounding took away, so many
-// elements on, for the gradients of A and B.  With `u` given, dw[t,k] = scale <u, sums>.
+// Sums the splits: sums[t*K + k][r] in fp32, and both parts of the tile's dense
+// matrix, zeros up to the next 64 columns.  With `u` given, dw[t,k] = scale <u, sums>.
 // A block takes 32 rows of a tile.  Latency: three loads one after the other (5 to 6 us).
 constexpr int kGatherRows = 32;
 // What two values lost in their bf16 forms `v`; nothing if those are not finite.
@@ -634,7 +641,7 @@ constexpr int kDensePad = BK;          // the project kernel takes whole stages 
 __global__ void __launch_bounds__(256)
 adapter_gather_kernel(Tiles m, const float *__restrict__ w, float scale, int slots, int deep,
                       const float *__restrict__ part, float *__restrict__ sums,
-                      uint16_t *__restrict__ dense, int64_t low, const float *__restrict__ u,
+                      uint16_t *__restrict__ dense, const float *__restrict__ u,
                       float *__restrict__ dw, int ntile, int32_t *__restrict__ num_invalid)
 {
     const int per = m.BM / kGatherRows;
@@ -648,8 +655,7 @@ adapter_gather_kernel(Tiles m, const float *__restrict__ w, float scale, int slo
     for (int i = tid; i < kGatherRows * pieces; i += 256) {
         uint16_t *o = dense + ((int64_t)tile * m.BM + row0 + i / pieces) * m.LW + i % pieces * 8;
         st16(o, zero4());
-        if (low)
-            st16(o + low, zero4());
+        st16(o + m.low, zero4());
     }
     __syncthreads();
     const int per_row = m.K * (m.r / 8);
@@ -689,9 +695,8 @@ adapter_gather_kernel(Tiles m, const float *__restrict__ w, float scale, int slo
                          pack_bf16_any(hi[0], hi[1]), pack_bf16_any(hi[2], hi[3])};
         uint16_t *to = dense + (int64_t)t * m.LW + l * m.rp + j;
         st16(to, v);
-        if (low)            // what the rounding took away
-            st16(to + low, u32x4{lower_part(lo[0], lo[1], v[0]), lower_part(lo[2], lo[3], v[1]),
-                                 lower_part(hi[0], hi[1], v[2]), lower_part(hi[2], hi[3], v[3])});
+        st16(to + m.low, u32x4{lower_part(lo[0], lo[1], v[0]), lower_part(lo[2], lo[3], v[1]),
+                               lower_part(hi[0], hi[1], v[2]), lower_part(hi[2], hi[3], v[3])});
     }
     if (u && dw) {
         __syncthreads();        // the block's own sums are read back
@@ -736,7 +741,9 @@ adapter_gather_kernel(Tiles m, const float *__restrict__ w, float scale, int slo
 
 // The adapters' part of 16 tokens (lane & 15: token t with its row u of U) by
 // columns c .. c+15, one adapter at a time, each for the tokens that name it
-// only: where the sum over U is not finite.
+// only: where the sum over U is not finite.  A sum over the upper part that is not
+// finite stands alone: the lower part may have other signs, and infinities of
+// both would be a NaN.
 template <bool NN>
 __device__ __forceinline__ f32x4 adapters_apart(const Tiles &m, const int32_t *list, int n_list,
                                                 const uint16_t *u, int t, const uint16_t *ad, int N,
@@ -750,13 +757,14 @@ __device__ __forceinline__ f32x4 adapters_apart(const Tiles &m, const int32_t *l
         bool named = false;
         for (int k = 0; t < m.T && k < m.K; ++k)
             named = named || m.idx[(int64_t)t * m.K + k] == (int)e;
-        f32x4 one = {0.0f, 0.0f, 0.0f, 0.0f};
+        f32x4 one = {0.0f, 0.0f, 0.0f, 0.0f}, rest = one;
 #pragma unroll 1
         for (int k0 = 0; k0 < m.rp; k0 += 32) {
             const int k = k0 + (lane >> 4) * 8;
-            u32x4 fu = zero4(), fa = zero4();
+            u32x4 fu = zero4(), fl = zero4(), fa = zero4();
             if (k < m.r) {
                 fu = ld16(u + l * m.rp + k);
+                fl = ld16(u + m.low + l * m.rp + k);
                 if (n < N) {
                     if constexpr (NN) {
                         const uint16_t *a = ad + (e * m.r + k) * N + n;
@@ -769,9 +777,12 @@ __device__ __forceinline__ f32x4 adapters_apart(const Tiles &m, const int32_t *l
                 }
             }
             one = mfma(__builtin_bit_cast(bf16x8, fa), __builtin_bit_cast(bf16x8, fu), one);
+            rest = mfma(__builtin_bit_cast(bf16x8, fa), __builtin_bit_cast(bf16x8, fl), rest);
         }
-        if (named)
-            sum += one;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (named)
+                sum[q] += fabsf(one[q]) < __builtin_huge_valf() ? one[q] + rest[q] : one[q];
     }
     return sum;
 }
@@ -811,12 +822,13 @@ adapter_project_kernel(Tiles m, const uint16_t *__restrict__ src, int D,
         }
         const int whole = BK / m.rp, rest = BK % m.rp, n_list = cols / m.rp;
         int k0 = 0;
-        p.run(lds, (cols + BK - 1) / BK, [&](char *buf, int i) {
+        int64_t part = 0;       // every stage with the upper part, then with the lower one
+        p.run(lds, (cols + BK - 1) / BK * 2, [&](char *buf, int i) {
             P::fetch(
                 buf, i,
                 [&](int i) {
                     const int q = i * P::threads + tid;
-                    return du + (int64_t)P::row_of(q) * m.LW + k0 + P::k_of(q);
+                    return du + part + (int64_t)P::row_of(q) * m.LW + k0 + P::k_of(q);
                 },
                 [&](int i) {
                     const int q = i * P::threads + tid;
@@ -826,6 +838,9 @@ adapter_project_kernel(Tiles m, const uint16_t *__restrict__ src, int D,
                               : ad + (e * N + least(n0 + P::row_of(q), N - 1)) * m.r + c;
                 });
         }, [&] {
+            part = part ? 0 : m.low;
+            if (part)
+                return;
             k0 += BK;
 #pragma unroll
             for (int i = 0; i < P::PB; ++i) {
@@ -904,13 +919,10 @@ adapter_project_kernel(Tiles m, const uint16_t *__restrict__ src, int D,
 // A block takes 128 columns of `big` and G = 128 / rp adapters with consecutive
 // ids, over the tiles of its split that name one of them; both operands lie
 // across and are read transposed.  64 tokens at a time, the next ones' loads in
-// flight over the MFMAs of the present ones.  Small calls take the dense
-// matrix in two parts of bf16 (`low`: the lower part lies that many elements
-// on): its rounding adds about as much error as the result's own
-// where many values average, and more where there are few.  The two parts of
-// the same tokens are two steps over one fragment of `big`.  With one split the
-// result is rounded and stored, else fp32 sums go to `part` (laid out like the
-// result) to be added.
+// flight over the MFMAs of the present ones.  The two parts of the dense matrix
+// are two steps over one fragment of `big`.  With one split the result is
+// rounded and stored, else fp32 sums go to `part` (laid out like the result)
+// to be added.
 constexpr int kGradCols = 128;
 constexpr int kGradBytes = BK * kGradCols * 2;
 constexpr int kGradWindow = 64;
@@ -921,8 +933,8 @@ struct GradJob {
     int N, splits, chunks;      // columns, splits of the tiles, blocks of 128 columns
 };
 template <bool OUTER>
-__device__ __forceinline__ void adapter_grads(const Tiles &m, const GradJob &g, int ntile, int64_t low, int block,
-                                              char *lds, int32_t *places)
+__device__ __forceinline__ void adapter_grads(const Tiles &m, const GradJob &g, int ntile, int block, char *lds,
+                                              int32_t *places)
 {
     const int G = kGradCols / m.rp, N = g.N;
     const int n0 = block % g.chunks * kGradCols;
@@ -962,7 +974,7 @@ __device__ __forceinline__ void adapter_grads(const Tiles &m, const GradJob &g, 
         }
         return tile;
     };
-    u32x4 rb[4], rd[4], rl[4] = {zero4(), zero4(), zero4(), zero4()};
+    u32x4 rb[4], rd[4], rl[4];
     int my_at = -1;         // dense columns of the thread's pieces, -1 if not in this tile's list
     auto load_at = [&](int tile) {
         const int c = tid % 16 * 8, q = c / m.rp;
@@ -982,15 +994,14 @@ __device__ __forceinline__ void adapter_grads(const Tiles &m, const GradJob &g, 
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
             const int64_t t = (int64_t)tile * m.BM + r0 + (p * 256 + tid) / 16;
-            rl[p] = t < m.T && my_at >= 0 ? ld16(g.dense + low + t * m.LW + my_at) : zero4();
+            rl[p] = t < m.T && my_at >= 0 ? ld16(g.dense + m.low + t * m.LW + my_at) : zero4();
         }
     };
     int tile = next_tile(i0), r0 = 0, buf = 0;
     if (tile < i1) {
         load_at(tile);
         load(tile, 0);
-        if (low)
-            load_low(tile, 0);
+        load_low(tile, 0);
     }
     // which of the wave's units the present tile has, and the next one
     bool on[4] = {false, false, false, false}, next_on[4];
@@ -1052,18 +1063,13 @@ __device__ __forceinline__ void adapter_grads(const Tiles &m, const GradJob &g, 
         multiply(l_hi, 0, fb0);
         multiply(l_hi, 1, fb1);
         // one barrier a step: what a step writes was read two steps ago at the
-        // latest (`big` by turns, the upper and the lower part one step each;
-        // without a lower part the step is only its barrier)
-        if (low) {
-            put(l_lo, rl);
-            if (tile2 < i1)
-                load_low(tile2, r2);
-        }
+        // latest (`big` by turns, the upper and the lower part one step each)
+        put(l_lo, rl);
+        if (tile2 < i1)
+            load_low(tile2, r2);
         __syncthreads();
-        if (low) {
-            multiply(l_lo, 0, fb0);
-            multiply(l_lo, 1, fb1);
-        }
+        multiply(l_lo, 0, fb0);
+        multiply(l_lo, 1, fb1);
         tile = tile2;
         r0 = r2;
         buf ^= 1;
@@ -1109,7 +1115,7 @@ __device__ __forceinline__ void adapter_grads(const Tiles &m, const GradJob &g, 
                             // alone could be two of opposite signs
                             const uint16_t x = g.big[t * N + bn + (OUTER ? 0 : q)];
                             const uint16_t *y = g.dense + t * m.LW + l * m.rp + j + (OUTER ? q : 0);
-                            v[q] = fmaf(bf16_lo(x), bf16_lo(*y) + (low ? bf16_lo(y[low]) : 0.0f), v[q]);
+                            v[q] = fmaf(bf16_lo(x), bf16_lo(*y) + bf16_lo(y[m.low]), v[q]);
                         }
                     }
                 }
@@ -1125,14 +1131,14 @@ __device__ __forceinline__ void adapter_grads(const Tiles &m, const GradJob &g, 
 }
 // Both gradients in one launch: `blocks_a` blocks of dA's, the rest dB's.
 __global__ void __launch_bounds__(256, 2)
-adapter_grads_kernel(Tiles m, GradJob a, GradJob b, int ntile, int64_t low, int blocks_a)
+adapter_grads_kernel(Tiles m, GradJob a, GradJob b, int ntile, int blocks_a)
 {
     __shared__ __attribute__((aligned(16))) char lds[4 * kGradBytes];
     __shared__ int32_t places[kGradWindow * kGradCols / 16];
     if ((int)blockIdx.x < blocks_a)
-        adapter_grads<false>(m, a, ntile, low, blockIdx.x, lds, places);
+        adapter_grads<false>(m, a, ntile, blockIdx.x, lds, places);
     else
-        adapter_grads<true>(m, b, ntile, low, blockIdx.x - blocks_a, lds, places);
+        adapter_grads<true>(m, b, ntile, blockIdx.x - blocks_a, lds, places);
 }
 
 // The splits' sums, in split order, rounded to bf16: of dA's values, then dB's.
@@ -1337,6 +1343,7 @@ Tiles make_tiles(const AdapterPlan &p, const int32_t *idx, char *state)
     m.BM = p.BM;
     m.Lmax = p.Lmax;
     m.LW = p.LW;
+    m.low = (int64_t)p.ntile * p.BM * p.LW;
     m.idx = idx;
     m.cnt = reinterpret_cast<int32_t *>(state + p.off_cnt);
     m.bad = m.cnt + p.ntile;
@@ -1344,9 +1351,6 @@ Tiles make_tiles(const AdapterPlan &p, const int32_t *idx, char *state)
     m.place = reinterpret_cast<int32_t *>(state + p.off_place);
     return m;
 }
-
-// Where the lower part of a dense matrix lies behind the upper one, 0 if there is none.
-int64_t low_part(const AdapterPlan &p) { return p.passes == 2 ? (int64_t)p.ntile * p.BM * p.LW : 0; }
 
 // More than 64 KB of shared memory need the attribute.
 template <typename F>
@@ -1412,7 +1416,7 @@ hipError_t gather(const AdapterPlan &p, const Tiles &m, const uint16_t *src, int
         return e;
     adapter_gather_kernel<<<p.ntile * (p.BM / kGatherRows), 256, 0, s>>>(
         m, w, scale, p.slots, shrink_depth(D), part, sums, dense,
-        low_part(p), u, dw, p.ntile, num_invalid);
+        u, dw, p.ntile, num_invalid);
     return hipGetLastError();
 }
 
@@ -1460,7 +1464,7 @@ hipError_t grads(const AdapterPlan &p, const Tiles &m, const uint16_t *x, const 
     const int blocks_b = db ? b.chunks * b.splits * groups : 0;
     if (blocks_a + blocks_b == 0)
         return hipSuccess;
-    adapter_grads_kernel<<<blocks_a + blocks_b, 256, 0, s>>>(m, a, b, p.ntile, low_part(p), blocks_a);
+    adapter_grads_kernel<<<blocks_a + blocks_b, 256, 0, s>>>(m, a, b, p.ntile, blocks_a);
     const hipError_t e = hipGetLastError();
     const int64_t sum_a = da && a.splits > 1 ? elems_a : 0, sum_b = db && b.splits > 1 ? elems_b : 0;
     if (e != hipSuccess || sum_a + sum_b == 0)
@@ -1471,11 +1475,6 @@ hipError_t grads(const AdapterPlan &p, const Tiles &m, const uint16_t *x, const 
 }
 
 }  // namespace
-
-// Calls with at most this many values of A x (and of B^T d) keep them in two
-// parts for the gradients: with N of them the share of their rounding in the
-// result's error strays by about 0.8 / sqrt(N) of itself.
-constexpr int kFewValues = 4096;
 
 int adapter_grad_splits(const AdapterPlan &p, int N)
 {
@@ -1506,7 +1505,6 @@ AdapterPlan make_adapter_plan(int T, int H, int O, int E, int K, int r)
     p.ntile = (T + p.BM - 1) / p.BM;
     const int64_t rows = T < p.BM ? T : p.BM;
     p.Lmax = (int)(rows * K < E ? (rows * K > 0 ? rows * K : 1) : E);
-    p.passes = (int64_t)T * K * r <= kFewValues ? 2 : 1;
     p.LW = (int)(((int64_t)p.Lmax * p.rp + kDensePad - 1) / kDensePad * kDensePad);
     // two blocks per CU
     const int rb = p.BM == 64 ? 64 : 128;
@@ -1524,7 +1522,7 @@ AdapterPlan make_adapter_plan(int T, int H, int O, int E, int K, int r)
     p.off_u = off;
     off = align256(off + entries);
     p.off_dense = off;
-    off = align256(off + (size_t)p.ntile * p.BM * p.LW * 2 * p.passes);
+    off = align256(off + (size_t)p.ntile * p.BM * p.LW * 2 * 2);
     const size_t state = off > 256 ? off : 256;
     p.small = T > 0 && T <= kSmallTokens;
     p.off_part = 0;
@@ -1553,7 +1551,7 @@ AdapterPlan make_adapter_plan(int T, int H, int O, int E, int K, int r)
     p.off_v = off;
     off = align256(off + entries);
     p.off_vdense = off;
-    off = align256(off + (size_t)p.ntile * p.BM * p.LW * 2 * p.passes);
+    off = align256(off + (size_t)p.ntile * p.BM * p.LW * 2 * 2);
     p.off_state = off;
     p.back_bytes = off + (p.small ? state : 256);
     return p;

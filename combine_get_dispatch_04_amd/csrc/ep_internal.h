@@ -136,7 +136,6 @@ struct AdapterPlan {
     int rp;           // r rounded up to 16
     int BM, ntile;    // tokens per tile, tiles
     int Lmax, LW;     // adapters a tile can name, columns of its dense matrix
-    int passes;       // parts of the dense matrix that the gradients take
     int slots;        // blocks that share a tile's shrink
     bool small;       // a few tokens: two launches, no tiles
     int wsplits, usplits;   // splits of the inner dimension then, for W x and A x

@@ -509,10 +509,11 @@ ep_status_t ep_router_backward(const void *logits, ep_dtype_t dtype, int T, int 
  * router's choice (K > 1, its topk_idx and topk_weights):
  *   out[t, :] = bf16( W x_t + sum over k with e = topk_idx[t,k] in [0, E) of
  *                     scale * w[t,k] * B_e (A_e x_t) ),   w = 1 if topk_weights is NULL.
- * bf16 operands, fp32 sums.  scale * w * (A_e x_t) is rounded to bf16 once (it is the
- * operand of the product with B_e; an expert that a token names twice has its
- * weights summed first; calls of few tokens keep it in more bits), and the
- * result once; likewise the gradients below.
+ * bf16 operands, fp32 sums.  The result is rounded to bf16 once; likewise the
+ * gradients below.  In between, scale * w * (A_e x_t) goes into its product with
+ * B_e within 2^-16 of its value (as two bf16; an expert that a token names
+ * twice has its weights summed first), or in fp32 for up to 128 tokens;
+ * scale * w * (B_e^T d_t) of the gradients within 2^-16, for any number.
  * An infinity or a NaN in one adapter, or in one token, stays with the tokens
  * that name the adapter, or with that token.
  */
@@ -534,7 +535,7 @@ size_t ep_adapter_workspace_bytes(int T, int H, int O, int E, int K, int r, int 
  *   num_invalid   [1] int32 out.
  *   state         >= ep_adapter_state_bytes bytes, 256-byte aligned: read by the
  *                 backward of this call; unused after it, or if there is none.
- *                 (For more than 128 tokens about 2 T min(E, 256 K) (r rounded up
+ *                 (For more than 128 tokens about 4 T min(E, 256 K) (r rounded up
  *                 to 16) bytes, a row of every adapter that a tile of 64 to 256
  *                 tokens may name; the backward's workspace has the same again.)
  *   ws, ws_bytes  >= ep_adapter_workspace_bytes(..., 0); free after the call.

@@ -6,7 +6,8 @@ bf16 values are exact in fp32; a sum of n of them in any order is off by at
 most 2 n u of the sum of their magnitudes (the factor 2 for the matrix
 instructions, whose inner additions need not round to nearest).  scale * w *
 (A_e x_t) has, besides the fp32 sum's error, three products (3u) and one
-rounding to bf16 (h of its value).  A result in bf16 is rounded once more.
+rounding to bf16 (`carried` = h of its value; two parts of bf16 leave h * h).
+A result in bf16 is rounded once more.
 Each quantity below comes with `mag`, the same sum over magnitudes.
 """
 import numpy as np
@@ -16,7 +17,7 @@ H = 2.0 ** -8
 TINY = 2.0 ** -120
 
 
-def forward(x, W, a, b, idx, w, scale):
+def forward(x, W, a, b, idx, w, scale, carried=H):
     """-> out, bound, and what the backward needs."""
     T, K = idx.shape
     E = a.shape[0]
@@ -37,14 +38,14 @@ def forward(x, W, a, b, idx, w, scale):
             u, um = a[e] @ x[t], np.abs(a[e]) @ np.abs(x[t])
             eu = 2 * D * U * um                                    # fp32 sum
             ec = abs(c) * eu + cm * (3 + len(ks)) * U * np.abs(u)     # times the coefficient
-            ec = ec + H * (np.abs(c * u) + ec)                     # rounded to bf16
+            ec = ec + carried * (np.abs(c * u) + ec)               # rounded to bf16
             out[t] += b[e] @ (c * u)
             bound[t] += np.abs(b[e]) @ (ec + 2 * (D + r * K + 64) * U * np.abs(c * u))
             saved["entries"].append((t, e, ks, c, cm, u, eu, ec))
     return out, bound + H * (np.abs(out) + bound) + TINY, saved
 
 
-def backward(x, W, a, b, idx, w, scale, dy, saved):
+def backward(x, W, a, b, idx, w, scale, dy, saved, carried=H):
     """-> {name: (value, bound)} for dx, da, db, dw."""
     T, K = idx.shape
     E, r, D = a.shape
@@ -58,7 +59,7 @@ def backward(x, W, a, b, idx, w, scale, dy, saved):
         v, vm = b[e].T @ dy[t], np.abs(b[e]).T @ np.abs(dy[t])
         ev = 2 * O * U * vm
         evc = abs(c) * ev + cm * (3 + len(ks)) * U * np.abs(v)
-        evc = evc + H * (np.abs(c * v) + evc)
+        evc = evc + carried * (np.abs(c * v) + evc)
         dx[t] += a[e].T @ (c * v)
         dxb[t] += np.abs(a[e]).T @ (evc + 2 * (O + r * K + 64) * U * np.abs(c * v))
         da[e] += np.outer(c * v, x[t])

@@ -491,7 +491,10 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? l
 // chunk c, row c + s of the partials gets the column sums of the
 // probabilities, the counts, the live rows and the bad data.  Chunks and
 // sequences both run along the tokens, so c + s is another row for every pair
-// that meets: nchunk + S rows hold all of them.
+// that meets: nchunk + S rows hold all of them.  A wave sums up to kSumRows of its
+// rows in fp32, and those sums, and the waves', in fp64: equal addends round
+// the same way each time, so that a sum in fp32 drifts with its length (200 u at
+// 2^24 equal rows, u = 2^-24).
 //   partial row: E floats (sums), E ints (counts), live, bad index, bad logit
 struct BalanceRow {
     float *sum;
@@ -503,6 +506,8 @@ __device__ __forceinline__ BalanceRow balance_row(float *part, int E, int64_t ro
     int32_t *c = reinterpret_cast<int32_t *>(p + E);
     return {p, c, c + E};
 }
+
+constexpr int kSumRows = 64;
 
 // Threads of a block by the row length: a wave keeps E column sums in shared
 // memory and 2 VPL values per lane in registers (48 KB at E = 4096, and no
@@ -549,9 +554,12 @@ balance_partial_kernel(const typename L::type *__restrict__ logits, int T, int E
         if (bad_i)
             atomicAdd(&misc[1], bad_i);
         float acc[VPL];
+        double sums[VPL];
 #pragma unroll
-        for (int j = 0; j < VPL; ++j)
+        for (int j = 0; j < VPL; ++j) {
             acc[j] = 0.0f;
+            sums[j] = 0.0;
+        }
         int live = 0, bad_z = 0;
         // the next row's loads are in flight over a row's sums
         float next[VPL];
@@ -574,7 +582,6 @@ balance_partial_kernel(const typename L::type *__restrict__ logits, int T, int E
             top = wave_max_f(top);
             if (!(top > kNegInf))
                 continue;
-            ++live;
 #pragma unroll
             for (int j = 0; j < VPL; ++j) {
                 z[j] = row_score(z[j], top, sigmoid);
@@ -584,12 +591,19 @@ balance_partial_kernel(const typename L::type *__restrict__ logits, int T, int E
 #pragma unroll
             for (int j = 0; j < VPL; ++j)
                 acc[j] = fmaf(z[j], inv, acc[j]);
+            if (++live % kSumRows == 0) {
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) {
+                    sums[j] += (double)acc[j];
+                    acc[j] = 0.0f;
+                }
+            }
         }
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
             const int e = Row<L, VPL, PAIR>::at(j, lane);
             if (e < E)
-                lds[wave * E + e] = acc[j];
+                lds[wave * E + e] = (float)(sums[j] + (double)acc[j]);
         }
         const int bz = wave_sum(bad_z);
         if (lane == 0) {
@@ -600,10 +614,10 @@ balance_partial_kernel(const typename L::type *__restrict__ logits, int T, int E
         __syncthreads();
         const BalanceRow r = balance_row(part, E, (int64_t)c + s);
         for (int e = tid; e < E; e += bd) {
-            float v = 0.0f;
+            double v = 0.0;
             for (int w = 0; w < nw; ++w)
-                v += lds[w * E + e];
-            r.sum[e] = v;
+                v += (double)lds[w * E + e];
+            r.sum[e] = (float)v;
             r.count[e] = hist[e];
         }
         if (tid < 3)

@@ -564,7 +564,7 @@ class BalanceLoss:
     loss: torch.Tensor                         # [1] float32
     num_tokens_per_expert: torch.Tensor        # [S, E] int32: entries of topk_idx per sequence
     num_invalid: torch.Tensor                  # [2] int32: bad entries of topk_idx, bad logits
-    state: torch.Tensor                        # what the gradient needs of the loss (the ABI's slope)
+    state: torch.Tensor                        # [S*E + 1] float32: what the gradient needs of the loss
     logits: torch.Tensor
     score: str
     seq_offsets: Optional[torch.Tensor]
@@ -628,16 +628,15 @@ def balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, *, score: str = "
     ws_bytes = N.ep_balance_workspace_bytes(T, E, S)
     if ws_bytes == 0:
         raise N.EpError("ep_balance_workspace_bytes", N.EP_ERR_INVALID_ARG)
-    # one allocation: the workspace, then the S*E + 1 floats of slope
-    state = torch.empty(ws_bytes + 4 * (S * E + 1), dtype=torch.uint8, device=dev)
-    ws = state.data_ptr()
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    state = torch.empty(S * E + 1, dtype=torch.float32, device=dev)
     counts = torch.empty((S, E), dtype=torch.int32, device=dev)
     loss = torch.empty(1, dtype=torch.float32, device=dev)
     ninv = torch.empty(2, dtype=torch.int32, device=dev)
     with _on(dev):
         N.ep_balance_loss(_ptr(logits), dt, T, E, _ptr(topk_idx), K, _SCORES[score],
-                          _ptr(seq_offsets), S, float(coef), _ptr(counts), ws + ws_bytes,
-                          _ptr(loss), _ptr(ninv), ws, ws_bytes, _stream(dev))
+                          _ptr(seq_offsets), S, float(coef), _ptr(counts), _ptr(state),
+                          _ptr(loss), _ptr(ninv), _ptr(ws), ws_bytes, _stream(dev))
     return BalanceLoss(loss, counts, ninv, state, logits, score, seq_offsets)
 
 
@@ -660,7 +659,7 @@ def _router_backward(logits, score, d_w, routing, d_loss, balance):
             raise ValueError("d_loss must be [1]")
         seq = balance.seq_offsets
         S = 1 if seq is None else seq.shape[0] - 1
-        slope = balance.state.data_ptr() + balance.state.numel() - 4 * (S * E + 1)
+        slope = _ptr(balance.state)
     _same_device(dev, d_weights=d_w, topk_idx=idx, d_loss=d_loss)
     d_logits = torch.empty_like(logits)
     with _on(dev):
@@ -704,6 +703,9 @@ def _apart(out: torch.Tensor, **inputs):
             raise ValueError(f"out must not overlap {name}")
 
 
+_NO_STATE = 256         # bytes of the stub that the ABI asks for where a call leaves no state
+
+
 @functools.lru_cache(maxsize=256)
 def _adapter_bytes(T: int, H: int, O: int, E: int, K: int, r: int):
     """The state's and the two workspaces' bytes, which go by the sizes alone."""
@@ -724,7 +726,7 @@ class AdapterHandle:
     topk_weights: Optional[torch.Tensor]
     scale: float
     num_invalid: torch.Tensor                  # [1] int32: entries neither -1 nor in [0, E)
-    state: torch.Tensor
+    state: Optional[torch.Tensor]              # None after a call of a few tokens, which leaves none
 
 
 def adapter_project(x: torch.Tensor, weight: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
@@ -765,18 +767,16 @@ def adapter_project(x: torch.Tensor, weight: torch.Tensor, a: torch.Tensor, b: t
     if given:
         _apart(out, x=x, weight=weight, a=a, b=b, topk_idx=topk_idx, topk_weights=topk_weights)
     ninv = torch.empty(1, dtype=torch.int32, device=dev)
-    if state_bytes <= 256:
-        # a few tokens leave no state: one allocation, kept with the handle
-        state = torch.empty(state_bytes + ws_bytes, dtype=torch.uint8, device=dev)
-        ws = state.data_ptr() + state_bytes
-    else:
-        state = torch.empty(state_bytes, dtype=torch.uint8, device=dev)
-        scratch = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-        ws = scratch.data_ptr()
+    # a call of a few tokens leaves nothing for its backward: one allocation for
+    # both, and none of it kept
+    state = torch.empty(state_bytes, dtype=torch.uint8, device=dev) if state_bytes > _NO_STATE else None
+    scratch = torch.empty(ws_bytes + (0 if state is not None else state_bytes), dtype=torch.uint8, device=dev)
+    ws = scratch.data_ptr()
+    at = ws + ws_bytes if state is None else state.data_ptr()
     with _on(dev):
         N.ep_adapter_project(_ptr(x), T, H, _ptr(weight), O, _ptr(a), _ptr(b), E, r,
                              _ptr(topk_idx), _ptr(topk_weights), K, float(scale), _ptr(out),
-                             _ptr(ninv), _ptr(state), state_bytes, ws, ws_bytes, _stream(dev))
+                             _ptr(ninv), at, state_bytes, ws, ws_bytes, _stream(dev))
     return out, AdapterHandle(x, weight, a, b, topk_idx, topk_weights, float(scale), ninv, state)
 
 
@@ -794,14 +794,16 @@ def adapter_project_backward(d_out: torch.Tensor, handle: AdapterHandle):
         raise ValueError(f"d_out must be {(T, O)}, got {tuple(d_out.shape)}")
     dev = x.device
     _same_device(dev, d_out=d_out)
-    ws_bytes = _adapter_bytes(T, H, O, E, K, r)[2]
-    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    state_bytes, _, ws_bytes = _adapter_bytes(T, H, O, E, K, r)
+    state = handle.state
+    ws = torch.empty(ws_bytes + (0 if state is not None else state_bytes), dtype=torch.uint8, device=dev)
+    at = ws.data_ptr() + ws_bytes if state is None else state.data_ptr()
     dx, da, db = torch.empty_like(x), torch.empty_like(a), torch.empty_like(b)
     dw = torch.empty((T, K), dtype=torch.float32, device=dev)
     with _on(dev):
         N.ep_adapter_project_backward(_ptr(d_out), _ptr(x), T, H, _ptr(weight), O, _ptr(a),
                                       _ptr(b), E, r, _ptr(idx), _ptr(handle.topk_weights), K,
-                                      handle.scale, _ptr(handle.state), handle.state.numel(),
+                                      handle.scale, at, state_bytes,
                                       _ptr(dx), _ptr(da), _ptr(db), _ptr(dw), _ptr(ws), ws_bytes,
                                       _stream(dev))
     return dx, da, db, dw

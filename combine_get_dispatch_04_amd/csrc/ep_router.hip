@@ -865,8 +865,8 @@ router_backward_kernel(const typename L::type *__restrict__ logits, int T, int E
 constexpr int kMaxRowBlocks = 1 << 20;
 int row_blocks(int T)
 {
-    const int b = (T + 3) / 4;
-    return b < kMaxRowBlocks ? b : kMaxRowBlocks;
+    const int64_t b = ((int64_t)T + 3) / 4;
+    return b < kMaxRowBlocks ? (int)b : kMaxRowBlocks;
 }
 
 // Values per lane for E experts: f(VPL).
@@ -947,11 +947,11 @@ BalancePlan make_balance_plan(int T, int E, int S)
     p.T = T;
     p.E = E;
     p.S = S;
-    // up to 256 chunks (one per CU) of at least 16 tokens
-    p.CT = (T + 255) / 256;
+    // up to 256 chunks (one per CU) of at least 16 tokens; T may be next to 2^31
+    p.CT = (int)(((int64_t)T + 255) / 256);
     if (p.CT < 16)
         p.CT = 16;
-    p.nchunk = T > 0 ? (T + p.CT - 1) / p.CT : 1;
+    p.nchunk = T > 0 ? (int)(((int64_t)T + p.CT - 1) / p.CT) : 1;
     p.eb = (E + kFinalCols - 1) / kFinalCols;
     size_t off = 0;
     p.off_arrived = off;

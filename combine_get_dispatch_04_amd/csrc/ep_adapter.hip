@@ -1512,6 +1512,8 @@ AdapterPlan make_adapter_plan(int T, int H, int O, int E, int K, int r)
     if (p.slots < 4)
         p.slots = 4;
     const size_t entries = (size_t)T * K * r * 4;
+    // what shrink_splits can come to, for any list
+    auto splits = [&](int D) { return (size_t)least(p.slots, shrink_depth(D)); };
     size_t off = 0;
     p.off_cnt = off;
     off = align256(off + 2 * (size_t)p.ntile * 4);
@@ -1536,11 +1538,11 @@ AdapterPlan make_adapter_plan(int T, int H, int O, int E, int K, int r)
         p.ws_bytes = p.off_partw + align256((size_t)p.wsplits * T * O * 4);
         p.state_bytes = 256;        // the backward makes its own
     } else {
-        p.ws_bytes = align256((size_t)p.slots * entries) + 256;
+        p.ws_bytes = align256(splits(H) * entries) + 256;
         p.state_bytes = state;
     }
     // backward: the splits' sums or those of the gradients, v and V
-    size_t part = (size_t)p.slots * entries;
+    size_t part = (splits(O) > splits(H) ? splits(O) : splits(H)) * entries;
     size_t both = 0;
     for (const int n : {H, O}) {
         const int z = adapter_grad_splits(p, n);

@@ -306,11 +306,11 @@ route_kernel(const typename L::type *__restrict__ logits, int T, int E, int K, i
         }
         const float low = -wave_max_f(-floor_key);
         const float per = 63.0f * __builtin_amdgcn_rcpf(top - low);
-        // 0 .. 63, monotone; NaN (no range to divide) gives 0; below low and masked: nowhere
+        // 0 .. 63, monotone; NaN (no range to divide) gives 0, as fmaxf leaves it
+        // out; below low and masked: nowhere
         auto step_of = [&](float k) {
-            const int b = (int)((k - low) * per);
-            const int c = b < 0 ? 0 : (b > kWave - 1 ? kWave - 1 : b);
-            return k >= low ? c : nowhere;
+            const float b = fminf(fmaxf((k - low) * per, 0.0f), (float)(kWave - 1));
+            return k >= low ? (int)b : nowhere;
         };
         int my_e = -1, rank = lane, n = 0;
         float my_z = kNegInf;

@@ -26,6 +26,16 @@ struct vpl_t {
 };
 constexpr float kSmallSigmoid = -20.0f;
 
+// Between a write to shared memory and another lane's read of it, and back: the
+// lanes of a wave run together and the LDS takes their accesses in order, so this
+// only keeps the compiler from moving them across.
+__device__ __forceinline__ void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // ---------------------------------------------------------------- a row
 // A logit as fp32; invalid ones (NaN, +inf) give -inf and are flagged.  The
 // addition of +0 turns -0 into +0, so that the two are one value in the order.
@@ -317,13 +327,13 @@ route_kernel(const typename L::type *__restrict__ logits, int T, int E, int K, i
         if (want > 0) {
             int at_step[VPL];
             steps[wave][lane] = 0;
-            __builtin_amdgcn_wave_barrier();
+            wave_sync();
 #pragma unroll
             for (int j = 0; j < VPL; ++j) {
                 at_step[j] = step_of(key[j]);
                 atomicAdd(&steps[wave][at_step[j]], 1);
             }
-            __builtin_amdgcn_wave_barrier();
+            wave_sync();
             const int upto = wave_inclusive_scan(steps[wave][kWave - 1 - lane], lane);
             const int at = __ffsll((unsigned long long)ballot(upto >= want)) - 1;
             const int border = kWave - 1 - at;
@@ -381,7 +391,7 @@ route_kernel(const typename L::type *__restrict__ logits, int T, int E, int K, i
                 }
                 n = base;
             }
-            __builtin_amdgcn_wave_barrier();
+            wave_sync();
             if (n <= kWave) {
                 if (lane < n) {
                     const u32x2 c = chosen[wave][lane];
@@ -436,7 +446,7 @@ route_kernel(const typename L::type *__restrict__ logits, int T, int E, int K, i
             } else {
                 choose_fp64<L>(row, bias, E, K, lane, my_e, my_z, rank);
             }
-            __builtin_amdgcn_wave_barrier();
+            wave_sync();
         }
 
         float w;
@@ -814,16 +824,16 @@ router_backward_kernel(const typename L::type *__restrict__ logits, int T, int E
                 if (c < E)
                     mine[c] = 0.0f;
             }
-            __builtin_amdgcn_wave_barrier();
+            wave_sync();
             if (in)
                 atomicAdd(&mine[e], v);
-            __builtin_amdgcn_wave_barrier();
+            wave_sync();
 #pragma unroll
             for (int j = 0; j < VPL; ++j) {
                 const int c = Row<L, VPL, PAIR>::at(j, lane);
                 d[j] = c < E ? mine[c] : 0.0f;
             }
-            __builtin_amdgcn_wave_barrier();
+            wave_sync();
             if (dense_w) {
                 float dot = 0.0f;
 #pragma unroll

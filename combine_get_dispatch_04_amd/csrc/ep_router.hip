@@ -8,12 +8,13 @@
 // lies below kSmallSigmoid, exp(z_e - m) stands for it, which differs from
 // s_e / s_m by less than 2^-28 and does not underflow.
 //
-// Everything here is one wave per row (lane l holds experts l, 64 + l, ...):
-// a row's logits are read once into registers, and sums, maxima and the
-// choice are reductions over the 64 lanes, with no shared memory but the
-// scatter of the backward.
+// Everything here is one wave per row: a row's logits are read once into
+// registers, and sums and maxima are reductions over the 64 lanes.  Shared memory
+// holds the choice's histogram and candidates, a block's column sums and counts for
+// the loss, and the scatter of the backward.
 #include "ep_common.h"
 #include "ep_internal.h"
+#include "ep_wave.h"
 
 namespace ep {
 

@@ -1427,22 +1427,15 @@ hipError_t project_any(const AdapterPlan &p, const Tiles &m, const uint16_t *src
                        uint16_t *out, hipStream_t s)
 {
     switch (p.BM) {
-    case 64: {
-        // a CU takes in about 31 bytes a cycle (64 x 64: 16 KB a stage in 0.25 us, 64 x 128:
-        // 24 KB in 0.35 us), so a tile costs its rows and columns, times the most
-        // tiles a CU gets: 1001 x 4096 x 1032: 24.0 us with 64 columns, 19.4 with 128;
-        // 960 x 1024 x 4096: 18.6 and 22.9
-        auto cost = [&](int cols) {
-            const int64_t tiles = (int64_t)p.ntile * ((N + cols - 1) / cols);
-            return (tiles + 255) / 256 * (64 + cols);
-        };
-        if constexpr (!NN)      // 1001 x 1032 x 4096 with 32 adapters: 27 us with 128 columns, 23 with 96
-            if (cost(96) < cost(64) && cost(96) < cost(128))
-                return project<64, 96, 2, 2, 4, NN>(p, m, src, D, weight, N, ad, dense, out, s);
-        if (cost(128) >= cost(64))
+    case 64:
+        switch (adapter_tile_columns(p, N, NN)) {
+        case 64:
             return project<64, 64, 2, 2, 4, NN>(p, m, src, D, weight, N, ad, dense, out, s);
+        case 96:
+            if constexpr (!NN)
+                return project<64, 96, 2, 2, 4, NN>(p, m, src, D, weight, N, ad, dense, out, s);
+        }
         return project<64, 128, NN ? 2 : 1, NN ? 2 : 4, 3, NN>(p, m, src, D, weight, N, ad, dense, out, s);
-    }
     case 128:
         return project<128, 128, 2, 2, 2, NN>(p, m, src, D, weight, N, ad, dense, out, s);
     }
@@ -1488,6 +1481,24 @@ int adapter_grad_splits(const AdapterPlan &p, int N)
     if (splits > p.ntile)
         splits = p.ntile;
     return splits < 1 ? 1 : (int)splits;
+}
+
+int adapter_tile_columns(const AdapterPlan &p, int N, bool across)
+{
+    if (p.BM > 64)
+        return p.BM;
+    // a CU takes in about 31 bytes a cycle (64 x 64: 16 KB a stage in 0.25 us, 64 x 128:
+    // 24 KB in 0.35 us), so a tile costs its rows and columns, times the most
+    // tiles a CU gets: 1001 x 4096 x 1032: 24.0 us with 64 columns, 19.4 with 128;
+    // 960 x 1024 x 4096: 18.6 and 22.9; 1001 x 1032 x 4096 with 32 adapters: 27 us with
+    // 128 columns, 23 with 96 (which a transposing read does not divide into)
+    auto cost = [&](int cols) {
+        const int64_t tiles = (int64_t)p.ntile * ((N + cols - 1) / cols);
+        return (tiles + 255) / 256 * (64 + cols);
+    };
+    if (!across && cost(96) < cost(64) && cost(96) < cost(128))
+        return 96;
+    return cost(128) >= cost(64) ? 64 : 128;
 }
 
 AdapterPlan make_adapter_plan(int T, int H, int O, int E, int K, int r)

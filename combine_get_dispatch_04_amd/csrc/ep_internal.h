@@ -146,6 +146,9 @@ struct AdapterPlan {
 };
 AdapterPlan make_adapter_plan(int T, int H, int O, int E, int K, int r);
 int adapter_grad_splits(const AdapterPlan &p, int N);
+// Columns of the projection's tiles of p.BM tokens: of N outputs, W read as it
+// lies or across (the gradient of x).
+int adapter_tile_columns(const AdapterPlan &p, int N, bool across);
 
 hipError_t launch_adapter(const AdapterPlan &p, const uint16_t *x, const uint16_t *weight,
                           const uint16_t *a, const uint16_t *b, const int32_t *idx, const float *w,

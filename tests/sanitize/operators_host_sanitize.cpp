@@ -3,13 +3,18 @@
 // they accept, and argument checks there, which return before anything is
 // enqueued.  Built with the host pass under AddressSanitizer and
 // UndefinedBehaviorSanitizer, so that an overflow in the size arithmetic is
-// reported.  Exit status 0 = clean.
+// reported.  Exit status 0 = clean.  With arguments "T,H,O,E,K,r" it prints the
+// form of the adapters' projection that each takes instead.
 // Test infrastructure: built and run by tests/test_operators_sanitize.py.
 #include <stdint.h>
 #include <stdio.h>
 #include <stdlib.h>
 
 #include "ep.h"
+
+#include <hip/hip_runtime.h>
+
+#include "ep_internal.h"
 
 static int failures = 0;
 
@@ -21,8 +26,24 @@ static void expect(bool ok, const char *what, long long a, long long b)
     }
 }
 
-int main()
+// Tokens of a tile, columns of the forward's tiles and of those of dx.
+static int print_form(const char *arg)
 {
+    int T, H, O, E, K, r;
+    if (sscanf(arg, "%d,%d,%d,%d,%d,%d", &T, &H, &O, &E, &K, &r) != 6)
+        return 1;
+    const ep::AdapterPlan p = ep::make_adapter_plan(T, H, O, E, K, r);
+    printf("%d,%d,%d\n", p.BM, ep::adapter_tile_columns(p, O, false), ep::adapter_tile_columns(p, H, true));
+    return 0;
+}
+
+int main(int argc, char **argv)
+{
+    for (int i = 1; i < argc; ++i)
+        if (print_form(argv[i]))
+            return 1;
+    if (argc > 1)
+        return 0;
     const long long kMost = 2147483647LL;
     const long long Ts[] = {0, 1, 15, 16, 17, 128, 129, 4095, 4096, 4097, 300000, 1 << 20, 1 << 28, 1LL << 30,
                             kMost - 8388607, kMost - 400, kMost - 1, kMost};

@@ -34,7 +34,6 @@
 // takes them again with every such product left out.
 #include "ep_common.h"
 #include "ep_internal.h"
-#include "ep_wave.h"
 
 namespace ep {
 

@@ -14,7 +14,6 @@
 // the loss, and the scatter of the backward.
 #include "ep_common.h"
 #include "ep_internal.h"
-#include "ep_wave.h"
 
 namespace ep {
 

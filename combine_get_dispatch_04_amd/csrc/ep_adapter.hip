@@ -18,8 +18,8 @@
 // gradients' error.  So they are two matrices of bf16 each, a value's
 // nearest and what that left over, together within 2^-16 of it; a product with
 // them is one with each.  At 4096 x 4096 x 4096, 2 of 8 adapters of rank 16,
-// the second one costs 6 and 7 us of the two projections' 129 and 141, and 12 of
-// the gradients' 41.
+// the second one costs 2 and 3 us of the two projections' 109 and 116, and 9 of
+// the gradients' 34.
 //
 //   shrink     the lists, and every adapter's place in them; A_e x_t (or B_e^T d_t)
 //              of every entry, MFMA over the list's rows, the inner dimension split
@@ -564,8 +564,8 @@ __device__ __forceinline__ void shrink_chunk(const Tiles &m, const uint16_t *src
         e_of[j] = n < cols && j_of[j] < m.r ? list[n / m.rp] : -1;
     }
     // the entries are read once each, and before the stores, which for all the
-    // compiler knows might be to them (read again for every fragment: 23 us
-    // instead of 17 at 4096 x 4096, K = 2)
+    // compiler knows might be to them (read again for every fragment, the kernel
+    // takes 1.35 times as long at 4096 x 4096, K = 2)
     const int ta = t0 + wave / P::WN * (P::BM / P::WM) + (lane & 15);
     for (int k = 0; k < m.K; ++k) {
         int named[P::TI];
@@ -733,11 +733,13 @@ adapter_gather_kernel(Tiles m, const float *__restrict__ w, float scale, int slo
 // out[t][n] = sum_l dense[t][l] adapter_l[.][n] + sum_k src[t][k] W: W [N, D]
 // and B [E, N, r] for the forward (NN = false), W [D, N] and A [E, r, N] for
 // the gradient of x (NN = true).
-// Measured, without adapters: 4096 x 4096 x 4096 113 us (1.21 PFLOP/s) and 115 us
-// (NN), 4001 x 7168 x 7168 300 to 347 us by card (1.37 to 1.18 PFLOP/s); eight
-// experts of rank 16 in every tile make the first two 116 and 126 us.  Bound by
-// the matrix pipes, busy 65 % of the time, with the waves waiting for 32 % of theirs
-// (with half of the loads left out 102 us of 105, with a quarter of the MFMAs 79).
+// Measured in a steady stream of calls: 4096 x 4096 x 4096 with eight adapters of
+// rank 16 in every tile 109 us (1.26 PFLOP/s) and 116 us (NN), 4001 x 7168 x 7168
+// 321 us, 346 where the gradient's product runs in turn with it (1.28 and 1.19
+// PFLOP/s); without adapters no less.  Bound by the matrix pipes, busy 58 % of the
+// time (52 % NN), with the waves at a wait for 25 to 33 % of theirs and at a pipe
+// that is taken for 50 % (with half of the loads left out 102 us of 105, with a
+// quarter of the MFMAs 79).
 
 // The adapters' part of 16 tokens (lane & 15: token t with its row u of U) by
 // columns c .. c+15, one adapter at a time, each for the tokens that name it
@@ -952,8 +954,8 @@ __device__ __forceinline__ void adapter_grads(const Tiles &m, const GradJob &g, 
         for (int d = 0; d < 4; ++d)
             acc[b][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     // the next tile from `tile` on that names one of the adapters; their places
-    // come in windows of kGradWindow tiles (one by one, a miss each: 26 us instead
-    // of 23 at 1001 tokens, 32 adapters)
+    // come in windows of kGradWindow tiles (one by one, a miss each: 3 us more of
+    // 27 at 1001 tokens, 32 adapters)
     int window = i0 - kGradWindow;
     auto next_tile = [&](int tile) {
         for (; tile < i1; ++tile) {
@@ -1488,9 +1490,10 @@ int adapter_tile_columns(const AdapterPlan &p, int N, bool across)
         return p.BM;
     // a CU takes in about 31 bytes a cycle (64 x 64: 16 KB a stage in 0.25 us, 64 x 128:
     // 24 KB in 0.35 us), so a tile costs its rows and columns, times the most
-    // tiles a CU gets: 1001 x 4096 x 1032: 24.0 us with 64 columns, 19.4 with 128;
-    // 960 x 1024 x 4096: 18.6 and 22.9; 1001 x 1032 x 4096 with 32 adapters: 27 us with
-    // 128 columns, 23 with 96 (which a transposing read does not divide into)
+    // tiles a CU gets.  Tokens x outputs x inner, with 64, 96 and 128 columns: 1001 x
+    // 4096 x 1032 24.4, 27.9 and 21.0 us; 960 x 1024 x 4096 16.5, 19.5 and 23.7; 1001 x
+    // 1032 x 4096 with 32 adapters 26.3, 21.5 and 25.6; the gradient of x of 960 x 4096 x
+    // 1024 18.5 with 64 and 15.6 with 128 (transposing reads do not divide 96 by waves)
     auto cost = [&](int cols) {
         const int64_t tiles = (int64_t)p.ntile * ((N + cols - 1) / cols);
         return (tiles + 255) / 256 * (64 + cols);

@@ -244,9 +244,9 @@ __device__ void choose_fp64(const typename L::type *row, const float *bias, int 
 // than 64 candidates (many equal keys, or a huge range) bisect the border
 // between the K and the rest instead, with ballots.
 // At 16384 x 384 in bf16, K = 16: K maxima over the wave, one after the other,
-// took 43.5 us; bisecting the border in every row 27 us; this 17 us, of which 4 are
-// the launch and the rest the issue of 463 vector and 158 scalar instructions a
-// row (the row's 13 MB are 3 us).  4096 x 256, K = 8, sigmoid and bias: 6.4 us.
+// took 43.5 us; bisecting the border in every row 27 us; this 16.5 us, of which 3 to 4
+// are the launch and the rest the issue of 465 vector and 158 scalar instructions a
+// row (the rows' 13 MB are 3 us).  4096 x 256, K = 8, sigmoid and bias: 6.4 us.
 template <typename L, int VPL>
 __global__ void __launch_bounds__(256)
 route_kernel(const typename L::type *__restrict__ logits, int T, int E, int K, int sigmoid,

@@ -540,7 +540,7 @@ size_t ep_adapter_workspace_bytes(int T, int H, int O, int E, int K, int r, int 
  *                 tokens may name; the backward's workspace has the same again.)
  *   ws, ws_bytes  >= ep_adapter_workspace_bytes(..., 0); free after the call.
  * Constraints: H % 8 == 0, O % 8 == 0, H, O <= 2^20, r % 8 == 0, r <= 128, E <= 4096,
- * K <= 64, T*K < 2^31, ceil(T / 128) * ceil(max(H, O) / 128) < 2^23,
+ * K <= 64, T*K < 2^31, ceil(T / 128) * max(16, ceil(max(H, O) / 128)) < 2^23,
  * E * ceil(max(H, O) / 128) < 2^22.
  */
 ep_status_t ep_adapter_project(const uint16_t *x, int T, int H, const uint16_t *weight, int O,

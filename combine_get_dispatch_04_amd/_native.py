@@ -19,6 +19,7 @@ EP_LAYOUT_CONTIGUOUS, EP_LAYOUT_PADDED = 0, 1
 
 EP_DTYPE_BF16, EP_DTYPE_F32 = 0, 1
 EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = 0, 1
+EP_ACT_NONE, EP_ACT_SWIGLU = 0, 1
 
 # name -> (restype, argtypes); every pointer is passed as an integer address
 _P = ctypes.c_void_p
@@ -58,6 +59,15 @@ SIGNATURES = {
                                  _SZ, _P, _SZ, _P]),
     "ep_adapter_project_backward": (_ST, [_P, _P, _I, _I, _P, _I, _P, _P, _I, _I, _P, _P, _I, _F,
                                           _P, _SZ, _P, _P, _P, _P, _P, _SZ, _P]),
+    "ep_mx_quantize": (_ST, [_P, _I, _I, _I, _P, _P, _P]),
+    "ep_mx_dequantize": (_ST, [_P, _P, _I, _I, _I, _P, _P]),
+    "ep_expert_product": (_ST, [_P, _P, _I, _I, _P, _P, _I, _I, _I, _P, _P, _I, _I, _I, _P, _P, _P]),
+    "ep_expert_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "ep_expert_product_backward": (_ST, [_P, _P, _P, _I, _I, _P, _P, _I, _I, _I, _P, _P, _I, _I, _P,
+                                         _P, _SZ, _P]),
+    "ep_low_latency_experts_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "ep_low_latency_experts": (_ST, [_P, _I, _I, _P, _P, _I, _P, _P, _P, _P, _I, _I, _P, _P, _P,
+                                     _SZ, _P]),
 }
 
 _lib = None
@@ -238,3 +248,44 @@ def ep_adapter_project_backward(d_out, x, T, H, weight, O, a, b, E, r, topk_idx,
                                            topk_weights, K, scale, state, state_bytes, dx, da, db,
                                            d_weights, ws, ws_bytes, stream)
     return _check("ep_adapter_project_backward", st) if check else st
+
+
+def ep_mx_quantize(x, rows, H, quant, codes, scales, stream, check=True):
+    st = lib().ep_mx_quantize(x, rows, H, quant, codes, scales, stream)
+    return _check("ep_mx_quantize", st) if check else st
+
+
+def ep_mx_dequantize(codes, scales, rows, H, quant, out, stream, check=True):
+    st = lib().ep_mx_dequantize(codes, scales, rows, H, quant, out, stream)
+    return _check("ep_mx_dequantize", st) if check else st
+
+
+def ep_expert_product(x, x_scales, x_quant, rows, weight, weight_scales, E, O, H, offsets, counts,
+                      cap, activation, y_quant, y, y_scales, stream, check=True):
+    st = lib().ep_expert_product(x, x_scales, x_quant, rows, weight, weight_scales, E, O, H,
+                                 offsets, counts, cap, activation, y_quant, y, y_scales, stream)
+    return _check("ep_expert_product", st) if check else st
+
+
+def ep_expert_workspace_bytes(rows: int, O: int, activation: int) -> int:
+    return lib().ep_expert_workspace_bytes(rows, O, activation)
+
+
+def ep_expert_product_backward(d_y, x, x_scales, x_quant, rows, weight, weight_scales, E, O, H,
+                               offsets, counts, cap, activation, dx, ws, ws_bytes, stream,
+                               check=True):
+    st = lib().ep_expert_product_backward(d_y, x, x_scales, x_quant, rows, weight, weight_scales,
+                                          E, O, H, offsets, counts, cap, activation, dx, ws,
+                                          ws_bytes, stream)
+    return _check("ep_expert_product_backward", st) if check else st
+
+
+def ep_low_latency_experts_workspace_bytes(T: int, K: int, E: int, H: int, I: int) -> int:
+    return lib().ep_low_latency_experts_workspace_bytes(T, K, E, H, I)
+
+
+def ep_low_latency_experts(x, T, H, topk_idx, topk_weights, K, up, up_scales, down, down_scales, E,
+                           I, out, num_invalid, ws, ws_bytes, stream, check=True):
+    st = lib().ep_low_latency_experts(x, T, H, topk_idx, topk_weights, K, up, up_scales, down,
+                                      down_scales, E, I, out, num_invalid, ws, ws_bytes, stream)
+    return _check("ep_low_latency_experts", st) if check else st

@@ -807,3 +807,261 @@ def adapter_project_backward(d_out: torch.Tensor, handle: AdapterHandle):
                                       _ptr(dx), _ptr(da), _ptr(db), _ptr(dw), _ptr(ws), ws_bytes,
                                       _stream(dev))
     return dx, da, db, dw
+
+
+# ---------------------------------------------------------------- the experts
+_MX_OF = {torch.uint8: "mxfp4_e2m1", torch.float8_e4m3fn: "mxfp8_e4m3", torch.float8_e5m2: "mxfp8_e5m2"}
+_ACTIVATIONS = {None: N.EP_ACT_NONE, "swiglu": N.EP_ACT_SWIGLU}
+
+
+def _mx_mode(quant: str) -> str:
+    quant = _QUANT_ALIASES.get(quant, quant)
+    if quant not in _MX_OF.values():
+        raise ValueError(f"quant must be an MX mode, got {quant!r}")
+    return quant
+
+
+def _need_codes(codes: torch.Tensor, scales: Optional[torch.Tensor], name: str, ndim: int):
+    """Checks a microscaled tensor; -> its mode and channels."""
+    if not isinstance(codes, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if codes.dtype not in _MX_OF:
+        raise ValueError(f"{name} must hold MX codes (uint8, float8_e4m3fn or float8_e5m2), got {codes.dtype}")
+    _need(codes, name, codes.dtype, ndim)
+    _need(scales, f"{name}'s scales", torch.uint8, ndim)
+    quant = _MX_OF[codes.dtype]
+    H = codes.shape[-1] * _QUANT[quant][2]
+    if H % 32 != 0 or tuple(scales.shape) != (*codes.shape[:-1], H // 32):
+        raise ValueError(f"{name} {tuple(codes.shape)} needs one scale per 32 channels, got {tuple(scales.shape)}")
+    _same_device(codes.device, **{f"{name}'s scales": scales})
+    return quant, H
+
+
+def mx_quantize(x: torch.Tensor, quant: str = "mxfp4_e2m1"):
+    """bf16 [..., H] (weights, activations) -> (codes, e8m0 scales [..., H/32]),
+    the ones that dispatch makes of such rows: "mxfp4_e2m1" uint8 [..., H/2],
+    "mxfp8_e4m3" and "mxfp8_e5m2" [..., H] of the torch type."""
+    quant = _mx_mode(quant)
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a tensor")
+    if x.dim() < 1:
+        raise ValueError("x must have a last dimension of channels")
+    _need(x, "x", torch.bfloat16, x.dim())
+    H = x.shape[-1]
+    q, dt, div, _ = _QUANT[quant]
+    if H < 32 or H % 32 != 0:
+        raise ValueError(f"x must have a multiple of 32 channels, got {H}")
+    dev = x.device
+    codes = torch.empty((*x.shape[:-1], H // div), dtype=dt, device=dev)
+    scales = torch.empty((*x.shape[:-1], H // 32), dtype=torch.uint8, device=dev)
+    with _on(dev):
+        N.ep_mx_quantize(_ptr(x), x.numel() // H, H, q, _ptr(codes), _ptr(scales), _stream(dev))
+    return codes, scales
+
+
+def mx_dequantize(codes: torch.Tensor, scales: torch.Tensor) -> torch.Tensor:
+    """bf16 [..., H] of codes and scales as mx_quantize and dispatch make them
+    (the mode is told by the codes' type)."""
+    if not isinstance(codes, torch.Tensor):
+        raise TypeError("codes must be a tensor")
+    if codes.dim() < 1:
+        raise ValueError("codes must have a last dimension of channels")
+    quant, H = _need_codes(codes, scales, "codes", codes.dim())
+    if H < 32:
+        raise ValueError("codes must have a multiple of 32 channels")
+    dev = codes.device
+    out = torch.empty((*codes.shape[:-1], H), dtype=torch.bfloat16, device=dev)
+    with _on(dev):
+        N.ep_mx_dequantize(_ptr(codes), _ptr(scales), out.numel() // H, H, _QUANT[quant][0], _ptr(out),
+                           _stream(dev))
+    return out
+
+
+@dataclass
+class ExpertHandle:
+    """What expert_product_backward needs from expert_product.  The operands must
+    still hold their values when the backward runs (without an activation x is not
+    looked at)."""
+    x: torch.Tensor
+    x_scales: Optional[torch.Tensor]
+    weight: torch.Tensor
+    weight_scales: torch.Tensor
+    offsets: Optional[torch.Tensor]
+    counts: Optional[torch.Tensor]
+    activation: Optional[str]
+
+
+def _expert_sizes(x, x_scales, weight, weight_scales, offsets, counts, activation):
+    """Checks the operands of an expert's product; -> quant, rows, cap, E, O, H."""
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"unknown activation {activation!r}")
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a tensor")
+    ndim = 3 if offsets is None else 2
+    if x.dtype == torch.bfloat16:
+        if x_scales is not None:
+            raise ValueError("bf16 rows have no scales")
+        _need(x, "x", torch.bfloat16, ndim)
+        quant, H = "bf16", x.shape[-1]
+    else:
+        quant, H = _need_codes(x, x_scales, "x", ndim)
+    mode, wH = _need_codes(weight, weight_scales, "weight", 3)
+    if mode != "mxfp4_e2m1":
+        raise ValueError("weight must be in MXFP4 (uint8 codes)")
+    E, O = weight.shape[:2]
+    if wH != H:
+        raise ValueError(f"weight has {wH} channels, the rows {H}")
+    if offsets is not None:
+        if counts is not None:
+            raise ValueError("rows go by offsets or by counts, not by both")
+        _need(offsets, "offsets", torch.int32, 1)
+        if offsets.shape[0] != E + 1:
+            raise ValueError(f"offsets must be [E + 1] = {E + 1}, got {offsets.shape[0]}")
+        rows, cap = x.shape[0], 0
+    else:
+        if x.shape[0] != E:
+            raise ValueError(f"padded rows must be [E, cap, ...] of the weight's {E} experts, got {tuple(x.shape)}")
+        if counts is not None:
+            _need(counts, "counts", torch.int32, 1)
+            if counts.shape[0] != E:
+                raise ValueError(f"counts must be [E] = {E}, got {counts.shape[0]}")
+        cap = x.shape[1]
+        rows = E * cap
+    _same_device(x.device, x_scales=x_scales, weight=weight, weight_scales=weight_scales, offsets=offsets,
+                 counts=counts)
+    return quant, rows, cap, E, O, H
+
+
+def _rows_out(out: Optional[torch.Tensor], shape, dt, dev: torch.device, **inputs) -> torch.Tensor:
+    """A caller's output rows, checked, or new ones."""
+    if out is None:
+        return torch.empty(shape, dtype=dt, device=dev)
+    _need(out, "out", dt, len(shape))
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"out must be {tuple(shape)}, got {tuple(out.shape)}")
+    _same_device(dev, out=out)
+    _apart(out, **inputs)
+    return out
+
+
+def expert_product(x: torch.Tensor, x_scales: Optional[torch.Tensor], weight: torch.Tensor,
+                   weight_scales: torch.Tensor, *, offsets: Optional[torch.Tensor] = None,
+                   counts: Optional[torch.Tensor] = None, activation: Optional[str] = None,
+                   quant: str = "bf16", out: Optional[torch.Tensor] = None):
+    """Every expert's matrix on the expert's rows, between dispatch and combine:
+    y[r] = weight[e] x[r], or with activation="swiglu" (weight [E, 2I, H])
+    silu(a) * b of its two halves.  weight, weight_scales: MXFP4, [E, O, H/2] and
+    [E, O, H/32] (mx_quantize).
+    x, x_scales: rows as dispatch makes them, MXFP4 or MXFP8 (quant "mxfp4_e2m1",
+    "mxfp8_e4m3", "mxfp8_e5m2"), or bf16 with None.  [rows, ...] with `offsets`
+    [E+1] (Layout.offsets), or the padded [E, cap, ...] with `counts` [E]
+    (Handle.recv_count; None: every row).  Rows that no expert has are neither
+    read nor written.
+    quant: "bf16", or an MX mode for the next product's rows.  `out` (bf16 only)
+    may not overlap an operand.
+    -> (y, y_scales or None, ExpertHandle).  Tensors carry no autograd graph: the
+    rows' gradient is expert_product_backward."""
+    mode, rows, cap, E, O, H = _expert_sizes(x, x_scales, weight, weight_scales, offsets, counts, activation)
+    width = O // 2 if activation else O
+    if activation and O % 2 != 0:
+        raise ValueError("swiglu needs an even number of weight rows")
+    if quant != "bf16":
+        quant = _mx_mode(quant)
+        if width % 32 != 0:
+            raise ValueError(f"quantised rows need a multiple of 32 channels, got {width}")
+        if out is not None:
+            raise ValueError("out is for bf16 rows")
+    q, dt, div, _ = _QUANT[quant]
+    dev = x.device
+    lead = tuple(x.shape[:-1])
+    y = _rows_out(out, (*lead, width // div), dt, dev, x=x, x_scales=x_scales, weight=weight,
+                  weight_scales=weight_scales, offsets=offsets, counts=counts)
+    scales = None if quant == "bf16" else torch.empty((*lead, width // 32), dtype=torch.uint8, device=dev)
+    with _on(dev):
+        N.ep_expert_product(_ptr(x), _ptr(x_scales), _QUANT[mode][0], rows, _ptr(weight), _ptr(weight_scales), E, O,
+                            H, _ptr(offsets), _ptr(counts), cap, _ACTIVATIONS[activation], q, _ptr(y),
+                            _ptr(scales), _stream(dev))
+    return y, scales, ExpertHandle(x, x_scales, weight, weight_scales, offsets, counts, activation)
+
+
+def expert_product_backward(d_y: torch.Tensor, handle: ExpertHandle, *,
+                            out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dx, bf16 rows like x, for d_y (bf16, like y).  The weight is frozen and has
+    no gradient; a quantisation of x or of y passes the gradient on as it is.
+    Rows that no expert has are not written."""
+    h = handle
+    mode, rows, cap, E, O, H = _expert_sizes(h.x, h.x_scales, h.weight, h.weight_scales, h.offsets, h.counts,
+                                             h.activation)
+    lead = tuple(h.x.shape[:-1])
+    _need(d_y, "d_y", torch.bfloat16, len(lead) + 1)
+    want = (*lead, O // 2 if h.activation else O)
+    if tuple(d_y.shape) != want:
+        raise ValueError(f"d_y must be {want}, got {tuple(d_y.shape)}")
+    dev = h.x.device
+    _same_device(dev, d_y=d_y)
+    dx = _rows_out(out, (*lead, H), torch.bfloat16, dev, d_y=d_y, x=h.x, x_scales=h.x_scales, weight=h.weight,
+                   weight_scales=h.weight_scales, offsets=h.offsets, counts=h.counts)
+    act = _ACTIVATIONS[h.activation]
+    ws_bytes = N.ep_expert_workspace_bytes(rows, O, act)
+    if ws_bytes == 0:
+        raise N.EpError("ep_expert_workspace_bytes", N.EP_ERR_INVALID_ARG)
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    with _on(dev):
+        N.ep_expert_product_backward(_ptr(d_y), _ptr(h.x), _ptr(h.x_scales), _QUANT[mode][0], rows, _ptr(h.weight),
+                                     _ptr(h.weight_scales), E, O, H, _ptr(h.offsets), _ptr(h.counts), cap, act,
+                                     _ptr(dx), _ptr(ws), ws_bytes, _stream(dev))
+    return dx
+
+
+@functools.lru_cache(maxsize=256)
+def _few_bytes(T: int, K: int, E: int, H: int, I: int) -> int:
+    return N.ep_low_latency_experts_workspace_bytes(T, K, E, H, I)
+
+
+def low_latency_experts(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: Optional[torch.Tensor],
+                        up: torch.Tensor, down: torch.Tensor, *, up_scales: Optional[torch.Tensor] = None,
+                        down_scales: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+    """A whole layer of experts for a decode batch (up to 128 tokens), instead of
+    low_latency_dispatch, the experts' products and low_latency_combine, in two
+    launches: out[t] = sum_k topk_weights[t,k] * down[e] (silu(a) * b), a and b the
+    halves of up[e] x_t, e = topk_idx[t,k] (-1 = none; weights 1 if None).
+    x [T, H] bf16; up [E, 2I, H] and down [E, H, I] in bf16, or both in MXFP4
+    (mx_quantize: codes, with up_scales and down_scales).  `out` may not overlap an
+    operand.  -> (out [T, H] bf16, num_invalid [1] int32: entries neither -1 nor in
+    [0, E))."""
+    _need(x, "x", torch.bfloat16, 2)
+    _need(topk_idx, "topk_idx", torch.int32, 2)
+    T, H = x.shape
+    if topk_idx.shape[0] != T:
+        raise ValueError("x and topk_idx disagree on the number of tokens")
+    K = topk_idx.shape[1]
+    if topk_weights is not None:
+        _need(topk_weights, "topk_weights", torch.float32, 2)
+        if tuple(topk_weights.shape) != (T, K):
+            raise ValueError("topk_weights must be [T, K]")
+    if up_scales is None and down_scales is None:
+        _need(up, "up", torch.bfloat16, 3)
+        _need(down, "down", torch.bfloat16, 3)
+        uH, I = up.shape[2], down.shape[2]
+    else:
+        if up_scales is None or down_scales is None:
+            raise ValueError("up and down are both in bf16 or both in MXFP4")
+        (mu, uH), (md, I) = _need_codes(up, up_scales, "up", 3), _need_codes(down, down_scales, "down", 3)
+        if mu != "mxfp4_e2m1" or md != "mxfp4_e2m1":
+            raise ValueError("up and down must be in MXFP4 (uint8 codes)")
+    E = up.shape[0]
+    if uH != H or tuple(up.shape[:2]) != (E, 2 * I) or tuple(down.shape[:2]) != (E, H):
+        raise ValueError(f"up must be [E, 2I, H] and down [E, H, I] with H = {H}")
+    dev = x.device
+    _same_device(dev, topk_idx=topk_idx, topk_weights=topk_weights, up=up, down=down, up_scales=up_scales,
+                 down_scales=down_scales)
+    out = _rows_out(out, (T, H), torch.bfloat16, dev, x=x, topk_idx=topk_idx, topk_weights=topk_weights, up=up,
+                    down=down, up_scales=up_scales, down_scales=down_scales)
+    ninv = torch.empty(1, dtype=torch.int32, device=dev)
+    ws_bytes = _few_bytes(T, K, E, H, I)
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    with _on(dev):
+        N.ep_low_latency_experts(_ptr(x), T, H, _ptr(topk_idx), _ptr(topk_weights), K, _ptr(up), _ptr(up_scales),
+                                 _ptr(down), _ptr(down_scales), E, I, _ptr(out), _ptr(ninv), _ptr(ws), ws_bytes,
+                                 _stream(dev))
+    return out, ninv

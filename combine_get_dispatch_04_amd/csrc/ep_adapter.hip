@@ -39,112 +39,6 @@ namespace ep {
 
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-constexpr int BK = 64;                 // inner elements per stage: two slices of 32, one MFMA each
-
-// ---------------------------------------------------------------- LDS tiles
-// A tile of rows with 64 consecutive inner elements: 8 pieces of 16 bytes per
-// row, piece c of row r in slot c ^ (r & 7), so that the 16 rows a fragment
-// reads at one c spread over the banks.
-__device__ __forceinline__ int off_k(int row, int piece)
-{
-    return row * 128 + ((piece ^ (row & 7)) << 4);
-}
-// A tile of 64 inner rows with consecutive columns, read transposed: blocks
-// of 64 columns, each 64 rows of 128 bytes, so that the loads fetch whole
-// 128-byte lines of 8 rows at a time as above.  A row has 4 units of 16
-// columns (32 bytes), unit u of row k in slot u ^ g(k).  A transposing read
-// takes rows {0..3, 8..11, 16..19, 24..27} of one unit: the row's parity and
-// g tell eight of them apart.
-__device__ __forceinline__ int unit_swizzle(int k) { return ((k >> 1) & 1) | ((k >> 2) & 2); }
-__device__ __forceinline__ int off_n(int k, int unit)
-{
-    return (unit >> 2) * (BK * 128) + k * 128 + (((unit & 3) ^ unit_swizzle(k)) << 5);
-}
-// A lane's operand of one 16 x 32 fragment: 8 consecutive inner elements from
-// ks*32 + (lane >> 4)*8, of row (or column) lane & 15 of its 16.  The lane's
-// own offset is worked out once (at_k, at_n); fragments, stages and halves are
-// constants on top of it, as row0 is a multiple of 16 and g(k) the same for k,
-// k + 4 and k + 32.
-__device__ __forceinline__ int at_k(int ks, int lane)
-{
-    return off_k(lane & 15, ks * 4 + (lane >> 4));
-}
-__device__ __forceinline__ bf16x8 frag_k(const char *tile, int row0, int at)
-{
-    return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(tile + row0 * 128 + at));
-}
-__device__ __forceinline__ int at_n(int unit, int lane)
-{
-    return off_n((lane >> 4) * 8 + ((lane & 15) >> 2), unit) + (lane & 3) * 8;
-}
-__device__ __forceinline__ bf16x8 frag_n(const char *tile, int ks, int at)
-{
-    typedef __attribute__((address_space(3))) s16x4 *lds4_ptr;
-    typedef short s16x8 __attribute__((ext_vector_type(8)));
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_ptr)(tile + at + ks * 32 * 128));
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_ptr)(tile + at + (ks * 32 + 4) * 128));
-    const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-    return __builtin_bit_cast(bf16x8, v);
-}
-// The operands of N neighbouring units at once, while loads into LDS are in
-// flight: the compiler would wait for those before each transposing read of
-// its own (it cannot tell their buffers apart), so the reads and their wait are
-// one block of assembly.  `at` is unit 0's address; unit j's differs in bits 5
-// and 6, the other half of a fragment lies 4 rows (512 bytes) on, slice 1 32
-// rows (4096 bytes).
-template <int KS>
-__device__ __forceinline__ void frags_n(const char *tile, int at, bf16x8 (&b)[4])
-{
-    typedef __attribute__((address_space(3))) const char *lds_char;
-    const uint32_t base = (uint32_t)(uintptr_t)(lds_char)tile;
-    const uint32_t p0 = base + at, p1 = base + (at ^ 32), p2 = base + (at ^ 64), p3 = base + (at ^ 96);
-    typedef uint32_t u2 __attribute__((ext_vector_type(2)));
-    u2 r0, r1, r2, r3, r4, r5, r6, r7;
-    asm volatile("ds_read_b64_tr_b16 %0, %8 offset:%12\n\t"
-                 "ds_read_b64_tr_b16 %1, %8 offset:%13\n\t"
-                 "ds_read_b64_tr_b16 %2, %9 offset:%12\n\t"
-                 "ds_read_b64_tr_b16 %3, %9 offset:%13\n\t"
-                 "ds_read_b64_tr_b16 %4, %10 offset:%12\n\t"
-                 "ds_read_b64_tr_b16 %5, %10 offset:%13\n\t"
-                 "ds_read_b64_tr_b16 %6, %11 offset:%12\n\t"
-                 "ds_read_b64_tr_b16 %7, %11 offset:%13\n\t"
-                 "s_waitcnt lgkmcnt(0)"
-                 : "=&v"(r0), "=&v"(r1), "=&v"(r2), "=&v"(r3), "=&v"(r4), "=&v"(r5), "=&v"(r6), "=&v"(r7)
-                 : "v"(p0), "v"(p1), "v"(p2), "v"(p3), "n"(KS * 4096), "n"(KS * 4096 + 512)
-                 : "memory");
-    b[0] = __builtin_bit_cast(bf16x8, u32x4{r0[0], r0[1], r1[0], r1[1]});
-    b[1] = __builtin_bit_cast(bf16x8, u32x4{r2[0], r2[1], r3[0], r3[1]});
-    b[2] = __builtin_bit_cast(bf16x8, u32x4{r4[0], r4[1], r5[0], r5[1]});
-    b[3] = __builtin_bit_cast(bf16x8, u32x4{r6[0], r6[1], r7[0], r7[1]});
-}
-template <int KS>
-__device__ __forceinline__ void frags_n(const char *tile, int at, bf16x8 (&b)[2])
-{
-    typedef __attribute__((address_space(3))) const char *lds_char;
-    const uint32_t base = (uint32_t)(uintptr_t)(lds_char)tile;
-    const uint32_t p0 = base + at, p1 = base + (at ^ 32);
-    typedef uint32_t u2 __attribute__((ext_vector_type(2)));
-    u2 r0, r1, r2, r3;
-    asm volatile("ds_read_b64_tr_b16 %0, %4 offset:%6\n\t"
-                 "ds_read_b64_tr_b16 %1, %4 offset:%7\n\t"
-                 "ds_read_b64_tr_b16 %2, %5 offset:%6\n\t"
-                 "ds_read_b64_tr_b16 %3, %5 offset:%7\n\t"
-                 "s_waitcnt lgkmcnt(0)"
-                 : "=&v"(r0), "=&v"(r1), "=&v"(r2), "=&v"(r3)
-                 : "v"(p0), "v"(p1), "n"(KS * 4096), "n"(KS * 4096 + 512)
-                 : "memory");
-    b[0] = __builtin_bit_cast(bf16x8, u32x4{r0[0], r0[1], r1[0], r1[1]});
-    b[1] = __builtin_bit_cast(bf16x8, u32x4{r2[0], r2[1], r3[0], r3[1]});
-}
-__device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c)
-{
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
-
 // ---------------------------------------------------------------- a block's product
 // BM tokens x BN columns, WM x WN waves.  acc[i][j]: token i*16 + (lane & 15)
 // of the wave's rows, columns j*16 + (lane >> 4)*4 ..+3 of its columns.  The
@@ -162,18 +56,6 @@ __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c)
 // once would keep the matrix pipe waiting for the memory pipe to take them.
 // One barrier per stage, some groups into its second slice, when every wave
 // holds the rest of the stage in registers: its buffer is free.
-typedef __attribute__((address_space(1))) const void *global_ptr;
-typedef __attribute__((address_space(3))) void *lds_ptr;
-
-template <int N>
-__device__ __forceinline__ void wait_and_meet()     // at most N loads in flight, no LDS access
-{
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
-
 template <int BM_, int BN_, int WM_, int WN_, int NS_, bool NN>
 struct Product {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_;
@@ -381,16 +263,6 @@ struct Product {
         return s == 0.0f;       // an infinity or a NaN anywhere makes it NaN
     }
 };
-
-__host__ __device__ __forceinline__ int least(int a, int b) { return a < b ? a : b; }
-
-// Blocks are dealt to the 8 XCDs in turn; this gives each XCD a run of
-// consecutive tiles, so that its L2 sees the operands they share.
-__device__ __forceinline__ int xcd_order(int b, int n)
-{
-    const int each = n / 8, rest = n % 8, x = b % 8;
-    return x * each + least(x, rest) + b / 8;
-}
 
 // ---------------------------------------------------------------- tiles
 struct Tiles {

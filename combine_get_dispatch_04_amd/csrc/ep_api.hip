@@ -681,4 +681,185 @@ ep_status_t ep_adapter_project_backward(const uint16_t *d_out, const uint16_t *x
         static_cast<char *>(ws), static_cast<hipStream_t>(stream)));
 }
 
+// ---------------------------------------------------------------- microscaled tensors
+namespace {
+
+bool is_mx(ep_quant_t quant)
+{
+    return quant == EP_QUANT_MXFP8_E4M3 || quant == EP_QUANT_MXFP8_E5M2 || quant == EP_QUANT_MXFP4_E2M1;
+}
+
+ep_status_t check_mx(const void *bf16, int rows, int H, ep_quant_t quant, const void *codes, const uint8_t *scales)
+{
+    if (rows < 0 || H < 32 || H % 32 != 0 || !is_mx(quant))
+        return EP_ERR_INVALID_ARG;
+    if (H > kMaxHidden || (int64_t)rows * (H / 8) > (int64_t)1 << 33)
+        return EP_ERR_UNSUPPORTED;
+    if (rows > 0 && (!bf16 || !codes || !scales))
+        return EP_ERR_INVALID_ARG;
+    if (!aligned(bf16, 16) || !aligned(codes, 16))
+        return EP_ERR_INVALID_ARG;
+    return EP_OK;
+}
+
+}  // namespace
+
+ep_status_t ep_mx_quantize(const uint16_t *x, int rows, int H, ep_quant_t quant, void *codes, uint8_t *scales,
+                           void *stream)
+{
+    const ep_status_t st = check_mx(x, rows, H, quant, codes, scales);
+    if (st != EP_OK)
+        return st;
+    return hip_status(ep::launch_mx_quantize(x, rows, H, quant, codes, scales, static_cast<hipStream_t>(stream)));
+}
+
+ep_status_t ep_mx_dequantize(const void *codes, const uint8_t *scales, int rows, int H, ep_quant_t quant,
+                             uint16_t *out, void *stream)
+{
+    const ep_status_t st = check_mx(out, rows, H, quant, codes, scales);
+    if (st != EP_OK)
+        return st;
+    return hip_status(ep::launch_mx_dequantize(codes, scales, rows, H, quant, out, static_cast<hipStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------- the experts' products
+namespace {
+
+// The rows, the weight, and the sizes of both directions.
+ep_status_t check_expert(const void *x, const uint8_t *x_scales, ep_quant_t x_quant, int rows, const uint8_t *weight,
+                         const uint8_t *weight_scales, int E, int O, int H, const int32_t *offsets,
+                         const int32_t *counts, int cap, ep_activation_t activation)
+{
+    if (rows < 0 || E < 1 || H < 32 || H % 32 != 0 || O < 8 || (x_quant != EP_QUANT_BF16 && !is_mx(x_quant)) ||
+        (activation != EP_ACT_NONE && activation != EP_ACT_SWIGLU))
+        return EP_ERR_INVALID_ARG;
+    if (O % (activation == EP_ACT_SWIGLU ? 16 : 8) != 0)
+        return EP_ERR_INVALID_ARG;
+    // rows by offsets, or E * cap of them
+    if (offsets ? (counts || cap != 0) : (cap < 0 || (int64_t)E * cap != rows))
+        return EP_ERR_INVALID_ARG;
+    if (E > kMaxExperts || H > ep::kMaxAdapterWidth || O > ep::kMaxAdapterWidth || (int64_t)O * H >= (int64_t)1 << 32)
+        return EP_ERR_UNSUPPORTED;
+    // tiles of 32 rows and more by 64 columns and more, 256 threads each: 32-bit grids
+    const int64_t tiles = ((int64_t)rows + 31) / 32 + E, blocks = ((H > O ? H : O) + 63) / 64;
+    if (tiles * blocks >= 1 << 23)
+        return EP_ERR_UNSUPPORTED;
+    if (!weight || !weight_scales || (rows > 0 && (!x || (x_quant != EP_QUANT_BF16 && !x_scales))))
+        return EP_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(weight, 16) || !aligned(offsets, 4) || !aligned(counts, 4))
+        return EP_ERR_INVALID_ARG;
+    return EP_OK;
+}
+
+}  // namespace
+
+ep_status_t ep_expert_product(const void *x, const uint8_t *x_scales, ep_quant_t x_quant, int rows,
+                              const uint8_t *weight, const uint8_t *weight_scales, int E, int O, int H,
+                              const int32_t *offsets, const int32_t *counts, int cap, ep_activation_t activation,
+                              ep_quant_t y_quant, void *y, uint8_t *y_scales, void *stream)
+{
+    const ep_status_t st = check_expert(x, x_scales, x_quant, rows, weight, weight_scales, E, O, H, offsets, counts,
+                                        cap, activation);
+    if (st != EP_OK)
+        return st;
+    const bool gated = activation == EP_ACT_SWIGLU;
+    const int width = gated ? O / 2 : O;
+    const bool coded = y_quant != EP_QUANT_BF16;
+    if ((coded && !is_mx(y_quant)) || (coded && width % 32 != 0) || (rows > 0 && (!y || (coded && !y_scales))) ||
+        !aligned(y, 16))
+        return EP_ERR_INVALID_ARG;
+    if (rows == 0)
+        return EP_OK;
+    const ep::ExpertRows m{offsets, counts, rows, cap, E};
+    const ep::ExpertIn in{x, x_scales, weight, weight_scales, O, H, gated ? O / 2 : 0};
+    const ep::ExpertOut out{y, y_scales, nullptr, width, gated ? ep::kExpertGated : ep::kExpertPlain, y_quant};
+    return hip_status(ep::launch_expert(m, in, out, x_quant, static_cast<hipStream_t>(stream)));
+}
+
+size_t ep_expert_workspace_bytes(int rows, int O, ep_activation_t activation)
+{
+    if (rows < 0 || O < 8 || (activation != EP_ACT_NONE && activation != EP_ACT_SWIGLU))
+        return 0;
+    return activation == EP_ACT_SWIGLU && rows > 0 ? ep::align256((size_t)rows * O * 2) : 256;
+}
+
+ep_status_t ep_expert_product_backward(const uint16_t *d_y, const void *x, const uint8_t *x_scales,
+                                       ep_quant_t x_quant, int rows, const uint8_t *weight,
+                                       const uint8_t *weight_scales, int E, int O, int H, const int32_t *offsets,
+                                       const int32_t *counts, int cap, ep_activation_t activation, uint16_t *dx,
+                                       void *ws, size_t ws_bytes, void *stream)
+{
+    // without an activation the rows themselves are not read
+    const bool gated = activation == EP_ACT_SWIGLU;
+    ep_status_t st = check_expert(gated ? x : d_y, gated ? x_scales : nullptr, gated ? x_quant : EP_QUANT_BF16, rows,
+                                  weight, weight_scales, E, O, H, offsets, counts, cap, activation);
+    if (st != EP_OK)
+        return st;
+    if ((rows > 0 && (!d_y || !dx)) || !aligned(d_y, 16) || !aligned(dx, 16))
+        return EP_ERR_INVALID_ARG;
+    if ((st = check_ws(ws, ws_bytes, ep_expert_workspace_bytes(rows, O, activation))) != EP_OK)
+        return st;
+    if (rows == 0)
+        return EP_OK;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const ep::ExpertRows m{offsets, counts, rows, cap, E};
+    const void *d = d_y;
+    if (gated) {
+        const ep::ExpertIn in{x, x_scales, weight, weight_scales, O, H, O / 2};
+        const ep::ExpertOut out{ws, nullptr, d_y, O / 2, ep::kExpertGrad, EP_QUANT_BF16};
+        if ((st = hip_status(ep::launch_expert(m, in, out, x_quant, s))) != EP_OK)
+            return st;
+        d = ws;
+    }
+    const ep::ExpertIn in{d, nullptr, weight, weight_scales, O, H, 0};
+    const ep::ExpertOut out{dx, nullptr, nullptr, H, ep::kExpertPlain, EP_QUANT_BF16};
+    return hip_status(ep::launch_expert_across(m, in, out, s));
+}
+
+// ---------------------------------------------------------------- a few tokens' layer
+namespace {
+
+ep_status_t check_few_sizes(int T, int K, int E, int H, int I)
+{
+    if (T < 0 || K < 1 || E < 1 || H < 8 || H % 8 != 0 || I < 8 || I % 8 != 0)
+        return EP_ERR_INVALID_ARG;
+    if (T > ep::kFewTokens || (int64_t)T * K > ep::kLlMaxEntries || K > ep::kLlMaxTopk || E > kMaxExperts ||
+        H > ep::kMaxAdapterWidth || I > ep::kMaxAdapterWidth)
+        return EP_ERR_UNSUPPORTED;
+    const int64_t most = (int64_t)T * K < E ? (int64_t)T * K : E;
+    if (most * ((H > I ? H : I) / 16 + 1) >= 1 << 22)       // blocks of up to 512 threads: 32-bit grids
+        return EP_ERR_UNSUPPORTED;
+    return EP_OK;
+}
+
+}  // namespace
+
+size_t ep_low_latency_experts_workspace_bytes(int T, int K, int E, int H, int I)
+{
+    return check_few_sizes(T, K, E, H, I) == EP_OK ? ep::make_few_plan(T, K, E, H, I).bytes : 0;
+}
+
+ep_status_t ep_low_latency_experts(const uint16_t *x, int T, int H, const int32_t *topk_idx,
+                                   const float *topk_weights, int K, const void *up, const uint8_t *up_scales,
+                                   const void *down, const uint8_t *down_scales, int E, int I, uint16_t *out,
+                                   int32_t *num_invalid, void *ws, size_t ws_bytes, void *stream)
+{
+    ep_status_t st = check_few_sizes(T, K, E, H, I);
+    if (st != EP_OK)
+        return st;
+    const bool coded = up_scales || down_scales;
+    if (coded && (!up_scales || !down_scales || H % 32 != 0 || I % 32 != 0))
+        return EP_ERR_INVALID_ARG;
+    if (!up || !down || !num_invalid || (T > 0 && (!x || !topk_idx || !out)))
+        return EP_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(up, 16) || !aligned(down, 16) || !aligned(out, 16) || !aligned(topk_idx, 4) ||
+        !aligned(topk_weights, 4) || !aligned(num_invalid, 4))
+        return EP_ERR_INVALID_ARG;
+    const ep::FewPlan p = ep::make_few_plan(T, K, E, H, I);
+    if ((st = check_ws(ws, ws_bytes, p.bytes)) != EP_OK)
+        return st;
+    return hip_status(ep::launch_few(p, x, topk_idx, topk_weights, up, up_scales, down, down_scales, out, num_invalid,
+                                     static_cast<char *>(ws), static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "ep_common.h"
+
 namespace ep {
 
 // How the layout splits topk_idx: blocks ("chunks") of CT whole tokens.
@@ -160,6 +162,58 @@ hipError_t launch_adapter_backward(const AdapterPlan &p, const uint16_t *d_out, 
                                    uint16_t *dx, uint16_t *da, uint16_t *db, float *dw, char *ws,
                                    hipStream_t s);
 
+// Microscaled tensors (ep_mx.hip): `mode` one of the kQuantMx* modes.
+hipError_t launch_mx_quantize(const uint16_t *x, int64_t rows, int H, int mode, void *codes, uint8_t *scales,
+                              hipStream_t s);
+hipError_t launch_mx_dequantize(const void *codes, const uint8_t *scales, int64_t rows, int H, int mode,
+                                uint16_t *out, hipStream_t s);
+
+// The experts' products (ep_expert.hip).  Rows of expert e: [offsets[e],
+// offsets[e+1]) of `rows`, or, with offsets NULL, the first counts[e] (all, if
+// NULL) of the `cap` rows from e * cap on.
+struct ExpertRows {
+    const int32_t *offsets, *counts;
+    int rows, cap, E;
+};
+struct ExpertIn {
+    const void *x;              // rows, in bf16 or codes
+    const uint8_t *x_scales;
+    const uint8_t *w, *w_scales;    // [E, O, H] in MXFP4
+    int O, H;
+    int half;                   // O / 2 where rows o and half + o of W are needed together, else 0
+};
+constexpr int kExpertPlain = 0, kExpertGated = 1, kExpertGrad = 2;
+struct ExpertOut {
+    void *y;
+    uint8_t *scales;
+    const uint16_t *d;          // kExpertGrad: the gradient of the gated rows
+    int width, kind, quant;     // columns of a row of y (kExpertGrad: of d; y has twice as many)
+};
+hipError_t launch_expert(const ExpertRows &m, const ExpertIn &in, const ExpertOut &out, int x_quant, hipStream_t s);
+// dx = W^T x for bf16 rows x of O values.
+hipError_t launch_expert_across(const ExpertRows &m, const ExpertIn &in, const ExpertOut &out, hipStream_t s);
+
+// A whole layer of experts for a few tokens (ep_expert_few.hip).
+constexpr int kFewTokens = 128;
+struct FewPlan {
+    int T, K, E, H, I;
+    int slices;             // blocks of H
+    int most;               // experts that the tokens can name
+    int64_t lower;          // h's lower part, so many elements behind the upper one
+    size_t off_arrived, off_named, off_expert, off_count, off_entry, off_coef, off_h, off_part, bytes;
+};
+// What the first launch leaves for the second: by the place of a named expert.
+struct FewTables {
+    unsigned *arrived;      // [slices]
+    int32_t *named, *expert, *count;
+    int32_t *entry;         // [most, T]
+    float *coef;
+};
+FewPlan make_few_plan(int T, int K, int E, int H, int I);
+hipError_t launch_few(const FewPlan &p, const uint16_t *x, const int32_t *idx, const float *weights, const void *up,
+                      const uint8_t *up_scales, const void *down, const uint8_t *down_scales, uint16_t *out,
+                      int32_t *num_invalid, char *ws, hipStream_t s);
+
 inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // LDS bytes one block may take on the current device (cached per device).
@@ -214,6 +268,185 @@ __device__ __forceinline__ float wave_max_f(float v)
     v = fmaxf(v, dpp_f<0x142, 0xA>(kNegInf, v));
     v = fmaxf(v, dpp_f<0x143, 0xC>(kNegInf, v));
     return last_lane(v);
+}
+
+// ---------------------------------------------------------------- tiles of a matrix product
+// What the adapters' and the experts' products share.
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int BK = 64;                 // inner elements per stage of bf16: two slices of 32, one MFMA each
+
+// ---------------------------------------------------------------- LDS tiles
+// A tile of rows with 64 consecutive inner elements: 8 pieces of 16 bytes per
+// row, piece c of row r in slot c ^ (r & 7), so that the 16 rows a fragment
+// reads at one c spread over the banks.
+__device__ __forceinline__ int off_k(int row, int piece)
+{
+    return row * 128 + ((piece ^ (row & 7)) << 4);
+}
+// A tile of 64 inner rows with consecutive columns, read transposed: blocks
+// of 64 columns, each 64 rows of 128 bytes, so that the loads fetch whole
+// 128-byte lines of 8 rows at a time as above.  A row has 4 units of 16
+// columns (32 bytes), unit u of row k in slot u ^ g(k).  A transposing read
+// takes rows {0..3, 8..11, 16..19, 24..27} of one unit: the row's parity and
+// g tell eight of them apart.
+__device__ __forceinline__ int unit_swizzle(int k) { return ((k >> 1) & 1) | ((k >> 2) & 2); }
+__device__ __forceinline__ int off_n(int k, int unit)
+{
+    return (unit >> 2) * (BK * 128) + k * 128 + (((unit & 3) ^ unit_swizzle(k)) << 5);
+}
+// A lane's operand of one 16 x 32 fragment: 8 consecutive inner elements from
+// ks*32 + (lane >> 4)*8, of row (or column) lane & 15 of its 16.  The lane's
+// own offset is worked out once (at_k, at_n); fragments, stages and halves are
+// constants on top of it, as row0 is a multiple of 16 and g(k) the same for k,
+// k + 4 and k + 32.
+__device__ __forceinline__ int at_k(int ks, int lane)
+{
+    return off_k(lane & 15, ks * 4 + (lane >> 4));
+}
+__device__ __forceinline__ bf16x8 frag_k(const char *tile, int row0, int at)
+{
+    return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(tile + row0 * 128 + at));
+}
+__device__ __forceinline__ int at_n(int unit, int lane)
+{
+    return off_n((lane >> 4) * 8 + ((lane & 15) >> 2), unit) + (lane & 3) * 8;
+}
+__device__ __forceinline__ bf16x8 frag_n(const char *tile, int ks, int at)
+{
+    typedef __attribute__((address_space(3))) s16x4 *lds4_ptr;
+    typedef short s16x8 __attribute__((ext_vector_type(8)));
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_ptr)(tile + at + ks * 32 * 128));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_ptr)(tile + at + (ks * 32 + 4) * 128));
+    const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    return __builtin_bit_cast(bf16x8, v);
+}
+// The operands of N neighbouring units at once, while loads into LDS are in
+// flight: the compiler would wait for those before each transposing read of
+// its own (it cannot tell their buffers apart), so the reads and their wait are
+// one block of assembly.  `at` is unit 0's address; unit j's differs in bits 5
+// and 6, the other half of a fragment lies 4 rows (512 bytes) on, slice 1 32
+// rows (4096 bytes).
+template <int KS>
+__device__ __forceinline__ void frags_n(const char *tile, int at, bf16x8 (&b)[4])
+{
+    typedef __attribute__((address_space(3))) const char *lds_char;
+    const uint32_t base = (uint32_t)(uintptr_t)(lds_char)tile;
+    const uint32_t p0 = base + at, p1 = base + (at ^ 32), p2 = base + (at ^ 64), p3 = base + (at ^ 96);
+    typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+    u2 r0, r1, r2, r3, r4, r5, r6, r7;
+    asm volatile("ds_read_b64_tr_b16 %0, %8 offset:%12\n\t"
+                 "ds_read_b64_tr_b16 %1, %8 offset:%13\n\t"
+                 "ds_read_b64_tr_b16 %2, %9 offset:%12\n\t"
+                 "ds_read_b64_tr_b16 %3, %9 offset:%13\n\t"
+                 "ds_read_b64_tr_b16 %4, %10 offset:%12\n\t"
+                 "ds_read_b64_tr_b16 %5, %10 offset:%13\n\t"
+                 "ds_read_b64_tr_b16 %6, %11 offset:%12\n\t"
+                 "ds_read_b64_tr_b16 %7, %11 offset:%13\n\t"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(r0), "=&v"(r1), "=&v"(r2), "=&v"(r3), "=&v"(r4), "=&v"(r5), "=&v"(r6), "=&v"(r7)
+                 : "v"(p0), "v"(p1), "v"(p2), "v"(p3), "n"(KS * 4096), "n"(KS * 4096 + 512)
+                 : "memory");
+    b[0] = __builtin_bit_cast(bf16x8, u32x4{r0[0], r0[1], r1[0], r1[1]});
+    b[1] = __builtin_bit_cast(bf16x8, u32x4{r2[0], r2[1], r3[0], r3[1]});
+    b[2] = __builtin_bit_cast(bf16x8, u32x4{r4[0], r4[1], r5[0], r5[1]});
+    b[3] = __builtin_bit_cast(bf16x8, u32x4{r6[0], r6[1], r7[0], r7[1]});
+}
+template <int KS>
+__device__ __forceinline__ void frags_n(const char *tile, int at, bf16x8 (&b)[2])
+{
+    typedef __attribute__((address_space(3))) const char *lds_char;
+    const uint32_t base = (uint32_t)(uintptr_t)(lds_char)tile;
+    const uint32_t p0 = base + at, p1 = base + (at ^ 32);
+    typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+    u2 r0, r1, r2, r3;
+    asm volatile("ds_read_b64_tr_b16 %0, %4 offset:%6\n\t"
+                 "ds_read_b64_tr_b16 %1, %4 offset:%7\n\t"
+                 "ds_read_b64_tr_b16 %2, %5 offset:%6\n\t"
+                 "ds_read_b64_tr_b16 %3, %5 offset:%7\n\t"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(r0), "=&v"(r1), "=&v"(r2), "=&v"(r3)
+                 : "v"(p0), "v"(p1), "n"(KS * 4096), "n"(KS * 4096 + 512)
+                 : "memory");
+    b[0] = __builtin_bit_cast(bf16x8, u32x4{r0[0], r0[1], r1[0], r1[1]});
+    b[1] = __builtin_bit_cast(bf16x8, u32x4{r2[0], r2[1], r3[0], r3[1]});
+}
+__device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+typedef __attribute__((address_space(1))) const void *global_ptr;
+typedef __attribute__((address_space(3))) void *lds_ptr;
+
+template <int N>
+__device__ __forceinline__ void wait_and_meet()     // at most N loads in flight, no LDS access
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+__host__ __device__ __forceinline__ int least(int a, int b) { return a < b ? a : b; }
+
+// Blocks are dealt to the 8 XCDs in turn; this gives each XCD a run of
+// consecutive tiles, so that its L2 sees the operands they share.
+__device__ __forceinline__ int xcd_order(int b, int n)
+{
+    const int each = n / 8, rest = n % 8, x = b % 8;
+    return x * each + least(x, rest) + b / 8;
+}
+
+// ---------------------------------------------------------------- microscaled codes
+// What a block's largest magnitude may come to, as a power of two.
+constexpr int mx_top_exponent(int mode) { return mode == kQuantMxE4M3 ? 8 : (mode == kQuantMxE5M2 ? 15 : 2); }
+// The e8m0 code of a block whose largest magnitude is `top`.
+template <int MODE>
+__device__ __forceinline__ uint32_t mx_scale_code(float top)
+{
+    return (uint32_t)(mx_shared_exponent(top, mx_top_exponent(MODE)) + 127);
+}
+// Four 8-bit codes of v * 2^-E, E + 127 = scale_code.  E is at most 127 minus the
+// format's exponent, so 2^-E is a normal number.
+template <int MODE>
+__device__ __forceinline__ uint32_t mx8x4(float a, float b, float c, float d, uint32_t scale_code)
+{
+    constexpr float top = MODE == kQuantMxE4M3 ? 448.0f : 57344.0f;
+    const float m = __uint_as_float((254u - scale_code) << 23);
+    const float p = __builtin_amdgcn_fmed3f(a * m, -top, top), q = __builtin_amdgcn_fmed3f(b * m, -top, top);
+    const float r = __builtin_amdgcn_fmed3f(c * m, -top, top), t = __builtin_amdgcn_fmed3f(d * m, -top, top);
+    return MODE == kQuantMxE4M3 ? e4m3x4(p, q, r, t) : e5m2x4(p, q, r, t);
+}
+// Eight values as bf16.  The conversions read the exponent field of their scale
+// only, and take 0 there as 2^-127.  A code times a scale has at most four
+// significant bits: exact in bf16 down to its subnormals.
+__device__ __forceinline__ u32x4 e2m1_bf16x8(uint32_t codes, uint32_t scale_code)
+{
+    const float s = __uint_as_float(scale_code << 23);
+    return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 0)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 1)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 2)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 3))};
+}
+template <int MODE>
+__device__ __forceinline__ u32x4 mx8_bf16x8(u32x2 codes, uint32_t scale_code)
+{
+    const float s = __uint_as_float(scale_code << 23);
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if constexpr (MODE == kQuantMxE4M3) {
+            v[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[i], s, false));
+            v[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[i], s, true));
+        } else {
+            v[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(codes[i], s, false));
+            v[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(codes[i], s, true));
+        }
+    }
+    return v;
 }
 
 }  // namespace ep

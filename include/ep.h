@@ -568,6 +568,112 @@ ep_status_t ep_adapter_project_backward(const uint16_t *d_out, const uint16_t *x
                                         uint16_t *da, uint16_t *db, float *d_weights, void *ws,
                                         size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The experts: what stands between the dispatch and the combine, in the
+ * microscaled formats that the dispatch's MX modes send (EP_QUANT_MXFP8_E4M3,
+ * EP_QUANT_MXFP8_E5M2, EP_QUANT_MXFP4_E2M1; "MX modes" below).
+ */
+
+/*
+ * ep_mx_quantize, ep_mx_dequantize -- any bf16 tensor of rows of H channels
+ * (weights, activations) to codes and e8m0 scales, and back.
+ *   x       [rows, H] bf16 in; finite (an infinity or NaN gives unspecified codes
+ *           and scale in its block).
+ *   codes   [rows, H] (8-bit modes) or [rows, H/2] (e2m1) uint8, and
+ *   scales  [rows, H/32] uint8: exactly what ep_dispatch writes for the row.
+ *   out     [rows, H] bf16 out: code * 2^(scale - 127), exact down to bf16's
+ *           subnormals.  A scale code of 255 gives unspecified values.
+ * Constraints: H % 32 == 0, H <= 2^24, rows * H <= 2^36; scales have any alignment.
+ */
+ep_status_t ep_mx_quantize(const uint16_t *x, int rows, int H, ep_quant_t quant, void *codes,
+                           uint8_t *scales, void *stream);
+ep_status_t ep_mx_dequantize(const void *codes, const uint8_t *scales, int rows, int H,
+                             ep_quant_t quant, uint16_t *out, void *stream);
+
+typedef int32_t ep_activation_t;
+enum {
+    EP_ACT_NONE = 0,
+    EP_ACT_SWIGLU = 1       /* silu(a) * b, a the first half of the outputs, b the second */
+};
+
+/*
+ * ep_expert_product -- every expert's matrix on the expert's rows:
+ *   a[r, o] = sum over h of W_e[o, h] * x[r, h]          (fp32 sums)
+ *   y[r, :] = a[r, :], or with EP_ACT_SWIGLU  silu(a[r, i]) * a[r, O/2 + i]
+ * rounded once, to bf16 or to codes and scales as ep_mx_quantize makes them
+ * (of the fp32 values).
+ *   x             [rows, H] bf16 in (x_quant EP_QUANT_BF16, x_scales NULL), or
+ *                 codes and scales of an MX mode, as ep_dispatch writes them.
+ *   weight, weight_scales   [E, O, H/2], [E, O, H/32] in: W_e in MXFP4.
+ *   offsets       [E+1] int32 in: expert e's rows are offsets[e] .. offsets[e+1]-1
+ *                 (a contiguous receive buffer; counts NULL, cap 0); or NULL:
+ *   counts, cap   rows = E * cap, expert e's rows are the first counts[e] (at most
+ *                 cap; all cap if counts is NULL) from e * cap on (a padded one).
+ *                 Offsets and counts are cut off at the buffer's ends.
+ *   y, y_scales   [rows, O or O/2] out, laid out like x, in y_quant (bf16, y_scales
+ *                 NULL, or an MX mode); rows that no expert has are neither read
+ *                 nor written.  y must not overlap an input.
+ * A row's result does not depend on the other rows' values, finite or not.
+ * Constraints: H % 32 == 0; O % 8 == 0, with EP_ACT_SWIGLU O % 16 == 0; for an MX
+ * y_quant rows of y are whole blocks of 32; E <= 4096; H, O <= 2^20; O * H < 2^32;
+ * (ceil(rows / 32) + E) * ceil(max(H, O) / 64) < 2^23.
+ */
+ep_status_t ep_expert_product(const void *x, const uint8_t *x_scales, ep_quant_t x_quant, int rows,
+                              const uint8_t *weight, const uint8_t *weight_scales, int E, int O,
+                              int H, const int32_t *offsets, const int32_t *counts, int cap,
+                              ep_activation_t activation, ep_quant_t y_quant, void *y,
+                              uint8_t *y_scales, void *stream);
+
+/*
+ * ep_expert_product_backward -- the gradient of the rows x for d_y [rows, O or
+ * O/2] bf16, the gradient of y.  W is frozen and has none; a quantisation of x or
+ * of y passes the gradient on as it is.  The operands are those of the forward
+ * call.  With EP_ACT_SWIGLU the forward's sums are made again from x, and their
+ * gradient is rounded to bf16 for its product with W; without, x, x_scales and
+ * x_quant are not looked at.
+ *   dx            [rows, H] bf16 out; rows that no expert has are not written.
+ *   ws, ws_bytes  >= ep_expert_workspace_bytes(rows, O, activation); free after the call.
+ */
+size_t ep_expert_workspace_bytes(int rows, int O, ep_activation_t activation);
+ep_status_t ep_expert_product_backward(const uint16_t *d_y, const void *x, const uint8_t *x_scales,
+                                       ep_quant_t x_quant, int rows, const uint8_t *weight,
+                                       const uint8_t *weight_scales, int E, int O, int H,
+                                       const int32_t *offsets, const int32_t *counts, int cap,
+                                       ep_activation_t activation, uint16_t *dx, void *ws,
+                                       size_t ws_bytes, void *stream);
+
+/*
+ * ep_low_latency_experts -- a whole layer of experts for a decode batch, without
+ * dispatch and combine, in two launches:
+ *   h[t, k, i] = silu(a) * b,  a = sum over c of up_e[i, c] * x[t, c],
+ *                b the same with up_e[I + i],  e = topk_idx[t, k]
+ *   out[t, :]  = bf16( sum over k, in that order, of topk_weights[t, k] * down_e h[t, k] )
+ * with fp32 sums; h goes into its product within 2^-16 of its value (as two
+ * bf16).  An expert that a token names twice has its weights summed first.
+ *   x             [T, H] bf16 in.
+ *   topk_idx      [T, K] int32 in: -1 = none; other values outside [0, E) are
+ *                 counted in num_invalid and skipped.
+ *   topk_weights  [T, K] fp32 in or NULL (1).
+ *   up, down      [E, 2I, H], [E, H, I] bf16 in (scales NULL), or both in MXFP4:
+ *                 codes [E, 2I, H/2], [E, H, I/2] with up_scales [E, 2I, H/32],
+ *                 down_scales [E, H, I/32].
+ *   out           [T, H] bf16 out; must not overlap an input.  A token without an
+ *                 expert gives +0.
+ *   num_invalid   [1] int32 out.
+ *   ws, ws_bytes  >= ep_low_latency_experts_workspace_bytes(T, K, E, H, I); free
+ *                 after the call.
+ * A token's result depends on no other token's values.
+ * Limits (EP_ERR_UNSUPPORTED beyond): T <= 128, T*K <= 4096, K <= 64, E <= 4096,
+ * H, I <= 2^20, min(T*K, E) * (max(H, I) / 16 + 1) < 2^22.  H % 8 == 0, I % 8 == 0;
+ * MXFP4 weights: % 32.
+ */
+size_t ep_low_latency_experts_workspace_bytes(int T, int K, int E, int H, int I);
+ep_status_t ep_low_latency_experts(const uint16_t *x, int T, int H, const int32_t *topk_idx,
+                                   const float *topk_weights, int K, const void *up,
+                                   const uint8_t *up_scales, const void *down,
+                                   const uint8_t *down_scales, int E, int I, uint16_t *out,
+                                   int32_t *num_invalid, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

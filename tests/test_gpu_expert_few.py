@@ -1,0 +1,115 @@
+"""The few tokens' layer against the definition in 64 bits."""
+import pytest
+import torch
+
+import expert_ref as R
+from combine_get_dispatch_04_amd import api
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def make(T, K, E, H, I, form, seed=0, same=False):
+    g = torch.Generator().manual_seed(seed)
+    bf = lambda *s, by=1.0: (torch.randn(s, generator=g) * by).to(torch.bfloat16)  # noqa: E731
+    x, up, down = bf(T, H), bf(E, 2 * I, H, by=H ** -0.5), bf(E, H, I, by=I ** -0.5)
+    us = ds = None
+    if form == R.FP4:
+        (up, us), (down, ds) = R.quantize(up, R.FP4), R.quantize(down, R.FP4)
+    if same:        # every token names the same experts
+        idx = torch.arange(K).expand(T, K) % E
+    else:
+        idx = torch.stack([torch.randperm(max(E, K), generator=g)[:K] % E for _ in range(T)])
+    w = torch.softmax(torch.randn((T, K), generator=g), 1)
+    return x, idx.to(torch.int32).contiguous(), w, up, us, down, ds
+
+
+def call(x, idx, w, up, us, down, ds):
+    c = lambda t: None if t is None else t.to(DEV)  # noqa: E731
+    return api.low_latency_experts(c(x), c(idx), c(w), c(up), c(down), up_scales=c(us), down_scales=c(ds))
+
+
+def check(x, idx, w, up, us, down, ds, bad=0):
+    out, n = call(x, idx, w, up, us, down, ds)
+    ref, off = R.layer(x.double(), idx.long(), w, R.values(up, us), R.values(down, ds))
+    R.assert_close(out, ref, off)
+    assert int(n) == bad
+    return out
+
+
+@pytest.mark.parametrize("form", ["bf16", R.FP4])
+@pytest.mark.parametrize("T,K,E", [(1, 1, 1), (1, 8, 16), (2, 2, 3), (7, 4, 5), (8, 1, 1), (9, 1, 1), (16, 2, 2), (17, 1, 1),
+                                   (33, 1, 1), (64, 3, 4), (65, 1, 1), (128, 2, 3), (128, 8, 40)])
+@pytest.mark.parametrize("H,I", [(32, 32), (96, 160), (544, 352)])
+def test_layer(T, K, E, H, I, form):
+    check(*make(T, K, E, H, I, form, seed=T + H))
+
+
+@pytest.mark.parametrize("H,I", [(8, 8), (40, 24), (72, 136), (1000, 8), (8, 1000)])
+def test_bf16_weights_of_odd_sizes(H, I):
+    check(*make(5, 2, 4, H, I, "bf16", seed=H))
+
+
+@pytest.mark.parametrize("form", ["bf16", R.FP4])
+def test_wide_layers_and_many_experts(form):
+    check(*make(3, 6, 8, 4096, 1056, form))
+    check(*make(4, 2, 3, 7168, 96, form))
+    check(*make(64, 64, 700, 64, 32, form))
+    check(*make(2, 3, 4096, 32, 32, form))
+
+
+@pytest.mark.parametrize("form", ["bf16", R.FP4])
+@pytest.mark.parametrize("T", [1, 8, 9, 16, 17, 31, 32, 33, 64, 65, 128])
+def test_every_token_at_one_expert(form, T):
+    check(*make(T, 2, 5, 160, 96, form, seed=T, same=True))
+
+
+@pytest.mark.parametrize("form", ["bf16", R.FP4])
+def test_entries_that_name_nothing_bad_ones_and_doubles(form):
+    x, idx, w, up, us, down, ds = make(20, 5, 6, 64, 96, form)
+    idx[3] = -1                                 # a token without an expert
+    idx[4, 1:] = -1
+    idx[5] = torch.tensor([2, 2, 2, 1, 2])      # the same expert again
+    idx[6] = torch.tensor([6, -2, 2 ** 31 - 1, -2 ** 31, 0])
+    w[7] = 0.0
+    w[8, 2] = -3.0
+    out = check(x, idx, w, up, us, down, ds, bad=4)
+    assert not out[3].any() and not torch.signbit(out[3].float()).any()
+    out, n = call(x, torch.full_like(idx, -1), w, up, us, down, ds)
+    assert not out.any() and int(n) == 0
+    ones = torch.ones_like(w)
+    assert torch.equal(call(x, idx, None, up, us, down, ds)[0], call(x, idx, ones, up, us, down, ds)[0])
+
+
+@pytest.mark.parametrize("form", ["bf16", R.FP4])
+def test_what_is_not_finite_stays_with_its_token(form):
+    x, idx, w, up, us, down, ds = make(24, 2, 3, 96, 64, form)
+    first, _ = call(x, idx, w, up, us, down, ds)
+    x[5, 7], x[11, 3] = float("nan"), float("inf")
+    w[17, 1] = float("nan")
+    out, _ = call(x, idx, w, up, us, down, ds)
+    keep = torch.ones(24, dtype=torch.bool)
+    keep[[5, 11, 17]] = False
+    assert torch.equal(out.cpu()[keep], first.cpu()[keep])
+    assert not torch.isfinite(out[5].float()).any() and torch.isnan(out[17].float()).all()
+    # an expert's weight: the tokens that name it, and no others
+    x, idx, w, up, us, down, ds = make(24, 2, 5, 96, 64, form)
+    first, _ = call(x, idx, w, up, us, down, ds)
+    if form == "bf16":
+        up[2] = float("nan")
+    else:
+        us[2] = 255
+    out, _ = call(x, idx, w, up, us, down, ds)
+    named = (idx == 2).any(1)
+    assert torch.equal(out.cpu()[~named], first.cpu()[~named]) and torch.isnan(out.cpu()[named].float()).all()
+
+
+@pytest.mark.parametrize("form", ["bf16", R.FP4])
+def test_the_same_bits_every_time_and_for_any_company(form):
+    """Twice the same; and a token alone as in a batch whose sizes take the same path."""
+    a = make(16, 4, 9, 256, 160, form)
+    first, _ = call(*a)
+    for _ in range(5):
+        assert torch.equal(first, call(*a)[0])
+    none, n = call(a[0][:0], a[1][:0], a[2][:0], *a[3:])
+    assert none.shape == (0, 256) and int(n) == 0

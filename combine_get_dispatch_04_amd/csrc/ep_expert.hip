@@ -69,32 +69,57 @@ __device__ bool find_tile(const ExpertRows &m, int nb, int group, Tile &t)
         }
     }
     __syncthreads();
-    t = found;
+    // in scalar registers, for the buffers' descriptors
+    t = Tile{__builtin_amdgcn_readfirstlane(found.e), __builtin_amdgcn_readfirstlane(found.first),
+             __builtin_amdgcn_readfirstlane(found.n), __builtin_amdgcn_readfirstlane(found.block)};
     return true;
 }
 
 // ---------------------------------------------------------------- behind the product
-__device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
+// 1 / (1 + exp(-v)) within 2^-21 of its value, by the units' own exponential (of 2) and
+// reciprocal, 7 instructions; what -v log2(e) loses to rounding is made good to first
+// order.  Results below 2^-126 are 0.
+__device__ __forceinline__ float sigmoid(float v)
+{
+    constexpr float l2e = 1.44269504f, ln2 = 0.693147181f, l2e_rest = 1.92596299e-8f;
+    const float t = -v * l2e, rest = fmaf(-v, l2e, -t) - v * l2e_rest;
+    const float p = __builtin_amdgcn_exp2f(t);
+    return __builtin_amdgcn_rcpf(1.0f + fmaf(p, rest * ln2, p));
+}
 
 // What becomes of a wave's sums: acc[i][j] holds row i*16 + (lane & 15) of its
 // TI * 16 rows, columns j*16 + (lane >> 4)*4 ..+3 of the tile's.  With a gate,
-// odd j are the other half's values of j - 1.
-template <int TI, int TJ>
-__device__ __forceinline__ void finish(const ExpertOut &o, f32x4 (&acc)[TI][TJ], const Tile &t, int row0, int c0)
+// odd j are the other half's values of j - 1.  The results go by LDS (`own`, the
+// wave's part of it: TI * TJ * 512 bytes), so that memory gets whole lines of a row
+// and not the few bytes that a lane has of it (at 256 x 256 the stores took 11 of a
+// tile's 46 us).
+template <int KIND, int BITS, int TI, int TJ>
+__device__ __forceinline__ void finish_as(const ExpertOut &o, const f32x4 (&acc)[TI][TJ], const Tile &t, int row0,
+                                          int c0, char *own)
 {
-    const int lane = threadIdx.x & (kWave - 1), at = (lane >> 4) * 4;
+    constexpr bool gated = KIND == kExpertGated, grad = KIND == kExpertGrad;
+    const int lane = threadIdx.x & (kWave - 1), r16 = lane & 15, at = (lane >> 4) * 4;
+    // pieces of 16 bytes in a row of the wave's results; piece c of row r goes to slot
+    // c ^ (the row's 128-byte line, up to 8), so that 16 rows' writes spread over the banks
+    constexpr int per = TJ * 16 / (gated ? 2 : 1) * BITS / 128, rows_in_line = per < 8 ? 8 / per : 1;
+    constexpr int most = per < 8 ? per - 1 : 7;
+    auto place = [&](int row, int byte) {
+        return own + (row * per + ((byte >> 4) ^ (row / rows_in_line & most))) * 16 + (byte & 15);
+    };
+    // of row i * 16 + r16: i is a constant behind it
+    auto put = [&](int i, int byte) { return place(r16, byte) + i * 16 * per * 16; };
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
-        const int r = row0 + i * 16 + (lane & 15);
+        const int r = row0 + i * 16 + r16;
         const bool live = r < t.n;
         const int64_t row = t.first + (live ? r : 0);
-        if (o.kind == kExpertGrad) {
+        if constexpr (grad) {
 #pragma unroll
             for (int j = 0; j + 1 < TJ; j += 2) {
                 const int c = c0 + j * 8 + at;
-                if (!live || c >= o.width)
-                    continue;
-                const u32x2 d2 = *reinterpret_cast<const u32x2 *>(o.d + row * o.width + c);
+                u32x2 d2 = {0u, 0u};
+                if (live && c < o.width)
+                    d2 = *reinterpret_cast<const u32x2 *>(o.d + row * o.width + c);
                 float dg[4], du[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -103,433 +128,527 @@ __device__ __forceinline__ void finish(const ExpertOut &o, f32x4 (&acc)[TI][TJ],
                     dg[q] = d * u * s * (1.0f + g * (1.0f - s));
                     du[q] = d * g * s;
                 }
-                uint16_t *to = static_cast<uint16_t *>(o.y) + row * (2 * (int64_t)o.width) + c;
-                *reinterpret_cast<u32x2 *>(to) = u32x2{pack_bf16_any(dg[0], dg[1]), pack_bf16_any(dg[2], dg[3])};
-                *reinterpret_cast<u32x2 *>(to + o.width) =
+                *reinterpret_cast<u32x2 *>(put(i, (j * 8 + at) * 2)) =
+                    u32x2{pack_bf16_any(dg[0], dg[1]), pack_bf16_any(dg[2], dg[3])};
+                *reinterpret_cast<u32x2 *>(put(i, (TJ * 8 + j * 8 + at) * 2)) =
                     u32x2{pack_bf16_any(du[0], du[1]), pack_bf16_any(du[2], du[3])};
             }
             continue;
         }
         // the output's columns, one fragment of 16 after the other
-        const bool gated = o.kind == kExpertGated;
-        f32x4 v[TJ];
+        constexpr int frags = gated ? TJ / 2 : TJ;
+        f32x4 v[frags];
 #pragma unroll
-        for (int j = 0; j < TJ; ++j) {
-            v[j] = acc[i][j];
-            if (gated && j % 2 == 1) {
+        for (int j = 0; j < frags; ++j) {
+            v[j] = acc[i][gated ? 2 * j : j];
+            if constexpr (gated) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    v[j / 2][q] = acc[i][j - 1][q] * sigmoid(acc[i][j - 1][q]) * acc[i][j][q];
+                    v[j][q] = v[j][q] * sigmoid(v[j][q]) * acc[i][2 * j + 1][q];
             }
         }
-        const int frags = gated ? TJ / 2 : TJ;
-        if (o.quant == kQuantBf16) {
+        if constexpr (BITS == 16) {
 #pragma unroll
-            for (int j = 0; j < TJ; ++j) {
-                const int c = c0 + j * 16 + at;
-                if (j < frags && live && c < o.width)
-                    *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(o.y) + row * o.width + c) =
-                        u32x2{pack_bf16_any(v[j][0], v[j][1]), pack_bf16_any(v[j][2], v[j][3])};
-            }
-            continue;
-        }
-        // blocks of 32 columns: two fragments, in the four lanes of a row
+            for (int j = 0; j < frags; ++j)
+                *reinterpret_cast<u32x2 *>(put(i, (j * 16 + at) * 2)) =
+                    u32x2{pack_bf16_any(v[j][0], v[j][1]), pack_bf16_any(v[j][2], v[j][3])};
+        } else {
+            // blocks of 32 columns: two fragments, in the four lanes of a row
 #pragma unroll
-        for (int j = 0; j + 1 < TJ; j += 2) {
-            if (j >= frags)
-                continue;
-            float top = 0.0f;
+            for (int j = 0; j < frags; j += 2) {
+                float top = 0.0f;
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                top = fmaxf(top, fmaxf(fabsf(v[j][q]), fabsf(v[j + 1][q])));
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            const int c = c0 + j * 16;
-            if (!live || c >= o.width)
-                continue;
-            uint8_t *y = static_cast<uint8_t *>(o.y);
-            uint32_t code;
-            if (o.quant == kQuantMxE2M1) {
-                code = mx_scale_code<kQuantMxE2M1>(top);
-                const float both[8] = {v[j][0], v[j][1], v[j][2], v[j][3],
-                                       v[j + 1][0], v[j + 1][1], v[j + 1][2], v[j + 1][3]};
-                const uint32_t w = e2m1x8_scaled(both, code);
-                uint8_t *to = y + row * (o.width / 2) + (c + at) / 2;
-                *reinterpret_cast<uint16_t *>(to) = (uint16_t)w;
-                *reinterpret_cast<uint16_t *>(to + 8) = (uint16_t)(w >> 16);
-            } else {
-                uint8_t *to = y + row * o.width + c + at;
-                uint32_t lo, hi;
-                if (o.quant == kQuantMxE4M3) {
-                    code = mx_scale_code<kQuantMxE4M3>(top);
-                    lo = mx8x4<kQuantMxE4M3>(v[j][0], v[j][1], v[j][2], v[j][3], code);
-                    hi = mx8x4<kQuantMxE4M3>(v[j + 1][0], v[j + 1][1], v[j + 1][2], v[j + 1][3], code);
+                for (int q = 0; q < 4; ++q)
+                    top = fmaxf(top, fmaxf(fabsf(v[j][q]), fabsf(v[j + 1][q])));
+                top = fmaxf(top, __shfl_xor(top, 16));
+                top = fmaxf(top, __shfl_xor(top, 32));
+                uint32_t code;
+                if constexpr (BITS == 4) {
+                    code = mx_scale_code<kQuantMxE2M1>(top);
+                    const float both[8] = {v[j][0], v[j][1], v[j][2], v[j][3],
+                                           v[j + 1][0], v[j + 1][1], v[j + 1][2], v[j + 1][3]};
+                    const uint32_t w = e2m1x8_scaled(both, code);
+                    *reinterpret_cast<uint16_t *>(put(i, (j * 16 + at) / 2)) = (uint16_t)w;
+                    *reinterpret_cast<uint16_t *>(put(i, (j * 16 + 16 + at) / 2)) = (uint16_t)(w >> 16);
                 } else {
-                    code = mx_scale_code<kQuantMxE5M2>(top);
-                    lo = mx8x4<kQuantMxE5M2>(v[j][0], v[j][1], v[j][2], v[j][3], code);
-                    hi = mx8x4<kQuantMxE5M2>(v[j + 1][0], v[j + 1][1], v[j + 1][2], v[j + 1][3], code);
+                    uint32_t lo, hi;
+                    if (o.quant == kQuantMxE4M3) {
+                        code = mx_scale_code<kQuantMxE4M3>(top);
+                        lo = mx8x4<kQuantMxE4M3>(v[j][0], v[j][1], v[j][2], v[j][3], code);
+                        hi = mx8x4<kQuantMxE4M3>(v[j + 1][0], v[j + 1][1], v[j + 1][2], v[j + 1][3], code);
+                    } else {
+                        code = mx_scale_code<kQuantMxE5M2>(top);
+                        lo = mx8x4<kQuantMxE5M2>(v[j][0], v[j][1], v[j][2], v[j][3], code);
+                        hi = mx8x4<kQuantMxE5M2>(v[j + 1][0], v[j + 1][1], v[j + 1][2], v[j + 1][3], code);
+                    }
+                    *reinterpret_cast<uint32_t *>(put(i, j * 16 + at)) = lo;
+                    *reinterpret_cast<uint32_t *>(put(i, j * 16 + 16 + at)) = hi;
                 }
-                *reinterpret_cast<uint32_t *>(to) = lo;
-                *reinterpret_cast<uint32_t *>(to + 16) = hi;
+                const int c = c0 + j * 16;
+                if (live && lane < 16 && c < o.width)
+                    o.scales[row * (o.width / 32) + c / 32] = (uint8_t)code;
             }
-            if (lane < 16)
-                o.scales[row * (o.width / 32) + c / 32] = (uint8_t)code;
         }
     }
+    // a wave's own results: its writes come before its reads, for the compiler too
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    constexpr int columns = 128 / BITS;         // of a piece
+    const int64_t line = (int64_t)o.width * (grad ? 32 : BITS) / 8;
+#pragma unroll 4
+    for (int p = lane; p < TI * 16 * per; p += kWave) {
+        const int r = p / per, piece = p % per, in_half = grad ? piece % (per / 2) : piece;
+        const int c = c0 + in_half * columns;
+        if (row0 + r < t.n && c < o.width)
+            st16(static_cast<char *>(o.y) + (t.first + row0 + r) * line + (int64_t)c * BITS / 8 +
+                     (in_half == piece ? 0 : (int64_t)o.width * 2),
+                 ld16(place(r, piece * 16)));
+    }
+}
+template <int TI, int TJ>
+__device__ __forceinline__ void finish(const ExpertOut &o, const f32x4 (&acc)[TI][TJ], const Tile &t, int row0, int c0,
+                                       char *own)
+{
+    if (o.kind == kExpertGrad)
+        finish_as<kExpertGrad, 16>(o, acc, t, row0, c0, own);
+    else if (o.quant == kQuantBf16 && o.kind == kExpertGated)
+        finish_as<kExpertGated, 16>(o, acc, t, row0, c0, own);
+    else if (o.quant == kQuantBf16)
+        finish_as<kExpertPlain, 16>(o, acc, t, row0, c0, own);
+    else if (o.quant == kQuantMxE2M1 && o.kind == kExpertGated)
+        finish_as<kExpertGated, 4>(o, acc, t, row0, c0, own);
+    else if (o.quant == kQuantMxE2M1)
+        finish_as<kExpertPlain, 4>(o, acc, t, row0, c0, own);
+    else if (o.kind == kExpertGated)
+        finish_as<kExpertGated, 8>(o, acc, t, row0, c0, own);
+    else
+        finish_as<kExpertPlain, 8>(o, acc, t, row0, c0, own);
 }
 
-// ---------------------------------------------------------------- microscaled rows
-// BM rows x BN weight rows, WM x WN waves, the inner dimension in stages of 256
-// channels (two MFMAs of 128).  A stage's codes go from memory straight to LDS,
-// rows of 128 bytes in 8 pieces of 16, piece c of row r in slot c ^ (r & 7), so
-// that the 16 rows a fragment reads at one c spread over the banks.  8-bit codes
-// have two such tiles, of 128 channels each.  What lies outside a tile's rows or
-// behind the last channel is fetched as zeros (an address outside the buffer).
-// The scales, 8 bytes of a row and stage, go through registers one stage ahead.
+// ---------------------------------------------------------------- a block's product
+// BM rows x BN weight rows, WM x WN waves.  The inner dimension goes in stages of two
+// slices, a slice one MFMA deep: 128 channels of codes, or 32 with bf16 rows.
+//
+//   kRowsMx*     codes by codes, with the scaled MFMAs.
+//   kRowsWide    bf16 rows: the weight's codes are widened to bf16 (exactly) on their
+//                way to LDS.
+//   kRowsAcross  the same for the gradient of the rows, dx = W^T d: the inner
+//                dimension is O, the weight lies across and is read transposed.
+//
+// Codes and bf16 rows go from memory straight to LDS, a slice into one of NS buffers;
+// what lies outside a tile's rows or behind the last channel is fetched as zeros (an
+// address outside the buffer).  A slice's row has 4 pieces of 16 bytes (8 of 8-bit
+// rows), piece c of row r in slot c ^ ((r >> 1) & 3) (c ^ (r & 7)), so that the 16 rows
+// a fragment reads at one place spread over the banks.  What has to be looked at on the way goes through registers,
+// into one of two buffers: the scales of codes (16 bytes of a row, for two stages: a
+// row's request to L2 is 64 bytes whatever it takes of them, and stage by stage they
+// were a third of all requests), a weight that is widened (a block of 32 codes and
+// its scale per thread and piece, a stage at a time).
 //
 // A lane's operand of a 4-bit MFMA is one block of 32 channels, 32 (lane >> 4) ..;
 // of an 8-bit one the channels 16 (lane >> 4) .. and 64 + 16 (lane >> 4) ..; its
 // scale operand belongs to the block 32 (lane >> 4) .. in either case.
-constexpr int kStage = 256;
+//
+// The MFMAs go in TI groups of TJ, one row of fragments each; after a group the
+// row's fragment of the next slice is read into the same registers, and a few of
+// the loads are started, so that LDS, memory and the matrix pipes stay busy
+// together.  One barrier per slice, some groups into it: every wave then holds the
+// slice in registers (its buffer is free), and the next one has arrived.
+constexpr int kRowsMx4 = 0, kRowsMxE4M3 = 1, kRowsMxE5M2 = 2, kRowsWide = 3, kRowsAcross = 4;
 constexpr uint32_t kNowhere = 0x80000000u;      // no buffer is larger than 2^31 bytes
 
-template <int BM_, int BN_, int WM_, int WN_, int NS_, int FORMAT>
-struct MxProduct {
+template <int BM_, int BN_, int WM_, int WN_, int NS_, int KIND>
+struct ExpertProduct {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_;
-    static constexpr bool wide = FORMAT != kQuantMxE2M1;        // 8-bit rows
+    static constexpr bool mx = KIND <= kRowsMxE5M2, wide8 = KIND == kRowsMxE4M3 || KIND == kRowsMxE5M2;
+    static constexpr bool across = KIND == kRowsAcross;
+    static constexpr int slice = mx ? 128 : 32, stage = 2 * slice;      // inner elements
     static constexpr int waves = WM * WN, threads = waves * kWave;
     static constexpr int TI = BM / WM / 16, TJ = BN / WN / 16;
-    static constexpr int bytes_a = BM * (wide ? 256 : 128), bytes_b = BN * 128, bytes = bytes_a + bytes_b;
-    static constexpr int scale_rows = BM + BN, scale_bytes = scale_rows * 8;
-    static constexpr int lds_bytes = NS * bytes + 2 * scale_bytes;
-    static constexpr int CA = bytes_a / 1024 / waves, CB = bytes_b / 1024 / waves, pieces = CA + CB;
-    static constexpr int SR = (scale_rows + threads - 1) / threads;
-    static_assert(CA * waves * 1024 == bytes_a && CB * waves * 1024 == bytes_b, "whole pieces per wave");
+    static constexpr int line_a = wide8 ? 128 : 64;                     // bytes of a row and slice
+    static constexpr int bytes_a = BM * line_a, bytes_b = mx ? BN * 64 : 0, bytes = bytes_a + bytes_b;
+    static constexpr int scale_rows = BM + BN, side_bytes = mx ? scale_rows * 16 : BN * 128;
+    static constexpr int lds_bytes = NS * bytes + 2 * side_bytes;
+    // loads of 1 KB a wave and slice; `pieces` of them at least
+    static constexpr int KA = bytes_a / 1024, CA = (KA + waves - 1) / waves, CB = bytes_b / 1024 / waves;
+    static constexpr int pieces = KA / waves + CB;
+    static constexpr int SR = (scale_rows + threads - 1) / threads, PB = BN * 2 / threads;
+    static_assert(KA * 1024 == bytes_a && CB * waves * 1024 == bytes_b, "whole loads");
+    static_assert(mx || PB * threads == BN * 2, "whole blocks per thread");
     static_assert(TJ % 4 == 0, "a block of 32 gated columns is four fragments of a wave");
+    static_assert(NS % 2 == 0, "a stage's two slices are fetched or not together");
+    static constexpr int LAG = TI > 2 ? 2 : 1;      // groups in front of the barrier
+
+    typedef u32x4 frag_a[wide8 ? 2 : 1];
+    typedef uint32_t scale_set[mx ? TI + TJ : 1];
+    // what goes through registers
+    struct Side {
+        uint64_t scales[mx ? SR : 1][2];
+        u32x4 codes[mx ? 1 : PB];
+        uint32_t cs[mx ? 1 : PB];
+    };
 
     f32x4 acc[TI][TJ];
 
-    __device__ __forceinline__ static f32x4 mfma(const u32x4 &w, int ws, const u32x4 (&x)[wide ? 2 : 1], int xs, f32x4 c)
+    const ExpertIn &in;
+    const Tile &t;
+    char *const lds;
+    int n;                          // slices
+    int lane, wave;
+    rsrc_t ra, rb, rs;
+    uint32_t oa[CA], ob[mx ? CB : PB], os[mx ? 1 : PB];
+    const uint8_t *ps[mx ? SR : 1];
+    int k_a, k_b;                   // a lane's first inner element of a slice in its loads
+
+    // The tile's row q of the weight, or -1.
+    __device__ __forceinline__ int weight_row(int q) const
     {
-        const i32x8 a = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
-        i32x8 b = {(int)x[0][0], (int)x[0][1], (int)x[0][2], (int)x[0][3], 0, 0, 0, 0};
-        if constexpr (wide) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                b[4 + i] = (int)x[1][i];
+        if (in.half == 0) {
+            const int r = t.block * BN + q;
+            return r < in.O ? r : -1;
         }
-        constexpr int fmt = FORMAT == kQuantMxE2M1 ? 4 : (FORMAT == kQuantMxE4M3 ? 0 : 1);
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, fmt, 0, ws, 0, xs);
+        const int r = t.block * (BN / 2) + (q >> 5) * 16 + (q & 15);
+        return r < in.half ? r + ((q >> 4) & 1) * in.half : -1;
     }
 
-    __device__ __forceinline__ void run(char *lds, const ExpertIn &in, const Tile &t)
+    __device__ __forceinline__ ExpertProduct(char *lds_, const ExpertIn &in_, const Tile &t_) : in(in_), t(t_), lds(lds_)
     {
-        const int tid = threadIdx.x, lane = tid & (kWave - 1);
-        const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-        const int H = in.H, HB = H / 32, n = (H + kStage - 1) / kStage;
-        const int row_a = wide ? H : H / 2, row_b = H / 2;      // bytes
-        const uint8_t *const xa = static_cast<const uint8_t *>(in.x) + (int64_t)t.first * row_a;
-        const uint8_t *const wb = in.w + (int64_t)t.e * in.O * row_b;
-        const rsrc_t ra = row_rsrc(xa, t.n * row_a);
-        const rsrc_t rb = row_rsrc(wb, (int)((int64_t)in.O * row_b));
-        // the tile's row q of the weight, or -1
-        auto weight_row = [&](int q) {
-            if (in.half == 0) {
-                const int r = t.block * BN + q;
-                return r < in.O ? r : -1;
-            }
-            const int r = t.block * (BN / 2) + (q >> 5) * 16 + (q & 15);
-            return r < in.half ? r + ((q >> 4) & 1) * in.half : -1;
-        };
-        // A lane's pieces: rows 8 apart, the same piece of each.
-        const int sub = lane >> 3, piece = (lane & 7) ^ sub;
-        uint32_t oa[CA], ob[CB];
+        const int tid = threadIdx.x;
+        lane = tid & (kWave - 1);
+        wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+        const int D = across ? in.O : in.H, HB = in.H / 32;
+        n = (D + stage - 1) / stage * 2;
+        const int row_a = mx ? (wide8 ? D : D / 2) : D * 2, row_b = in.H / 2;       // bytes
+        ra = row_rsrc(static_cast<const uint8_t *>(in.x) + (int64_t)t.first * row_a, t.n * row_a);
+        rb = row_rsrc(in.w + (int64_t)t.e * in.O * row_b, (int)((int64_t)in.O * row_b));
+        // a lane's pieces of the loads into LDS: of 16 rows by 4, or 8 rows by 8
+        const int sub4 = lane >> 2, piece4 = (lane & 3) ^ ((lane >> 3) & 3);
+        const int sub8 = lane >> 3, piece8 = (lane & 7) ^ sub8;
+        k_a = wide8 ? piece8 * 16 : piece4 * (mx ? 32 : 8);
+        k_b = piece4 * 32;
 #pragma unroll
         for (int i = 0; i < CA; ++i) {
-            const int c = i * waves + wave, r = c % (BM / 8) * 8 + sub;
-            oa[i] = r < t.n ? (uint32_t)(r * row_a + c / (BM / 8) * 128 + piece * 16) : kNowhere;
+            const int c = i * waves + wave, r = wide8 ? c * 8 + sub8 : c * 16 + sub4;
+            oa[i] = r < t.n ? (uint32_t)(r * row_a + (wide8 ? piece8 : piece4) * 16) : kNowhere;
         }
+        if constexpr (mx) {
 #pragma unroll
-        for (int i = 0; i < CB; ++i) {
-            const int r = weight_row((i * waves + wave) * 8 + sub);
-            ob[i] = r >= 0 ? (uint32_t)r * row_b + piece * 16 : kNowhere;
-        }
-        char *const mine = lds + wave * 1024;
-        auto fetch = [&](int s) {
-            char *const buf = mine + s % NS * bytes;
-            const int left = H - s * kStage;            // channels
-            const bool whole = left >= kStage;
-#pragma unroll
-            for (int i = 0; i < CA; ++i) {
-                const int k = wide ? (i * waves + wave) / (BM / 8) * 128 + piece * 16 : piece * 32;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr)(buf + i * waves * 1024), 16,
-                                                         whole || k < left ? oa[i] : kNowhere,
-                                                         s * (wide ? 256 : 128), 0, 0);
+            for (int i = 0; i < CB; ++i) {
+                const int r = weight_row((i * waves + wave) * 16 + sub4);
+                ob[i] = r >= 0 ? (uint32_t)r * row_b + piece4 * 16 : kNowhere;
             }
-#pragma unroll
-            for (int i = 0; i < CB; ++i)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr)(buf + bytes_a + i * waves * 1024), 16,
-                                                         whole || piece * 32 < left ? ob[i] : kNowhere, s * 128, 0, 0);
-        };
-        // Scales: 8 of a row and stage, 1.0 where there is none.
-        const uint8_t *ps[SR];
-#pragma unroll
-        for (int i = 0; i < SR; ++i) {
-            const int q = i * threads + tid;
-            ps[i] = nullptr;
-            if (q < BM) {
-                if (q < t.n)
-                    ps[i] = in.x_scales + (int64_t)(t.first + q) * HB;
-            } else if (q < scale_rows) {
-                const int r = weight_row(q - BM);
-                if (r >= 0)
-                    ps[i] = in.w_scales + ((int64_t)t.e * in.O + r) * HB;
-            }
-        }
-        auto load_scales = [&](int s, uint64_t (&v)[SR]) {
+            // rows that the tile does not have take the scales of one that exists:
+            // their results are not stored
 #pragma unroll
             for (int i = 0; i < SR; ++i) {
-                v[i] = 0x7F7F7F7F7F7F7F7Full;
-                if (!ps[i])
-                    continue;
-                if (s * 8 + 8 <= HB)
-                    __builtin_memcpy(&v[i], ps[i] + s * 8, 8);
-                else
-                    for (int b = s * 8; b < HB; ++b) {
-                        const int at = (b & 7) * 8;
-                        v[i] = (v[i] & ~(0xFFull << at)) | ((uint64_t)ps[i][b] << at);
-                    }
-            }
-        };
-        char *const scales = lds + NS * bytes;
-        auto store_scales = [&](int s, const uint64_t (&v)[SR]) {
-#pragma unroll
-            for (int i = 0; i < SR; ++i)
-                if (i * threads + tid < scale_rows)
-                    *reinterpret_cast<uint64_t *>(scales + (s & 1) * scale_bytes + (i * threads + tid) * 8) = v[i];
-        };
-        // Fragments.
-        const int wm = wave / WN, wn = wave % WN;
-        const int r16 = lane & 15, g = lane >> 4;
-        const int fa = (wm * (BM / WM) + r16) * 128, fb = bytes_a + (wn * (BN / WN) + r16) * 128;
-        const int slot0 = (g ^ (r16 & 7)) << 4;         // piece g; piece 4 + g is bit 6 apart
-        const int sa = (wm * (BM / WM) + r16) * 8, sb = (BM + wn * (BN / WN) + r16) * 8;
-#pragma unroll
-        for (int i = 0; i < TI; ++i)
-#pragma unroll
-            for (int j = 0; j < TJ; ++j)
-                acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        uint64_t sc[SR];
-        load_scales(0, sc);
-        for (int s = 0; s < NS - 1 && s < n; ++s)
-            fetch(s);
-        store_scales(0, sc);
-        if (n > 1)
-            load_scales(1, sc);
-        for (int s = 0; s < n; ++s) {
-            if (s + NS - 1 <= n)
-                wait_and_meet<(NS - 2) * pieces>();
-            else
-                wait_and_meet<0>();
-            if (s + 1 < n)
-                store_scales(s + 1, sc);
-            if (s + 2 < n)
-                load_scales(s + 2, sc);
-            if (s + NS - 1 < n)
-                fetch(s + NS - 1);
-            const char *const buf = lds + s % NS * bytes;
-            const char *const sbuf = scales + (s & 1) * scale_bytes;
-            u32x2 qa[TI], qb[TJ];
-#pragma unroll
-            for (int i = 0; i < TI; ++i)
-                qa[i] = *reinterpret_cast<const u32x2 *>(sbuf + sa + i * 128);
-#pragma unroll
-            for (int j = 0; j < TJ; ++j)
-                qb[j] = *reinterpret_cast<const u32x2 *>(sbuf + sb + j * 128);
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                u32x4 b[TJ], a[wide ? 2 : 1];
-#pragma unroll
-                for (int j = 0; j < TJ; ++j)
-                    b[j] = ld16(buf + fb + j * 2048 + (slot0 ^ (ks * 64)));
-#pragma unroll
-                for (int i = 0; i < TI; ++i) {
-                    if constexpr (wide) {
-                        a[0] = ld16(buf + fa + ks * (BM * 128) + i * 2048 + slot0);
-                        a[1] = ld16(buf + fa + ks * (BM * 128) + i * 2048 + (slot0 ^ 64));
-                    } else {
-                        a[0] = ld16(buf + fa + i * 2048 + (slot0 ^ (ks * 64)));
-                    }
-#pragma unroll
-                    for (int j = 0; j < TJ; ++j)
-                        acc[i][j] = mfma(b[j], (int)(qb[j][ks] >> (8 * g)), a, (int)(qa[i][ks] >> (8 * g)), acc[i][j]);
-                }
-            }
-        }
-    }
-};
-
-// ---------------------------------------------------------------- bf16 rows
-// The same with rows in bf16: the weight's codes are widened to bf16 (exactly) on
-// their way to LDS, and the product is one of bf16 MFMAs.  Across = false:
-// y = W x, inner dimension H.  Across = true: the gradient of the rows, dx =
-// W^T d, inner dimension O: the weight lies across and is read transposed.
-// A stage is 64 inner elements.  The rows go from memory straight to LDS; of the
-// weight each thread takes one block of 32 codes and its scale, through registers,
-// one stage ahead.
-template <int BM_, int BN_, int WM_, int WN_, int NS_, bool ACROSS>
-struct WideProduct {
-    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_;
-    static constexpr int waves = WM * WN, threads = waves * kWave;
-    static constexpr int TI = BM / WM / 16, TJ = BN / WN / 16;
-    static constexpr int bytes_a = BM * 128, bytes_b = BN * 128, lds_bytes = NS * bytes_a + 2 * bytes_b;
-    static constexpr int CA = bytes_a / 1024 / waves, PB = BN * 2 / threads;
-    static_assert(CA * waves * 1024 == bytes_a && PB * threads == BN * 2, "whole pieces");
-    static_assert(TJ == 4, "gated blocks of 32, and units read four at a time");
-
-    f32x4 acc[TI][TJ];
-
-    __device__ __forceinline__ void run(char *lds, const ExpertIn &in, const Tile &t)
-    {
-        const int tid = threadIdx.x, lane = tid & (kWave - 1);
-        const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-        const int D = ACROSS ? in.O : in.H, n = (D + BK - 1) / BK;
-        const int HB = in.H / 32;
-        const rsrc_t ra = row_rsrc(static_cast<const uint16_t *>(in.x) + (int64_t)t.first * D, t.n * D * 2);
-        const int sub = lane >> 3, piece = (lane & 7) ^ sub;
-        uint32_t oa[CA];
-#pragma unroll
-        for (int i = 0; i < CA; ++i) {
-            const int r = (i * waves + wave) * 8 + sub;
-            oa[i] = r < t.n ? (uint32_t)(r * D * 2 + piece * 16) : kNowhere;
-        }
-        char *const mine = lds + wave * 1024;
-        auto fetch = [&](int s) {
-            const bool there = s * BK + piece * 8 < D;
-#pragma unroll
-            for (int i = 0; i < CA; ++i)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr)(mine + s % NS * bytes_a + i * waves * 1024), 16,
-                                                         there ? oa[i] : kNowhere, s * BK * 2, 0, 0);
-        };
-        // A thread's blocks: weight row and block of the stage, or (across) inner row
-        // and block of the tile's columns.
-        const uint8_t *const wb = in.w + (int64_t)t.e * in.O * (in.H / 2);
-        const uint8_t *const sb = in.w_scales + (int64_t)t.e * in.O * HB;
-        int row[PB], blk[PB];       // row -1: none
-#pragma unroll
-        for (int i = 0; i < PB; ++i) {
-            const int p = i * threads + tid;
-            if constexpr (ACROSS) {
-                row[i] = p / (BN / 32);
-                blk[i] = t.block * (BN / 32) + p % (BN / 32);
-                if (blk[i] >= HB)
-                    row[i] = -1;
-            } else {
-                const int q = p >> 1;
-                blk[i] = p & 1;
-                if (in.half == 0) {
-                    row[i] = t.block * BN + q < in.O ? t.block * BN + q : -1;
+                const int q = least(i * threads + tid, scale_rows - 1);
+                if (q < BM) {
+                    ps[i] = in.x_scales + (int64_t)(t.first + least(q, t.n - 1)) * HB;
                 } else {
-                    const int r = t.block * (BN / 2) + (q >> 5) * 16 + (q & 15);
-                    row[i] = r < in.half ? r + ((q >> 4) & 1) * in.half : -1;
+                    const int r = weight_row(q - BM);
+                    ps[i] = in.w_scales + ((int64_t)t.e * in.O + (r < 0 ? 0 : r)) * HB;
                 }
             }
-        }
-        u32x4 codes[PB];
-        uint32_t sc[PB];
-        auto load_w = [&](int s) {
-#pragma unroll
-            for (int i = 0; i < PB; ++i) {
-                const int r = ACROSS ? s * BK + row[i] : row[i], b = ACROSS ? blk[i] : s * 2 + blk[i];
-                codes[i] = u32x4{0u, 0u, 0u, 0u};
-                sc[i] = 127u;
-                if (row[i] >= 0 && r < in.O && b < HB) {
-                    const int64_t at = (int64_t)r * HB + b;
-                    codes[i] = ld16(wb + at * 16);
-                    sc[i] = sb[at];
-                }
-            }
-        };
-        char *const lb = lds + NS * bytes_a;
-        auto store_w = [&](int s) {
+        } else {
+            rs = row_rsrc(in.w_scales + (int64_t)t.e * in.O * HB, in.O * HB);
+            // a thread's blocks: weight row and block of the stage, or (across) inner row
+            // and block of the tile's columns
 #pragma unroll
             for (int i = 0; i < PB; ++i) {
                 const int p = i * threads + tid;
-                char *const to = lb + (s & 1) * bytes_b;
+                int r, b;
+                if constexpr (across) {
+                    r = p / (BN / 32);
+                    b = t.block * (BN / 32) + p % (BN / 32);
+                    if (b >= HB)
+                        r = -1;
+                } else {
+                    r = weight_row(p >> 1);
+                    b = p & 1;
+                }
+                os[i] = r >= 0 ? (uint32_t)r * HB + b : kNowhere;
+                ob[i] = r >= 0 ? os[i] * 16 : kNowhere;
+            }
+        }
+    }
+
+    // Starts the wave's load i of slice q into LDS.
+    __device__ __forceinline__ void fetch(int q, int i)
+    {
+        char *const to = lds + q % NS * bytes + wave * 1024;
+        const int D = across ? in.O : in.H;
+        if (i < CA) {
+            if (CA * waves == KA || i * waves + wave < KA)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr)(to + i * waves * 1024), 16,
+                                                         q * slice + k_a < D ? oa[i] : kNowhere, q * line_a, 0, 0);
+        } else if constexpr (mx) {
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr)(to + bytes_a + (i - CA) * waves * 1024), 16,
+                                                     q * slice + k_b < D ? ob[i - CA] : kNowhere, q * 64, 0, 0);
+        }
+    }
+    // What goes through registers, of the stages `s` (codes: 2s and 2s + 1): from memory ...
+    // SHORT: rows may have less than 16 scales (and then there are no further stages).
+    template <bool SHORT>
+    __device__ __forceinline__ void side_load(int s, Side &v) const
+    {
+        const int HB = in.H / 32;
+        if constexpr (mx) {
+            // the row's last sixteen at most (see side_store)
+            const int at = least(s * 16, HB - 16);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const u32x4 v = e2m1_bf16x8(codes[i][c], sc[i]);
-                    if constexpr (ACROSS)
-                        *reinterpret_cast<u32x4 *>(to + off_n(p / (BN / 32), p % (BN / 32) * 2 + (c >> 1)) + (c & 1) * 16) = v;
-                    else
-                        *reinterpret_cast<u32x4 *>(to + off_k(p >> 1, (p & 1) * 4 + c)) = v;
+            for (int i = 0; i < SR; ++i) {
+                if (HB >= 16) {
+                    __builtin_memcpy(v.scales[i], ps[i] + at, 16);
+                    continue;
+                }
+                v.scales[i][0] = v.scales[i][1] = 0;
+                if constexpr (SHORT) {
+#pragma unroll
+                    for (int b = 0; b < 15; ++b)
+                        v.scales[i][b / 8] |= b < HB ? (uint64_t)ps[i][b] << (8 * (b % 8)) : 0;
                 }
             }
-        };
-        const int wm = wave / WN, wn = wave % WN;
-        const int fa = wm * (BM / WM) * 128 + at_k(0, lane);
-        const int fb = ACROSS ? at_n(wn * TJ, lane) : wn * (BN / WN) * 128 + at_k(0, lane);
+        } else {
+#pragma unroll
+            for (int i = 0; i < PB; ++i) {
+                const int p = i * threads + threadIdx.x;
+                const bool there = across ? s * stage + p / (BN / 32) < in.O : s * 2 + (p & 1) < HB;
+                const int step = across ? s * stage * HB : s * 2;
+                v.codes[i] = __builtin_amdgcn_raw_buffer_load_b128(rb, there ? ob[i] : kNowhere, step * 16, 0);
+                v.cs[i] = __builtin_amdgcn_raw_buffer_load_b8(rs, there ? os[i] : kNowhere, step, 0);
+            }
+        }
+    }
+    // ... and to LDS, in `parts` parts.
+    static constexpr int parts = mx ? 1 : PB * 4;
+    __device__ __forceinline__ void side_store(int s, int part, const Side &v) const
+    {
+        char *const to = lds + NS * bytes + (s & 1) * side_bytes;
+        if constexpr (mx) {
+            // behind a row's last scales come zeros: the scale 2^-127, for codes that are
+            // zeros as well.  (Shifted here: behind the load it would be waited for.)
+            const int HB = in.H / 32, over = HB >= 16 && s * 16 > HB - 16 ? (s * 16 - (HB - 16)) * 8 : 0;
+#pragma unroll
+            for (int i = 0; i < SR; ++i) {
+                const int q = i * threads + threadIdx.x;
+                const uint64_t lo = over >= 64 ? v.scales[i][1] >> (over - 64)
+                                    : over > 0 ? v.scales[i][0] >> over | v.scales[i][1] << (64 - over)
+                                               : v.scales[i][0];
+                const uint64_t hi = over >= 64 ? 0 : v.scales[i][1] >> over;
+                // the blocks of a stage's slices side by side, so that a lane reads its own two
+                const uint32_t a = (uint32_t)lo, b = (uint32_t)(lo >> 32), c = (uint32_t)hi, d = (uint32_t)(hi >> 32);
+                if (SR * threads == scale_rows || q < scale_rows)
+                    *reinterpret_cast<u32x4 *>(to + q * 16) =
+                        u32x4{__builtin_amdgcn_perm(b, a, 0x05010400u), __builtin_amdgcn_perm(b, a, 0x07030602u),
+                              __builtin_amdgcn_perm(d, c, 0x05010400u), __builtin_amdgcn_perm(d, c, 0x07030602u)};
+            }
+        } else {
+            const int i = part / 4, c = part % 4, p = i * threads + threadIdx.x;
+            const u32x4 w = e2m1_bf16x8(v.codes[i][c], v.cs[i]);
+            if constexpr (across)
+                *reinterpret_cast<u32x4 *>(to + off_n(p / (BN / 32), p % (BN / 32) * 2 + (c >> 1)) + (c & 1) * 16) = w;
+            else
+                *reinterpret_cast<u32x4 *>(to + off_k(p >> 1, (p & 1) * 4 + c)) = w;
+        }
+    }
+
+    // Fragments of slice q, the KS-th of its stage.
+    __device__ __forceinline__ void read_a(frag_a &a, int q, int i) const
+    {
+        const char *const from = lds + q % NS * bytes + (wave / WN * (BM / WM) + i * 16 + (lane & 15)) * line_a;
+        if constexpr (wide8) {
+            const int slot = ((lane >> 4) ^ (lane & 7)) << 4;       // piece lane >> 4; the one 4 on is bit 6 apart
+            a[0] = ld16(from + slot);
+            a[1] = ld16(from + (slot ^ 64));
+        } else {
+            a[0] = ld16(from + (((lane >> 4) ^ ((lane >> 1) & 3)) << 4));
+        }
+    }
+    template <int KS>
+    __device__ __forceinline__ void read_b(u32x4 (&b)[TJ], int q, int j) const
+    {
+        const char *const side = lds + NS * bytes + ((q >> 1) & 1) * side_bytes;
+        const int row = wave % WN * (BN / WN) + j * 16 + (lane & 15);
+        if constexpr (mx) {
+            b[j] = ld16(lds + q % NS * bytes + bytes_a + row * 64 + (((lane >> 4) ^ ((lane >> 1) & 3)) << 4));
+        } else if constexpr (across) {
+            if (j % 4 != 0)
+                return;
+            bf16x8 v[4];
+            frags_n<KS>(side, at_n(wave % WN * TJ + j, lane), v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                b[j + i] = __builtin_bit_cast(u32x4, v[i]);
+        } else {
+            b[j] = ld16(side + row * 128 + ((((lane >> 4) ^ (lane & 7)) << 4) ^ (KS * 64)));
+        }
+    }
+    // A lane's scales of both slices of stage s, for the wave's fragment f of the rows
+    // (< TI) or the weight.
+    __device__ __forceinline__ uint32_t read_scale(int s, int f) const
+    {
+        const int row = f < TI ? wave / WN * (BM / WM) + f * 16 : BM + wave % WN * (BN / WN) + (f - TI) * 16;
+        return *reinterpret_cast<const uint16_t *>(lds + NS * bytes + ((s >> 1) & 1) * side_bytes +
+                                                   (row + (lane & 15)) * 16 + (s & 1) * 8 + (lane >> 4) * 2);
+    }
+
+    template <int KS>
+    __device__ __forceinline__ void group(int i, const frag_a &x, const u32x4 (&b)[TJ], const scale_set &scale)
+    {
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) {
+            if constexpr (mx) {
+                const i32x8 w = {(int)b[j][0], (int)b[j][1], (int)b[j][2], (int)b[j][3], 0, 0, 0, 0};
+                i32x8 r = {(int)x[0][0], (int)x[0][1], (int)x[0][2], (int)x[0][3], 0, 0, 0, 0};
+                if constexpr (wide8) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        r[4 + c] = (int)x[1][c];
+                }
+                constexpr int fmt = KIND == kRowsMx4 ? 4 : (KIND == kRowsMxE4M3 ? 0 : 1);
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, r, acc[i][j], 4, fmt, KS,
+                                                                             (int)scale[TI + j], KS, (int)scale[i]);
+            } else {
+                acc[i][j] = mfma(__builtin_bit_cast(bf16x8, b[j]), __builtin_bit_cast(bf16x8, x[0]), acc[i][j]);
+            }
+        }
+    }
+
+    // Slice q, the KS-th of its stage: b holds its weight fragments, b_next takes the
+    // next one's.  NEXT: there is another one; FETCH: and a slice NS on.
+    template <int KS, bool NEXT, bool FETCH>
+    __device__ __forceinline__ void step(int q, frag_a (&a)[TI], const u32x4 (&b)[TJ], u32x4 (&b_next)[TJ],
+                                         scale_set &scale, Side &side)
+    {
+#pragma unroll
+        for (int g = 0; g < LAG; ++g)
+            group<KS>(g, a[g], b, scale);
+        if constexpr (!NEXT) {
+#pragma unroll
+            for (int g = LAG; g < TI; ++g)
+                group<KS>(g, a[g], b, scale);
+            return;
+        }
+        if constexpr (FETCH)
+            wait_and_meet<(NS - 2) * pieces>();
+        else
+            wait_and_meet<0>();
+        constexpr int rest = TI - LAG > 0 ? TI - LAG : 1;
+        constexpr int loads = CA + CB;
+        constexpr int RF = (loads + rest - 1) / rest, RN = (TJ + rest - 1) / rest, RP = (parts + rest - 1) / rest;
+        uint32_t next[mx ? TJ : 1];
+        // the stages after the next ones; the next ones' go to LDS below.  (Behind the last
+        // stage the last ones again, not used.)
+        constexpr int lg = mx ? 2 : 1;          // slices of a side's stages
+        const bool turn = !mx || (q & 2);
+        const int sides = mx ? (n + 3) >> 2 : n >> 1;
+        if (KS == 1 && turn)
+            side_load<false>(least((q >> lg) + 2, sides - 1), side);
+#pragma unroll
+        for (int h = 0; h < rest; ++h) {
+            const int g = LAG + h;
+            if (g < TI)
+                group<KS>(g, a[g], b, scale);
+            // not before these MFMAs, which would wait for the reads as well
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int j = h * RN; j < (h + 1) * RN && j < TJ; ++j) {
+                read_b<1 - KS>(b_next, q + 1, j);
+                if constexpr (mx && KS == 1)
+                    next[j] = read_scale(q / 2 + 1, TI + j);
+            }
+#pragma unroll
+            for (int i = h == 0 ? 0 : g; i <= g && i < TI; ++i) {
+                read_a(a[i], q + 1, i);
+                if constexpr (mx && KS == 1)
+                    scale[i] = read_scale(q / 2 + 1, i);
+            }
+            if constexpr (FETCH) {
+#pragma unroll
+                for (int i = h * RF; i < (h + 1) * RF && i < loads; ++i)
+                    fetch(q + NS, i);
+            }
+            if (KS == 0 && turn) {
+#pragma unroll
+                for (int p = h * RP; p < (h + 1) * RP && p < parts; ++p)
+                    side_store((q >> lg) + 1, p, side);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (mx && KS == 1) {
+#pragma unroll
+            for (int j = 0; j < TJ; ++j)
+                scale[TI + j] = next[j];
+        }
+    }
+
+    __device__ __forceinline__ void run()
+    {
 #pragma unroll
         for (int i = 0; i < TI; ++i)
 #pragma unroll
             for (int j = 0; j < TJ; ++j)
                 acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        load_w(0);
-        for (int s = 0; s < NS - 1 && s < n; ++s)
-            fetch(s);
-        store_w(0);
-        if (n > 1)
-            load_w(1);
-        for (int s = 0; s < n; ++s) {
-            if (s + NS - 1 <= n)
-                wait_and_meet<(NS - 2) * CA>();
-            else
-                wait_and_meet<0>();
-            if (s + 1 < n)
-                store_w(s + 1);
-            if (s + 2 < n)
-                load_w(s + 2);
-            if (s + NS - 1 < n)
-                fetch(s + NS - 1);
-            const char *const ba = lds + s % NS * bytes_a, *const bb = lb + (s & 1) * bytes_b;
+        Side first, side;
+        side_load<true>(0, first);
+        side_load<false>(least(1, (mx ? (n + 3) >> 2 : n >> 1) - 1), side);
+        for (int q = 0; q < NS && q < n; ++q)
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                bf16x8 b[TJ];
-                if constexpr (ACROSS) {
-                    if (ks == 0)
-                        frags_n<0>(bb, fb, b);
-                    else
-                        frags_n<1>(bb, fb, b);
-                } else {
+            for (int i = 0; i < CA + CB; ++i)
+                fetch(q, i);
 #pragma unroll
-                    for (int j = 0; j < TJ; ++j)
-                        b[j] = frag_k(bb, j * 16, fb ^ (ks * 64));
-                }
+        for (int p = 0; p < parts; ++p)
+            side_store(0, p, first);
+        if (n >= NS)
+            wait_and_meet<(NS - 1) * pieces>();
+        else
+            wait_and_meet<0>();
+        frag_a a[TI];
+        u32x4 b0[TJ], b1[TJ];
+        scale_set scale;
 #pragma unroll
-                for (int i = 0; i < TI; ++i) {
-                    const bf16x8 a = frag_k(ba, i * 16, fa ^ (ks * 64));
+        for (int j = 0; j < TJ; ++j)
+            read_b<0>(b0, 0, j);
 #pragma unroll
-                    for (int j = 0; j < TJ; ++j)
-                        acc[i][j] = mfma(b[j], a, acc[i][j]);
-                }
-            }
+        for (int i = 0; i < TI; ++i)
+            read_a(a[i], 0, i);
+        if constexpr (mx) {
+#pragma unroll
+            for (int f = 0; f < TI + TJ; ++f)
+                scale[f] = read_scale(0, f);
         }
+        int q = 0;
+        for (; q + NS < n; q += 2) {
+            step<0, true, true>(q, a, b0, b1, scale, side);
+            step<1, true, true>(q + 1, a, b1, b0, scale, side);
+        }
+#pragma unroll 1
+        for (; q + 2 < n; q += 2) {
+            step<0, true, false>(q, a, b0, b1, scale, side);
+            step<1, true, false>(q + 1, a, b1, b0, scale, side);
+        }
+        step<0, true, false>(q, a, b0, b1, scale, side);
+        step<1, false, false>(q + 1, a, b1, b0, scale, side);
     }
 };
 
 template <typename P>
-__global__ void __launch_bounds__(P::threads, P::BM * P::BN >= 256 * 128 ? 2 : 1)
+__global__ void __launch_bounds__(P::threads, P::waves / 4)
 expert_kernel(ExpertRows m, ExpertIn in, ExpertOut out, int nb, int group)
 {
     extern __shared__ __attribute__((aligned(16))) char lds[];
     Tile t;
     if (!find_tile<P::BM>(m, nb, group, t))
         return;
-    P p;
-    p.run(lds, in, t);
+    P p(lds, in, t);
+    p.run();
     const int wave = threadIdx.x / kWave, wm = wave / P::WN, wn = wave % P::WN;
     const int columns = in.half ? P::BN / 2 : P::BN;
-    finish(out, p.acc, t, wm * (P::BM / P::WM), t.block * columns + wn * (columns / P::WN));
+    static_assert(P::BM * P::BN * 2 <= P::lds_bytes, "a tile's results fit where its operands were");
+    __syncthreads();
+    finish(out, p.acc, t, wm * (P::BM / P::WM), t.block * columns + wn * (columns / P::WN),
+           lds + wave * (P::TI * P::TJ * 512));
 }
 
 // Row tiles that there can be.
@@ -563,32 +682,22 @@ hipError_t product(const ExpertRows &m, const ExpertIn &in, const ExpertOut &out
 // An expert's rows on average: what the host knows of them.
 int64_t mean_rows(const ExpertRows &m) { return (m.offsets ? m.rows : (int64_t)m.E * m.cap) / m.E; }
 
-template <int FORMAT>
-hipError_t product_mx(const ExpertRows &m, const ExpertIn &in, const ExpertOut &out, hipStream_t s)
+template <int KIND>
+hipError_t product_any(const ExpertRows &m, const ExpertIn &in, const ExpertOut &out, hipStream_t s)
 {
-    const int cover = in.half ? in.half : in.O;
+    const int cover = KIND == kRowsAcross ? in.H : in.half ? in.half : in.O;
     const int64_t each = mean_rows(m);
     if (each >= 160) {
-        if constexpr (FORMAT == kQuantMxE2M1)
-            return product<MxProduct<256, 256, 2, 4, 2, FORMAT>>(m, in, out, cover, s);
+        if constexpr (KIND == kRowsMxE4M3 || KIND == kRowsMxE5M2)
+            return product<ExpertProduct<128, 256, 2, 2, 4, KIND>>(m, in, out, cover, s);
+        else if constexpr (KIND == kRowsMx4)
+            return product<ExpertProduct<256, 256, 2, 4, 4, KIND>>(m, in, out, cover, s);
         else
-            return product<MxProduct<128, 256, 2, 4, 2, FORMAT>>(m, in, out, cover, s);
+            return product<ExpertProduct<256, 256, 2, 4, 4, KIND>>(m, in, out, cover, s);
     }
     if (each >= 48)
-        return product<MxProduct<128, 128, 2, 2, 2, FORMAT>>(m, in, out, cover, s);
-    return product<MxProduct<32, 128, 2, 2, 4, FORMAT>>(m, in, out, cover, s);
-}
-
-template <bool ACROSS>
-hipError_t product_wide(const ExpertRows &m, const ExpertIn &in, const ExpertOut &out, hipStream_t s)
-{
-    const int cover = ACROSS ? in.H : in.half ? in.half : in.O;
-    const int64_t each = mean_rows(m);
-    if (each >= 160)
-        return product<WideProduct<256, 256, 2, 4, 2, ACROSS>>(m, in, out, cover, s);
-    if (each >= 48)
-        return product<WideProduct<128, 128, 2, 2, 2, ACROSS>>(m, in, out, cover, s);
-    return product<WideProduct<32, 128, 2, 2, 4, ACROSS>>(m, in, out, cover, s);
+        return product<ExpertProduct<128, 128, 2, 2, 4, KIND>>(m, in, out, cover, s);
+    return product<ExpertProduct<32, 128, 2, 2, 6, KIND>>(m, in, out, cover, s);
 }
 
 }  // namespace
@@ -596,16 +705,16 @@ hipError_t product_wide(const ExpertRows &m, const ExpertIn &in, const ExpertOut
 hipError_t launch_expert(const ExpertRows &m, const ExpertIn &in, const ExpertOut &out, int x_quant, hipStream_t s)
 {
     switch (x_quant) {
-        case kQuantBf16: return product_wide<false>(m, in, out, s);
-        case kQuantMxE4M3: return product_mx<kQuantMxE4M3>(m, in, out, s);
-        case kQuantMxE5M2: return product_mx<kQuantMxE5M2>(m, in, out, s);
-        default: return product_mx<kQuantMxE2M1>(m, in, out, s);
+        case kQuantBf16: return product_any<kRowsWide>(m, in, out, s);
+        case kQuantMxE4M3: return product_any<kRowsMxE4M3>(m, in, out, s);
+        case kQuantMxE5M2: return product_any<kRowsMxE5M2>(m, in, out, s);
+        default: return product_any<kRowsMx4>(m, in, out, s);
     }
 }
 
 hipError_t launch_expert_across(const ExpertRows &m, const ExpertIn &in, const ExpertOut &out, hipStream_t s)
 {
-    return product_wide<true>(m, in, out, s);
+    return product_any<kRowsAcross>(m, in, out, s);
 }
 
 }  // namespace ep

@@ -5,8 +5,8 @@
 // with up = [Wg; Wu] [E, 2I, H] and down = Wd [E, H, I] in bf16 or MXFP4.
 //
 // Bound by the weights' bytes: every expert that a token names is read once, by
-// blocks of 32 weight rows (16 gates and their 16 ups in the first launch) that
-// go through all of its tokens.  The n-th named expert's blocks find it
+// blocks of 32 or 128 weight rows (half of them gates and half their ups in the first
+// launch) that go through all of its tokens.  The n-th named expert's blocks find it
 // themselves, from topk_idx; what they found is left for the second launch.
 //
 // The weight rows are the rows of MFMAs, straight from memory to registers, the
@@ -26,86 +26,179 @@ namespace ep {
 
 namespace {
 
-constexpr int kRows = 32;               // weight rows of a block
-constexpr int kMaxWaves = 8;
+constexpr int kMaxWaves = 4;
 
-// What a lane fetches of its weight rows and columns: bf16.
+// A block's columns in LDS, if they fit: rows of bf16, 64 bytes apart beyond their
+// length so that 16 columns' reads spread over the banks.  For MXFP4 weights the
+// pieces of 8 channels lie in the order of their use: of four blocks of 32 their
+// first pieces, their second ones, ...  Zeros behind the last channel.
+template <bool FP4>
+__host__ __device__ __forceinline__ int column_bytes(int D)
+{
+    return FP4 ? (D + 127) / 128 * 256 + 64 : (D + 31) / 32 * 64 + 64;
+}
+template <bool FP4>
+__device__ __forceinline__ int column_place(int piece)
+{
+    return FP4 ? piece / 16 * 256 + (piece & 3) * 64 + (piece >> 2 & 3) * 16 : piece * 16;
+}
+constexpr int kStageBytes = 32 << 10;   // of a block, at most
+
+// F fragments of 16 weight rows by NT of 16 columns, from memory or (STAGED) from LDS.
 // acc[f][n]: rows f*16 + (lane >> 4)*4 ..+3 by column n*16 + (lane & 15).
-template <bool FP4, int NT>
+template <bool FP4, int F, int NT, bool STAGED>
 struct Few {
-    f32x4 acc[2][NT];
+    f32x4 acc[F][NT];
+    const uint8_t *w[F], *scales[F];    // the lane's weight rows
+    const uint16_t *col[NT];            // its columns
+    uint32_t at[NT];                    // the same in LDS
+    const char *lds;
 
-    __device__ __forceinline__ void zero()
+    __device__ __forceinline__ u32x4 column(int n, int piece) const
+    {
+        if constexpr (STAGED)
+            return ld16(lds + at[n] + column_place<FP4>(piece));
+        else
+            return ld16(col[n] + piece * 8);
+    }
+    // Inner elements [32 s0, 32 s1) of D, in blocks of 32.  Every wave of a block comes here:
+    // staged columns, on their way, are met behind its own first loads.
+    __device__ __forceinline__ void run(int s0, int s1, int D)
     {
 #pragma unroll
-        for (int f = 0; f < 2; ++f)
+        for (int f = 0; f < F; ++f)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
                 acc[f][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (FP4)
+            run_fp4(s0, s1, D / 32);
+        else
+            run_bf16(s0, s1, D);
     }
-    // Inner elements [32 s0, 32 s1) of D, in blocks of 32: w[f] and scales[f] are the
-    // lane's weight rows, col[n] its columns.
-    __device__ __forceinline__ void run(const uint8_t *const (&w)[2], const uint8_t *const (&scales)[2],
-                                        const uint16_t *const (&col)[NT], int s0, int s1, int D)
+    // Four blocks at a time, one per 16 lanes.  The weight comes from memory and is asked
+    // for AHEAD steps before its use, the columns from a cache or LDS, one step.  The
+    // scales come sixteen at a time: a row's request is 64 bytes whatever it takes of them.
+    __device__ __forceinline__ void run_fp4(int s0, int s1, int HB)
     {
+        // (128 registers with F = 2, 256 with F = 4)
+        constexpr int SLOTS = 4, AHEAD = F * NT > 2 ? 1 : 3, XS = NT > 1 ? 1 : 2;
+        const int g = (threadIdx.x & (kWave - 1)) >> 4, last = s1 - 1;
+        u32x4 c[SLOTS][F], x[XS][NT][4], sc[F];
+        // behind the last block: the last one again, its columns as zeros and its scales
+        // as 1 (an infinite one times 0 would be a NaN)
+        auto load_w = [&](int s, int slot) {
+            const int b = least(s + g, last);
+#pragma unroll
+            for (int f = 0; f < F; ++f)
+                c[slot][f] = ld16_nt(w[f] + (int64_t)b * 16);
+        };
+        auto load_scales = [&](int s) {
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+                if (s + 16 <= HB) {
+                    __builtin_memcpy(&sc[f], scales[f] + s, 16);
+                } else {        // the lane's own ones
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        sc[f][j] = (uint32_t)scales[f][least(s + 4 * j + g, last)] << (8 * g);
+                }
+            }
+        };
+        auto load_x = [&](int s, int slot) {
+            const int b = STAGED ? s + g : least(s + g, last);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    x[slot][n][q] = column(n, b * 4 + q);
+        };
+        auto multiply = [&](int s, int j, int xslot) {
+            const bool behind = s + g >= s1;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                bf16x8 v[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    v[n] = __builtin_bit_cast(bf16x8, behind ? u32x4{0u, 0u, 0u, 0u} : x[xslot][n][q]);
+#pragma unroll
+                for (int f = 0; f < F; ++f) {
+                    const uint32_t one = behind ? 127u : sc[f][j] >> (8 * g) & 255u;
+                    const bf16x8 a = __builtin_bit_cast(bf16x8, e2m1_bf16x8(c[j][f][q], one));
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        acc[f][n] = mfma(a, v[n], acc[f][n]);
+                }
+            }
+        };
+        if (s0 >= s1) {
+            if constexpr (STAGED)
+                wait_and_meet<0>();
+            return;
+        }
+        load_scales(s0);
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j)
+            load_w(s0 + 4 * j, j);
+        if constexpr (STAGED)
+            wait_and_meet<AHEAD * F>();         // the loads of the columns came before these
+        load_x(s0, 0);
+        for (int s = s0; s < s1; s += 4 * SLOTS) {
+#pragma unroll
+            for (int j = 0; j < SLOTS; ++j) {
+                const int now = s + 4 * j;
+                if (now >= s1)
+                    break;
+                load_w(now + 4 * AHEAD, (j + AHEAD) % SLOTS);
+                if constexpr (XS == 2) {
+                    if (now + 4 < s1)
+                        load_x(now + 4, (j + 1) % 2);
+                    multiply(now, j, j % 2);
+                } else {
+                    multiply(now, j, 0);
+                    if (now + 4 < s1)
+                        load_x(now + 4, 0);
+                }
+                if (j == SLOTS - 1 && now + 4 < s1)
+                    load_scales(now + 4);
+            }
+        }
+    }
+    __device__ __forceinline__ void run_bf16(int s0, int s1, int D)
+    {
+        constexpr int U = F * NT > 4 ? 2 : 4;
         const int g = (threadIdx.x & (kWave - 1)) >> 4;
-        if constexpr (FP4) {
-            // four blocks at a time, one per 16 lanes
-            constexpr int U = NT <= 2 ? 2 : 1;
-            for (int s = s0; s < s1; s += 4 * U) {
-                u32x4 c[U][2], x[U][NT][4];
-                uint32_t sc[U][2];
+        u32x4 c[U][F];
+        auto load_w = [&](int s) {
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int b = s + u * 4 + g;
-                    const bool there = b < s1;
+            for (int u = 0; u < U; ++u) {
+                const int k = (s + u) * 32 + g * 8;
 #pragma unroll
-                    for (int f = 0; f < 2; ++f) {
-                        c[u][f] = there ? ld16_nt(w[f] + (int64_t)b * 16) : u32x4{0u, 0u, 0u, 0u};
-                        sc[u][f] = there ? scales[f][b] : 127u;
-                    }
+                for (int f = 0; f < F; ++f)
+                    c[u][f] = s + u < s1 && k < D ? ld16_nt(w[f] + (int64_t)k * 2) : u32x4{0u, 0u, 0u, 0u};
+            }
+        };
+        load_w(s0);
+        if constexpr (STAGED)
+            wait_and_meet<0>();
+        for (int s = s0; s < s1; s += U) {
+            u32x4 x[U][NT];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const bool there = s + u < s1 && (STAGED || (s + u) * 32 + g * 8 < D);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    x[u][n] = there ? column(n, (s + u) * 4 + g) : u32x4{0u, 0u, 0u, 0u};
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int f = 0; f < F; ++f)
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            x[u][n][q] = there ? ld16(col[n] + b * 32 + q * 8) : u32x4{0u, 0u, 0u, 0u};
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-#pragma unroll
-                        for (int f = 0; f < 2; ++f) {
-                            const bf16x8 a = __builtin_bit_cast(bf16x8, e2m1_bf16x8(c[u][f][q], sc[u][f]));
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                acc[f][n] = mfma(a, __builtin_bit_cast(bf16x8, x[u][n][q]), acc[f][n]);
-                        }
-            }
-        } else {
-            constexpr int U = NT <= 2 ? 4 : 2;
-            for (int s = s0; s < s1; s += U) {
-                u32x4 c[U][2], x[U][NT];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int k = (s + u) * 32 + g * 8;
-                    const bool there = s + u < s1 && k < D;
-#pragma unroll
-                    for (int f = 0; f < 2; ++f)
-                        c[u][f] = there ? ld16_nt(w[f] + (int64_t)k * 2) : u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        x[u][n] = there ? ld16(col[n] + k) : u32x4{0u, 0u, 0u, 0u};
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int f = 0; f < 2; ++f)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            acc[f][n] = mfma(__builtin_bit_cast(bf16x8, c[u][f]),
-                                             __builtin_bit_cast(bf16x8, x[u][n]), acc[f][n]);
-            }
+                        acc[f][n] = mfma(__builtin_bit_cast(bf16x8, c[u][f]), __builtin_bit_cast(bf16x8, x[u][n]),
+                                         acc[f][n]);
+            if (s + U < s1)
+                load_w(s + U);
         }
     }
     // Every wave's sums to LDS: red[wave][f][n] of 16 x 16, column by column.
@@ -113,20 +206,20 @@ struct Few {
     {
         const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
 #pragma unroll
-        for (int f = 0; f < 2; ++f)
+        for (int f = 0; f < F; ++f)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                *reinterpret_cast<f32x4 *>(red + (((wave * 2 + f) * NT + n) * 16 + (lane & 15)) * 16 + (lane >> 4) * 4) =
+                *reinterpret_cast<f32x4 *>(red + (((wave * F + f) * NT + n) * 16 + (lane & 15)) * 16 + (lane >> 4) * 4) =
                     acc[f][n];
     }
 };
 // Row r of fragment f, column c, summed over the waves.
-template <int NT>
+template <int F, int NT>
 __device__ __forceinline__ float added(const float *red, int waves, int f, int c, int r)
 {
     float v = 0.0f;
     for (int w = 0; w < waves; ++w)
-        v += red[(((w * 2 + f) * NT + (c >> 4)) * 16 + (c & 15)) * 16 + r];
+        v += red[(((w * F + f) * NT + (c >> 4)) * 16 + (c & 15)) * 16 + r];
     return v;
 }
 
@@ -137,6 +230,146 @@ __device__ __forceinline__ void share(int D, int step, int wave, int waves, int 
     s0 = steps * wave / waves * step;
     s1 = least(steps * (wave + 1) / waves * step, blocks);
 }
+
+// Starts the loads of `n` columns into LDS: column i's bf16 lie at element from(i) of
+// the array, which has less than 2^31 bytes.
+constexpr uint32_t kNowhere = 0x80000000u;
+template <bool FP4, typename C>
+__device__ __forceinline__ void stage_columns(char *to, const uint16_t *array, int64_t elements, int n, int D, C from)
+{
+    const rsrc_t r = row_rsrc(array, (int)(elements * 2));
+    const int slots = column_bytes<FP4>(D) / 16, all = n * slots;
+    const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    for (int p0 = wave * kWave; p0 < all; p0 += blockDim.x) {
+        const int p = p0 + lane, c = least(p / slots, n - 1), slot = p % slots;
+        // column_place's inverse
+        const int piece = FP4 ? (slot & ~15) + (slot & 3) * 4 + (slot >> 2 & 3) : slot;
+        const bool there = p < all && slot < slots - 4 && piece * 8 < D;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(to + p0 * 16), 16,
+                                                 there ? (uint32_t)(from(c) * 2) + piece * 16 : kNowhere, 0, 0, 0);
+    }
+}
+// Whether so many columns of an array can be staged (in whole loads of a wave).
+template <bool FP4>
+__device__ __forceinline__ bool can_stage(const FewPlan &p, int n, int D, int64_t elements)
+{
+    return (n * (int64_t)column_bytes<FP4>(D) + 1023) / 1024 * 1024 <= p.stage_bytes && elements < 1 << 30;
+}
+
+// ---------------------------------------------------------------- some tokens for each expert
+// Where an expert has many tokens, their columns are what the CUs have to take in: a
+// block's four waves then share them, by LDS, and take 32 weight rows each through
+// the whole inner dimension.  Steps of 128 elements; a step's columns are rows of
+// 256 bytes, piece c of column r in slot c ^ (r & 15), loaded three steps ahead, as
+// is the weight (four buffers).
+template <bool FP4, int NT>
+struct Shared {
+    static constexpr int SLOTS = 4, AHEAD = 3, bytes = NT * 4096, WL = FP4 ? 1 : 4;
+    f32x4 acc[2][NT];
+    const uint8_t *w[2], *scales[2];    // the lane's weight rows
+    uint32_t col[NT];                   // offset of the column whose piece the lane loads, or kNowhere
+    rsrc_t from;
+    char *lds;
+
+    __device__ __forceinline__ void run(int D)
+    {
+        const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+        const int g = lane >> 4, n = (D + 127) / 128, HB = D / 32;
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+#pragma unroll
+            for (int c = 0; c < NT; ++c)
+                acc[f][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        u32x4 c[SLOTS][2][WL], sc[2];
+        // the columns behind the last element are zeros; the weight's elements there have
+        // to be finite
+        auto load_w = [&](int s, int slot) {
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                if constexpr (FP4) {
+                    c[slot][f][0] = ld16_nt(w[f] + (int64_t)least(s * 4 + g, HB - 1) * 16);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int k = s * 128 + q * 32 + g * 8;
+                        c[slot][f][q] = k < D ? ld16_nt(w[f] + (int64_t)k * 2) : u32x4{0u, 0u, 0u, 0u};
+                    }
+                }
+            }
+        };
+        auto load_scales = [&](int s) {
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                if (s * 4 + 16 <= HB) {
+                    __builtin_memcpy(&sc[f], scales[f] + s * 4, 16);
+                } else {        // the lane's own ones; 1 behind the last
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int b = (s + j) * 4 + g;
+                        sc[f][j] = (b < HB ? (uint32_t)scales[f][b] : 127u) << (8 * g);
+                    }
+                }
+            }
+        };
+        const int piece = (lane & 15) ^ ((wave * 4 + g) & 15);
+        auto load_x = [&](int s) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_ptr)(lds + s % SLOTS * bytes + (i * 4 + wave) * 1024), 16,
+                                                         s * 128 + piece * 8 < D ? col[i] : kNowhere, s * 256, 0, 0);
+        };
+        auto multiply = [&](int s, int j) {
+            const char *const tile = lds + s % SLOTS * bytes + (lane & 15) * 256;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                bf16x8 x[NT];
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+                    x[i] = __builtin_bit_cast(bf16x8, ld16(tile + i * 4096 + (((FP4 ? g * 4 + q : q * 4 + g) ^ (lane & 15)) << 4)));
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    bf16x8 a;
+                    if constexpr (FP4)
+                        a = __builtin_bit_cast(bf16x8, e2m1_bf16x8(c[j][f][0][q], sc[f][j] >> (8 * g) & 255u));
+                    else
+                        a = __builtin_bit_cast(bf16x8, c[j][f][q]);
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+                        acc[f][i] = mfma(a, x[i], acc[f][i]);
+                }
+            }
+        };
+        if constexpr (FP4)
+            load_scales(0);
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j)
+            if (j < n) {
+                load_x(j);
+                load_w(j, j);
+            }
+        for (int s = 0; s < n; s += SLOTS) {
+#pragma unroll
+            for (int j = 0; j < SLOTS; ++j) {
+                const int now = s + j;
+                if (now >= n)
+                    break;
+                // a step's columns come before its weight and two more steps
+                if (now + AHEAD <= n)
+                    wait_and_meet<(AHEAD - 1) * (NT + 2 * WL) + (FP4 ? 2 : 0)>();
+                else
+                    wait_and_meet<0>();
+                if (now + AHEAD < n) {
+                    load_x(now + AHEAD);
+                    load_w(now + AHEAD, (j + AHEAD) % SLOTS);
+                }
+                multiply(now, j);
+                if (FP4 && j == SLOTS - 1 && now + 1 < n)
+                    load_scales(now + 1);
+            }
+        }
+        __syncthreads();        // the buffers are free
+    }
+};
 
 // ---------------------------------------------------------------- the first launch
 // The n-th of the experts that topk_idx names, ascending, or -1; their number.
@@ -190,59 +423,104 @@ struct Token {
     float coef;         // the weights of all that do
 };
 
-// The tokens that name expert e, in order.  T <= 128: a token per thread of two
-// waves.
+// The tokens that name expert e, in order.  T <= 128: a token per lane, 64 at a time.
 __device__ int tokens_of(const FewPlan &p, const int32_t *idx, const float *w, int e, Token *list, int *counts)
 {
-    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-    int first = -1;
-    float coef = 0.0f;
-    if (tid < p.T)
-        for (int k = 0; k < p.K; ++k)
-            if (idx[tid * p.K + k] == e) {
-                coef += w ? w[tid * p.K + k] : 1.0f;
-                if (first < 0)
-                    first = tid * p.K + k;
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, waves = blockDim.x / kWave;
+    Token mine[2];
+    uint64_t has[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int part = wave + i * waves, t = part * kWave + lane;
+        mine[i] = Token{-1, 0.0f};
+        if (part < 2 && t < p.T) {
+#pragma unroll 8
+            for (int k = p.K - 1; k >= 0; --k) {
+                const bool same = idx[t * p.K + k] == e;
+                const float c = w ? w[t * p.K + k] : 1.0f;
+                mine[i].coef += same ? c : 0.0f;
+                mine[i].entry = same ? t * p.K + k : mine[i].entry;
             }
-    const uint64_t has = ballot(first >= 0);
-    if (wave < 2 && lane == 0)
-        counts[wave] = __popcll(has);
+        }
+        has[i] = ballot(mine[i].entry >= 0);
+        if (part < 2 && lane == 0)
+            counts[part] = __popcll(has[i]);
+    }
     __syncthreads();
-    if (first >= 0)
-        list[(wave ? counts[0] : 0) + lanes_below(has)] = Token{first, coef};
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (mine[i].entry >= 0)
+            list[(wave + i * waves ? counts[0] : 0) + lanes_below(has[i])] = mine[i];
     __syncthreads();
     return counts[0] + counts[1];
 }
+// Each token's entries that stand for an expert, the first of each, as bits, and the
+// number of all: left for the second launch.  `sum`: a word of shared memory.
+__device__ void first_entries(const FewPlan &p, const int32_t *idx, uint64_t *firsts, int *sum, int32_t *total)
+{
+    if (threadIdx.x == 0)
+        *sum = 0;
+    __syncthreads();
+    for (int t = threadIdx.x; t < p.T; t += blockDim.x) {
+        uint64_t m = 0;
+        for (int k = 0; k < p.K; ++k) {
+            const int e = idx[t * p.K + k];
+            bool again = false;
+#pragma unroll 8
+            for (int o = 0; o < k; ++o)
+                again |= idx[t * p.K + o] == e;
+            m |= (uint64_t)((unsigned)e < (unsigned)p.E && !again) << k;
+        }
+        firsts[t] = m;
+        atomicAdd(sum, __popcll(m));
+    }
+    __syncthreads();
+    if (threadIdx.x == 0)
+        *total = *sum;
+}
 
-template <bool FP4, int NT>
+// Fragments: the gates of F/2 * 16 of the I columns from i0 on, then their ups.
+template <bool FP4, int F, int NT, bool STAGED>
 __device__ __forceinline__ void up_group(const FewPlan &p, const uint16_t *x, const uint8_t *w, const uint8_t *ws,
                                          int e, int i0, const Token *list, int n, float *red, uint16_t *h)
 {
+    constexpr int cols = F * 8;
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave, waves = blockDim.x / kWave;
-    const int row = least(i0 + (lane & 15), p.I - 1);
-    const uint8_t *rows[2], *scales[2];
+    Few<FP4, F, NT, STAGED> a;
+    a.lds = reinterpret_cast<const char *>(red);
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
-        const int64_t r = (int64_t)e * 2 * p.I + f * p.I + row;
-        rows[f] = w + r * (FP4 ? p.H / 2 : p.H * 2);
-        scales[f] = FP4 ? ws + r * (p.H / 32) : nullptr;
+    for (int f = 0; f < F; ++f) {
+        const int row = least(i0 + f % (F / 2) * 16 + (lane & 15), p.I - 1);
+        const int64_t r = (int64_t)e * 2 * p.I + f / (F / 2) * p.I + row;
+        a.w[f] = w + r * (FP4 ? p.H / 2 : p.H * 2);
+        a.scales[f] = FP4 ? ws + r * (p.H / 32) : nullptr;
     }
-    const uint16_t *col[NT];
 #pragma unroll
-    for (int c = 0; c < NT; ++c)
-        col[c] = x + (int64_t)(list[least(c * 16 + (lane & 15), n - 1)].entry / p.K) * p.H;
-    Few<FP4, NT> a;
-    a.zero();
+    for (int c = 0; c < NT; ++c) {
+        const int i = least(c * 16 + (lane & 15), n - 1);
+        if constexpr (STAGED)
+            a.at[c] = i * column_bytes<FP4>(p.H);
+        else
+            a.col[c] = x + (int64_t)(list[i].entry / p.K) * p.H;
+    }
     int s0, s1;
     share(p.H, FP4 ? 4 : 1, wave, waves, s0, s1);
-    a.run(rows, scales, col, s0, s1, p.H);
+    if constexpr (STAGED) {
+        stage_columns<FP4>(reinterpret_cast<char *>(red), x, (int64_t)p.T * p.H, n, p.H,
+                           [&](int i) { return (int64_t)(list[i].entry / p.K) * p.H; });
+        a.run(s0, s1, p.H);
+        __syncthreads();        // `red` is the columns' memory
+    } else {
+        a.run(s0, s1, p.H);
+    }
     a.put(red);
     __syncthreads();
-    for (int i = tid; i < 16 * least(n, 16 * NT); i += blockDim.x) {
-        const int c = i >> 4, r = i & 15;
+    for (int i = tid; i < cols * least(n, 16 * NT); i += blockDim.x) {
+        const int c = i / cols, r = i % cols;
         if (i0 + r >= p.I)
             continue;
-        const float gate = added<NT>(red, waves, 0, c, r), up = added<NT>(red, waves, 1, c, r);
+        const float gate = added<F, NT>(red, waves, r >> 4, c, r & 15),
+                    up = added<F, NT>(red, waves, F / 2 + (r >> 4), c, r & 15);
         const float v = gate / (1.0f + expf(-gate)) * up;
         const uint32_t hi = pack_bf16_any(v, 0.0f);
         const float rest = v - bf16_lo(hi);
@@ -254,8 +532,54 @@ __device__ __forceinline__ void up_group(const FewPlan &p, const uint16_t *x, co
     __syncthreads();        // `red` is free
 }
 
-template <bool FP4>
-__global__ void __launch_bounds__(kMaxWaves *kWave, 4)
+// The same with shared columns: a wave's fragments are 16 gates and their ups.
+template <bool FP4, int NT>
+__device__ __forceinline__ void up_shared(const FewPlan &p, const uint16_t *x, const uint8_t *w, const uint8_t *ws,
+                                          int e, int i0, const Token *list, int n, char *lds, uint16_t *h)
+{
+    const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    Shared<FP4, NT> a;
+    a.lds = lds;
+    a.from = row_rsrc(x, p.T * p.H * 2);
+    const int row = i0 + wave * 16;
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+        const int64_t r = (int64_t)e * 2 * p.I + f * p.I + least(row + (lane & 15), p.I - 1);
+        a.w[f] = w + r * (FP4 ? p.H / 2 : p.H * 2);
+        a.scales[f] = FP4 ? ws + r * (p.H / 32) : nullptr;
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const int c = (i * 4 + wave) * 4 + (lane >> 4);
+        a.col[i] = c < n ? (uint32_t)(list[least(c, n - 1)].entry / p.K) * p.H * 2 + (((lane & 15) ^ (c & 15)) << 4) : kNowhere;
+    }
+    a.run(p.H);
+    const int at = row + (lane >> 4) * 4;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const int c = i * 16 + (lane & 15);
+        if (c >= n || at >= p.I)        // (n may be more than the 16 NT that are these)
+            continue;
+        float v[4], rest[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float gate = a.acc[0][i][q];
+            v[q] = gate / (1.0f + expf(-gate)) * a.acc[1][i][q];
+        }
+        const u32x2 hi = {pack_bf16_any(v[0], v[1]), pack_bf16_any(v[2], v[3])};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float r = v[q] - (q & 1 ? bf16_hi(hi[q >> 1]) : bf16_lo(hi[q >> 1]));
+            rest[q] = fabsf(r) < __builtin_huge_valf() ? r : 0.0f;      // an infinity or a NaN has no rest
+        }
+        uint16_t *to = h + (int64_t)list[c].entry * p.I + at;
+        *reinterpret_cast<u32x2 *>(to) = hi;
+        *reinterpret_cast<u32x2 *>(to + p.lower) = u32x2{pack_bf16_any(rest[0], rest[1]), pack_bf16_any(rest[2], rest[3])};
+    }
+}
+
+template <bool FP4, bool WIDE>
+__global__ void __launch_bounds__(kMaxWaves *kWave, WIDE ? 2 : 4)
 few_up_kernel(FewPlan p, const uint16_t *__restrict__ x, const int32_t *__restrict__ idx,
               const float *__restrict__ weights, const uint8_t *__restrict__ w, const uint8_t *__restrict__ ws,
               FewTables t, uint16_t *__restrict__ h, int32_t *__restrict__ num_invalid)
@@ -265,7 +589,9 @@ few_up_kernel(FewPlan p, const uint16_t *__restrict__ x, const int32_t *__restri
     __shared__ int found[3], counts[2];
     __shared__ Token list[kFewTokens];
     const int tid = threadIdx.x;
-    const int slices = (p.I + 15) / 16, slice = blockIdx.x % slices, at = blockIdx.x / slices;
+    // tokens go 64 at a time, each lot to a block of its own
+    const int slices = p.slices_up, lots = WIDE ? (p.T + 63) / 64 : 1, slice = blockIdx.x % slices;
+    const int at = blockIdx.x / slices / lots, lot = blockIdx.x / slices % lots, i0 = slice * (WIDE ? 64 : 16);
     // the second launch's counters
     for (int i = blockIdx.x * blockDim.x + tid; i < p.slices; i += gridDim.x * blockDim.x)
         t.arrived[i] = 0u;
@@ -275,10 +601,12 @@ few_up_kernel(FewPlan p, const uint16_t *__restrict__ x, const int32_t *__restri
         t.named[0] = named;
         num_invalid[0] = bad;
     }
+    if (blockIdx.x == gridDim.x - 1)
+        first_entries(p, idx, t.firsts, counts, t.named + 1);
     if (e < 0)
         return;
     const int n = tokens_of(p, idx, weights, e, list, counts);
-    if (slice == 0) {
+    if (slice == 0 && lot == 0) {
         if (tid == 0) {
             t.expert[at] = e;
             t.count[at] = n;
@@ -288,48 +616,69 @@ few_up_kernel(FewPlan p, const uint16_t *__restrict__ x, const int32_t *__restri
             t.coef[at * p.T + i] = list[i].coef;
         }
     }
-    if (n <= 16)
-        up_group<FP4, 1>(p, x, w, ws, e, slice * 16, list, n, red, h);
-    else if (n <= 32)
-        up_group<FP4, 2>(p, x, w, ws, e, slice * 16, list, n, red, h);
-    else
-        for (int g = 0; g < n; g += 64)
-            up_group<FP4, 4>(p, x, w, ws, e, slice * 16, list + g, n - g, red, h);
+    if constexpr (WIDE) {
+        char *const lds = reinterpret_cast<char *>(red);
+        const Token *mine = list + lot * 64;
+        const int m = n - lot * 64;
+        if (m > 32)
+            up_shared<FP4, 4>(p, x, w, ws, e, i0, mine, m, lds, h);
+        else if (m > 16)
+            up_shared<FP4, 2>(p, x, w, ws, e, i0, mine, m, lds, h);
+        else if (m > 0)
+            up_shared<FP4, 1>(p, x, w, ws, e, i0, mine, m, lds, h);
+    } else {
+        if (n <= 16 && can_stage<FP4>(p, n, p.H, (int64_t)p.T * p.H))
+            up_group<FP4, 2, 1, true>(p, x, w, ws, e, i0, list, n, red, h);
+        else if (n <= 16)
+            up_group<FP4, 2, 1, false>(p, x, w, ws, e, i0, list, n, red, h);
+        else
+            for (int g = 0; g < n; g += 32)
+                up_group<FP4, 2, 2, false>(p, x, w, ws, e, i0, list + g, n - g, red, h);
+    }
 }
 
 // ---------------------------------------------------------------- the second launch
 // Columns: `half` tokens' nearest bf16, then what those left over.
-template <bool FP4, int NT>
+template <bool FP4, int F, int NT, bool STAGED>
 __device__ __forceinline__ void down_group(const FewPlan &p, const uint16_t *h, const uint8_t *w, const uint8_t *ws,
                                            int e, int r0, const Token *list, int n, float *red, float *part)
 {
-    constexpr int half = NT * 8;
+    constexpr int half = NT * 8, cols = F * 16;
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave, waves = blockDim.x / kWave;
-    const uint8_t *rows[2], *scales[2];
+    Few<FP4, F, NT, STAGED> a;
+    a.lds = reinterpret_cast<const char *>(red);
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
+    for (int f = 0; f < F; ++f) {
         const int64_t r = (int64_t)e * p.H + least(r0 + f * 16 + (lane & 15), p.H - 1);
-        rows[f] = w + r * (FP4 ? p.I / 2 : p.I * 2);
-        scales[f] = FP4 ? ws + r * (p.I / 32) : nullptr;
+        a.w[f] = w + r * (FP4 ? p.I / 2 : p.I * 2);
+        a.scales[f] = FP4 ? ws + r * (p.I / 32) : nullptr;
     }
-    const uint16_t *col[NT];
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
-        const int v = c * 16 + (lane & 15);
-        col[c] = h + (int64_t)list[least(v % half, n - 1)].entry * p.I + (v < half ? 0 : p.lower);
+        const int v = c * 16 + (lane & 15), i = least(v % half, n - 1);
+        if constexpr (STAGED)
+            a.at[c] = (v < half ? i : n + i) * column_bytes<FP4>(p.I);
+        else
+            a.col[c] = h + (int64_t)list[i].entry * p.I + (v < half ? 0 : p.lower);
     }
-    Few<FP4, NT> a;
-    a.zero();
     int s0, s1;
     share(p.I, FP4 ? 4 : 1, wave, waves, s0, s1);
-    a.run(rows, scales, col, s0, s1, p.I);
+    if constexpr (STAGED) {
+        stage_columns<FP4>(reinterpret_cast<char *>(red), h, 2 * p.lower, 2 * n, p.I, [&](int i) {
+            return (int64_t)list[i < n ? i : i - n].entry * p.I + (i < n ? 0 : p.lower);
+        });
+        a.run(s0, s1, p.I);
+        __syncthreads();        // `red` is the columns' memory
+    } else {
+        a.run(s0, s1, p.I);
+    }
     a.put(red);
     __syncthreads();
-    for (int i = tid; i < kRows * least(n, half); i += blockDim.x) {
-        const int c = i / kRows, r = i % kRows;
+    for (int i = tid; i < cols * least(n, half); i += blockDim.x) {
+        const int c = i / cols, r = i % cols;
         if (r0 + r >= p.H)
             continue;
-        const float v = added<NT>(red, waves, r >> 4, c, r & 15) + added<NT>(red, waves, r >> 4, half + c, r & 15);
+        const float v = added<F, NT>(red, waves, r >> 4, c, r & 15) + added<F, NT>(red, waves, r >> 4, half + c, r & 15);
         // read by a block on any XCD: not left in this one's L2
         __hip_atomic_store(part + (int64_t)list[c].entry * p.H + r0 + r, list[c].coef * v, __ATOMIC_RELAXED,
                            __HIP_MEMORY_SCOPE_AGENT);
@@ -337,32 +686,88 @@ __device__ __forceinline__ void down_group(const FewPlan &p, const uint16_t *h, 
     __syncthreads();
 }
 
-template <bool FP4>
-__global__ void __launch_bounds__(kMaxWaves *kWave, 4)
+template <bool FP4, int NT>
+__device__ __forceinline__ void down_shared(const FewPlan &p, const uint16_t *h, const uint8_t *w, const uint8_t *ws,
+                                            int e, int r0, const Token *list, int n, char *lds, float *part)
+{
+    constexpr int half = NT * 8;
+    const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    Shared<FP4, NT> a;
+    a.lds = lds;
+    a.from = row_rsrc(h, (int)(2 * p.lower * 2));
+    const int row = r0 + wave * 32;
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+        const int64_t r = (int64_t)e * p.H + least(row + f * 16 + (lane & 15), p.H - 1);
+        a.w[f] = w + r * (FP4 ? p.I / 2 : p.I * 2);
+        a.scales[f] = FP4 ? ws + r * (p.I / 32) : nullptr;
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const int c = (i * 4 + wave) * 4 + (lane >> 4), token = c % half;
+        a.col[i] = token < n ? (uint32_t)(((int64_t)list[least(token, n - 1)].entry * p.I + (c < half ? 0 : p.lower)) * 2) +
+                                   (((lane & 15) ^ (c & 15)) << 4)
+                             : kNowhere;
+    }
+    a.run(p.I);
+#pragma unroll
+    for (int i = 0; i < NT / 2; ++i) {
+        const int c = i * 16 + (lane & 15);
+        if (c >= n)
+            continue;
+        const Token t = list[c];
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            const int at = row + f * 16 + (lane >> 4) * 4;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (at + q < p.H)
+                    __hip_atomic_store(part + (int64_t)t.entry * p.H + at + q, t.coef * (a.acc[f][i][q] + a.acc[f][i + NT / 2][q]),
+                                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+    }
+}
+
+template <bool FP4, bool WIDE>
+__global__ void __launch_bounds__(kMaxWaves *kWave, WIDE ? 2 : 4)
 few_down_kernel(FewPlan p, const uint16_t *__restrict__ h, const int32_t *__restrict__ idx,
                 const uint8_t *__restrict__ w, const uint8_t *__restrict__ ws, FewTables t, float *part,
                 uint16_t *__restrict__ out)
 {
     extern __shared__ __attribute__((aligned(16))) float red[];
     __shared__ Token list[kFewTokens];
-    __shared__ uint64_t firsts[kFewTokens];
     __shared__ bool last;
-    const int tid = threadIdx.x, slice = blockIdx.x % p.slices, at = blockIdx.x / p.slices, r0 = slice * kRows;
-    const int named = t.named[0];
-    if (at >= named && at > 0)
+    constexpr int cols = WIDE ? 128 : 32;
+    // tokens go 32 at a time, each lot to a block of its own
+    const int lots = WIDE ? (p.T + 31) / 32 : 1;
+    const int tid = threadIdx.x, slice = blockIdx.x % p.slices, r0 = slice * cols;
+    const int at = blockIdx.x / p.slices / lots, lot = blockIdx.x / p.slices % lots;
+    // (at < p.most: in the tables, if not of use)
+    const int named = t.named[0], e = t.expert[at], n = t.count[at];
+    const int total = t.named[1];
+    if (named == 0 ? at + lot > 0 : at >= named || lot * 32 * WIDE >= n)
         return;
     if (named > 0) {
-        const int e = t.expert[at], n = t.count[at];
         for (int i = tid; i < n; i += blockDim.x)
             list[i] = Token{t.entry[at * p.T + i], t.coef[at * p.T + i]};
         __syncthreads();
-        if (n <= 8)
-            down_group<FP4, 1>(p, h, w, ws, e, r0, list, n, red, part);
-        else if (n <= 16)
-            down_group<FP4, 2>(p, h, w, ws, e, r0, list, n, red, part);
-        else
-            for (int g = 0; g < n; g += 32)
-                down_group<FP4, 4>(p, h, w, ws, e, r0, list + g, n - g, red, part);
+        if constexpr (WIDE) {
+            char *const lds = reinterpret_cast<char *>(red);
+            const Token *mine = list + lot * 32;
+            const int m = least(n - lot * 32, 32);
+            if (m <= 16)
+                down_shared<FP4, 2>(p, h, w, ws, e, r0, mine, m, lds, part);
+            else
+                down_shared<FP4, 4>(p, h, w, ws, e, r0, mine, m, lds, part);
+        } else {
+            if (n <= 8 && can_stage<FP4>(p, 2 * n, p.I, 2 * p.lower))
+                down_group<FP4, 2, 1, true>(p, h, w, ws, e, r0, list, n, red, part);
+            else if (n <= 8)
+                down_group<FP4, 2, 1, false>(p, h, w, ws, e, r0, list, n, red, part);
+            else
+                for (int g = 0; g < n; g += 16)
+                    down_group<FP4, 2, 2, false>(p, h, w, ws, e, r0, list + g, n - g, red, part);
+        }
     }
     // Every wave's parts have arrived where all XCDs see them before the block counts
     // itself, and the last block reads them there: the parts' accesses go past the
@@ -370,42 +775,91 @@ few_down_kernel(FewPlan p, const uint16_t *__restrict__ h, const int32_t *__rest
     // cost the other blocks what they have there of h).
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (tid == 0)
-        last = named == 0 || __hip_atomic_fetch_add(t.arrived + slice, 1u, __ATOMIC_RELAXED,
-                                                    __HIP_MEMORY_SCOPE_AGENT) == (unsigned)named - 1u;
+    // (it counts the tokens that it brings)
+    if (tid == 0) {
+        const unsigned brings = WIDE ? least(n - lot * 32, 32) : n;
+        last = named == 0 || __hip_atomic_fetch_add(t.arrived + slice, brings, __ATOMIC_RELAXED,
+                                                    __HIP_MEMORY_SCOPE_AGENT) + brings == (unsigned)total;
+    }
     __syncthreads();
     if (!last)
         return;
-    // each token's entries that stand for an expert: the first one of each
-    for (int i = tid; i < p.T; i += blockDim.x) {
-        uint64_t m = 0;
-        for (int k = 0; k < p.K; ++k) {
-            const int e = idx[i * p.K + k];
-            bool first = (unsigned)e < (unsigned)p.E;
-            for (int o = 0; first && o < k; ++o)
-                first = idx[i * p.K + o] != e;
-            m |= (uint64_t)first << k;
+    // pairs of columns, four at a time, and of each four parts at a time, in the order of k
+    constexpr int U = 4, KC = 4;
+    const int all = p.T * (cols / 2), step = blockDim.x;
+    for (int i0 = tid; i0 < all; i0 += U * step) {
+        float a[U], b[U];
+        uint64_t firsts[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            a[u] = b[u] = 0.0f;
+            const int i = i0 + u * step;
+            firsts[u] = i < all && r0 + i % (cols / 2) * 2 < p.H ? t.firsts[i / (cols / 2)] : 0;
         }
-        firsts[i] = m;
-    }
-    __syncthreads();
-    for (int i = tid; i < p.T * (kRows / 2); i += blockDim.x) {
-        const int token = i / (kRows / 2), c = r0 + i % (kRows / 2) * 2;
-        if (c >= p.H)
-            continue;
-        float a = 0.0f, b = 0.0f;
-        for (uint64_t m = firsts[token]; m; m &= m - 1) {
-            float *from = part + ((int64_t)token * p.K + __ffsll((unsigned long long)m) - 1) * p.H + c;
-            a += __hip_atomic_load(from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            b += __hip_atomic_load(from + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        for (int k0 = 0; k0 < p.K; k0 += KC) {
+            uint64_t v[U][KC];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < KC; ++k) {
+                    const int i = i0 + u * step;
+                    const float *from = part + ((int64_t)(i / (cols / 2)) * p.K + k0 + k) * p.H + r0 + i % (cols / 2) * 2;
+                    v[u][k] = 0;
+                    if (k0 + k < p.K && firsts[u] >> (k0 + k) & 1)
+                        v[u][k] = __hip_atomic_load(reinterpret_cast<const uint64_t *>(from), __ATOMIC_RELAXED,
+                                                    __HIP_MEMORY_SCOPE_AGENT);
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < KC; ++k) {
+                    a[u] += __uint_as_float((uint32_t)v[u][k]);
+                    b[u] += __uint_as_float((uint32_t)(v[u][k] >> 32));
+                }
         }
-        *reinterpret_cast<uint32_t *>(out + (int64_t)token * p.H + c) = pack_bf16_any(a, b);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * step, c = r0 + i % (cols / 2) * 2;
+            if (i < all && c < p.H)
+                *reinterpret_cast<uint32_t *>(out + (int64_t)(i / (cols / 2)) * p.H + c) = pack_bf16_any(a[u], b[u]);
+        }
     }
 }
 
 __global__ void few_zero_kernel(int32_t *p) { *p = 0; }
 
-int reduce_bytes(int waves) { return waves * 2 * 4 * 256 * 4; }
+// The waves of a block, by the inner dimension: about eight loads of a weight row for
+// each.
+int waves_of(int D, bool fp4)
+{
+    const int steps = (D + (fp4 ? 127 : 31)) / (fp4 ? 128 : 32), per = fp4 ? 6 : 8;
+    return steps >= 4 * per ? 4 : (steps >= 2 * per ? 2 : 1);
+}
+
+template <bool FP4, bool WIDE>
+hipError_t launch_few_as(const FewPlan &p, const uint16_t *x, const int32_t *idx, const float *weights,
+                         const uint8_t *up, const uint8_t *up_scales, const uint8_t *down, const uint8_t *down_scales,
+                         const FewTables &t, uint16_t *h, float *part, uint16_t *out, int32_t *num_invalid,
+                         hipStream_t s)
+{
+    const int wu = WIDE ? kMaxWaves : waves_of(p.H, FP4), wd = WIDE ? kMaxWaves : waves_of(p.I, FP4);
+    // four buffers of 64 columns; or the waves' sums of 2 x 2 fragments, or the columns
+    auto lds = [&](int waves) { return WIDE ? 4 * 4 * 4096 : waves * 4096 > p.stage_bytes ? waves * 4096 : p.stage_bytes; };
+    // beyond the 64 KB that a block has without asking
+    const void *kernels[2] = {reinterpret_cast<const void *>(few_up_kernel<FP4, WIDE>),
+                              reinterpret_cast<const void *>(few_down_kernel<FP4, WIDE>)};
+    for (const void *k : kernels) {
+        const hipError_t e = WIDE ? hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, lds(kMaxWaves))
+                                  : hipSuccess;
+        if (e != hipSuccess)
+            return e;
+    }
+    const int lots_up = WIDE ? (p.T + 63) / 64 : 1, lots_down = WIDE ? (p.T + 31) / 32 : 1;
+    few_up_kernel<FP4, WIDE><<<p.most * lots_up * p.slices_up, wu * kWave, lds(wu), s>>>(p, x, idx, weights, up, up_scales, t, h,
+                                                                              num_invalid);
+    few_down_kernel<FP4, WIDE><<<p.most * lots_down * p.slices, wd * kWave, lds(wd), s>>>(p, h, idx, down, down_scales, t, part, out);
+    return hipGetLastError();
+}
 
 }  // namespace
 
@@ -417,8 +871,17 @@ FewPlan make_few_plan(int T, int K, int E, int H, int I)
     p.E = E;
     p.H = H;
     p.I = I;
-    p.slices = (H + kRows - 1) / kRows;
     p.most = least(T * K, E);
+    // experts with some tokens each: blocks of 128 weight rows, that share the tokens'
+    // columns (whose arrays a buffer has to reach)
+    p.wide = T * K >= 12 * p.most && (int64_t)T * K * I < 1 << 29;
+    const int rows = p.wide ? 128 : 32;
+    // what an expert's tokens take of LDS, on average; twice that at most
+    const int mean = (T * K + p.most - 1) / (p.most > 0 ? p.most : 1), wide = H > 2 * I ? H : 2 * I;
+    const int64_t want = ((int64_t)2 * mean * (wide * 2 + 256 + 64) + 1023) / 1024 * 1024;
+    p.stage_bytes = (int)(want < kStageBytes ? want : kStageBytes);
+    p.slices = (H + rows - 1) / rows;
+    p.slices_up = (I + rows / 2 - 1) / (rows / 2);
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -428,11 +891,12 @@ FewPlan make_few_plan(int T, int K, int E, int H, int I)
     const size_t entries = (size_t)T * K;
     p.lower = (int64_t)entries * I;
     p.off_arrived = take((size_t)p.slices * 4);
-    p.off_named = take(4);
+    p.off_named = take(8);
     p.off_expert = take((size_t)p.most * 4);
     p.off_count = take((size_t)p.most * 4);
     p.off_entry = take((size_t)p.most * T * 4);
     p.off_coef = take((size_t)p.most * T * 4);
+    p.off_firsts = take((size_t)T * 8);
     p.off_h = take(entries * I * 2 * 2);
     p.off_part = take(entries * H * 4);
     p.bytes = off > 256 ? off : 256;
@@ -454,20 +918,17 @@ hipError_t launch_few(const FewPlan &p, const uint16_t *x, const int32_t *idx, c
     t.count = reinterpret_cast<int32_t *>(ws + p.off_count);
     t.entry = reinterpret_cast<int32_t *>(ws + p.off_entry);
     t.coef = reinterpret_cast<float *>(ws + p.off_coef);
+    t.firsts = reinterpret_cast<uint64_t *>(ws + p.off_firsts);
     uint16_t *h = reinterpret_cast<uint16_t *>(ws + p.off_h);
     float *part = reinterpret_cast<float *>(ws + p.off_part);
     const uint8_t *u = static_cast<const uint8_t *>(up), *d = static_cast<const uint8_t *>(down);
-    const int64_t blocks_up = (int64_t)p.most * ((p.I + 15) / 16), blocks_down = (int64_t)p.most * p.slices;
-    const int waves = 4;
-    const int lds = reduce_bytes(waves);
-    if (up_scales) {
-        few_up_kernel<true><<<(unsigned)blocks_up, waves * kWave, lds, s>>>(p, x, idx, weights, u, up_scales, t, h, num_invalid);
-        few_down_kernel<true><<<(unsigned)blocks_down, waves * kWave, lds, s>>>(p, h, idx, d, down_scales, t, part, out);
-    } else {
-        few_up_kernel<false><<<(unsigned)blocks_up, waves * kWave, lds, s>>>(p, x, idx, weights, u, nullptr, t, h, num_invalid);
-        few_down_kernel<false><<<(unsigned)blocks_down, waves * kWave, lds, s>>>(p, h, idx, d, nullptr, t, part, out);
-    }
-    return hipGetLastError();
+    if (up_scales && p.wide)
+        return launch_few_as<true, true>(p, x, idx, weights, u, up_scales, d, down_scales, t, h, part, out, num_invalid, s);
+    if (up_scales)
+        return launch_few_as<true, false>(p, x, idx, weights, u, up_scales, d, down_scales, t, h, part, out, num_invalid, s);
+    if (p.wide)
+        return launch_few_as<false, true>(p, x, idx, weights, u, nullptr, d, nullptr, t, h, part, out, num_invalid, s);
+    return launch_few_as<false, false>(p, x, idx, weights, u, nullptr, d, nullptr, t, h, part, out, num_invalid, s);
 }
 
 }  // namespace ep

@@ -197,10 +197,12 @@ hipError_t launch_expert_across(const ExpertRows &m, const ExpertIn &in, const E
 constexpr int kFewTokens = 128;
 struct FewPlan {
     int T, K, E, H, I;
-    int slices;             // blocks of H
     int most;               // experts that the tokens can name
+    bool wide;              // blocks of 128 weight rows, else of 32
+    int slices, slices_up;  // blocks of H, of I
+    int stage_bytes;        // LDS of a block for its tokens
     int64_t lower;          // h's lower part, so many elements behind the upper one
-    size_t off_arrived, off_named, off_expert, off_count, off_entry, off_coef, off_h, off_part, bytes;
+    size_t off_arrived, off_named, off_expert, off_count, off_entry, off_coef, off_firsts, off_h, off_part, bytes;
 };
 // What the first launch leaves for the second: by the place of a named expert.
 struct FewTables {
@@ -208,6 +210,7 @@ struct FewTables {
     int32_t *named, *expert, *count;
     int32_t *entry;         // [most, T]
     float *coef;
+    uint64_t *firsts;       // [T]
 };
 FewPlan make_few_plan(int T, int K, int E, int H, int I);
 hipError_t launch_few(const FewPlan &p, const uint16_t *x, const int32_t *idx, const float *weights, const void *up,

@@ -198,7 +198,7 @@ __device__ __forceinline__ void finish_as(const ExpertOut &o, const f32x4 (&acc)
     const int64_t line = (int64_t)o.width * (grad ? 32 : BITS) / 8;
 #pragma unroll 4
     for (int p = lane; p < TI * 16 * per; p += kWave) {
-        const int r = p / per, piece = p % per, in_half = grad ? piece % (per / 2) : piece;
+        const int r = p / per, piece = p % per, in_half = grad ? piece % (per > 1 ? per / 2 : 1) : piece;
         const int c = c0 + in_half * columns;
         if (row0 + r < t.n && c < o.width)
             st16(static_cast<char *>(o.y) + (t.first + row0 + r) * line + (int64_t)c * BITS / 8 +
@@ -679,25 +679,38 @@ hipError_t product(const ExpertRows &m, const ExpertIn &in, const ExpertOut &out
     return hipGetLastError();
 }
 
-// An expert's rows on average: what the host knows of them.
-int64_t mean_rows(const ExpertRows &m) { return (m.offsets ? m.rows : (int64_t)m.E * m.cap) / m.E; }
-
+// The tile, by what the host knows: an expert's rows on average, and how many blocks
+// there would be (a ragged end for every second expert).  Large tiles take in the
+// least, small ones leave no CU idle and waste less of a short expert.  us with 256 x
+// 256, 128 x 256, 128 x 128 and 64 x 128 (4096 x 4096 weights unless said):
+//   MXFP4, 64 experts   512 rows each 429, 493, 517, 654     64 rows 172, 162, 157, 171
+//                       16 rows (7168) 243, 206, 224, 215
+//   MXFP8, 64 experts   512 rows -, 605, 798, 767            64 rows -, 180, 209, 182
+//                       16 rows (7168) -, 227, 291, 224
+//   bf16, and back      8 experts of 1024 rows 902, 1079, 1077, 1348
+//                       12 of 167 (1120 x 1032) 63, 50, 39, 42
 template <int KIND>
 hipError_t product_any(const ExpertRows &m, const ExpertIn &in, const ExpertOut &out, hipStream_t s)
 {
     const int cover = KIND == kRowsAcross ? in.H : in.half ? in.half : in.O;
-    const int64_t each = mean_rows(m);
-    if (each >= 160) {
-        if constexpr (KIND == kRowsMxE4M3 || KIND == kRowsMxE5M2)
-            return product<ExpertProduct<128, 256, 2, 2, 4, KIND>>(m, in, out, cover, s);
-        else if constexpr (KIND == kRowsMx4)
-            return product<ExpertProduct<256, 256, 2, 4, 4, KIND>>(m, in, out, cover, s);
-        else
+    const int64_t each = (m.offsets ? m.rows : (int64_t)m.E * m.cap) / m.E;
+    auto enough = [&](int BM, int BN) {
+        const int64_t tiles = (each * m.E) / BM + (m.E + 1) / 2;
+        return tiles * ((cover * (in.half ? 2 : 1) + BN - 1) / BN) >= 192;
+    };
+    constexpr bool mx8 = KIND == kRowsMxE4M3 || KIND == kRowsMxE5M2;
+    if constexpr (!mx8) {
+        if (each >= 160 && enough(256, 256))
             return product<ExpertProduct<256, 256, 2, 4, 4, KIND>>(m, in, out, cover, s);
     }
-    if (each >= 48)
-        return product<ExpertProduct<128, 128, 2, 2, 4, KIND>>(m, in, out, cover, s);
-    return product<ExpertProduct<32, 128, 2, 2, 6, KIND>>(m, in, out, cover, s);
+    if constexpr (KIND == kRowsWide || KIND == kRowsAcross) {
+        if (each >= 48 && enough(128, 128))
+            return product<ExpertProduct<128, 128, 2, 2, 4, KIND>>(m, in, out, cover, s);
+    } else {
+        if (each >= 48 && enough(128, 256))
+            return product<ExpertProduct<128, 256, 2, 4, 4, KIND>>(m, in, out, cover, s);
+    }
+    return product<ExpertProduct<64, 128, 2, 2, 4, KIND>>(m, in, out, cover, s);
 }
 
 }  // namespace

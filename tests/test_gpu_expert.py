@@ -94,6 +94,57 @@ def test_every_width_of_the_last_tile(O):
         check(form, [170, 3], 64, 2 * O, "swiglu", seed=O)
 
 
+# enough blocks for the large tiles: 256 x 256 (128 x 256 with 8-bit rows) and 128 x 256 (128 x 128 with bf16)
+LARGE = [[200, 0, 300], [60, 0, 70, 50]]
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("counts", LARGE, ids=str)
+@pytest.mark.parametrize("act", [None, "swiglu"])
+@pytest.mark.parametrize("H", [96, 288])
+def test_large_tiles(form, counts, act, H):
+    check(form, counts, H, 24656, act, seed=H, back=False)
+
+
+@pytest.mark.parametrize("counts", LARGE, ids=str)
+@pytest.mark.parametrize("act,O", [(None, 40), (None, 200), ("swiglu", 80)])
+def test_large_tiles_of_the_gradient(counts, act, O):
+    for form in ("bf16", R.FP4):
+        check(form, counts, 24640, O, act, seed=O)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("act", [None, "swiglu"])
+def test_large_tiles_of_long_rows(form, act):
+    check(form, [600, 0, 700, 1500], 2080, 4160, act, seed=3, back=act is None and form == "bf16")
+
+
+@pytest.mark.parametrize("form", [R.FP4, R.E4M3, "bf16"])
+@pytest.mark.parametrize("counts", LARGE, ids=str)
+def test_large_tiles_write_their_rows_only(form, counts):
+    """Rows that no expert has, and what lies behind a row's last column, in every tile's way of storing."""
+    E, cap, H, O = len(counts), max(counts) + 5, 64, 24640
+    g = gen(31)
+    x = bf(g, E, cap, H)
+    x, xs = (x, None) if form == "bf16" else R.quantize(x, form)
+    w, ws = R.quantize(bf(g, E, O, H, by=0.1), R.FP4)
+    cnt = torch.tensor(counts, dtype=torch.int32)
+    dx_, ds_, dw_, dws_, dc = on(x, xs, w, ws, cnt)
+    for act in (None, "swiglu"):
+        y = torch.full((E, cap, O // 2 if act else O), 7.0, dtype=torch.bfloat16, device=DEV)
+        api.expert_product(dx_, ds_, dw_, dws_, counts=dc, activation=act, out=y)
+        q, s, _ = api.expert_product(dx_, ds_, dw_, dws_, counts=dc, activation=act, quant=R.E4M3)
+        for e in range(E):
+            n = counts[e]
+            assert (y[e, n:] == 7).all() and not (y[e, :n] == 7).all(dim=1).any()
+            if n:       # the codes are those of the same sums, of which y are the nearest bf16
+                v = api.mx_dequantize(q[e, :n].contiguous(), s[e, :n].contiguous()).float()
+                top = y[e, :n].float().abs().unflatten(-1, (-1, 32)).amax(-1, keepdim=True)
+                # half a step of e4m3 (2^-4 of a value, or of the largest's 2^-14), saturation (512 to 448), bf16's own
+                tol = y[e, :n].float().abs().unflatten(-1, (-1, 32)) * (2.0 ** -3 + 2.0 ** -7) + top * 2.0 ** -14
+                assert ((v - y[e, :n].float()).abs().unflatten(-1, (-1, 32)) <= tol).all()
+
+
 @pytest.mark.parametrize("quant", [R.FP4, R.E4M3, R.E5M2])
 @pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("counts", [[4, 0, 9], [60, 100], [300]], ids=str)

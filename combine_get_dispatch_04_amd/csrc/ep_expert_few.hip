@@ -373,9 +373,15 @@ struct Shared {
 
 // ---------------------------------------------------------------- the first launch
 // The n-th of the experts that topk_idx names, ascending, or -1; their number.
-// `bits`: kMaxWords words of shared memory.
+// `bits`: kMaxWords words of shared memory; `entries`: the entries' experts and weights
+// there, for what comes after (both loads at once: each is a miss).
 constexpr int kMaxWords = 4096 / 32;
-__device__ int nth_expert(const FewPlan &p, const int32_t *idx, int n, uint32_t *bits, int *found, int &named, int &bad)
+struct Entry {
+    int e;
+    float w;
+};
+__device__ int nth_expert(const FewPlan &p, const int32_t *idx, const float *w, int n, uint32_t *bits, Entry *entries,
+                          int *found, int &named, int &bad)
 {
     const int tid = threadIdx.x, words = (p.E + 31) / 32;
     for (int i = tid; i < kMaxWords; i += blockDim.x)
@@ -384,10 +390,12 @@ __device__ int nth_expert(const FewPlan &p, const int32_t *idx, int n, uint32_t 
         found[0] = -1;
         found[2] = 0;
     }
+    for (int i = tid; i < p.T * p.K; i += blockDim.x)
+        entries[i] = Entry{idx[i], w ? w[i] : 1.0f};
     __syncthreads();
     int wrong = 0;
     for (int i = tid; i < p.T * p.K; i += blockDim.x) {
-        const int e = idx[i];
+        const int e = entries[i].e;
         if ((unsigned)e < (unsigned)p.E)
             atomicOr(&bits[e >> 5], 1u << (e & 31));
         else
@@ -424,7 +432,7 @@ struct Token {
 };
 
 // The tokens that name expert e, in order.  T <= 128: a token per lane, 64 at a time.
-__device__ int tokens_of(const FewPlan &p, const int32_t *idx, const float *w, int e, Token *list, int *counts)
+__device__ int tokens_of(const FewPlan &p, const Entry *entries, int e, Token *list, int *counts)
 {
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, waves = blockDim.x / kWave;
     Token mine[2];
@@ -436,9 +444,9 @@ __device__ int tokens_of(const FewPlan &p, const int32_t *idx, const float *w, i
         if (part < 2 && t < p.T) {
 #pragma unroll 8
             for (int k = p.K - 1; k >= 0; --k) {
-                const bool same = idx[t * p.K + k] == e;
-                const float c = w ? w[t * p.K + k] : 1.0f;
-                mine[i].coef += same ? c : 0.0f;
+                const Entry v = entries[t * p.K + k];
+                const bool same = v.e == e;
+                mine[i].coef += same ? v.w : 0.0f;
                 mine[i].entry = same ? t * p.K + k : mine[i].entry;
             }
         }
@@ -456,7 +464,7 @@ __device__ int tokens_of(const FewPlan &p, const int32_t *idx, const float *w, i
 }
 // Each token's entries that stand for an expert, the first of each, as bits, and the
 // number of all: left for the second launch.  `sum`: a word of shared memory.
-__device__ void first_entries(const FewPlan &p, const int32_t *idx, uint64_t *firsts, int *sum, int32_t *total)
+__device__ void first_entries(const FewPlan &p, const Entry *entries, uint64_t *firsts, int *sum, int32_t *total)
 {
     if (threadIdx.x == 0)
         *sum = 0;
@@ -464,11 +472,11 @@ __device__ void first_entries(const FewPlan &p, const int32_t *idx, uint64_t *fi
     for (int t = threadIdx.x; t < p.T; t += blockDim.x) {
         uint64_t m = 0;
         for (int k = 0; k < p.K; ++k) {
-            const int e = idx[t * p.K + k];
+            const int e = entries[t * p.K + k].e;
             bool again = false;
 #pragma unroll 8
             for (int o = 0; o < k; ++o)
-                again |= idx[t * p.K + o] == e;
+                again |= entries[t * p.K + o].e == e;
             m |= (uint64_t)((unsigned)e < (unsigned)p.E && !again) << k;
         }
         firsts[t] = m;
@@ -596,16 +604,18 @@ few_up_kernel(FewPlan p, const uint16_t *__restrict__ x, const int32_t *__restri
     for (int i = blockIdx.x * blockDim.x + tid; i < p.slices; i += gridDim.x * blockDim.x)
         t.arrived[i] = 0u;
     int named, bad;
-    const int e = nth_expert(p, idx, at, bits, found, named, bad);
+    // (in the memory of the columns, which come later)
+    Entry *const entries = reinterpret_cast<Entry *>(red);
+    const int e = nth_expert(p, idx, weights, at, bits, entries, found, named, bad);
     if (blockIdx.x == 0 && tid == 0) {
         t.named[0] = named;
         num_invalid[0] = bad;
     }
     if (blockIdx.x == gridDim.x - 1)
-        first_entries(p, idx, t.firsts, counts, t.named + 1);
+        first_entries(p, entries, t.firsts, counts, t.named + 1);
     if (e < 0)
         return;
-    const int n = tokens_of(p, idx, weights, e, list, counts);
+    const int n = tokens_of(p, entries, e, list, counts);
     if (slice == 0 && lot == 0) {
         if (tid == 0) {
             t.expert[at] = e;
@@ -745,11 +755,12 @@ few_down_kernel(FewPlan p, const uint16_t *__restrict__ h, const int32_t *__rest
     // (at < p.most: in the tables, if not of use)
     const int named = t.named[0], e = t.expert[at], n = t.count[at];
     const int total = t.named[1];
+    // (before the numbers are here: what lies behind the n-th is of no use)
+    for (int i = tid; i < p.T; i += blockDim.x)
+        list[i] = Token{t.entry[at * p.T + i], t.coef[at * p.T + i]};
     if (named == 0 ? at + lot > 0 : at >= named || lot * 32 * WIDE >= n)
         return;
     if (named > 0) {
-        for (int i = tid; i < n; i += blockDim.x)
-            list[i] = Token{t.entry[at * p.T + i], t.coef[at * p.T + i]};
         __syncthreads();
         if constexpr (WIDE) {
             char *const lds = reinterpret_cast<char *>(red);
@@ -844,7 +855,11 @@ hipError_t launch_few_as(const FewPlan &p, const uint16_t *x, const int32_t *idx
 {
     const int wu = WIDE ? kMaxWaves : waves_of(p.H, FP4), wd = WIDE ? kMaxWaves : waves_of(p.I, FP4);
     // four buffers of 64 columns; or the waves' sums of 2 x 2 fragments, or the columns
-    auto lds = [&](int waves) { return WIDE ? 4 * 4 * 4096 : waves * 4096 > p.stage_bytes ? waves * 4096 : p.stage_bytes; };
+    // and the entries
+    auto lds = [&](int waves) {
+        const int own = WIDE ? 4 * 4 * 4096 : waves * 4096 > p.stage_bytes ? waves * 4096 : p.stage_bytes;
+        return own > p.T * p.K * 8 ? own : p.T * p.K * 8;
+    };
     // beyond the 64 KB that a block has without asking
     const void *kernels[2] = {reinterpret_cast<const void *>(few_up_kernel<FP4, WIDE>),
                               reinterpret_cast<const void *>(few_down_kernel<FP4, WIDE>)};

@@ -515,20 +515,19 @@ struct ExpertProduct {
     }
 
     // Slice q, the KS-th of its stage: b holds its weight fragments, b_next takes the
-    // next one's.  NEXT: there is another one; FETCH: and a slice NS on.
-    template <int KS, bool NEXT, bool FETCH>
+    // next one's.  NEXT: there is another one; FETCH: and a slice NS on.  ROWS: the wave
+    // has rows of the tile (else it only loads for the others).
+    template <int KS, bool NEXT, bool FETCH, bool ROWS>
     __device__ __forceinline__ void step(int q, frag_a (&a)[TI], const u32x4 (&b)[TJ], u32x4 (&b_next)[TJ],
                                          scale_set &scale, Side &side)
     {
+        if constexpr (ROWS) {
 #pragma unroll
-        for (int g = 0; g < LAG; ++g)
-            group<KS>(g, a[g], b, scale);
-        if constexpr (!NEXT) {
-#pragma unroll
-            for (int g = LAG; g < TI; ++g)
+            for (int g = 0; g < (NEXT ? LAG : TI); ++g)
                 group<KS>(g, a[g], b, scale);
-            return;
         }
+        if constexpr (!NEXT)
+            return;
         if constexpr (FETCH)
             wait_and_meet<(NS - 2) * pieces>();
         else
@@ -547,21 +546,23 @@ struct ExpertProduct {
 #pragma unroll
         for (int h = 0; h < rest; ++h) {
             const int g = LAG + h;
-            if (g < TI)
+            if (ROWS && g < TI)
                 group<KS>(g, a[g], b, scale);
             // not before these MFMAs, which would wait for the reads as well
             __builtin_amdgcn_sched_barrier(0);
+            if constexpr (ROWS) {
 #pragma unroll
-            for (int j = h * RN; j < (h + 1) * RN && j < TJ; ++j) {
-                read_b<1 - KS>(b_next, q + 1, j);
-                if constexpr (mx && KS == 1)
-                    next[j] = read_scale(q / 2 + 1, TI + j);
-            }
+                for (int j = h * RN; j < (h + 1) * RN && j < TJ; ++j) {
+                    read_b<1 - KS>(b_next, q + 1, j);
+                    if constexpr (mx && KS == 1)
+                        next[j] = read_scale(q / 2 + 1, TI + j);
+                }
 #pragma unroll
-            for (int i = h == 0 ? 0 : g; i <= g && i < TI; ++i) {
-                read_a(a[i], q + 1, i);
-                if constexpr (mx && KS == 1)
-                    scale[i] = read_scale(q / 2 + 1, i);
+                for (int i = h == 0 ? 0 : g; i <= g && i < TI; ++i) {
+                    read_a(a[i], q + 1, i);
+                    if constexpr (mx && KS == 1)
+                        scale[i] = read_scale(q / 2 + 1, i);
+                }
             }
             if constexpr (FETCH) {
 #pragma unroll
@@ -575,20 +576,24 @@ struct ExpertProduct {
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-        if constexpr (mx && KS == 1) {
+        if constexpr (mx && KS == 1 && ROWS) {
 #pragma unroll
             for (int j = 0; j < TJ; ++j)
                 scale[TI + j] = next[j];
         }
     }
 
+    // Every wave of the block comes here, with ROWS or without: they meet at the same
+    // number of barriers.
+    template <bool ROWS>
     __device__ __forceinline__ void run()
     {
+        if constexpr (ROWS)
 #pragma unroll
-        for (int i = 0; i < TI; ++i)
+            for (int i = 0; i < TI; ++i)
 #pragma unroll
-            for (int j = 0; j < TJ; ++j)
-                acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                for (int j = 0; j < TJ; ++j)
+                    acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         Side first, side;
 #pragma unroll
         for (int i = 0; i < CA + CB; ++i)
@@ -610,29 +615,31 @@ struct ExpertProduct {
         frag_a a[TI];
         u32x4 b0[TJ], b1[TJ];
         scale_set scale;
+        if constexpr (ROWS) {
 #pragma unroll
-        for (int j = 0; j < TJ; ++j)
-            read_b<0>(b0, 0, j);
+            for (int j = 0; j < TJ; ++j)
+                read_b<0>(b0, 0, j);
 #pragma unroll
-        for (int i = 0; i < TI; ++i)
-            read_a(a[i], 0, i);
-        if constexpr (mx) {
+            for (int i = 0; i < TI; ++i)
+                read_a(a[i], 0, i);
+            if constexpr (mx) {
 #pragma unroll
-            for (int f = 0; f < TI + TJ; ++f)
-                scale[f] = read_scale(0, f);
+                for (int f = 0; f < TI + TJ; ++f)
+                    scale[f] = read_scale(0, f);
+            }
         }
         int q = 0;
         for (; q + NS < n; q += 2) {
-            step<0, true, true>(q, a, b0, b1, scale, side);
-            step<1, true, true>(q + 1, a, b1, b0, scale, side);
+            step<0, true, true, ROWS>(q, a, b0, b1, scale, side);
+            step<1, true, true, ROWS>(q + 1, a, b1, b0, scale, side);
         }
 #pragma unroll 1
         for (; q + 2 < n; q += 2) {
-            step<0, true, false>(q, a, b0, b1, scale, side);
-            step<1, true, false>(q + 1, a, b1, b0, scale, side);
+            step<0, true, false, ROWS>(q, a, b0, b1, scale, side);
+            step<1, true, false, ROWS>(q + 1, a, b1, b0, scale, side);
         }
-        step<0, true, false>(q, a, b0, b1, scale, side);
-        step<1, false, false>(q + 1, a, b1, b0, scale, side);
+        step<0, true, false, ROWS>(q, a, b0, b1, scale, side);
+        step<1, false, false, ROWS>(q + 1, a, b1, b0, scale, side);
     }
 };
 
@@ -645,11 +652,19 @@ expert_kernel(ExpertRows m, ExpertIn in, ExpertOut out, int nb, int group)
     if (!find_tile<P::BM>(m, nb, group, t))
         return;
     P p(lds, in, t);
-    p.run();
-    const int wave = threadIdx.x / kWave, wm = wave / P::WN, wn = wave % P::WN;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), wm = wave / P::WN, wn = wave % P::WN;
+    // an expert's last tile may leave the lower waves without rows: the matrix pipes are
+    // then the upper ones' alone
+    const bool rows = wm * (P::BM / P::WM) < t.n;
+    if (rows)
+        p.template run<true>();
+    else
+        p.template run<false>();
     const int columns = in.half ? P::BN / 2 : P::BN;
     static_assert(P::BM * P::BN * 2 <= P::lds_bytes, "a tile's results fit where its operands were");
     __syncthreads();
+    if (!rows)
+        return;
     finish(out, p.acc, t, wm * (P::BM / P::WM), t.block * columns + wn * (columns / P::WN),
            lds + wave * (P::TI * P::TJ * 512));
 }

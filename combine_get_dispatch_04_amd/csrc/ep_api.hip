@@ -738,7 +738,7 @@ ep_status_t check_expert(const void *x, const uint8_t *x_scales, ep_quant_t x_qu
     // rows by offsets, or E * cap of them
     if (offsets ? (counts || cap != 0) : (cap < 0 || (int64_t)E * cap != rows))
         return EP_ERR_INVALID_ARG;
-    if (E > kMaxExperts || H > ep::kMaxAdapterWidth || O > ep::kMaxAdapterWidth || (int64_t)O * H >= (int64_t)1 << 32)
+    if (E > kMaxExperts || H > ep::kMaxAdapterWidth || O > ep::kMaxAdapterWidth || (int64_t)O * H >= (int64_t)1 << 31)
         return EP_ERR_UNSUPPORTED;
     // tiles of 32 rows and more by 64 columns and more, 256 threads each: 32-bit grids
     const int64_t tiles = ((int64_t)rows + 31) / 32 + E, blocks = ((H > O ? H : O) + 63) / 64;

@@ -39,7 +39,7 @@ struct Tile {
 // Every wave finds it for itself, a lane for every 64th of the experts: no barrier (of a
 // tile of 256 x 256 this takes 1 us of 40).
 template <int BM>
-__device__ __forceinline__ bool find_tile(const ExpertRows &m, int nb, int group, Tile &t)
+__device__ __forceinline__ bool find_tile(const ExpertRows &m, int most, int nb, int group, Tile &t)
 {
     const int lane = threadIdx.x & (kWave - 1), per = (m.E + kWave - 1) / kWave;
     const int e0 = least(lane * per, m.E), e1 = least(e0 + per, m.E);
@@ -47,10 +47,11 @@ __device__ __forceinline__ bool find_tile(const ExpertRows &m, int nb, int group
 #pragma unroll 4
     for (int e = e0; e < e1; ++e) {
         rows_of(m, e, first, n);
-        mine += (n + BM - 1) / BM;
+        mine = least(mine + (n + BM - 1) / BM, most);
     }
+    // offsets that overlap may ask for more tiles than there are rows: the first `most`
     const int upto = wave_inclusive_scan(mine, lane);
-    const int total = __builtin_amdgcn_readlane(upto, kWave - 1);
+    const int total = least(__builtin_amdgcn_readlane(upto, kWave - 1), most);
     // 32-bit: the host bounds row tiles times columns
     if ((int64_t)blockIdx.x >= (int64_t)total * nb)
         return false;
@@ -255,7 +256,9 @@ __device__ __forceinline__ void finish(const ExpertOut &o, const f32x4 (&acc)[TI
 // together.  One barrier per slice, some groups into it: every wave then holds the
 // slice in registers (its buffer is free), and the next one has arrived.
 constexpr int kRowsMx4 = 0, kRowsMxE4M3 = 1, kRowsMxE5M2 = 2, kRowsWide = 3, kRowsAcross = 4;
-constexpr uint32_t kNowhere = 0x80000000u;      // no buffer is larger than 2^31 bytes
+// Outside every buffer, and with a stage's offset still below 2^32: no operand of a tile
+// is larger than 2^30 bytes.
+constexpr uint32_t kNowhere = 0x80000000u;
 
 template <int BM_, int BN_, int WM_, int WN_, int NS_, int KIND>
 struct ExpertProduct {
@@ -645,11 +648,11 @@ struct ExpertProduct {
 
 template <typename P>
 __global__ void __launch_bounds__(P::threads, P::waves / 4)
-expert_kernel(ExpertRows m, ExpertIn in, ExpertOut out, int nb, int group)
+expert_kernel(ExpertRows m, ExpertIn in, ExpertOut out, int most, int nb, int group)
 {
     extern __shared__ __attribute__((aligned(16))) char lds[];
     Tile t;
-    if (!find_tile<P::BM>(m, nb, group, t))
+    if (!find_tile<P::BM>(m, most, nb, group, t))
         return;
     P p(lds, in, t);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), wm = wave / P::WN, wn = wave % P::WN;
@@ -687,13 +690,13 @@ hipError_t product(const ExpertRows &m, const ExpertIn &in, const ExpertOut &out
     const int64_t blocks = row_tiles(m, P::BM) * nb;
     if (blocks == 0)
         return hipSuccess;
-    if (blocks >= 1 << 22)          // a grid's threads are 32 bits
+    if (blocks >= 1 << 23)          // a grid's threads are 32 bits
         return hipErrorInvalidValue;
     hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(expert_kernel<P>),
                                        hipFuncAttributeMaxDynamicSharedMemorySize, P::lds_bytes);
     if (e != hipSuccess)
         return e;
-    expert_kernel<P><<<(unsigned)blocks, P::threads, P::lds_bytes, s>>>(m, in, out, nb, 4);
+    expert_kernel<P><<<(unsigned)blocks, P::threads, P::lds_bytes, s>>>(m, in, out, (int)(blocks / nb), nb, 4);
     return hipGetLastError();
 }
 

@@ -247,6 +247,22 @@ def test_rows_behind_the_last_expert_and_broken_offsets(form, per):
 
 
 @pytest.mark.parametrize("form", FORMS)
+def test_offsets_that_overlap_ask_for_no_more_than_there_is(form):
+    """Every second expert has all rows: more tiles than the rows make; nothing outside the arrays."""
+    E, n, H, O = 300, 700, 64, 128
+    g = gen(12)
+    x = bf(g, n, H)
+    x, xs = (x, None) if form == "bf16" else R.quantize(x, form)
+    w, ws = R.quantize(bf(g, E, O, H), R.FP4)
+    dx_, ds_, dw_, dws_ = on(x, xs, w, ws)
+    off = torch.tensor([0, n] * (E // 2) + [0], dtype=torch.int32, device=DEV)
+    guard = torch.full((n + 64, O), 7.0, dtype=torch.bfloat16, device=DEV)
+    api.expert_product(dx_, ds_, dw_, dws_, offsets=off, out=guard[:n])
+    torch.cuda.synchronize()
+    assert (guard[n:] == 7).all() and torch.isfinite(guard.float()).all()
+
+
+@pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("counts", [[3, 4], [80, 70], [300, 200]], ids=str)
 @pytest.mark.parametrize("act", [None, "swiglu"])
 def test_what_is_not_finite_stays_in_its_row(form, counts, act):

@@ -248,3 +248,56 @@ def test_refusals():
             call()
             print("not refused:", i)
     torch.cuda.synchronize()
+
+
+def test_arrays_past_4_gib():
+    g = torch.Generator().manual_seed(1)
+    bf = lambda *s, by=1.0: (torch.randn(s, generator=g) * by).to(torch.bfloat16)  # noqa: E731
+    # rows
+    n, H, O, last = 600_000, 4096, 64, 301
+    x = torch.zeros((n, H), dtype=torch.bfloat16, device=DEV)
+    tail = bf(last, H)
+    x[-last:] = tail.to(DEV)
+    w, ws = R.quantize(bf(2, O, H, by=H ** -0.5), R.FP4)
+    off = torch.tensor([0, n - last, n], dtype=torch.int32, device=DEV)
+    want = R.product(tail.double(), R.values(w, ws)[1], False)
+    y, _, h = api.expert_product(x, None, w.to(DEV), ws.to(DEV), offsets=off)
+    R.assert_close(y[-last:], *want)
+    assert not y[:-last].any()
+    d = torch.zeros((n, O), dtype=torch.bfloat16, device=DEV)
+    d[-last:] = bf(last, O).to(DEV)
+    dx = api.expert_product_backward(d, h)
+    R.assert_close(dx[-last:], *R.product(tail.double(), R.values(w, ws)[1], False, d[-last:].cpu().double())[2:])
+    assert not dx[:-last].any()
+    codes, scales = api.mx_quantize(x)
+    del x, y, d, dx, h
+    big = torch.zeros((4 * n, H // 2), dtype=torch.uint8, device=DEV)
+    big_s = torch.zeros((4 * n, H // 32), dtype=torch.uint8, device=DEV)
+    big[-last:], big_s[-last:] = codes[-last:], scales[-last:]
+    off = torch.tensor([0, last, 4 * n], dtype=torch.int32, device=DEV)
+    y, _, _ = api.expert_product(big[-2 * last:], big_s[-2 * last:], w.to(DEV), ws.to(DEV),
+                                 offsets=torch.tensor([0, last, 2 * last], dtype=torch.int32, device=DEV))
+    z, _, _ = api.expert_product(big, big_s, w.to(DEV), ws.to(DEV), offsets=off)
+    v, tol = R.product(R.values(codes[-last:].cpu(), scales[-last:].cpu()), R.values(w, ws)[1], False)
+    R.assert_close(y[-last:], v, tol)
+    R.assert_close(z[-last:], v, tol)
+    del big, big_s, y, z
+    # weights
+    E, H, I = 200, 4096, 2048
+    up = torch.zeros((E, 2 * I, H), dtype=torch.bfloat16, device=DEV)
+    down = torch.zeros((E, H, I), dtype=torch.bfloat16, device=DEV)
+    up[-1], down[-1] = bf(2 * I, H, by=H ** -0.5).to(DEV), bf(H, I, by=I ** -0.5).to(DEV)
+    xs, idx = bf(1, H).to(DEV), torch.tensor([[E - 1]], dtype=torch.int32, device=DEV)
+    out, _ = api.low_latency_experts(xs, idx, None, up, down)
+    one, _ = api.low_latency_experts(xs, idx * 0, None, up[-1:], down[-1:])
+    assert torch.equal(out, one) and out.any()
+    uc, us = api.mx_quantize(up[-1:])
+    codes = torch.zeros((600, 2 * I, H // 2), dtype=torch.uint8, device=DEV)
+    sc = torch.zeros((600, 2 * I, H // 32), dtype=torch.uint8, device=DEV)
+    codes[-1], sc[-1] = uc[0], us[0]
+    rows = xs.repeat(3, 1)
+    off = torch.zeros(601, dtype=torch.int32, device=DEV)
+    off[-1] = 3
+    y, _, _ = api.expert_product(rows, None, codes, sc, offsets=off)
+    one, _, _ = api.expert_product(rows, None, uc, us, offsets=torch.tensor([0, 3], dtype=torch.int32, device=DEV))
+    assert torch.equal(y, one) and y.any()

@@ -836,7 +836,7 @@ ep_status_t check_few_sizes(int T, int K, int E, int H, int I)
 
 size_t ep_low_latency_experts_workspace_bytes(int T, int K, int E, int H, int I)
 {
-    return check_few_sizes(T, K, E, H, I) == EP_OK ? ep::make_few_plan(T, K, E, H, I).bytes : 0;
+    return check_few_sizes(T, K, E, H, I) == EP_OK ? ep::make_few_plan(T, K, E, H, I, false).bytes : 0;
 }
 
 ep_status_t ep_low_latency_experts(const uint16_t *x, int T, int H, const int32_t *topk_idx,
@@ -855,7 +855,7 @@ ep_status_t ep_low_latency_experts(const uint16_t *x, int T, int H, const int32_
     if (!aligned(x, 16) || !aligned(up, 16) || !aligned(down, 16) || !aligned(out, 16) || !aligned(topk_idx, 4) ||
         !aligned(topk_weights, 4) || !aligned(num_invalid, 4))
         return EP_ERR_INVALID_ARG;
-    const ep::FewPlan p = ep::make_few_plan(T, K, E, H, I);
+    const ep::FewPlan p = ep::make_few_plan(T, K, E, H, I, coded);
     if ((st = check_ws(ws, ws_bytes, p.bytes)) != EP_OK)
         return st;
     return hip_status(ep::launch_few(p, x, topk_idx, topk_weights, up, up_scales, down, down_scales, out, num_invalid,

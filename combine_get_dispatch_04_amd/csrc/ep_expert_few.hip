@@ -77,13 +77,14 @@ struct Few {
     }
     // Four blocks at a time, one per 16 lanes.  The weight comes from memory and is asked
     // for AHEAD steps before its use, the columns from a cache or LDS, one step.  The
-    // scales come sixteen at a time: a row's request is 64 bytes whatever it takes of them.
+    // scales come sixteen at a time (a row's request is 64 bytes whatever it takes of
+    // them), and four steps ahead: loads come back in their order, so that to wait for
+    // the last one is to wait for all.
     __device__ __forceinline__ void run_fp4(int s0, int s1, int HB)
     {
-        // (128 registers with F = 2, 256 with F = 4)
-        constexpr int SLOTS = 4, AHEAD = F * NT > 2 ? 1 : 3, XS = NT > 1 ? 1 : 2;
+        constexpr int SLOTS = 4, AHEAD = F * NT > 2 ? 1 : 2, RING = AHEAD > 1 ? 4 : 2, XS = NT > 1 ? 1 : 2;
         const int g = (threadIdx.x & (kWave - 1)) >> 4, last = s1 - 1;
-        u32x4 c[SLOTS][F], x[XS][NT][4], sc[F];
+        u32x4 c[RING][F], x[XS][NT][4], sc[F], next[F];
         // behind the last block: the last one again, its columns as zeros and its scales
         // as 1 (an infinite one times 0 would be a NaN)
         auto load_w = [&](int s, int slot) {
@@ -96,11 +97,11 @@ struct Few {
 #pragma unroll
             for (int f = 0; f < F; ++f) {
                 if (s + 16 <= HB) {
-                    __builtin_memcpy(&sc[f], scales[f] + s, 16);
+                    __builtin_memcpy(&next[f], scales[f] + s, 16);
                 } else {        // the lane's own ones
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        sc[f][j] = (uint32_t)scales[f][least(s + 4 * j + g, last)] << (8 * g);
+                        next[f][j] = (uint32_t)scales[f][least(s + 4 * j + g, last)] << (8 * g);
                 }
             }
         };
@@ -123,7 +124,7 @@ struct Few {
 #pragma unroll
                 for (int f = 0; f < F; ++f) {
                     const uint32_t one = behind ? 127u : sc[f][j] >> (8 * g) & 255u;
-                    const bf16x8 a = __builtin_bit_cast(bf16x8, e2m1_bf16x8(c[j][f][q], one));
+                    const bf16x8 a = __builtin_bit_cast(bf16x8, e2m1_bf16x8(c[j % RING][f][q], one));
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
                         acc[f][n] = mfma(a, v[n], acc[f][n]);
@@ -144,11 +145,16 @@ struct Few {
         load_x(s0, 0);
         for (int s = s0; s < s1; s += 4 * SLOTS) {
 #pragma unroll
+            for (int f = 0; f < F; ++f)
+                sc[f] = next[f];
+            if (s + 4 * SLOTS < s1)
+                load_scales(s + 4 * SLOTS);
+#pragma unroll
             for (int j = 0; j < SLOTS; ++j) {
                 const int now = s + 4 * j;
                 if (now >= s1)
                     break;
-                load_w(now + 4 * AHEAD, (j + AHEAD) % SLOTS);
+                load_w(now + 4 * AHEAD, (j + AHEAD) % RING);
                 if constexpr (XS == 2) {
                     if (now + 4 < s1)
                         load_x(now + 4, (j + 1) % 2);
@@ -158,8 +164,6 @@ struct Few {
                     if (now + 4 < s1)
                         load_x(now + 4, 0);
                 }
-                if (j == SLOTS - 1 && now + 4 < s1)
-                    load_scales(now + 4);
             }
         }
     }
@@ -257,14 +261,15 @@ __device__ __forceinline__ bool can_stage(const FewPlan &p, int n, int D, int64_
 }
 
 // ---------------------------------------------------------------- some tokens for each expert
-// Where an expert has many tokens, their columns are what the CUs have to take in: a
+// Where experts have some tokens each, the columns are what the CUs have to take in: a
 // block's four waves then share them, by LDS, and take 32 weight rows each through
 // the whole inner dimension.  Steps of 128 elements; a step's columns are rows of
-// 256 bytes, piece c of column r in slot c ^ (r & 15), loaded three steps ahead, as
-// is the weight (four buffers).
+// 256 bytes, piece c of column r in slot c ^ (r & 15).  Columns and weight are asked for
+// AHEAD steps before their use: seven where the buffers (64 KB, of two blocks on a CU)
+// and the registers reach that far, else three.
 template <bool FP4, int NT>
 struct Shared {
-    static constexpr int SLOTS = 4, AHEAD = 3, bytes = NT * 4096, WL = FP4 ? 1 : 4;
+    static constexpr int SLOTS = FP4 && NT <= 2 ? 8 : 4, AHEAD = SLOTS - 1, bytes = NT * 4096, WL = FP4 ? 1 : 4;
     f32x4 acc[2][NT];
     const uint8_t *w[2], *scales[2];    // the lane's weight rows
     uint32_t col[NT];                   // offset of the column whose piece the lane loads, or kNowhere
@@ -280,7 +285,7 @@ struct Shared {
 #pragma unroll
             for (int c = 0; c < NT; ++c)
                 acc[f][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        u32x4 c[SLOTS][2][WL], sc[2];
+        u32x4 c[SLOTS][2][WL], sc[2], next[2];
         // the columns behind the last element are zeros; the weight's elements there have
         // to be finite
         auto load_w = [&](int s, int slot) {
@@ -301,12 +306,12 @@ struct Shared {
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
                 if (s * 4 + 16 <= HB) {
-                    __builtin_memcpy(&sc[f], scales[f] + s * 4, 16);
+                    __builtin_memcpy(&next[f], scales[f] + s * 4, 16);
                 } else {        // the lane's own ones; 1 behind the last
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int b = (s + j) * 4 + g;
-                        sc[f][j] = (b < HB ? (uint32_t)scales[f][b] : 127u) << (8 * g);
+                        next[f][j] = (b < HB ? (uint32_t)scales[f][b] : 127u) << (8 * g);
                     }
                 }
             }
@@ -330,7 +335,7 @@ struct Shared {
                 for (int f = 0; f < 2; ++f) {
                     bf16x8 a;
                     if constexpr (FP4)
-                        a = __builtin_bit_cast(bf16x8, e2m1_bf16x8(c[j][f][0][q], sc[f][j] >> (8 * g) & 255u));
+                        a = __builtin_bit_cast(bf16x8, e2m1_bf16x8(c[j][f][0][q], sc[f][j % 4] >> (8 * g) & 255u));
                     else
                         a = __builtin_bit_cast(bf16x8, c[j][f][q]);
 #pragma unroll
@@ -353,6 +358,12 @@ struct Shared {
                 const int now = s + j;
                 if (now >= n)
                     break;
+                if (FP4 && j % 4 == 0) {        // four steps ahead, as above
+                    sc[0] = next[0];
+                    sc[1] = next[1];
+                    if (now + 4 < n)
+                        load_scales(now + 4);
+                }
                 // a step's columns come before its weight and two more steps
                 if (now + AHEAD <= n)
                     wait_and_meet<(AHEAD - 1) * (NT + 2 * WL) + (FP4 ? 2 : 0)>();
@@ -363,8 +374,6 @@ struct Shared {
                     load_w(now + AHEAD, (j + AHEAD) % SLOTS);
                 }
                 multiply(now, j);
-                if (FP4 && j == SLOTS - 1 && now + 1 < n)
-                    load_scales(now + 1);
             }
         }
         __syncthreads();        // the buffers are free
@@ -597,9 +606,9 @@ few_up_kernel(FewPlan p, const uint16_t *__restrict__ x, const int32_t *__restri
     __shared__ int found[3], counts[2];
     __shared__ Token list[kFewTokens];
     const int tid = threadIdx.x;
-    // tokens go 64 at a time, each lot to a block of its own
-    const int slices = p.slices_up, lots = WIDE ? (p.T + 63) / 64 : 1, slice = blockIdx.x % slices;
-    const int at = blockIdx.x / slices / lots, lot = blockIdx.x / slices % lots, i0 = slice * (WIDE ? 64 : 16);
+    // tokens go 64 at a time, each lot to a block of its own; the first lots first
+    const int slices = p.slices_up, slice = blockIdx.x % slices, i0 = slice * (WIDE ? 64 : 16);
+    const int at = blockIdx.x / slices % p.most, lot = WIDE ? blockIdx.x / slices / p.most : 0;
     // the second launch's counters
     for (int i = blockIdx.x * blockDim.x + tid; i < p.slices; i += gridDim.x * blockDim.x)
         t.arrived[i] = 0u;
@@ -721,19 +730,79 @@ __device__ __forceinline__ void down_shared(const FewPlan &p, const uint16_t *h,
     }
     a.run(p.I);
 #pragma unroll
-    for (int i = 0; i < NT / 2; ++i) {
+    for (int i = 0; i < (NT + 1) / 2; ++i) {
         const int c = i * 16 + (lane & 15);
-        if (c >= n)
+        f32x4 sum[2];
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            if constexpr (NT > 1) {
+                sum[f] = a.acc[f][i] + a.acc[f][i + NT / 2];
+            } else {            // eight lanes on
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    sum[f][q] = a.acc[f][0][q] + dpp_f<0x128, 0xF>(0.0f, a.acc[f][0][q]);
+            }
+        }
+        if (c >= least(n, half))
             continue;
         const Token t = list[c];
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
             const int at = row + f * 16 + (lane >> 4) * 4;
+            const f32x4 v = t.coef * sum[f];
+            uint64_t *to = reinterpret_cast<uint64_t *>(part + (int64_t)t.entry * p.H + at);
+            if (at < p.H) {         // (H % 8 == 0)
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (at + q < p.H)
-                    __hip_atomic_store(part + (int64_t)t.entry * p.H + at + q, t.coef * (a.acc[f][i][q] + a.acc[f][i + NT / 2][q]),
+                for (int q = 0; q < 2; ++q)
+                    __hip_atomic_store(to + q, (uint64_t)__float_as_uint(v[2 * q + 1]) << 32 | __float_as_uint(v[2 * q]),
                                        __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+        }
+    }
+}
+
+// The tokens' parts of the columns [r0, r0 + COLS), added up in the order of k: pairs of
+// columns, U of them at a time and of each KC parts, all asked for together (a round is
+// a miss to memory).
+template <int U, int KC, int COLS>
+__device__ __forceinline__ void add_parts(const FewPlan &p, const float *part, const uint64_t *firsts, int r0, uint16_t *out)
+{
+    const int all = p.T * (COLS / 2), step = blockDim.x;
+    for (int i0 = threadIdx.x; i0 < all; i0 += U * step) {
+        float a[U], b[U];
+        uint64_t has[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            a[u] = b[u] = 0.0f;
+            const int i = i0 + u * step;
+            has[u] = i < all && r0 + i % (COLS / 2) * 2 < p.H ? firsts[i / (COLS / 2)] : 0;
+        }
+        for (int k0 = 0; k0 < p.K; k0 += KC) {
+            uint64_t v[U][KC];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < KC; ++k) {
+                    const int i = i0 + u * step;
+                    const float *from = part + ((int64_t)(i / (COLS / 2)) * p.K + k0 + k) * p.H + r0 + i % (COLS / 2) * 2;
+                    v[u][k] = 0;
+                    if (k0 + k < p.K && has[u] >> (k0 + k) & 1)
+                        v[u][k] = __hip_atomic_load(reinterpret_cast<const uint64_t *>(from), __ATOMIC_RELAXED,
+                                                    __HIP_MEMORY_SCOPE_AGENT);
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < KC; ++k) {
+                    a[u] += __uint_as_float((uint32_t)v[u][k]);
+                    b[u] += __uint_as_float((uint32_t)(v[u][k] >> 32));
+                }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * step, c = r0 + i % (COLS / 2) * 2;
+            if (i < all && c < p.H)
+                *reinterpret_cast<uint32_t *>(out + (int64_t)(i / (COLS / 2)) * p.H + c) = pack_bf16_any(a[u], b[u]);
         }
     }
 }
@@ -748,10 +817,9 @@ few_down_kernel(FewPlan p, const uint16_t *__restrict__ h, const int32_t *__rest
     __shared__ Token list[kFewTokens];
     __shared__ bool last;
     constexpr int cols = WIDE ? 128 : 32;
-    // tokens go 32 at a time, each lot to a block of its own
-    const int lots = WIDE ? (p.T + 31) / 32 : 1;
+    // tokens go 32 at a time, each lot to a block of its own; the first lots first
     const int tid = threadIdx.x, slice = blockIdx.x % p.slices, r0 = slice * cols;
-    const int at = blockIdx.x / p.slices / lots, lot = blockIdx.x / p.slices % lots;
+    const int at = blockIdx.x / p.slices % p.most, lot = WIDE ? blockIdx.x / p.slices / p.most : 0;
     // (at < p.most: in the tables, if not of use)
     const int named = t.named[0], e = t.expert[at], n = t.count[at];
     const int total = t.named[1];
@@ -766,7 +834,9 @@ few_down_kernel(FewPlan p, const uint16_t *__restrict__ h, const int32_t *__rest
             char *const lds = reinterpret_cast<char *>(red);
             const Token *mine = list + lot * 32;
             const int m = least(n - lot * 32, 32);
-            if (m <= 16)
+            if (m <= 8)
+                down_shared<FP4, 1>(p, h, w, ws, e, r0, mine, m, lds, part);
+            else if (m <= 16)
                 down_shared<FP4, 2>(p, h, w, ws, e, r0, mine, m, lds, part);
             else
                 down_shared<FP4, 4>(p, h, w, ws, e, r0, mine, m, lds, part);
@@ -795,46 +865,10 @@ few_down_kernel(FewPlan p, const uint16_t *__restrict__ h, const int32_t *__rest
     __syncthreads();
     if (!last)
         return;
-    // pairs of columns, four at a time, and of each four parts at a time, in the order of k
-    constexpr int U = 4, KC = 4;
-    const int all = p.T * (cols / 2), step = blockDim.x;
-    for (int i0 = tid; i0 < all; i0 += U * step) {
-        float a[U], b[U];
-        uint64_t firsts[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            a[u] = b[u] = 0.0f;
-            const int i = i0 + u * step;
-            firsts[u] = i < all && r0 + i % (cols / 2) * 2 < p.H ? t.firsts[i / (cols / 2)] : 0;
-        }
-        for (int k0 = 0; k0 < p.K; k0 += KC) {
-            uint64_t v[U][KC];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int k = 0; k < KC; ++k) {
-                    const int i = i0 + u * step;
-                    const float *from = part + ((int64_t)(i / (cols / 2)) * p.K + k0 + k) * p.H + r0 + i % (cols / 2) * 2;
-                    v[u][k] = 0;
-                    if (k0 + k < p.K && firsts[u] >> (k0 + k) & 1)
-                        v[u][k] = __hip_atomic_load(reinterpret_cast<const uint64_t *>(from), __ATOMIC_RELAXED,
-                                                    __HIP_MEMORY_SCOPE_AGENT);
-                }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int k = 0; k < KC; ++k) {
-                    a[u] += __uint_as_float((uint32_t)v[u][k]);
-                    b[u] += __uint_as_float((uint32_t)(v[u][k] >> 32));
-                }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = i0 + u * step, c = r0 + i % (cols / 2) * 2;
-            if (i < all && c < p.H)
-                *reinterpret_cast<uint32_t *>(out + (int64_t)(i / (cols / 2)) * p.H + c) = pack_bf16_any(a[u], b[u]);
-        }
-    }
+    if (p.K <= 2)
+        add_parts<WIDE ? 16 : 8, 2, cols>(p, part, t.firsts, r0, out);
+    else
+        add_parts<WIDE ? 4 : 2, 8, cols>(p, part, t.firsts, r0, out);
 }
 
 __global__ void few_zero_kernel(int32_t *p) { *p = 0; }
@@ -843,7 +877,7 @@ __global__ void few_zero_kernel(int32_t *p) { *p = 0; }
 // each.
 int waves_of(int D, bool fp4)
 {
-    const int steps = (D + (fp4 ? 127 : 31)) / (fp4 ? 128 : 32), per = fp4 ? 6 : 8;
+    const int steps = (D + (fp4 ? 127 : 31)) / (fp4 ? 128 : 32), per = fp4 ? 4 : 8;
     return steps >= 4 * per ? 4 : (steps >= 2 * per ? 2 : 1);
 }
 
@@ -878,7 +912,7 @@ hipError_t launch_few_as(const FewPlan &p, const uint16_t *x, const int32_t *idx
 
 }  // namespace
 
-FewPlan make_few_plan(int T, int K, int E, int H, int I)
+FewPlan make_few_plan(int T, int K, int E, int H, int I, bool fp4)
 {
     FewPlan p{};
     p.T = T;
@@ -887,9 +921,18 @@ FewPlan make_few_plan(int T, int K, int E, int H, int I)
     p.H = H;
     p.I = I;
     p.most = least(T * K, E);
-    // experts with some tokens each: blocks of 128 weight rows, that share the tokens'
-    // columns (whose arrays a buffer has to reach)
-    p.wide = T * K >= 12 * p.most && (int64_t)T * K * I < 1 << 29;
+    // Blocks of 128 weight rows, that share the tokens' columns (whose arrays a buffer has
+    // to reach), or of 32.  Large ones need work for the card: tokens' entries times
+    // blocks of an expert.  MXFP4 (us with 32 and with 128; T, K, E, H, I):
+    //   4, 2, 8, 4096, 4096 (512 of them)      45   51    16, 4, 16, 4096, 1024 (1024)  52   38
+    //   16, 4, 64, 2048, 512 (512)             36   31    8, 8, 64, 7168, 2048 (2048)  258  225
+    //   16, 2, 8, 2048, 1024 (512)             23   27    80, 8, 64, 7168, 2048        757  433
+    // bf16, whose rows' bytes keep the small ones busy, needs more tokens for each expert too:
+    //   32, 8, 8, 1024, 512 (2048)             27   36    64, 8, 64, 4096, 1024        368  336
+    //   48, 8, 64, 4096, 1024 (6144)          322  319    128, 8, 16, 2048, 1024       224  131
+    //   16, 8, 64, 4096, 1024                 229  235    32, 2, 8, 4096, 4096         170  178
+    const int64_t work = (int64_t)T * K * ((I + 63) / 64);
+    p.wide = (int64_t)T * K * I < 1 << 29 && (fp4 ? work >= 1024 : work >= 4096 && T * K >= 8 * p.most);
     const int rows = p.wide ? 128 : 32;
     // what an expert's tokens take of LDS, on average; twice that at most
     const int mean = (T * K + p.most - 1) / (p.most > 0 ? p.most : 1), wide = H > 2 * I ? H : 2 * I;
@@ -905,7 +948,7 @@ FewPlan make_few_plan(int T, int K, int E, int H, int I)
     };
     const size_t entries = (size_t)T * K;
     p.lower = (int64_t)entries * I;
-    p.off_arrived = take((size_t)p.slices * 4);
+    p.off_arrived = take((size_t)((H + 31) / 32) * 4);      // (for either type of weights)
     p.off_named = take(8);
     p.off_expert = take((size_t)p.most * 4);
     p.off_count = take((size_t)p.most * 4);

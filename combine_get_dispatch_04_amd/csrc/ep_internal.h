@@ -212,7 +212,7 @@ struct FewTables {
     float *coef;
     uint64_t *firsts;       // [T]
 };
-FewPlan make_few_plan(int T, int K, int E, int H, int I);
+FewPlan make_few_plan(int T, int K, int E, int H, int I, bool fp4);
 hipError_t launch_few(const FewPlan &p, const uint16_t *x, const int32_t *idx, const float *weights, const void *up,
                       const uint8_t *up_scales, const void *down, const uint8_t *down_scales, uint16_t *out,
                       int32_t *num_invalid, char *ws, hipStream_t s);

@@ -113,3 +113,37 @@ def test_the_same_bits_every_time_and_for_any_company(form):
         assert torch.equal(first, call(*a)[0])
     none, n = call(a[0][:0], a[1][:0], a[2][:0], *a[3:])
     assert none.shape == (0, 256) and int(n) == 0
+
+
+# blocks of 128 weight rows, whose waves share the columns: by lots of 8 to 64 tokens of
+# an expert, inner dimensions from less than one step to more than all buffers hold
+SHARED = [(R.FP4, 1, 8, 16, 64, 8192), (R.FP4, 2, 8, 12, 1056, 4128), (R.FP4, 128, 8, 256, 96, 64),
+          (R.FP4, 128, 8, 200, 608, 96), (R.FP4, 128, 8, 100, 1184, 160), (R.FP4, 128, 8, 40, 288, 608),
+          (R.FP4, 128, 8, 16, 32, 32 * 33), (R.FP4, 33, 32, 33, 160, 64), (R.FP4, 128, 2, 8, 2080, 256),
+          ("bf16", 128, 8, 8, 72, 264), ("bf16", 128, 8, 100, 200, 256), ("bf16", 128, 8, 128, 40, 1000),
+          ("bf16", 64, 16, 16, 136, 1032), ("bf16", 128, 8, 64, 1160, 256)]
+
+
+@pytest.mark.parametrize("form,T,K,E,H,I", SHARED)
+def test_shared_columns(form, T, K, E, H, I):
+    check(*make(T, K, E, H, I, form, seed=E))
+
+
+@pytest.mark.parametrize("form,T,K,E,H,I", [s for s in SHARED if s[1] == 128])
+def test_shared_columns_with_gaps_doubles_and_what_is_not_finite(form, T, K, E, H, I):
+    x, idx, w, up, us, down, ds = make(T, K, E, H, I, form, seed=E)
+    g = torch.Generator().manual_seed(E)
+    idx[torch.rand(idx.shape, generator=g) < 0.2] = -1
+    idx[3] = -1
+    idx[4] = idx[4, 0]
+    idx[5, 1] = E
+    first = check(x, idx, w, up, us, down, ds, bad=1)
+    assert torch.equal(first, call(x, idx, w, up, us, down, ds)[0])
+    x[7, 1], x[12, 9], w[20, 0] = float("nan"), float("inf"), float("nan")
+    idx[[7, 12, 20], 0] = 0
+    first = call(torch.nan_to_num(x, 1.0, 1.0, 1.0), idx, torch.nan_to_num(w, 1.0), up, us, down, ds)[0]
+    out, _ = call(x, idx, w, up, us, down, ds)
+    keep = torch.ones(T, dtype=torch.bool)
+    keep[[7, 12, 20]] = False
+    assert torch.equal(out.cpu()[keep], first.cpu()[keep])
+    assert not torch.isfinite(out.cpu()[~keep].float()).any()

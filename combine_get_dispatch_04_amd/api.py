@@ -8,7 +8,10 @@ Request] Support Expert-Choice Routing via Native Expert-Centric API"
 In front of them, the router that makes topk_idx and topk_weights, with its
 balance loss and gradients (route, balance_loss, route_backward); and, over
 the same topk_idx, low-rank adapters beside a shared projection
-(adapter_project and its backward).
+(adapter_project and its backward).  Between dispatch and combine, the experts:
+their weights in MXFP4 (mx_quantize), the products on the dispatched rows
+(expert_product and its backward), and for a few tokens the whole layer in one
+call (low_latency_experts).
 
 torch only allocates device memory and supplies the current stream; every
 step runs in the HIP kernels of libep.so.  Errors from the library raise

@@ -36,8 +36,8 @@ struct Tile {
 // none (the host knows how many there may be at most, the device how many there
 // are).  Of the tiles that there are, `group` row tiles by all columns go to an
 // XCD in a row, column by column.
-// Every wave finds it for itself, a lane for every 64th of the experts: no barrier (of a
-// tile of 256 x 256 this takes 1 us of 40).
+// Every wave finds it for itself, a lane for every 64th of the experts: no barrier (one
+// of them and the table behind it in LDS took 3 % of a tile of 256 x 256).
 template <int BM>
 __device__ __forceinline__ bool find_tile(const ExpertRows &m, int most, int nb, int group, Tile &t)
 {
@@ -91,8 +91,8 @@ __device__ __forceinline__ float sigmoid(float v)
 // TI * 16 rows, columns j*16 + (lane >> 4)*4 ..+3 of the tile's.  With a gate,
 // odd j are the other half's values of j - 1.  The results go by LDS (`own`, the
 // wave's part of it: TI * TJ * 512 bytes), so that memory gets whole lines of a row
-// and not the few bytes that a lane has of it (at 256 x 256 the stores took 11 of a
-// tile's 46 us).
+// and not the few bytes that a lane has of it (at 256 x 256 the stores took 13 of a
+// tile's 84 thousand cycles, now 8).
 template <int KIND, int BITS, int TI, int TJ>
 __device__ __forceinline__ void finish_as(const ExpertOut &o, const f32x4 (&acc)[TI][TJ], const Tile &t, int row0,
                                           int c0, char *own)
@@ -240,15 +240,24 @@ __device__ __forceinline__ void finish(const ExpertOut &o, const f32x4 (&acc)[TI
 // what lies outside a tile's rows or behind the last channel is fetched as zeros (an
 // address outside the buffer).  A slice's row has 4 pieces of 16 bytes (8 of 8-bit
 // rows), piece c of row r in slot c ^ ((r >> 1) & 3) (c ^ (r & 7)), so that the 16 rows
-// a fragment reads at one place spread over the banks.  What has to be looked at on the way goes through registers,
-// into one of two buffers: the scales of codes (16 bytes of a row, for two stages: a
-// row's request to L2 is 64 bytes whatever it takes of them, and stage by stage they
-// were a third of all requests), a weight that is widened (a block of 32 codes and
-// its scale per thread and piece, a stage at a time).
+// a fragment reads at one place spread over the banks.  What has to be looked at on the
+// way goes through registers, into one of two buffers: the scales of codes (16 bytes of a
+// row, for two stages: a row's request to L2 is 64 bytes whatever it takes of them, and
+// stage by stage they were a third of all requests), a weight that is widened (a block
+// of 32 codes and its scale per thread and piece, a stage at a time).
 //
 // A lane's operand of a 4-bit MFMA is one block of 32 channels, 32 (lane >> 4) ..;
 // of an 8-bit one the channels 16 (lane >> 4) .. and 64 + 16 (lane >> 4) ..; its
 // scale operand belongs to the block 32 (lane >> 4) .. in either case.
+//
+// What bounds it: with few rows the weight's bytes (128 rows over 64 experts of 4096 x
+// 7168, MXFP8 rows: 216 us, 4.9 TB/s, which is what a large copy reaches).  With many,
+// no single thing: MXFP4 rows by 256 x 256 tiles reach 2.6 PFLOP/s (512 rows for each of
+// 64 experts, 4096 x 4096: 416 us), the matrix pipes busy for a third of it; without
+// its loads the main loop is 25 % shorter, without the scales 10 %, without the LDS
+// reads 10 %, and a tile of 4096 channels spends 59 of its 84 thousand cycles there
+// (14 to fill the buffers, 8 for the results).  bf16 rows: 0.93 PFLOP/s (1024 rows for
+// each of 8 experts, 297 us, as 2.25 rounds of 256 CUs), the pipes busy 39 %.
 //
 // The MFMAs go in TI groups of TJ, one row of fragments each; after a group the
 // row's fragment of the next slice is read into the same registers, and a few of

@@ -19,6 +19,13 @@
 // An expert's part of a token's output goes to memory in fp32; the block that
 // arrives last at its columns adds the parts up in the order of k, so that the
 // result does not depend on which block that is.
+//
+// Measured, the first launch and the second: one token, 8 of 64 experts (bf16, H 4096,
+// I 2048) 50 + 30 us for 403 MB; the same in MXFP4 with H 7168 35 + 25 for 187 MB, where
+// a launch's own time, the search for the expert and the first loads are a third of it;
+// 32 tokens in bf16 349 + 193 for 3.2 GB (5.8 TB/s); 128 tokens, 2 of 8 experts in MXFP4
+// (H = I = 4096) 54 + 66 for 214 MB, where what the CUs take in of the columns bounds it
+// (16 KB by DMA and 64 KB by reads a step of a block, whose matrix work is 0.2 us).
 #include "ep_common.h"
 #include "ep_internal.h"
 
@@ -43,13 +50,14 @@ __device__ __forceinline__ int column_place(int piece)
     return FP4 ? piece / 16 * 256 + (piece & 3) * 64 + (piece >> 2 & 3) * 16 : piece * 16;
 }
 constexpr int kStageBytes = 32 << 10;   // of a block, at most
+constexpr int kFrags = 2;
 
-// F fragments of 16 weight rows by NT of 16 columns, from memory or (STAGED) from LDS.
+// Two fragments of 16 weight rows by NT of 16 columns, from memory or (STAGED) from LDS.
 // acc[f][n]: rows f*16 + (lane >> 4)*4 ..+3 by column n*16 + (lane & 15).
-template <bool FP4, int F, int NT, bool STAGED>
+template <bool FP4, int NT, bool STAGED>
 struct Few {
-    f32x4 acc[F][NT];
-    const uint8_t *w[F], *scales[F];    // the lane's weight rows
+    f32x4 acc[kFrags][NT];
+    const uint8_t *w[kFrags], *scales[kFrags];    // the lane's weight rows
     const uint16_t *col[NT];            // its columns
     uint32_t at[NT];                    // the same in LDS
     const char *lds;
@@ -66,7 +74,7 @@ struct Few {
     __device__ __forceinline__ void run(int s0, int s1, int D)
     {
 #pragma unroll
-        for (int f = 0; f < F; ++f)
+        for (int f = 0; f < kFrags; ++f)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
                 acc[f][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -79,23 +87,24 @@ struct Few {
     // for AHEAD steps before its use, the columns from a cache or LDS, one step.  The
     // scales come sixteen at a time (a row's request is 64 bytes whatever it takes of
     // them), and four steps ahead: loads come back in their order, so that to wait for
-    // the last one is to wait for all.
+    // the last one is to wait for all.  (One token, 8 of 64 experts, H 7168, I 2048: with 1,
+    // 2 and 3 steps ahead 68, 61 and 66 us: registers.)
     __device__ __forceinline__ void run_fp4(int s0, int s1, int HB)
     {
-        constexpr int SLOTS = 4, AHEAD = F * NT > 2 ? 1 : 2, RING = AHEAD > 1 ? 4 : 2, XS = NT > 1 ? 1 : 2;
+        constexpr int SLOTS = 4, AHEAD = NT > 1 ? 1 : 2, RING = AHEAD > 1 ? 4 : 2, XS = NT > 1 ? 1 : 2;
         const int g = (threadIdx.x & (kWave - 1)) >> 4, last = s1 - 1;
-        u32x4 c[RING][F], x[XS][NT][4], sc[F], next[F];
+        u32x4 c[RING][kFrags], x[XS][NT][4], sc[kFrags], next[kFrags];
         // behind the last block: the last one again, its columns as zeros and its scales
         // as 1 (an infinite one times 0 would be a NaN)
         auto load_w = [&](int s, int slot) {
             const int b = least(s + g, last);
 #pragma unroll
-            for (int f = 0; f < F; ++f)
+            for (int f = 0; f < kFrags; ++f)
                 c[slot][f] = ld16_nt(w[f] + (int64_t)b * 16);
         };
         auto load_scales = [&](int s) {
 #pragma unroll
-            for (int f = 0; f < F; ++f) {
+            for (int f = 0; f < kFrags; ++f) {
                 if (s + 16 <= HB) {
                     __builtin_memcpy(&next[f], scales[f] + s, 16);
                 } else {        // the lane's own ones
@@ -122,7 +131,7 @@ struct Few {
                 for (int n = 0; n < NT; ++n)
                     v[n] = __builtin_bit_cast(bf16x8, behind ? u32x4{0u, 0u, 0u, 0u} : x[xslot][n][q]);
 #pragma unroll
-                for (int f = 0; f < F; ++f) {
+                for (int f = 0; f < kFrags; ++f) {
                     const uint32_t one = behind ? 127u : sc[f][j] >> (8 * g) & 255u;
                     const bf16x8 a = __builtin_bit_cast(bf16x8, e2m1_bf16x8(c[j % RING][f][q], one));
 #pragma unroll
@@ -141,11 +150,11 @@ struct Few {
         for (int j = 0; j < AHEAD; ++j)
             load_w(s0 + 4 * j, j);
         if constexpr (STAGED)
-            wait_and_meet<AHEAD * F>();         // the loads of the columns came before these
+            wait_and_meet<AHEAD * kFrags>();         // the loads of the columns came before these
         load_x(s0, 0);
         for (int s = s0; s < s1; s += 4 * SLOTS) {
 #pragma unroll
-            for (int f = 0; f < F; ++f)
+            for (int f = 0; f < kFrags; ++f)
                 sc[f] = next[f];
             if (s + 4 * SLOTS < s1)
                 load_scales(s + 4 * SLOTS);
@@ -169,15 +178,15 @@ struct Few {
     }
     __device__ __forceinline__ void run_bf16(int s0, int s1, int D)
     {
-        constexpr int U = F * NT > 4 ? 2 : 4;
+        constexpr int U = 4;
         const int g = (threadIdx.x & (kWave - 1)) >> 4;
-        u32x4 c[U][F];
+        u32x4 c[U][kFrags];
         auto load_w = [&](int s) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int k = (s + u) * 32 + g * 8;
 #pragma unroll
-                for (int f = 0; f < F; ++f)
+                for (int f = 0; f < kFrags; ++f)
                     c[u][f] = s + u < s1 && k < D ? ld16_nt(w[f] + (int64_t)k * 2) : u32x4{0u, 0u, 0u, 0u};
             }
         };
@@ -196,7 +205,7 @@ struct Few {
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int f = 0; f < F; ++f)
+                for (int f = 0; f < kFrags; ++f)
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
                         acc[f][n] = mfma(__builtin_bit_cast(bf16x8, c[u][f]), __builtin_bit_cast(bf16x8, x[u][n]),
@@ -210,20 +219,20 @@ struct Few {
     {
         const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
 #pragma unroll
-        for (int f = 0; f < F; ++f)
+        for (int f = 0; f < kFrags; ++f)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                *reinterpret_cast<f32x4 *>(red + (((wave * F + f) * NT + n) * 16 + (lane & 15)) * 16 + (lane >> 4) * 4) =
+                *reinterpret_cast<f32x4 *>(red + (((wave * kFrags + f) * NT + n) * 16 + (lane & 15)) * 16 + (lane >> 4) * 4) =
                     acc[f][n];
     }
 };
 // Row r of fragment f, column c, summed over the waves.
-template <int F, int NT>
+template <int NT>
 __device__ __forceinline__ float added(const float *red, int waves, int f, int c, int r)
 {
     float v = 0.0f;
     for (int w = 0; w < waves; ++w)
-        v += red[(((w * F + f) * NT + (c >> 4)) * 16 + (c & 15)) * 16 + r];
+        v += red[(((w * kFrags + f) * NT + (c >> 4)) * 16 + (c & 15)) * 16 + r];
     return v;
 }
 
@@ -496,19 +505,19 @@ __device__ void first_entries(const FewPlan &p, const Entry *entries, uint64_t *
         *total = *sum;
 }
 
-// Fragments: the gates of F/2 * 16 of the I columns from i0 on, then their ups.
-template <bool FP4, int F, int NT, bool STAGED>
+// Fragments: the gates of 16 of the I columns from i0 on, then their ups.
+template <bool FP4, int NT, bool STAGED>
 __device__ __forceinline__ void up_group(const FewPlan &p, const uint16_t *x, const uint8_t *w, const uint8_t *ws,
                                          int e, int i0, const Token *list, int n, float *red, uint16_t *h)
 {
-    constexpr int cols = F * 8;
+    constexpr int cols = kFrags * 8;
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave, waves = blockDim.x / kWave;
-    Few<FP4, F, NT, STAGED> a;
+    Few<FP4, NT, STAGED> a;
     a.lds = reinterpret_cast<const char *>(red);
 #pragma unroll
-    for (int f = 0; f < F; ++f) {
-        const int row = least(i0 + f % (F / 2) * 16 + (lane & 15), p.I - 1);
-        const int64_t r = (int64_t)e * 2 * p.I + f / (F / 2) * p.I + row;
+    for (int f = 0; f < kFrags; ++f) {
+        const int row = least(i0 + f % (kFrags / 2) * 16 + (lane & 15), p.I - 1);
+        const int64_t r = (int64_t)e * 2 * p.I + f / (kFrags / 2) * p.I + row;
         a.w[f] = w + r * (FP4 ? p.H / 2 : p.H * 2);
         a.scales[f] = FP4 ? ws + r * (p.H / 32) : nullptr;
     }
@@ -536,8 +545,8 @@ __device__ __forceinline__ void up_group(const FewPlan &p, const uint16_t *x, co
         const int c = i / cols, r = i % cols;
         if (i0 + r >= p.I)
             continue;
-        const float gate = added<F, NT>(red, waves, r >> 4, c, r & 15),
-                    up = added<F, NT>(red, waves, F / 2 + (r >> 4), c, r & 15);
+        const float gate = added<NT>(red, waves, r >> 4, c, r & 15),
+                    up = added<NT>(red, waves, kFrags / 2 + (r >> 4), c, r & 15);
         const float v = gate / (1.0f + expf(-gate)) * up;
         const uint32_t hi = pack_bf16_any(v, 0.0f);
         const float rest = v - bf16_lo(hi);
@@ -647,27 +656,27 @@ few_up_kernel(FewPlan p, const uint16_t *__restrict__ x, const int32_t *__restri
             up_shared<FP4, 1>(p, x, w, ws, e, i0, mine, m, lds, h);
     } else {
         if (n <= 16 && can_stage<FP4>(p, n, p.H, (int64_t)p.T * p.H))
-            up_group<FP4, 2, 1, true>(p, x, w, ws, e, i0, list, n, red, h);
+            up_group<FP4, 1, true>(p, x, w, ws, e, i0, list, n, red, h);
         else if (n <= 16)
-            up_group<FP4, 2, 1, false>(p, x, w, ws, e, i0, list, n, red, h);
+            up_group<FP4, 1, false>(p, x, w, ws, e, i0, list, n, red, h);
         else
             for (int g = 0; g < n; g += 32)
-                up_group<FP4, 2, 2, false>(p, x, w, ws, e, i0, list + g, n - g, red, h);
+                up_group<FP4, 2, false>(p, x, w, ws, e, i0, list + g, n - g, red, h);
     }
 }
 
 // ---------------------------------------------------------------- the second launch
 // Columns: `half` tokens' nearest bf16, then what those left over.
-template <bool FP4, int F, int NT, bool STAGED>
+template <bool FP4, int NT, bool STAGED>
 __device__ __forceinline__ void down_group(const FewPlan &p, const uint16_t *h, const uint8_t *w, const uint8_t *ws,
                                            int e, int r0, const Token *list, int n, float *red, float *part)
 {
-    constexpr int half = NT * 8, cols = F * 16;
+    constexpr int half = NT * 8, cols = kFrags * 16;
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave, waves = blockDim.x / kWave;
-    Few<FP4, F, NT, STAGED> a;
+    Few<FP4, NT, STAGED> a;
     a.lds = reinterpret_cast<const char *>(red);
 #pragma unroll
-    for (int f = 0; f < F; ++f) {
+    for (int f = 0; f < kFrags; ++f) {
         const int64_t r = (int64_t)e * p.H + least(r0 + f * 16 + (lane & 15), p.H - 1);
         a.w[f] = w + r * (FP4 ? p.I / 2 : p.I * 2);
         a.scales[f] = FP4 ? ws + r * (p.I / 32) : nullptr;
@@ -697,7 +706,7 @@ __device__ __forceinline__ void down_group(const FewPlan &p, const uint16_t *h, 
         const int c = i / cols, r = i % cols;
         if (r0 + r >= p.H)
             continue;
-        const float v = added<F, NT>(red, waves, r >> 4, c, r & 15) + added<F, NT>(red, waves, r >> 4, half + c, r & 15);
+        const float v = added<NT>(red, waves, r >> 4, c, r & 15) + added<NT>(red, waves, r >> 4, half + c, r & 15);
         // read by a block on any XCD: not left in this one's L2
         __hip_atomic_store(part + (int64_t)list[c].entry * p.H + r0 + r, list[c].coef * v, __ATOMIC_RELAXED,
                            __HIP_MEMORY_SCOPE_AGENT);
@@ -842,12 +851,12 @@ few_down_kernel(FewPlan p, const uint16_t *__restrict__ h, const int32_t *__rest
                 down_shared<FP4, 4>(p, h, w, ws, e, r0, mine, m, lds, part);
         } else {
             if (n <= 8 && can_stage<FP4>(p, 2 * n, p.I, 2 * p.lower))
-                down_group<FP4, 2, 1, true>(p, h, w, ws, e, r0, list, n, red, part);
+                down_group<FP4, 1, true>(p, h, w, ws, e, r0, list, n, red, part);
             else if (n <= 8)
-                down_group<FP4, 2, 1, false>(p, h, w, ws, e, r0, list, n, red, part);
+                down_group<FP4, 1, false>(p, h, w, ws, e, r0, list, n, red, part);
             else
                 for (int g = 0; g < n; g += 16)
-                    down_group<FP4, 2, 2, false>(p, h, w, ws, e, r0, list + g, n - g, red, part);
+                    down_group<FP4, 2, false>(p, h, w, ws, e, r0, list + g, n - g, red, part);
         }
     }
     // Every wave's parts have arrived where all XCDs see them before the block counts
@@ -873,8 +882,8 @@ few_down_kernel(FewPlan p, const uint16_t *__restrict__ h, const int32_t *__rest
 
 __global__ void few_zero_kernel(int32_t *p) { *p = 0; }
 
-// The waves of a block, by the inner dimension: about eight loads of a weight row for
-// each.
+// The waves of a block, by the inner dimension: eight steps of 32 for each, or four of
+// 128 (one token, H 7168, I 2048: 59.8 us, with six steps 61.2, with sixteen 63).
 int waves_of(int D, bool fp4)
 {
     const int steps = (D + (fp4 ? 127 : 31)) / (fp4 ? 128 : 32), per = fp4 ? 4 : 8;

@@ -7,7 +7,9 @@
 //
 // Bound by memory: 2 bytes in and 17/32 (or 33/32) out for a channel.  A lane
 // takes 8 channels (16 bytes), four lanes a block; the maximum goes round by
-// quad permutations.
+// quad permutations.  470 M values (16 matrices of 4096 x 7168) to MXFP4 in 178 us
+// and back in 166 (6.7 and 7.2 TB/s); 128 rows of 7168 to MXFP8 in 3.1 and back in
+// 2.9, the launch's own time.
 #include "ep_common.h"
 #include "ep_internal.h"
 

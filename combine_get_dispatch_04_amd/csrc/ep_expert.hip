@@ -34,8 +34,9 @@ struct Tile {
 };
 // The block's tile.  Row tiles go by expert; the blocks behind the last one have
 // none (the host knows how many there may be at most, the device how many there
-// are).  Of the tiles that there are, `group` row tiles by all columns go to an
-// XCD in a row, column by column.
+// are).  Experts' last tiles of at most half the rows, which take less time, come
+// after all others, for the CUs that the last full round leaves idle.  Of either
+// kind, `group` row tiles by all columns go to an XCD in a row, column by column.
 // Every wave finds it for itself, a lane for every 64th of the experts: no barrier (one
 // of them and the table behind it in LDS took 3 % of a tile of 256 x 256).
 template <int BM>
@@ -43,33 +44,42 @@ __device__ __forceinline__ bool find_tile(const ExpertRows &m, int most, int nb,
 {
     const int lane = threadIdx.x & (kWave - 1), per = (m.E + kWave - 1) / kWave;
     const int e0 = least(lane * per, m.E), e1 = least(e0 + per, m.E);
-    int mine = 0, first, n;
+    int first, n, longs = 0, shorts = 0;
+    auto last_is_short = [](int rows) { return rows > 0 && (rows - 1) % BM < BM / 2; };
 #pragma unroll 4
     for (int e = e0; e < e1; ++e) {
         rows_of(m, e, first, n);
-        mine = least(mine + (n + BM - 1) / BM, most);
+        const int s = last_is_short(n);
+        longs = least(longs + (n + BM - 1) / BM - s, most);
+        shorts += s;
     }
     // offsets that overlap may ask for more tiles than there are rows: the first `most`
-    const int upto = wave_inclusive_scan(mine, lane);
-    const int total = least(__builtin_amdgcn_readlane(upto, kWave - 1), most);
+    const int upto_longs = wave_inclusive_scan(longs, lane), upto_shorts = wave_inclusive_scan(shorts, lane);
+    const int all_longs = least(__builtin_amdgcn_readlane(upto_longs, kWave - 1), most);
+    const int all_shorts = least(__builtin_amdgcn_readlane(upto_shorts, kWave - 1), most - all_longs);
     // 32-bit: the host bounds row tiles times columns
-    if ((int64_t)blockIdx.x >= (int64_t)total * nb)
+    const bool is_short = (int)blockIdx.x >= all_longs * nb;
+    const int block = blockIdx.x - (is_short ? all_longs * nb : 0), total = is_short ? all_shorts : all_longs;
+    if (block >= total * nb)
         return false;
-    const int id = xcd_order(blockIdx.x, total * nb);
+    const int id = xcd_order(block, total * nb);
     const int g0 = id / (group * nb) * group, rows = least(group, total - g0), at = id - g0 * nb;
     const int slot = g0 + at % rows;
-    int before = upto - mine, e = e0;
+    const int upto = is_short ? upto_shorts : upto_longs;
+    int before = upto - (is_short ? shorts : longs), e = e0, r0 = 0;
     const bool here = slot >= before && slot < upto;
     if (here)
         for (; e < e1; ++e) {
             rows_of(m, e, first, n);
-            const int tiles = (n + BM - 1) / BM;
-            if (slot < before + tiles)
+            const int tiles = (n + BM - 1) / BM, s = last_is_short(n), mine = is_short ? s : tiles - s;
+            if (slot < before + mine) {
+                r0 = (is_short ? tiles - 1 : slot - before) * BM;
                 break;
-            before += tiles;
+            }
+            before += mine;
         }
     // in scalar registers, for the buffers' descriptors
-    const int from = __ffsll((unsigned long long)ballot(here)) - 1, r0 = (slot - before) * BM;
+    const int from = __ffsll((unsigned long long)ballot(here)) - 1;
     t = Tile{__builtin_amdgcn_readlane(e, from), __builtin_amdgcn_readlane(first + r0, from),
              __builtin_amdgcn_readlane(least(BM, n - r0), from), at / rows};
     return true;

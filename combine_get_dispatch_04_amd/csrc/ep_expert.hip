@@ -35,8 +35,10 @@ struct Tile {
 // The block's tile.  Row tiles go by expert; the blocks behind the last one have
 // none (the host knows how many there may be at most, the device how many there
 // are).  Experts' last tiles of at most half the rows, which take less time, come
-// after all others, for the CUs that the last full round leaves idle.  Of either
-// kind, `group` row tiles by all columns go to an XCD in a row, column by column.
+// after all others, for the CUs that the last full round leaves idle (bf16, 8 experts of
+// 1024 rows: 901 -> 872 us for the three products of a step; MXFP4, 64 experts of 512 rows: the
+// same within 1 %).  Of either kind, `group` row tiles by all columns go to an XCD in
+// a row, column by column.
 // Every wave finds it for itself, a lane for every 64th of the experts: no barrier (one
 // of them and the table behind it in LDS took 3 % of a tile of 256 x 256).
 template <int BM>
@@ -266,8 +268,9 @@ __device__ __forceinline__ void finish(const ExpertOut &o, const f32x4 (&acc)[TI
 // 64 experts, 4096 x 4096: 416 us), the matrix pipes busy for a third of it; without
 // its loads the main loop is 25 % shorter, without the scales 10 %, without the LDS
 // reads 10 %, and a tile of 4096 channels spends 59 of its 84 thousand cycles there
-// (14 to fill the buffers, 8 for the results).  bf16 rows: 0.93 PFLOP/s (1024 rows for
-// each of 8 experts, 297 us, as 2.25 rounds of 256 CUs), the pipes busy 39 %.
+// (14 to fill the buffers, 8 for the results).  bf16 rows: 0.96 PFLOP/s (1024 rows for
+// each of 8 experts, 288 us: two rounds of 256 CUs and the short last tiles), the pipes
+// busy 40 %.
 //
 // The MFMAs go in TI groups of TJ, one row of fragments each; after a group the
 // row's fragment of the next slice is read into the same registers, and a few of

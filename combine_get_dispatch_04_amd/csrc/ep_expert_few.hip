@@ -944,7 +944,7 @@ FewPlan make_few_plan(int T, int K, int E, int H, int I, bool fp4)
     p.wide = (int64_t)T * K * I < 1 << 29 && (fp4 ? work >= 1024 : work >= 4096 && T * K >= 8 * p.most);
     const int rows = p.wide ? 128 : 32;
     // what an expert's tokens take of LDS, on average; twice that at most
-    const int mean = (T * K + p.most - 1) / (p.most > 0 ? p.most : 1), wide = H > 2 * I ? H : 2 * I;
+    const int mean = p.most > 0 ? (T * K + p.most - 1) / p.most : 0, wide = H > 2 * I ? H : 2 * I;
     const int64_t want = ((int64_t)2 * mean * (wide * 2 + 256 + 64) + 1023) / 1024 * 1024;
     p.stage_bytes = (int)(want < kStageBytes ? want : kStageBytes);
     p.slices = (H + rows - 1) / rows;

@@ -24,8 +24,9 @@
 // I 2048) 50 + 30 us for 403 MB; the same in MXFP4 with H 7168 35 + 25 for 187 MB, where
 // a launch's own time, the search for the expert and the first loads are a third of it;
 // 32 tokens in bf16 349 + 193 for 3.2 GB (5.8 TB/s); 128 tokens, 2 of 8 experts in MXFP4
-// (H = I = 4096) 54 + 66 for 214 MB, where what the CUs take in of the columns bounds it
-// (16 KB by DMA and 64 KB by reads a step of a block, whose matrix work is 0.2 us).
+// (H = I = 4096) 54 + 66 for 214 MB: a step of 128 channels takes a block 1.6 us, of which
+// its matrix work and its reads of LDS are 0.2 each and its 24 vector memory
+// instructions, at about 60 cycles, 0.6; the rest is latency (two blocks to a CU).
 #include "ep_common.h"
 #include "ep_internal.h"
 
@@ -826,7 +827,9 @@ few_down_kernel(FewPlan p, const uint16_t *__restrict__ h, const int32_t *__rest
     __shared__ Token list[kFewTokens];
     __shared__ bool last;
     constexpr int cols = WIDE ? 128 : 32;
-    // tokens go 32 at a time, each lot to a block of its own; the first lots first
+    // tokens go 32 at a time, each lot to a block of its own; the first lots first.  (An
+    // expert's blocks on one XCD, whose L2 would then have the columns once: 121 -> 129 us
+    // with 128 tokens, 2 of 8 experts of unequal numbers.)
     const int tid = threadIdx.x, slice = blockIdx.x % p.slices, r0 = slice * cols;
     const int at = blockIdx.x / p.slices % p.most, lot = WIDE ? blockIdx.x / p.slices / p.most : 0;
     // (at < p.most: in the tables, if not of use)

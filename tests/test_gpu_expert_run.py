@@ -301,3 +301,39 @@ def test_arrays_past_4_gib():
     y, _, _ = api.expert_product(rows, None, codes, sc, offsets=off)
     one, _, _ = api.expert_product(rows, None, uc, us, offsets=torch.tensor([0, 3], dtype=torch.int32, device=DEV))
     assert torch.equal(y, one) and y.any()
+
+
+@pytest.mark.parametrize("fp4,T,K,E,H,I", [(True, 128, 8, 40, 288, 608), (False, 128, 8, 16, 136, 1032),
+                                           (True, 2, 8, 12, 1056, 4128), (True, 100, 2, 3, 96, 32)])
+def test_few_tokens_layers_in_a_graph(fp4, T, K, E, H, I):
+    """Replayed with other tokens and other numbers of them for each expert, eager calls in between."""
+    x, up, down, idx, w = layer(T, K, E, H, I, 3)
+    us = ds = None
+    if fp4:
+        (up, us), (down, ds) = api.mx_quantize(up), api.mx_quantize(down)
+    run = lambda x, idx, w: api.low_latency_experts(x, idx, w, up, down, up_scales=us, down_scales=ds)  # noqa: E731
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run(x, idx, w)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got, bad = run(x, idx, w)
+    for r in range(5):
+        x2, _, _, idx2, w2 = layer(T, K, E, H, I, 50 + r)
+        if r == 2:
+            idx2[:] = -1
+        if r == 3:
+            idx2[:] = idx2[:1]          # all tokens at the same experts
+            idx2[-1, 0] = E
+        x.copy_(x2)
+        idx.copy_(idx2)
+        w.copy_(w2)
+        graph.replay()
+        torch.cuda.synchronize()
+        want, n = run(x2, idx2, w2)
+        torch.cuda.synchronize()
+        assert torch.equal(got.view(torch.int16), want.view(torch.int16)) and int(bad) == int(n) == (r == 3), r

@@ -88,15 +88,17 @@ __device__ __forceinline__ bool find_tile(const ExpertRows &m, int most, int nb,
 }
 
 // ---------------------------------------------------------------- behind the product
-// 1 / (1 + exp(-v)) within 2^-21 of its value, by the units' own exponential (of 2) and
-// reciprocal, 7 instructions; what -v log2(e) loses to rounding is made good to first
-// order.  Results below 2^-126 are 0.
+// 1 / (1 + exp(-v)) within 2^-20 of its value, and 0 where that is below 2^-128 (v < -88.7),
+// by the units' own exponential (of 2) and reciprocal, 10 instructions; what -v log2(e)
+// loses to rounding is made good to first order.  From t = 128 on the exponential is
+// infinite (a correction times it would be a NaN), and beyond |v| = 2.36e38 t is: no
+// correction there.  The reciprocal is that of a quarter, as the unit gives no subnormals.
 __device__ __forceinline__ float sigmoid(float v)
 {
     constexpr float l2e = 1.44269504f, ln2 = 0.693147181f, l2e_rest = 1.92596299e-8f;
     const float t = -v * l2e, rest = fmaf(-v, l2e, -t) - v * l2e_rest;
-    const float p = __builtin_amdgcn_exp2f(t);
-    return __builtin_amdgcn_rcpf(1.0f + fmaf(p, rest * ln2, p));
+    const float p = __builtin_amdgcn_exp2f(t), q = fabsf(t) < 128.0f ? fmaf(p, rest * ln2, p) : p;
+    return 0.25f * __builtin_amdgcn_rcpf(fmaf(q, 0.25f, 0.25f));
 }
 
 // What becomes of a wave's sums: acc[i][j] holds row i*16 + (lane & 15) of its

@@ -139,8 +139,9 @@ __device__ __forceinline__ void finish_as(const ExpertOut &o, const f32x4 (&acc)
                 for (int q = 0; q < 4; ++q) {
                     const float d = q & 1 ? bf16_hi(d2[q >> 1]) : bf16_lo(d2[q >> 1]);
                     const float g = acc[i][j][q], u = acc[i][j + 1][q], s = sigmoid(g);
-                    dg[q] = d * u * s * (1.0f + g * (1.0f - s));
-                    du[q] = d * g * s;
+                    // d last: d u and d g may be beyond fp32 where the results are not
+                    dg[q] = s * (1.0f + g * (1.0f - s)) * u * d;
+                    du[q] = g * s * d;
                 }
                 *reinterpret_cast<u32x2 *>(put(i, (j * 8 + at) * 2)) =
                     u32x2{pack_bf16_any(dg[0], dg[1]), pack_bf16_any(dg[2], dg[3])};

@@ -667,6 +667,14 @@ few_up_kernel(FewPlan p, const uint16_t *__restrict__ x, const int32_t *__restri
 }
 
 // ---------------------------------------------------------------- the second launch
+// The sum of a product with h's two parts.  An infinite weight gives an infinity or a NaN with
+// the first one; what it gives with the second (a NaN, where nothing was left over, or an
+// infinity of the other sign) is not part of the result.
+__device__ __forceinline__ float joined(float nearest, float rest)
+{
+    return fabsf(nearest) < __builtin_huge_valf() ? nearest + rest : nearest;
+}
+
 // Columns: `half` tokens' nearest bf16, then what those left over.
 template <bool FP4, int NT, bool STAGED>
 __device__ __forceinline__ void down_group(const FewPlan &p, const uint16_t *h, const uint8_t *w, const uint8_t *ws,
@@ -707,7 +715,7 @@ __device__ __forceinline__ void down_group(const FewPlan &p, const uint16_t *h, 
         const int c = i / cols, r = i % cols;
         if (r0 + r >= p.H)
             continue;
-        const float v = added<NT>(red, waves, r >> 4, c, r & 15) + added<NT>(red, waves, r >> 4, half + c, r & 15);
+        const float v = joined(added<NT>(red, waves, r >> 4, c, r & 15), added<NT>(red, waves, r >> 4, half + c, r & 15));
         // read by a block on any XCD: not left in this one's L2
         __hip_atomic_store(part + (int64_t)list[c].entry * p.H + r0 + r, list[c].coef * v, __ATOMIC_RELAXED,
                            __HIP_MEMORY_SCOPE_AGENT);
@@ -745,12 +753,12 @@ __device__ __forceinline__ void down_shared(const FewPlan &p, const uint16_t *h,
         f32x4 sum[2];
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-            if constexpr (NT > 1) {
-                sum[f] = a.acc[f][i] + a.acc[f][i + NT / 2];
-            } else {            // eight lanes on
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    sum[f][q] = a.acc[f][0][q] + dpp_f<0x128, 0xF>(0.0f, a.acc[f][0][q]);
+            for (int q = 0; q < 4; ++q) {
+                if constexpr (NT > 1)
+                    sum[f][q] = joined(a.acc[f][i][q], a.acc[f][i + NT / 2][q]);
+                else            // eight lanes on
+                    sum[f][q] = joined(a.acc[f][0][q], dpp_f<0x128, 0xF>(0.0f, a.acc[f][0][q]));
             }
         }
         if (c >= least(n, half))

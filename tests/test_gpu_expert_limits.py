@@ -1,9 +1,11 @@
-"""The experts at the ends of what a call may hold: gradients whose factors overflow between them."""
+"""The experts at the ends of what a call may hold: gradients whose factors overflow between them, weights that
+are infinite."""
 import pytest
 import torch
 
 import expert_ref as R
 from combine_get_dispatch_04_amd import api
+from test_gpu_expert_few import call, make
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -30,3 +32,23 @@ def test_gradients_whose_factors_overflow_between_them(g, u, d):
     off = 2.0 ** -19 * back.abs() + (0 if s >= 2.0 ** -128 else back.abs())
     off = off + R.HALF * (back.abs() + off)
     R.assert_close(dx, back @ w[0].double(), R.steps(2 * I) * (back.abs() @ w[0].double()) + off @ w[0].double())
+
+
+@pytest.mark.parametrize("T,K,E,H,I", [(6, 2, 3, 96, 64), (24, 2, 5, 352, 264), (128, 8, 8, 72, 264), (64, 16, 16, 136, 1032)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_an_infinite_weight_of_the_second_product(T, K, E, H, I, sign):
+    """h goes into the product as two parts: what the second one makes of an infinite weight is not part of the result."""
+    x, idx, w, up, us, down, ds = make(T, K, E, H, I, "bf16", seed=T)
+    w = w + 0.1
+    finite, _ = call(x, idx, w, up, us, down, ds)
+    down[1, 5, 3] = sign * float("inf")
+    out, _ = call(x, idx, w, up, us, down, ds)
+    out, finite = out.cpu().float(), finite.cpu().float()
+    named = (idx == 1).any(1)
+    assert named.any()
+    other = torch.ones(H, dtype=torch.bool)
+    other[5] = False
+    assert torch.equal(out[:, other], finite[:, other]) and torch.equal(out[~named], finite[~named])
+    h = R.gated(x.double() @ up[1].double().T, torch.zeros(T, 2 * I, dtype=torch.float64))[0][:, 3]
+    assert (h[named] != 0).all()
+    assert torch.equal(out[named, 5], (sign * torch.sign(h[named])).float() * float("inf"))

@@ -1,5 +1,5 @@
 """The experts at the ends of what a call may hold: gradients whose factors overflow between them, weights that
-are infinite."""
+are infinite, a token among any others."""
 import pytest
 import torch
 
@@ -52,3 +52,28 @@ def test_an_infinite_weight_of_the_second_product(T, K, E, H, I, sign):
     h = R.gated(x.double() @ up[1].double().T, torch.zeros(T, 2 * I, dtype=torch.float64))[0][:, 3]
     assert (h[named] != 0).all()
     assert torch.equal(out[named, 5], (sign * torch.sign(h[named])).float() * float("inf"))
+
+
+# (narrow and wide forms of both kinds of weights)
+@pytest.mark.parametrize("form,T,K,E,H,I", [("bf16", 16, 4, 9, 256, 160), (R.FP4, 16, 4, 9, 256, 160),
+                                            ("bf16", 128, 8, 100, 200, 256), (R.FP4, 128, 8, 100, 1184, 160),
+                                            ("bf16", 128, 1, 64, 96, 72), (R.FP4, 33, 2, 3, 4096, 96)])
+def test_a_token_gives_the_same_bits_in_any_company(form, T, K, E, H, I):
+    """One token's row, entries and weights stay; all others get other values, other experts, the same ones, or none."""
+    x, idx, w, up, us, down, ds = make(T, K, E, H, I, form, seed=H)
+    t = T // 2
+    first = call(x, idx, w, up, us, down, ds)[0][t]
+    g = torch.Generator().manual_seed(1)
+    for kind in ("values", "experts", "the same experts", "none"):
+        x2 = (torch.randn((T, H), generator=g) * 3).to(torch.bfloat16)
+        w2, idx2 = torch.randn((T, K), generator=g), idx.clone()
+        if kind == "experts":
+            idx2 = torch.randint(-1, E, (T, K), generator=g, dtype=torch.int32)
+        elif kind == "the same experts":
+            idx2[:] = idx[t]
+        elif kind == "none":
+            idx2[:] = -1
+        x2[t], w2[t], idx2[t] = x[t], w[t], idx[t]
+        out = call(x2, idx2, w2, up, us, down, ds)[0]
+        assert torch.equal(out[t], first), kind
+        assert kind == "none" or not torch.equal(out[t - 1], first)

@@ -817,6 +817,12 @@ _MX_OF = {torch.uint8: "mxfp4_e2m1", torch.float8_e4m3fn: "mxfp8_e4m3", torch.fl
 _ACTIVATIONS = {None: N.EP_ACT_NONE, "swiglu": N.EP_ACT_SWIGLU}
 
 
+def _sizes(call: str, *sizes: int):
+    """The C calls' sizes are 32 bits: a larger one would arrive as what is left of it."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise N.EpError(call, N.EP_ERR_UNSUPPORTED)
+
+
 def _mx_mode(quant: str) -> str:
     quant = _QUANT_ALIASES.get(quant, quant)
     if quant not in _MX_OF.values():
@@ -854,6 +860,7 @@ def mx_quantize(x: torch.Tensor, quant: str = "mxfp4_e2m1"):
     q, dt, div, _ = _QUANT[quant]
     if H < 32 or H % 32 != 0:
         raise ValueError(f"x must have a multiple of 32 channels, got {H}")
+    _sizes("ep_mx_quantize", x.numel() // H, H)
     dev = x.device
     codes = torch.empty((*x.shape[:-1], H // div), dtype=dt, device=dev)
     scales = torch.empty((*x.shape[:-1], H // 32), dtype=torch.uint8, device=dev)
@@ -872,6 +879,7 @@ def mx_dequantize(codes: torch.Tensor, scales: torch.Tensor) -> torch.Tensor:
     quant, H = _need_codes(codes, scales, "codes", codes.dim())
     if H < 32:
         raise ValueError("codes must have a multiple of 32 channels")
+    _sizes("ep_mx_dequantize", scales.numel() * 32 // H, H)
     dev = codes.device
     out = torch.empty((*codes.shape[:-1], H), dtype=torch.bfloat16, device=dev)
     with _on(dev):
@@ -930,6 +938,7 @@ def _expert_sizes(x, x_scales, weight, weight_scales, offsets, counts, activatio
                 raise ValueError(f"counts must be [E] = {E}, got {counts.shape[0]}")
         cap = x.shape[1]
         rows = E * cap
+    _sizes("ep_expert_product", rows, cap, E, O, H)
     _same_device(x.device, x_scales=x_scales, weight=weight, weight_scales=weight_scales, offsets=offsets,
                  counts=counts)
     return quant, rows, cap, E, O, H
@@ -1055,6 +1064,7 @@ def low_latency_experts(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: O
     E = up.shape[0]
     if uH != H or tuple(up.shape[:2]) != (E, 2 * I) or tuple(down.shape[:2]) != (E, H):
         raise ValueError(f"up must be [E, 2I, H] and down [E, H, I] with H = {H}")
+    _sizes("ep_low_latency_experts", T, K, E, H, I)
     dev = x.device
     _same_device(dev, topk_idx=topk_idx, topk_weights=topk_weights, up=up, down=down, up_scales=up_scales,
                  down_scales=down_scales)

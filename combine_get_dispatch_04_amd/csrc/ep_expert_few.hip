@@ -53,6 +53,15 @@ __device__ __forceinline__ int column_place(int piece)
 constexpr int kStageBytes = 32 << 10;   // of a block, at most
 constexpr int kFrags = 2;
 
+// The waits for columns on their way to LDS count the loads behind them, so the weight's
+// loads have to stay behind the columns' and in front of the next ones: nothing else tells
+// the compiler so, which sees two kinds of memory.
+__device__ __forceinline__ void loads_stay_in_order()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 // Two fragments of 16 weight rows by NT of 16 columns, from memory or (STAGED) from LDS.
 // acc[f][n]: rows f*16 + (lane >> 4)*4 ..+3 by column n*16 + (lane & 15).
 template <bool FP4, int NT, bool STAGED>
@@ -146,12 +155,16 @@ struct Few {
                 wait_and_meet<0>();
             return;
         }
+        if constexpr (STAGED)
+            loads_stay_in_order();
         load_scales(s0);
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j)
             load_w(s0 + 4 * j, j);
-        if constexpr (STAGED)
+        if constexpr (STAGED) {
+            loads_stay_in_order();
             wait_and_meet<AHEAD * kFrags>();         // the loads of the columns came before these
+        }
         load_x(s0, 0);
         for (int s = s0; s < s1; s += 4 * SLOTS) {
 #pragma unroll
@@ -333,6 +346,12 @@ struct Shared {
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_ptr)(lds + s % SLOTS * bytes + (i * 4 + wave) * 1024), 16,
                                                          s * 128 + piece * 8 < D ? col[i] : kNowhere, s * 256, 0, 0);
         };
+        auto load_step = [&](int s, int slot) {
+            load_x(s);
+            loads_stay_in_order();
+            load_w(s, slot);
+            loads_stay_in_order();
+        };
         auto multiply = [&](int s, int j) {
             const char *const tile = lds + s % SLOTS * bytes + (lane & 15) * 256;
 #pragma unroll
@@ -358,10 +377,8 @@ struct Shared {
             load_scales(0);
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j)
-            if (j < n) {
-                load_x(j);
-                load_w(j, j);
-            }
+            if (j < n)
+                load_step(j, j);
         for (int s = 0; s < n; s += SLOTS) {
 #pragma unroll
             for (int j = 0; j < SLOTS; ++j) {
@@ -374,15 +391,14 @@ struct Shared {
                     if (now + 4 < n)
                         load_scales(now + 4);
                 }
-                // a step's columns come before its weight and two more steps
+                // behind a step's columns come its own weight (in bf16 the last step's may be
+                // six loads short, for which it is not counted) and AHEAD - 1 steps
                 if (now + AHEAD <= n)
                     wait_and_meet<(AHEAD - 1) * (NT + 2 * WL) + (FP4 ? 2 : 0)>();
                 else
                     wait_and_meet<0>();
-                if (now + AHEAD < n) {
-                    load_x(now + AHEAD);
-                    load_w(now + AHEAD, (j + AHEAD) % SLOTS);
-                }
+                if (now + AHEAD < n)
+                    load_step(now + AHEAD, (j + AHEAD) % SLOTS);
                 multiply(now, j);
             }
         }

@@ -265,15 +265,22 @@ __device__ __forceinline__ void finish(const ExpertOut &o, const f32x4 (&acc)[TI
 // of an 8-bit one the channels 16 (lane >> 4) .. and 64 + 16 (lane >> 4) ..; its
 // scale operand belongs to the block 32 (lane >> 4) .. in either case.
 //
-// What bounds it: with few rows the weight's bytes (128 rows over 64 experts of 4096 x
-// 7168, MXFP8 rows: 216 us, 4.9 TB/s, which is what a large copy reaches).  With many,
+// What bounds it: with few rows the weight's bytes, and how little of a block's time they
+// stream (16 rows for each of 64 experts of 4096 x 7168, MXFP8 rows: 216 us, 4.7 TB/s of
+// the 7.1 that reading alone reaches; 4 rows for each of 256: 600 us, 6.6 TB/s): 64
+// experts make four rounds of blocks, by 128 x 256 tiles as by 64 x 128, each with its own
+// filling and end, and row fragments without a row are multiplied too.  With many rows,
 // no single thing: MXFP4 rows by 256 x 256 tiles reach 2.6 PFLOP/s (512 rows for each of
-// 64 experts, 4096 x 4096: 416 us), the matrix pipes busy for a third of it; without
+// 64 experts, 4096 x 4096 with SwiGLU: 424 us), the matrix pipes busy for a third of it (by
+// count LDS's reads and writes for a slice take as long as its MFMAs); without
 // its loads the main loop is 25 % shorter, without the scales 10 %, without the LDS
 // reads 10 %, and a tile of 4096 channels spends 59 of its 84 thousand cycles there
-// (14 to fill the buffers, 8 for the results).  bf16 rows: 0.96 PFLOP/s (1024 rows for
-// each of 8 experts, 288 us: two rounds of 256 CUs and the short last tiles), the pipes
-// busy 40 %.
+// (14 to fill the buffers, 8 for the results).  Its registers are all taken: 20 bytes a lane
+// lie in scratch from before the loop until behind it.  bf16 rows: 0.94 PFLOP/s (1024 rows for
+// each of 8 experts, 293 us: two rounds of 256 CUs and the short last tiles), the pipes
+// busy 40 %.  8-bit rows: 1.76 PFLOP/s (512 rows for each of 64 experts, 4096 x 4096: 623 us,
+// where MXFP4 rows take 427) by 128 x 256 tiles, as four buffers of 256 x 256 would need more
+// than a CU's LDS.
 //
 // The MFMAs go in TI groups of TJ, one row of fragments each; after a group the
 // row's fragment of the next slice is read into the same registers, and a few of
@@ -725,9 +732,12 @@ hipError_t product(const ExpertRows &m, const ExpertIn &in, const ExpertOut &out
     return hipGetLastError();
 }
 
-// The tile, by what the host knows: an expert's rows on average, and how many blocks
+// The tile, by what the host knows: an expert's rows on average (of a padded buffer the
+// capacity, whatever the counts: a decode batch may get a larger tile padded than
+// contiguous; 16 rows for each of 64 experts take 216 us either way), and how many blocks
 // there would be (a ragged end for every second expert).  Large tiles take in the
-// least, small ones leave no CU idle and waste less of a short expert.  us with 256 x
+// least, small ones leave no CU idle and waste less of a short expert; the limits between
+// them are simple ones, up to 8 % behind the best of a line below.  us with 256 x
 // 256, 128 x 256, 128 x 128 and 64 x 128 (4096 x 4096 weights unless said):
 //   MXFP4, 64 experts   512 rows each 429, 493, 517, 654     64 rows 172, 162, 157, 171
 //                       16 rows (7168) 243, 206, 224, 215

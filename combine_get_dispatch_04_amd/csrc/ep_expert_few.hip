@@ -4,10 +4,15 @@
 //   out_t  = sum_k w[t,k] Wd_e h[t,e]
 // with up = [Wg; Wu] [E, 2I, H] and down = Wd [E, H, I] in bf16 or MXFP4.
 //
-// Bound by the weights' bytes: every expert that a token names is read once, by
-// blocks of 32 or 128 weight rows (half of them gates and half their ups in the first
-// launch) that go through all of its tokens.  The n-th named expert's blocks find it
-// themselves, from topk_idx; what they found is left for the second launch.
+// Bound by the weights' bytes: an expert that a token names is read by blocks of 32 or 128
+// weight rows (half of them gates and half their ups in the first launch).  Blocks of 32
+// go through its n tokens in ceil(n / 32) passes over the weight in the first launch and
+// ceil(n / 16) in the second; of 128 rows there are ceil(n / 64) and ceil(n / 32) blocks, a
+// pass each.  The form is chosen by the sizes alone, whatever the tokens name: 128 tokens,
+// 1 of 64 experts (bf16, H 4096, I 2048), take 577 us spread evenly, 352 with 96 of them at
+// one expert, and 169 with all there, whose 50 MB are then read four and eight times.  The
+// n-th named expert's blocks find it themselves, from topk_idx; what they found is left
+// for the second launch.
 //
 // The weight rows are the rows of MFMAs, straight from memory to registers, the
 // tokens their columns; a block's waves share the inner dimension and add up in
@@ -26,7 +31,8 @@
 // 32 tokens in bf16 349 + 193 for 3.2 GB (5.8 TB/s); 128 tokens, 2 of 8 experts in MXFP4
 // (H = I = 4096) 54 + 66 for 214 MB: a step of 128 channels takes a block 1.6 us, of which
 // its matrix work and its reads of LDS are 0.2 each and its 24 vector memory
-// instructions, at about 60 cycles, 0.6; the rest is latency (two blocks to a CU).
+// instructions, at about 60 cycles, 0.6; the rest is latency (two blocks to a CU), some of
+// it a wait for all loads in flight once in four steps (see run_fp4).
 #include "ep_common.h"
 #include "ep_internal.h"
 
@@ -96,9 +102,12 @@ struct Few {
     // Four blocks at a time, one per 16 lanes.  The weight comes from memory and is asked
     // for AHEAD steps before its use, the columns from a cache or LDS, one step.  The
     // scales come sixteen at a time (a row's request is 64 bytes whatever it takes of
-    // them), and four steps ahead: loads come back in their order, so that to wait for
-    // the last one is to wait for all.  (One token, 8 of 64 experts, H 7168, I 2048: with 1,
-    // 2 and 3 steps ahead 68, 61 and 66 us: registers.)
+    // them), four steps ahead, as loads come back in their order.  But they are loaded in
+    // one of two ways, so the compiler cannot count what is in flight behind them, and
+    // waits for all of it once in four steps.  (One token, 8 of 64 experts, H 7168, I 2048:
+    // with 1, 2 and 3 steps ahead 68, 61 and 66 us: registers.  Without staging they do not
+    // suffice as it is: of the 128 that four waves on a SIMD have each, pointers mostly lie
+    // in scratch, up to 124 bytes a lane.)
     __device__ __forceinline__ void run_fp4(int s0, int s1, int HB)
     {
         constexpr int SLOTS = 4, AHEAD = NT > 1 ? 1 : 2, RING = AHEAD > 1 ? 4 : 2, XS = NT > 1 ? 1 : 2;
@@ -289,7 +298,8 @@ __device__ __forceinline__ bool can_stage(const FewPlan &p, int n, int D, int64_
 // the whole inner dimension.  Steps of 128 elements; a step's columns are rows of
 // 256 bytes, piece c of column r in slot c ^ (r & 15).  Columns and weight are asked for
 // AHEAD steps before their use: seven where the buffers (64 KB, of two blocks on a CU)
-// and the registers reach that far, else three.
+// and the registers reach that far, else three (MXFP4: less behind every fourth step, which
+// waits for all loads).
 template <bool FP4, int NT>
 struct Shared {
     static constexpr int SLOTS = FP4 && NT <= 2 ? 8 : 4, AHEAD = SLOTS - 1, bytes = NT * 4096, WL = FP4 ? 1 : 4;
@@ -385,7 +395,7 @@ struct Shared {
                 const int now = s + j;
                 if (now >= n)
                     break;
-                if (FP4 && j % 4 == 0) {        // four steps ahead, as above
+                if (FP4 && j % 4 == 0) {        // four steps ahead, and a wait for all loads, as above
                     sc[0] = next[0];
                     sc[1] = next[1];
                     if (now + 4 < n)

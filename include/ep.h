@@ -654,7 +654,7 @@ ep_status_t ep_expert_product_backward(const uint16_t *d_y, const void *x, const
  *                b the same with up_e[I + i],  e = topk_idx[t, k]
  *   out[t, :]  = bf16( sum over k, in that order, of topk_weights[t, k] * down_e h[t, k] )
  * with fp32 sums; h goes into its product within 2^-16 of its value (as two
- * bf16).  An expert that a token names twice has its weights summed first.
+ * bf16; beyond bf16's largest, 3.39e38, as an infinity).  An expert that a token names twice has its weights summed first.
  *   x             [T, H] bf16 in.
  *   topk_idx      [T, K] int32 in: -1 = none; other values outside [0, E) are
  *                 counted in num_invalid and skipped.
